@@ -353,6 +353,119 @@ int qmx_qmm_gather_sorted(const uint32_t* w_packed, const void* scales, const vo
 int qmx_plan_batched(int batch, int M, int N, int K, int bits, int group_size, int dtype,
                      int num_cus, int* route, int* splits);
 
+/* ------------------------------------------------------------------------
+ * Paged key/value cache held in 4 bits.
+ *
+ * The affine format of the weights above, at 4 bits, for what an attention
+ * layer keeps of its tokens: a token's keys (and values) of one head are cut
+ * into groups of group_size elements, a group has a scale s and a bias b in
+ * `dtype`, and an element with code c stands for c * s + b.  Writing takes
+ * lo and hi, the group's least and greatest element: b = lo,
+ * s = (hi - lo) / 15 rounded to `dtype`, c = (x - b) / s rounded to nearest
+ * even and kept within 0..15 (0 where s is 0).  A group that holds a NaN or
+ * whose hi - lo is infinite reads back as NaN or infinite, whole.
+ *
+ * Tokens live in pages of page_size; token `at` of page p has the slot
+ * p * page_size + at.  With D = head_dim and G = D / group_size:
+ *   k_codes, v_codes : uint32 [num_pages, kv_heads, page_size * D / 8]
+ *   k_sb, v_sb       : [num_pages, kv_heads, page_size, G, 2] in `dtype`,
+ *                      scale then bias.
+ * A page and head holds page_size / 16 blocks of 16 tokens, 2 * D words each:
+ *   keys:   word (h * 16 + token) * (D / 32) + j holds elements
+ *           32j + 8h + e, e = 0..7, element e at bit 4 * (e / 2) + 16 * (e % 2)
+ *           (h = 0..3);
+ *   values: 16-bit half ((h * 16 + n) * (D / 64) + a) * 4 + i holds token
+ *           4h + i's elements 16 * (4a + f) + n, f = 0..3, at bit 4f
+ *           (n = 0..15),
+ * which is how the matrix cores take them: a lane's operand is one load.
+ *
+ * Supported: dtype QMX_F16 or QMX_BF16; head_dim 64, 128 or 256; group_size
+ * 32, 64 or 128, at most head_dim; page_size 16, 32, ..., a power of two up
+ * to 1024.  The four arrays are 16-byte aligned.
+ */
+typedef struct qmx_kv4_cache {
+    uint32_t* k_codes;
+    void* k_sb;
+    uint32_t* v_codes;
+    void* v_sb;
+    int num_pages, kv_heads, head_dim, page_size, group_size, dtype;
+} qmx_kv4_cache;
+
+/* qmx_kv_maps -- block table entries and slot maps of one step, from the
+ * requests' lengths, in one launch.  Request r has past[r] tokens in its
+ * pages and gets fresh[r] more (negative lengths count as 0):
+ *   query_offsets [requests + 1] : running sum of fresh, held to `tokens`;
+ *   kv_lens [requests]           : past[r] + its tokens within `tokens`;
+ *   block_table [requests, columns], rows table_stride apart: the pages that
+ *       request r lacks, ceil(kv_lens[r] / page_size) - ceil(past[r] /
+ *       page_size), are taken from free_pages in order, request after
+ *       request, and entered behind those it has (-1 where free_pages ends;
+ *       nothing is entered past `columns`); other entries stay;
+ *   slots, positions, request_ids [tokens] : of each new token, request after
+ *       request; slot -1 where its page is missing (an entry below 0, a column
+ *       past the table, a slot past 2^31 - 1), and all three -1 behind the last
+ *       token;
+ *   counts [2] : the sum of fresh, and the pages wanted (a caller sees here
+ *       that `tokens` or num_free was too small).
+ * page_size: any size of at least 1.  requests * columns is at most 2^31 - 1. */
+int qmx_kv_maps(const int32_t* past, const int32_t* fresh, int32_t* block_table,
+                const int32_t* free_pages, int requests, int columns, long long table_stride,
+                int num_free, int page_size, int tokens, int32_t* query_offsets, int32_t* kv_lens,
+                int32_t* slots, int32_t* positions, int32_t* request_ids, int32_t* counts,
+                void* stream);
+
+/* qmx_kv4_write -- quantises new tokens into the cache.  k, v: [tokens,
+ * kv_heads, head_dim] in the cache's dtype with unit element stride, tokens
+ * and heads *_token_stride and *_head_stride elements apart (any alignment
+ * of whole elements; 16-byte aligned rows are read faster).  slots: int32
+ * [tokens]; a slot below 0 or past the cache is skipped.  Slots of one call
+ * are distinct. */
+int qmx_kv4_write(const qmx_kv4_cache* cache, const void* k, const void* v, long long k_token_stride,
+                  long long k_head_stride, long long v_token_stride, long long v_head_stride,
+                  const int32_t* slots, int tokens, void* stream);
+
+/* qmx_kv4_read -- the values that cached tokens stand for, c * s + b rounded
+ * to dtype: k_out, v_out [tokens, kv_heads, head_dim], 16-byte aligned; zeros
+ * where the slot is below 0 or past the cache. */
+int qmx_kv4_read(const qmx_kv4_cache* cache, void* k_out, void* v_out, const int32_t* slots,
+                 int tokens, void* stream);
+
+/* qmx_kv4_attention -- causal attention of new tokens over the cache, which
+ * holds them already:
+ *   out[t, a] = sum_j softmax_j(scale * q[t, a] . k_j) v_j
+ * over the keys j of t's request that t sees.  Request r has the tokens
+ * query_offsets[r] .. query_offsets[r + 1] - 1, the last of its kv_lens[r]
+ * cached ones: the token at position p sees positions 0..p, with window > 0
+ * only the last `window` of them; a position whose block_table entry is
+ * outside 0..num_pages - 1, or past max_kv_len, is not seen.  Head a reads key
+ * head a / (heads / kv_heads).  A token that sees nothing, or belongs to no
+ * request, gets zeros.  What is not seen may hold anything, NaN included.
+ *   q     : [tokens, heads, head_dim], unit element stride, other strides in
+ *           elements; out: contiguous, 16-byte aligned; both in the cache's
+ *           dtype.
+ *   lse   : float32 [tokens, heads] or NULL: log of the sum of exp of the
+ *           scaled scores (-inf where nothing is seen).
+ *   max_query_len, max_kv_len : at least the longest request's new and cached
+ *           tokens (host numbers: they size the launch; queries of a request
+ *           past max_query_len are left unwritten).
+ *   scale : finite and above 0.
+ *   workspace : qmx_kv4_attention_workspace_bytes bytes, 16-byte aligned (NULL
+ *           where that is 0), overwritten; calls that share it are ordered.
+ * Scores and sums are float32 on exact codes; what multiplies the value codes,
+ * a probability times a scale, is rounded to dtype.  The split of the keys
+ * depends on the host arguments only, so reruns are bit-identical. */
+int qmx_kv4_attention(const qmx_kv4_cache* cache, const void* q, long long q_token_stride,
+                      long long q_head_stride, void* out, float* lse, const int32_t* block_table,
+                      int columns, long long table_stride, const int32_t* kv_lens,
+                      const int32_t* query_offsets, int requests, int tokens, int heads,
+                      int max_query_len, int max_kv_len, int window, float scale, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Workspace bytes qmx_kv4_attention needs (0 for arguments it refuses).
+ * Depends on the compute units of the current device. */
+size_t qmx_kv4_attention_workspace_bytes(int kv_heads, int head_dim, int requests, int tokens,
+                                         int heads, int max_query_len, int max_kv_len, int window);
+
 #ifdef __cplusplus
 }
 #endif

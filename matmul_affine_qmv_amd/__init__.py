@@ -59,6 +59,15 @@ _EXPORTS = {
                               + [ctypes.c_int] * 3 + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "qmx_qmm_gather_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 8 + [ctypes.c_void_p]
                                        + [ctypes.c_longlong] * 2),
+    "qmx_kv_maps": (ctypes.c_int, [ctypes.c_void_p] * 4 + [ctypes.c_int] * 2 + [ctypes.c_longlong]
+                    + [ctypes.c_int] * 3 + [ctypes.c_void_p] * 7),
+    "qmx_kv4_write": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_longlong] * 4
+                      + [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]),
+    "qmx_kv4_read": (ctypes.c_int, [ctypes.c_void_p] * 4 + [ctypes.c_int, ctypes.c_void_p]),
+    "qmx_kv4_attention_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 8),
+    "qmx_kv4_attention": (ctypes.c_int, [ctypes.c_void_p] * 2 + [ctypes.c_longlong] * 2 + [ctypes.c_void_p] * 3
+                          + [ctypes.c_int, ctypes.c_longlong] + [ctypes.c_void_p] * 2 + [ctypes.c_int] * 6
+                          + [ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "qmx_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "qmx_api_version": (ctypes.c_int, []),
 }
@@ -474,7 +483,12 @@ def tensor_bits(t: torch.Tensor):
     return t.numpy()
 
 
-__all__ = ["qmv", "qmm_t", "qmm_t_splitk", "qmm_t_splitk_noalloc", "qmm", "qmm_batched", "gather_qmm", "plan", "plan_batched",
+from .kv4 import (Kv4Cache, KvMaps, kv4_attention, kv4_attention_workspace_bytes, kv4_read,  # noqa: E402
+                  kv4_write, kv_maps)
+
+__all__ = ["Kv4Cache", "KvMaps", "kv_maps", "kv4_write", "kv4_read", "kv4_attention",
+           "kv4_attention_workspace_bytes",
+           "qmv", "qmm_t", "qmm_t_splitk", "qmm_t_splitk_noalloc", "qmm", "qmm_batched", "gather_qmm", "plan", "plan_batched",
            "matvec_q8_0",
            "matvec_q4_k", "matvec_q8_i8",
            "splitk_workspace_bytes", "qmm_workspace_bytes", "strerror", "api_version", "lib",

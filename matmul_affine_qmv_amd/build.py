@@ -24,7 +24,9 @@ LIB = os.path.join(PKG, "libqmx.so")
 CALIB_LIB = os.path.join(PKG, "libqmx_calib.so")
 
 SOURCES = ["qmv.hip", "qmm_b4.hip", "qmm_b8.hip", "qmm_b2.hip", "qmm_b3.hip", "qmm_b6.hip", "qmm_b5.hip",
-           "qmm_b1.hip", "blocks.hip", "q8_i8.hip", "qmm.hip", "qmx_api.cpp", "noalloc.hip"]
+           "qmm_b1.hip", "blocks.hip", "q8_i8.hip", "qmm.hip", "qmx_api.cpp", "noalloc.hip",
+           "kv4_attn_d256_bf16.hip", "kv4_attn_d256_f16.hip", "kv4_attn_d128_bf16.hip", "kv4_attn_d128_f16.hip",
+           "kv4_attn_d64_bf16.hip", "kv4_attn_d64_f16.hip", "kv4_cache.hip", "kv_maps.hip", "kv4_api.cpp"]
 CALIB_SOURCES = ["calib.hip"]
 ARCH = "gfx950"
 

@@ -1,0 +1,215 @@
+// kv4_api.cpp -- the C ABI of the paged 4-bit key/value cache: host-side
+// validation, how an attention call is cut up, and the launches.  Every check
+// runs before any launch.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "kv4.h"
+#include "kv4_attn_impl.h"
+#include "qmx.h"
+#include "qmx_internal.h"
+
+namespace {
+
+bool is_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int launch_status(hipError_t e) { return e == hipSuccess ? QMX_OK : QMX_ERR_LAUNCH; }
+
+int check_cache(const qmx_kv4_cache* c) {
+    if (!c) return QMX_ERR_NULL;
+    if (c->dtype != QMX_F16 && c->dtype != QMX_BF16) return QMX_ERR_DTYPE;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return QMX_ERR_SHAPE;
+    if ((c->group_size != 32 && c->group_size != 64 && c->group_size != 128) || c->group_size > c->head_dim)
+        return QMX_ERR_GROUP;
+    if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1))) return QMX_ERR_SHAPE;
+    if (c->num_pages < 0 || c->kv_heads < 1 || c->kv_heads > 1024) return QMX_ERR_SHAPE;
+    if (c->num_pages > 0) {
+        if (!c->k_codes || !c->k_sb || !c->v_codes || !c->v_sb) return QMX_ERR_NULL;
+        if (!is_aligned(c->k_codes, 16) || !is_aligned(c->k_sb, 16) || !is_aligned(c->v_codes, 16) ||
+            !is_aligned(c->v_sb, 16))
+            return QMX_ERR_ALIGN;
+    }
+    return QMX_OK;
+}
+
+qmx::Kv4View view(const qmx_kv4_cache* c) {
+    int shift = 0;
+    while ((16 << shift) < c->page_size) ++shift;
+    return {c->k_codes, static_cast<uint32_t*>(c->k_sb), c->v_codes, static_cast<uint32_t*>(c->v_sb),
+            c->num_pages, c->kv_heads, c->head_dim, shift, c->group_size, c->dtype};
+}
+
+bool good_heads(int heads, int kv_heads) {
+    return kv_heads >= 1 && kv_heads <= 1024 && heads >= kv_heads && heads <= 65536 && heads % kv_heads == 0;
+}
+
+// How a call is cut up; the one rule of the call and of its workspace's size.
+qmx::Kv4AttnPlan plan_for(int requests, int heads, int kv_heads, int dim, int max_query, int max_kv, int window) {
+    const int cus = qmx::device_cu_count();
+    return qmx::kv4_attn_plan(std::max(1, requests), heads, kv_heads, dim, std::max(1, max_query), max_kv, window,
+                              cus > 0 ? cus : 256);
+}
+
+size_t part_bytes(const qmx::Kv4AttnPlan& p, int tokens, int heads, int dim) {
+    return p.splits > 1 ? (size_t)p.splits * tokens * heads * (dim + 2) * sizeof(float) : 0;
+}
+
+}  // namespace
+
+namespace qmx {
+
+Kv4AttnPlan kv4_attn_plan(int requests, int heads, int kv_heads, int dim, int max_query, int max_kv, int window,
+                          int cus) {
+    Kv4AttnPlan p;
+    const long long rows = (long long)max_query * (heads / kv_heads);
+    const long long keys = std::max(1ll, window ? std::min((long long)max_kv, (long long)window + max_query + 31)
+                                                : (long long)max_kv);
+    long long most;   // splits that still have enough keys each
+    long long want;   // work-groups that fill the device
+    if (rows > 64) {
+        p.rt = 2, p.wm = 4, p.wk = 1;
+        want = 2ll * cus;
+        most = keys / 512;
+    } else {
+        p.rt = 1, p.wm = 1, p.wk = dim == 256 ? 4 : 8;
+        want = 4ll * cus;
+        most = keys / 512;
+    }
+    p.tiles = (int)((rows + 16 * p.rt * p.wm - 1) / (16 * p.rt * p.wm));
+    const long long items = std::max(1ll, (long long)requests * kv_heads * p.tiles);
+    long long splits = std::min((want + items - 1) / items, most);
+    if (p.wk > 1 && splits > 1) splits = std::max(splits, keys / 1024);
+    splits = std::max(1ll, std::min(splits, 256ll));
+    p.chunk = (int)std::min((long long)INT_MAX & ~31, ((keys + splits - 1) / splits + 31) / 32 * 32);
+    p.splits = (int)((keys + p.chunk - 1) / p.chunk);
+    return p;
+}
+
+hipError_t launch_kv4_attn(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t st) {
+    const bool half = a.c.dt == DT_F16;
+    switch (a.c.dim) {
+        case 64: return half ? kv4::launch_dim<64, DT_F16>(a, p, st) : kv4::launch_dim<64, DT_BF16>(a, p, st);
+        case 128: return half ? kv4::launch_dim<128, DT_F16>(a, p, st) : kv4::launch_dim<128, DT_BF16>(a, p, st);
+        default: return half ? kv4::launch_dim<256, DT_F16>(a, p, st) : kv4::launch_dim<256, DT_BF16>(a, p, st);
+    }
+}
+
+}  // namespace qmx
+
+extern "C" {
+
+int qmx_kv_maps(const int32_t* past, const int32_t* fresh, int32_t* block_table, const int32_t* free_pages,
+                int requests, int columns, long long table_stride, int num_free, int page_size, int tokens,
+                int32_t* query_offsets, int32_t* kv_lens, int32_t* slots, int32_t* positions,
+                int32_t* request_ids, int32_t* counts, void* stream) {
+    if (requests < 0 || columns < 0 || num_free < 0 || tokens < 0 || page_size < 1) return QMX_ERR_SHAPE;
+    if ((long long)requests * columns > INT_MAX || requests == INT_MAX) return QMX_ERR_SHAPE;
+    if (requests > 1 && table_stride < columns) return QMX_ERR_SHAPE;
+    if (!query_offsets || !counts) return QMX_ERR_NULL;
+    if (requests > 0 && (!past || !fresh || !kv_lens)) return QMX_ERR_NULL;
+    if (requests > 0 && columns > 0 && !block_table) return QMX_ERR_NULL;
+    if (num_free > 0 && !free_pages) return QMX_ERR_NULL;
+    if (tokens > 0 && (!slots || !positions || !request_ids)) return QMX_ERR_NULL;
+    for (const void* p : {(const void*)past, (const void*)fresh, (const void*)block_table, (const void*)free_pages,
+                          (const void*)query_offsets, (const void*)kv_lens, (const void*)slots,
+                          (const void*)positions, (const void*)request_ids, (const void*)counts})
+        if (!is_aligned(p, 4)) return QMX_ERR_ALIGN;
+    const qmx::KvMapsArgs a = {past, fresh, block_table, free_pages, table_stride, requests, columns, num_free,
+                               page_size, tokens, query_offsets, kv_lens, slots, positions, request_ids, counts};
+    return launch_status(qmx::launch_kv_maps(a, static_cast<hipStream_t>(stream)));
+}
+
+int qmx_kv4_write(const qmx_kv4_cache* cache, const void* k, const void* v, long long k_token_stride,
+                  long long k_head_stride, long long v_token_stride, long long v_head_stride,
+                  const int32_t* slots, int tokens, void* stream) {
+    const int rc = check_cache(cache);
+    if (rc) return rc;
+    if (tokens < 0 || (long long)tokens * cache->kv_heads > (1ll << 31)) return QMX_ERR_SHAPE;
+    if (tokens == 0 || cache->num_pages == 0) return QMX_OK;
+    if (!k || !v || !slots) return QMX_ERR_NULL;
+    if (!is_aligned(k, 2) || !is_aligned(v, 2) || !is_aligned(slots, 4)) return QMX_ERR_ALIGN;
+    return launch_status(qmx::launch_kv4_write(view(cache), k, v, k_token_stride, k_head_stride, v_token_stride,
+                                               v_head_stride, slots, tokens, static_cast<hipStream_t>(stream)));
+}
+
+int qmx_kv4_read(const qmx_kv4_cache* cache, void* k_out, void* v_out, const int32_t* slots, int tokens,
+                 void* stream) {
+    const int rc = check_cache(cache);
+    if (rc) return rc;
+    if (tokens < 0 || (long long)tokens * cache->kv_heads > (1ll << 31)) return QMX_ERR_SHAPE;
+    if (tokens == 0) return QMX_OK;
+    if (!k_out || !v_out || !slots) return QMX_ERR_NULL;
+    if (!is_aligned(k_out, 16) || !is_aligned(v_out, 16) || !is_aligned(slots, 4)) return QMX_ERR_ALIGN;
+    return launch_status(qmx::launch_kv4_read(view(cache), k_out, v_out, slots, tokens,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+size_t qmx_kv4_attention_workspace_bytes(int kv_heads, int head_dim, int requests, int tokens, int heads,
+                                         int max_query_len, int max_kv_len, int window) {
+    if (!good_heads(heads, kv_heads) || (head_dim != 64 && head_dim != 128 && head_dim != 256) || requests < 0 ||
+        tokens < 0 || max_query_len < 0 || max_kv_len < 0 || max_kv_len > INT_MAX - 64 || window < 0)
+        return 0;
+    return part_bytes(plan_for(requests, heads, kv_heads, head_dim, max_query_len, max_kv_len, window), tokens,
+                      heads, head_dim);
+}
+
+int qmx_kv4_attention(const qmx_kv4_cache* cache, const void* q, long long q_token_stride, long long q_head_stride,
+                      void* out, float* lse, const int32_t* block_table, int columns, long long table_stride,
+                      const int32_t* kv_lens, const int32_t* query_offsets, int requests, int tokens, int heads,
+                      int max_query_len, int max_kv_len, int window, float scale, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    const int rc = check_cache(cache);
+    if (rc) return rc;
+    if (!good_heads(heads, cache->kv_heads)) return QMX_ERR_SHAPE;
+    if (requests < 0 || tokens < 0 || columns < 0 || max_query_len < 0 || max_kv_len < 0 || window < 0)
+        return QMX_ERR_SHAPE;
+    if (max_query_len > tokens || max_kv_len > INT_MAX - 64 || requests > (1 << 24)) return QMX_ERR_SHAPE;
+    if (!std::isfinite(scale) || scale <= 0.0f) return QMX_ERR_SHAPE;
+    if ((long long)columns * cache->page_size > INT_MAX) return QMX_ERR_SHAPE;
+    if (requests > 1 && table_stride < columns) return QMX_ERR_SHAPE;
+    if (tokens == 0) return QMX_OK;
+    if (!q || !out || !query_offsets) return QMX_ERR_NULL;
+    if (requests > 0 && (!kv_lens || (columns > 0 && !block_table))) return QMX_ERR_NULL;
+    if (!is_aligned(q, 2) || !is_aligned(out, 16) || !is_aligned(lse, 4) || !is_aligned(block_table, 4) ||
+        !is_aligned(kv_lens, 4) || !is_aligned(query_offsets, 4))
+        return QMX_ERR_ALIGN;
+    const int queries = std::max(1, max_query_len);
+    const auto p = plan_for(requests, heads, cache->kv_heads, cache->head_dim, max_query_len, max_kv_len, window);
+    const long long groups = (long long)p.splits * (requests + 1) * p.tiles * cache->kv_heads;
+    if (groups > INT_MAX || (long long)(requests + 1) * queries * heads > INT_MAX) return QMX_ERR_SHAPE;
+    if (p.splits > 1 && (!workspace || !is_aligned(workspace, 16) ||
+                         workspace_bytes < part_bytes(p, tokens, heads, cache->head_dim)))
+        return QMX_ERR_WORKSPACE;
+    qmx::Kv4AttnArgs a = {};
+    a.c = view(cache);
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.part = static_cast<float*>(workspace);
+    a.table = block_table;
+    a.kv_lens = kv_lens;
+    a.offsets = query_offsets;
+    a.q_ts = q_token_stride;
+    a.q_hs = q_head_stride;
+    a.table_stride = table_stride;
+    a.requests = requests;
+    a.tokens = tokens;
+    a.heads = heads;
+    a.each = heads / cache->kv_heads;
+    a.columns = columns;
+    a.max_query = queries;
+    // With no page in the cache nothing is seen, and no address formed.
+    a.max_kv = cache->num_pages > 0 ? max_kv_len : 0;
+    a.window = window;
+    a.splits = p.splits;
+    a.chunk = p.chunk;
+    a.tiles = p.tiles;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    return launch_status(qmx::launch_kv4_attn(a, p, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
