@@ -9,7 +9,7 @@
 #include <cstdint>
 
 #include "kv4.h"
-#include "kv4_attn_impl.h"
+#include "kv4_attn_launch.h"
 #include "qmx.h"
 #include "qmx_internal.h"
 
@@ -50,12 +50,8 @@ bool good_heads(int heads, int kv_heads) {
 // How a call is cut up; the one rule of the call and of its workspace's size.
 qmx::Kv4AttnPlan plan_for(int requests, int heads, int kv_heads, int dim, int max_query, int max_kv, int window) {
     const int cus = qmx::device_cu_count();
-    return qmx::kv4_attn_plan(std::max(1, requests), heads, kv_heads, dim, std::max(1, max_query), max_kv, window,
+    return qmx::kv4_attn_plan(requests, heads, kv_heads, dim, std::max(1, max_query), max_kv, window,
                               cus > 0 ? cus : 256);
-}
-
-size_t part_bytes(const qmx::Kv4AttnPlan& p, int tokens, int heads, int dim) {
-    return p.splits > 1 ? (size_t)p.splits * tokens * heads * (dim + 2) * sizeof(float) : 0;
 }
 
 }  // namespace
@@ -66,35 +62,28 @@ Kv4AttnPlan kv4_attn_plan(int requests, int heads, int kv_heads, int dim, int ma
                           int cus) {
     Kv4AttnPlan p;
     const long long rows = (long long)max_query * (heads / kv_heads);
-    const long long keys = std::max(1ll, window ? std::min((long long)max_kv, (long long)window + max_query + 31)
-                                                : (long long)max_kv);
-    long long most;   // splits that still have enough keys each
-    long long want;   // work-groups that fill the device
-    if (rows > 64) {
-        p.rt = 2, p.wm = 4, p.wk = 1;
-        want = 2ll * cus;
-        most = keys / 512;
-    } else {
-        p.rt = 1, p.wm = 1, p.wk = dim == 256 ? 4 : 8;
-        want = 4ll * cus;
-        most = keys / 512;
-    }
-    p.tiles = (int)((rows + 16 * p.rt * p.wm - 1) / (16 * p.rt * p.wm));
-    const long long items = std::max(1ll, (long long)requests * kv_heads * p.tiles);
-    long long splits = std::min((want + items - 1) / items, most);
-    if (p.wk > 1 && splits > 1) splits = std::max(splits, keys / 1024);
-    splits = std::max(1ll, std::min(splits, 256ll));
-    p.chunk = (int)std::min((long long)INT_MAX & ~31, ((keys + splits - 1) / splits + 31) / 32 * 32);
-    p.splits = (int)((keys + p.chunk - 1) / p.chunk);
+    const long long keys = window ? std::min((long long)max_kv, (long long)window + max_query) : (long long)max_kv;
+    const bool prompt = rows > 64;
+    p.rows = prompt ? kv4::PROMPT_ROWS : 16;
+    p.tiles = (int)((rows + p.rows - 1) / p.rows);
+    const long long units = (long long)requests * p.tiles;
+    const bool line = keys > 1024 && (!prompt || units * kv_heads < 4 * cus) && units > 0 &&
+                      units <= KV4_LINE_UNITS && units * (keys / 32 + 32) <= INT_MAX;
+    p.waves = prompt ? kv4::PROMPT_WAVES : line || dim == 256 ? 4 : 8;
+    p.lines = line ? std::max(1, (prompt ? 1 : 2) * cus / kv_heads) : 0;
+    // A unit's queries, first loads and joining waves wait on memory about four
+    // times, as long as its work-group takes for some 16 steps of 16 rows.
+    p.cost = prompt ? 8 : 16;
+    p.least = 8;
     return p;
 }
 
-hipError_t launch_kv4_attn(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t st) {
+hipError_t launch_kv4_attn(const Kv4AttnArgs& a, hipStream_t st) {
     const bool half = a.c.dt == DT_F16;
     switch (a.c.dim) {
-        case 64: return half ? kv4::launch_dim<64, DT_F16>(a, p, st) : kv4::launch_dim<64, DT_BF16>(a, p, st);
-        case 128: return half ? kv4::launch_dim<128, DT_F16>(a, p, st) : kv4::launch_dim<128, DT_BF16>(a, p, st);
-        default: return half ? kv4::launch_dim<256, DT_F16>(a, p, st) : kv4::launch_dim<256, DT_BF16>(a, p, st);
+        case 64: return half ? kv4::launch_dim<64, DT_F16>(a, st) : kv4::launch_dim<64, DT_BF16>(a, st);
+        case 128: return half ? kv4::launch_dim<128, DT_F16>(a, st) : kv4::launch_dim<128, DT_BF16>(a, st);
+        default: return half ? kv4::launch_dim<256, DT_F16>(a, st) : kv4::launch_dim<256, DT_BF16>(a, st);
     }
 }
 
@@ -153,8 +142,8 @@ size_t qmx_kv4_attention_workspace_bytes(int kv_heads, int head_dim, int request
     if (!good_heads(heads, kv_heads) || (head_dim != 64 && head_dim != 128 && head_dim != 256) || requests < 0 ||
         tokens < 0 || max_query_len < 0 || max_kv_len < 0 || max_kv_len > INT_MAX - 64 || window < 0)
         return 0;
-    return part_bytes(plan_for(requests, heads, kv_heads, head_dim, max_query_len, max_kv_len, window), tokens,
-                      heads, head_dim);
+    return qmx::kv4_attn_workspace(plan_for(requests, heads, kv_heads, head_dim, max_query_len, max_kv_len, window),
+                                   requests, kv_heads, head_dim);
 }
 
 int qmx_kv4_attention(const qmx_kv4_cache* cache, const void* q, long long q_token_stride, long long q_head_stride,
@@ -179,17 +168,23 @@ int qmx_kv4_attention(const qmx_kv4_cache* cache, const void* q, long long q_tok
         return QMX_ERR_ALIGN;
     const int queries = std::max(1, max_query_len);
     const auto p = plan_for(requests, heads, cache->kv_heads, cache->head_dim, max_query_len, max_kv_len, window);
-    const long long groups = (long long)p.splits * (requests + 1) * p.tiles * cache->kv_heads;
-    if (groups > INT_MAX || (long long)(requests + 1) * queries * heads > INT_MAX) return QMX_ERR_SHAPE;
-    if (p.splits > 1 && (!workspace || !is_aligned(workspace, 16) ||
-                         workspace_bytes < part_bytes(p, tokens, heads, cache->head_dim)))
-        return QMX_ERR_WORKSPACE;
+    const size_t need = qmx::kv4_attn_workspace(p, requests, cache->kv_heads, cache->head_dim);
+    if (need && (!workspace || !is_aligned(workspace, 16) || workspace_bytes < need)) return QMX_ERR_WORKSPACE;
+    if ((long long)(requests + 1) * std::max<long long>((long long)p.tiles * cache->kv_heads,
+                                                        (long long)queries * heads) > INT_MAX)
+        return QMX_ERR_SHAPE;
     qmx::Kv4AttnArgs a = {};
     a.c = view(cache);
     a.q = q;
     a.out = out;
     a.lse = lse;
-    a.part = static_cast<float*>(workspace);
+    a.p = p;
+    if (need) {
+        const size_t places = (size_t)2 * p.lines * cache->kv_heads * p.rows;
+        a.part = static_cast<float*>(workspace);
+        a.stat = a.part + places * cache->head_dim;
+        a.pos = reinterpret_cast<int*>(a.stat + 2 * places);
+    }
     a.table = block_table;
     a.kv_lens = kv_lens;
     a.offsets = query_offsets;
@@ -205,11 +200,8 @@ int qmx_kv4_attention(const qmx_kv4_cache* cache, const void* q, long long q_tok
     // With no page in the cache nothing is seen, and no address formed.
     a.max_kv = cache->num_pages > 0 ? max_kv_len : 0;
     a.window = window;
-    a.splits = p.splits;
-    a.chunk = p.chunk;
-    a.tiles = p.tiles;
     a.scale_log2 = scale * 1.4426950408889634f;
-    return launch_status(qmx::launch_kv4_attn(a, p, static_cast<hipStream_t>(stream)));
+    return launch_status(qmx::launch_kv4_attn(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

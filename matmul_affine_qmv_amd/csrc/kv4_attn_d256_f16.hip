@@ -1,8 +1,8 @@
 // kv4_attn_d256_f16.hip -- attention over the 4-bit cache, head size 256, float16.
-#include "kv4_attn_impl.h"
+#include "kv4_attn_launch.h"
 
 namespace qmx {
 namespace kv4 {
-template hipError_t launch_dim<256, DT_F16>(const Kv4AttnArgs&, const Kv4AttnPlan&, hipStream_t);
+template hipError_t launch_dim<256, DT_F16>(const Kv4AttnArgs&, hipStream_t);
 }  // namespace kv4
 }  // namespace qmx

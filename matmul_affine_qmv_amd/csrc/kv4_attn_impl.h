@@ -24,19 +24,20 @@
 // that of p_t s_tg (half a step: 2^-8 of it in bfloat16, 2^-11 in float16), which
 // the matrix cores need.
 //
-// The running maximum is raised only when a score passes it by more than
+// One work-group of WK waves takes a unit (kv4.h); the waves take every WK-th
+// step and are joined in LDS.  The running maximum is raised only when a score passes it by more than
 // kSlack (in powers of two); until then no lane needs another's scores.
 #pragma once
 
 #include <type_traits>
 
 #include "kv4.h"
+#include "kv4_units.h"
 #include "qmx_device.h"
 
 namespace qmx {
 namespace kv4 {
 
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
@@ -100,11 +101,45 @@ __device__ __forceinline__ float row_max(float v) {
     return fmaxf(v, __shfl_xor(v, 32, 64));
 }
 
-// The codes and pairs of 32 tokens, as one lane holds them.
-template <int NJ, int G>
-struct Tokens {
-    uint32_t k[2][NJ], v[2][NJ], ks[2][4 * G], vs[2][4 * G];
-    bool there[2];   // the block's page is in the cache
+// Lane k's value of each row of 16 lanes, for all of the row; k is a constant
+// once loops are unrolled.  The move folds into the product that takes it.
+__device__ __forceinline__ float row_lane(float v, int k) {
+    const int x = __float_as_int(v);
+#define QMX_ROW_LANE(K) \
+    case K: return __int_as_float(__builtin_amdgcn_mov_dpp(x, 0x150 + K, 0xf, 0xf, true));
+    switch (k) {
+        QMX_ROW_LANE(0) QMX_ROW_LANE(1) QMX_ROW_LANE(2) QMX_ROW_LANE(3) QMX_ROW_LANE(4) QMX_ROW_LANE(5)
+        QMX_ROW_LANE(6) QMX_ROW_LANE(7) QMX_ROW_LANE(8) QMX_ROW_LANE(9) QMX_ROW_LANE(10) QMX_ROW_LANE(11)
+        QMX_ROW_LANE(12) QMX_ROW_LANE(13) QMX_ROW_LANE(14) QMX_ROW_LANE(15)
+    }
+#undef QMX_ROW_LANE
+    return v;
+}
+
+// The (scale, bias) pairs of a block's tokens.  The 16 lanes of a row all need
+// the 4 * G pairs of the row's four tokens, keys' and values': each lane holds
+// its share, as numbers, and row_lane passes them round.  The biases are set
+// right for the codes' offset: keys' b - OFF s, values' b + 8 s.
+template <int DT, int G>
+struct Pairs {
+    static constexpr int PAIRS = (8 * G + 15) / 16;
+    float s[PAIRS], b[PAIRS];
+    __device__ __forceinline__ void set(const uint32_t (&w)[PAIRS]) {
+#pragma unroll
+        for (int r = 0; r < PAIRS; ++r) {
+            const float shift = ((16 * r + (int)(threadIdx.x & 15)) & (4 * G)) ? 8.0f : -Half<DT>::OFF;
+            s[r] = half_lo<DT>(w[r]);
+            b[r] = fmaf(shift, s[r], half_hi<DT>(w[r]));
+        }
+    }
+    __device__ __forceinline__ float scale(bool value, int i, int g) const {
+        const int at = (value ? 4 * G : 0) + i * G + g;
+        return row_lane(s[at / 16], at % 16);
+    }
+    __device__ __forceinline__ float bias(bool value, int i, int g) const {
+        const int at = (value ? 4 * G : 0) + i * G + g;
+        return row_lane(b[at / 16], at % 16);
+    }
 };
 
 template <int N>
@@ -123,347 +158,290 @@ __device__ __forceinline__ void load_words(uint32_t (&to)[N], const uint32_t* fr
     }
 }
 
-// One wave's rows and its state.
-template <int D, int GS, int DT, int RT>
+// One wave's 16 rows, its state, and the 32 tokens at hand.
+template <int D, int GS, int DT>
 struct Rows {
     static constexpr int NJ = D / 32, G = D / GS, NB = D / 16;
     using H = Half<DT>;
-    u32x4 q[RT][NJ];
-    float qsum[RT][G];
-    float m[RT], top[RT], l[RT];   // the maximum taken off (0 at first), what a score may reach, the sum
-    float fix[RT][G];              // sum p b + the offsets of V's codes, this lane's tokens
-    f32x4 o[RT][NB];
-    int lo[RT], hi[RT];            // keys the row sees
+    u32x4 q[NJ];
+    float qsum[G];
+    float m, top, l;   // the maximum taken off (0 at first), what a score may reach, the sum
+    float fix[G];      // sum p b + the offsets of V's codes, this lane's tokens
+    f32x4 o[NB];
+    int lo, hi;        // keys the row sees
+    uint32_t k[2][NJ], v[2][NJ], sb[2][Pairs<DT, G>::PAIRS];
+    float s[8];        // scores, then probabilities
 
     __device__ __forceinline__ void clear() {
+        m = 0.0f;
+        top = -INFINITY;
+        l = 0.0f;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            m[r] = 0.0f;
-            top[r] = -INFINITY;
-            l[r] = 0.0f;
+        for (int g = 0; g < G; ++g) fix[g] = 0.0f;
 #pragma unroll
-            for (int g = 0; g < G; ++g) fix[r][g] = 0.0f;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) o[r][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        }
+        for (int b = 0; b < NB; ++b) o[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    // 32 tokens from `key` on.  MASK: some row does not see all of them.
-    template <bool MASK>
-    __device__ __forceinline__ void step(const Tokens<NJ, G>& x, int key, float scale) {
-        const int h = (threadIdx.x & 63) >> 4;
-        float s[RT][8];
+    // `at`: the numbers of the two blocks.
+    __device__ __forceinline__ void load_pairs(const Kv4View& c, const size_t (&at)[2]) {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int r = 0; r < Pairs<DT, G>::PAIRS; ++r) {
+                const int w = 16 * r + (lane & 15);   // of the row's 8 * G pairs (fewer than 16: the rest repeat)
+                const uint32_t* from = (w & (4 * G)) ? c.vs : c.ks;
+                sb[i][r] = from[at[i] * (16 * G) + (lane >> 4) * (4 * G) + (w & (4 * G - 1))];
+            }
+    }
+    __device__ __forceinline__ void load_codes(uint32_t (&to)[2][NJ], const uint32_t* codes, const size_t (&at)[2]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) load_words(to[i], codes + at[i] * (64 * NJ) + (threadIdx.x & 63) * NJ);
+    }
+
+    __device__ __forceinline__ void scores(const Pairs<DT, G> (&pair)[2]) {
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                f32x4 part[RT];
-#pragma unroll
-                for (int r = 0; r < RT; ++r) part[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int j = g * (GS / 32); j < (g + 1) * (GS / 32); ++j) {
-                    const uint32_t w = x.k[blk][j];
+                    const uint32_t w = k[blk][j];
                     const u32x4 a = {H::codes(w, 0), H::codes(w, 1), H::codes(w, 2), H::codes(w, 3)};
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) part[r] = H::mfma(a, q[r][j], part[r]);
+                    part = H::mfma(a, q[j], part);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t sb = x.ks[blk][i * G + g];
-                    const float sc = half_lo<DT>(sb), b = fmaf(-H::OFF, sc, half_hi<DT>(sb));
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        float& to = s[r][4 * blk + i];
-                        to = g == 0 ? b * qsum[r][g] : fmaf(b, qsum[r][g], to);
-                        to = fmaf(sc, part[r][i], to);
-                    }
+                    float& to = s[4 * blk + i];
+                    const float b = pair[blk].bias(false, i, g);
+                    to = g == 0 ? b * qsum[g] : fmaf(b, qsum[g], to);
+                    to = fmaf(pair[blk].scale(false, i, g), part[i], to);
                 }
             }
         }
-        uint32_t seen[RT];   // a bit for each of the lane's tokens
+    }
+
+    // The tokens from `key` on that the row sees, a bit each.
+    __device__ __forceinline__ uint32_t hide(int key, bool there0, bool there1) {
+        const int h = (threadIdx.x & 63) >> 4;
+        uint32_t seen = 0;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            seen[r] = 0xffu;
-            if constexpr (MASK) {
-                seen[r] = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int t = key + 16 * (e / 4) + 4 * h + e % 4;
-                    const bool see = t >= lo[r] && t <= hi[r] && x.there[e / 4];
-                    seen[r] |= (see ? 1u : 0u) << e;
-                    s[r][e] = see ? s[r][e] : -INFINITY;
-                }
-            }
-            float mx = s[r][0];
-#pragma unroll
-            for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[r][e]);
-            mx *= scale;
-            if (__any(mx > top[r])) {
-                const float now = row_max(fmaxf(mx, top[r] - H::kSlack));
-                const float safe = now > -INFINITY ? now : 0.0f;
-                const float fade = top[r] > -INFINITY ? __builtin_amdgcn_exp2f(m[r] - safe) : 0.0f;
-                top[r] = now + H::kSlack;
-                m[r] = safe;
-                l[r] *= fade;
-#pragma unroll
-                for (int g = 0; g < G; ++g) fix[r][g] *= fade;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) o[r][b] *= fade;
-            }
+        for (int e = 0; e < 8; ++e) {
+            const int t = key + 16 * (e / 4) + 4 * h + e % 4;
+            const bool see = t >= lo && t <= hi && (e < 4 ? there0 : there1);
+            seen |= (see ? 1u : 0u) << e;
+            s[e] = see ? s[e] : -INFINITY;
         }
-        // p, and p s as the matrix cores take it
-        u32x4 ps[RT][G];
+        return seen;
+    }
+
+    __device__ __forceinline__ void probabilities(float scale) {
+        float mx = s[0];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
+        for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[e]);
+        mx *= scale;
+        if (__any(mx > top)) {
+            const float now = row_max(fmaxf(mx, top - H::kSlack));
+            const float safe = now > -INFINITY ? now : 0.0f;
+            const float fade = top > -INFINITY ? __builtin_amdgcn_exp2f(m - safe) : 0.0f;
+            top = now + H::kSlack;
+            m = safe;
+            l *= fade;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                s[r][e] = __builtin_amdgcn_exp2f(fmaf(s[r][e], scale, -m[r]));
-                if constexpr (MASK) s[r][e] = (seen[r] >> e) & 1u ? s[r][e] : 0.0f;
-                l[r] += s[r][e];
-            }
+            for (int g = 0; g < G; ++g) fix[g] *= fade;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) o[b] *= fade;
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], scale, -m));
+            l += s[e];
+        }
+    }
+
+    // all: every row sees every token; else `seen` says.  What is not seen has a
+    // probability of 0, but its scale and bias may be infinite.
+    __device__ __forceinline__ void values(const Pairs<DT, G> (&pair)[2], bool all, uint32_t seen) {
+        u32x4 ps[G];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            float sc[8], b[8];
+            float w[8], y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const uint32_t sb = x.vs[e / 4][(e % 4) * G + g];
-                sc[e] = half_lo<DT>(sb);
-                b[e] = fmaf(8.0f, sc[e], half_hi<DT>(sb));
+                w[e] = s[e] * pair[e / 4].scale(true, e % 4, g);
+                y[e] = pair[e / 4].bias(true, e % 4, g);
             }
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                float w[8];
+            if (!all) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const bool see = !MASK || ((seen[r] >> e) & 1u);   // what is not seen may hold infinities
-                    w[e] = see ? s[r][e] * sc[e] : 0.0f;
-                    fix[r][g] = see ? fmaf(s[r][e], b[e], fix[r][g]) : fix[r][g];
+                    w[e] = (seen >> e) & 1u ? w[e] : 0.0f;
+                    y[e] = (seen >> e) & 1u ? y[e] : 0.0f;
                 }
-                float sum = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    ps[r][g][e] = H::pack(w[2 * e], w[2 * e + 1]);
-                    sum = H::dot2(ps[r][g][e], H::ONES, sum);
-                }
-                fix[r][g] = fmaf(-(H::OFF + 8.0f), sum, fix[r][g]);
             }
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) fix[g] = fmaf(s[e], y[e], fix[g]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                ps[g][e] = H::pack(w[2 * e], w[2 * e + 1]);
+                sum = H::dot2(ps[g][e], H::ONES, sum);
+            }
+            fix[g] = fmaf(-(H::OFF + 8.0f), sum, fix[g]);
         }
 #pragma unroll
         for (int a = 0; a < D / 64; ++a) {
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
-                const u32x4 v = {H::codes(x.v[0][2 * a], f), H::codes(x.v[0][2 * a + 1], f),
-                                 H::codes(x.v[1][2 * a], f), H::codes(x.v[1][2 * a + 1], f)};
+                const u32x4 x = {H::codes(v[0][2 * a], f), H::codes(v[0][2 * a + 1], f),
+                                 H::codes(v[1][2 * a], f), H::codes(v[1][2 * a + 1], f)};
                 const int nb = 4 * a + f;
-#pragma unroll
-                for (int r = 0; r < RT; ++r) o[r][nb] = H::mfma(v, ps[r][nb * 16 / GS], o[r][nb]);
+                o[nb] = H::mfma(x, ps[nb * 16 / GS], o[nb]);
             }
         }
     }
 
     // Adds the lanes' parts: after this o is the row's sum of p v, l of p.
     __device__ __forceinline__ void join() {
+        l = row_sum(l);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            l[r] = row_sum(l[r]);
+        for (int g = 0; g < G; ++g) fix[g] = row_sum(fix[g]);
 #pragma unroll
-            for (int g = 0; g < G; ++g) fix[r][g] = row_sum(fix[r][g]);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) o[r][b] += fix[r][b * 16 / GS];
-        }
+        for (int b = 0; b < NB; ++b) o[b] += fix[b * 16 / GS];
     }
 };
 
-// 32 tokens from step * 32 on into registers.  `table` is the request's row of
-// the block table; blocks from `blocks` on are not read.
-template <int NJ, int G>
-__device__ __forceinline__ void load_tokens(Tokens<NJ, G>& x, const Kv4View& c, const int* table, int blocks,
-                                            int head, int step) {
-    const int lane = threadIdx.x & 63;
+// A request's row of the block table, read a step (two blocks) at a time.
+struct Pages {
+    const int* table;
+    int blocks;   // those from here on are not there
+    int page[2];
+    __device__ __forceinline__ void read(const Kv4View& c, int step) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int blk = 2 * step + i;
-        int page = blk < blocks ? table[blk >> c.page_shift] : -1;
-        x.there[i] = page >= 0 && page < c.num_pages;
-        if (!x.there[i]) page = 0;
-        const size_t at = (((size_t)page * c.heads + head) << c.page_shift) + (blk & ((1 << c.page_shift) - 1));
-        load_words(x.k[i], c.kc + at * (64 * NJ) + lane * NJ);
-        load_words(x.v[i], c.vc + at * (64 * NJ) + lane * NJ);
-        load_words(x.ks[i], c.ks + at * (16 * G) + (lane >> 4) * (4 * G));
-        load_words(x.vs[i], c.vs + at * (16 * G) + (lane >> 4) * (4 * G));
+        for (int i = 0; i < 2; ++i) page[i] = 2 * step + i < blocks ? table[(2 * step + i) >> c.page_shift] : -1;
     }
-}
+    __device__ __forceinline__ bool there(const Kv4View& c, int i) const {
+        return page[i] >= 0 && page[i] < c.num_pages;
+    }
+    // The two blocks' numbers in the cache (page 0's where there is none: its
+    // tokens are hidden).
+    __device__ __forceinline__ void place(const Kv4View& c, int head, int step, size_t (&at)[2]) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            at[i] = (((size_t)(there(c, i) ? page[i] : 0) * c.heads + head) << c.page_shift) +
+                    ((2 * step + i) & ((1 << c.page_shift) - 1));
+    }
+};
 
-// Keys that a request's splits divide: from the first that its first query
-// sees (a multiple of 32) to the end.
-__device__ __forceinline__ void key_span(const Kv4AttnArgs& a, int kv, int count, int& begin, int& end) {
-    const int first = kv - count;
-    begin = a.window ? max(0, first - a.window + 1) & ~31 : 0;
-    end = min(kv, a.max_kv);
-}
-
-// WM waves along the rows, each with its own RT tiles; WK waves along the keys,
-// which take every WK-th step of 32 tokens and are joined in LDS.
-template <int D, int GS, int DT, int RT, int WM, int WK>
-__global__ __launch_bounds__(64 * WM * WK) void kv4_attn_kernel(Kv4AttnArgs a) {
-    static_assert(WM == 1 || WK == 1, "waves are along one axis");
-    using R = Rows<D, GS, DT, RT>;
+// WK waves on units of 16 rows.
+template <int D, int GS, int DT, int WK>
+__global__ __launch_bounds__(64 * WK, 2) void kv4_attn_kernel(Kv4AttnArgs a) {
+    using R = Rows<D, GS, DT>;
     constexpr int NJ = R::NJ, G = R::G, NB = R::NB, PITCH = D + 4;
-    __shared__ float s_o[WK > 1 ? WK : 1][WK > 1 ? 16 * PITCH : 1];
+    __shared__ float s_o[WK][16 * PITCH];
     __shared__ float s_m[WK][16], s_l[WK][16];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
     const Kv4View& c = a.c;
-
-    int id = blockIdx.x;
-    const int head = id % c.heads;
-    id /= c.heads;
-    const int tile = a.tiles - 1 - id % a.tiles;   // the tiles that see most keys first
-    id /= a.tiles;
-    const int req = id % (a.requests + 1);
-    const int split = id / (a.requests + 1);
-
-    if (req == a.requests) {   // the tokens of no request
-        if (split || a.splits > 1) return;
-        const int begin = max(a.offsets[a.requests], 0);
-        const long long per = (long long)a.each * D / 8;
-        const long long all = max(0, a.tokens - begin) * per;
-        for (long long i = (long long)tile * blockDim.x + threadIdx.x; i < all; i += (long long)a.tiles * blockDim.x) {
-            const long long at = (begin + i / per) * a.heads + (long long)head * a.each;
-            reinterpret_cast<u32x4*>(a.out)[at * (D / 8) + i % per] = u32x4{0, 0, 0, 0};
-            if (a.lse && i % per < a.each) a.lse[at + i % per] = -INFINITY;
-        }
-        return;
-    }
-
-    const int start = max(a.offsets[req], 0), kv = a.kv_lens[req];
-    const int count = min(min(a.offsets[req + 1], a.tokens) - start, a.max_query);
-    const int rows = count * a.each;
-    const int row0 = (tile * WM + (WM > 1 ? wave : 0)) * 16 * RT;
-    const bool mine = row0 < rows;
-    if (WK > 1 && !mine) return;   // the whole work-group
-
-    int begin, end;
-    key_span(a, kv, a.offsets[req + 1] - start, begin, end);
-    if (a.splits > 1) {
-        begin += split * a.chunk;
-        if (begin >= end) return;
-        end = min(end, begin + a.chunk);
-    }
-
-    R x;
-    x.clear();
-    const int back = kv - (a.offsets[req + 1] - start);   // the first query's position
-    const int last_row = min(row0 + 16 * RT, rows) - 1;
-    const int pos0 = back + row0 / a.each, pos1 = back + last_row / a.each;
     const float scale = a.scale_log2;
-    long long token[RT];
-    int qhead[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const int row = min(row0 + 16 * r + n, last_row);
-        const int i = mine ? row / a.each : 0;
-        token[r] = (long long)start + i;
-        qhead[r] = head * a.each + (mine ? row - i * a.each : 0);
-        const int pos = back + i;
-        x.lo[r] = a.window ? pos - a.window + 1 : 0;
-        x.hi[r] = min(pos, end - 1);
-    }
-    if (mine) {
-        const uint16_t* q = static_cast<const uint16_t*>(a.q);
+    const int head = blockIdx.x % c.heads;
+
+    Units<64 * WK> units(a, blockIdx.x / c.heads, head);
+    for (Unit u; units.next(a, u);) {
+        const int last = u.rows - 1;
+        const int row = min(n, last);
+        const int i = (u.row0 + row) / a.each;
+        const long long token = (long long)u.start + i;
+        const int qhead = head * a.each + u.row0 + row - i * a.each;
+        R x;
+        x.clear();
+        x.lo = a.window ? u.back + i - a.window + 1 : 0;
+        x.hi = min(u.back + i, u.end - 1);
+        const uint16_t* q = static_cast<const uint16_t*>(a.q) + token * a.q_ts + qhead * a.q_hs + 8 * h;
         const bool vec = (((uintptr_t)a.q & 15) | ((a.q_ts | a.q_hs) & 7)) == 0;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const uint16_t* from = q + token[r] * a.q_ts + qhead[r] * a.q_hs + 8 * h;
+        for (int j = 0; j < NJ; ++j) {
+            if (vec) {
+                x.q[j] = *reinterpret_cast<const u32x4*>(q + 32 * j);
+            } else {
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                if (vec) {
-                    x.q[r][j] = *reinterpret_cast<const u32x4*>(from + 32 * j);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        x.q[r][j][e] = (uint32_t)from[32 * j + 2 * e] | ((uint32_t)from[32 * j + 2 * e + 1] << 16);
-                }
-            }
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                float sum = 0.0f;
-#pragma unroll
-                for (int j = g * (GS / 32); j < (g + 1) * (GS / 32); ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sum += half_lo<DT>(x.q[r][j][e]) + half_hi<DT>(x.q[r][j][e]);
-                x.qsum[r][g] = row_sum(sum);
+                for (int e = 0; e < 4; ++e)
+                    x.q[j][e] = (uint32_t)q[32 * j + 2 * e] | ((uint32_t)q[32 * j + 2 * e + 1] << 16);
             }
         }
-        const int first = max(begin, a.window ? pos0 - a.window + 1 : 0);
-        const int stop = min(end, pos1 + 1);
-        const int full_lo = a.window ? pos1 - a.window + 1 : 0, full_hi = min(pos0, end - 1);
-        const int* table = a.table + req * a.table_stride;
-        const int blocks = min(((stop + 15) >> 4), a.columns << c.page_shift);
-        int step = first >> 5;
-        if (WK > 1) step += wave;
-        const int steps = (stop + 31) >> 5;
-        Tokens<NJ, G> t[2];
-        auto work = [&](const Tokens<NJ, G>& y, int at) {
-            const int key = at * 32;
-            if (key >= full_lo && key + 31 <= full_hi && y.there[0] && y.there[1])
-                x.template step<false>(y, key, scale);
-            else
-                x.template step<true>(y, key, scale);
-        };
-        if (step < steps) load_tokens(t[0], c, table, blocks, head, step);
-        while (step < steps) {
-            if (step + WK < steps) load_tokens(t[1], c, table, blocks, head, step + WK);
-            work(t[0], step);
-            step += WK;
-            if (step >= steps) break;
-            if (step + WK < steps) load_tokens(t[0], c, table, blocks, head, step + WK);
-            work(t[1], step);
-            step += WK;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = g * (GS / 32); j < (g + 1) * (GS / 32); ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum += half_lo<DT>(x.q[j][e]) + half_hi<DT>(x.q[j][e]);
+            x.qsum[g] = row_sum(sum);
+        }
+        Pages pages{a.table + u.req * a.table_stride, min((u.end + 15) >> 4, a.columns << c.page_shift), {-1, -1}};
+        const int steps = u.step + u.steps;
+        int step = u.step + wave;
+        if (step < steps) {
+            // A step's loads go out as soon as the step before has used the same
+            // registers, its block table entries another step ahead.
+            size_t at[2];
+            pages.read(c, step);
+            pages.place(c, head, step, at);
+            bool there0 = pages.there(c, 0), there1 = pages.there(c, 1);
+            x.load_pairs(c, at);
+            x.load_codes(x.k, c.kc, at);
+            x.load_codes(x.v, c.vc, at);
+            pages.read(c, step + WK);
+            for (;;) {
+                const int key = step * 32;
+                const bool all = key >= u.full_lo && key + 31 <= u.full_hi && there0 && there1;
+                step += WK;
+                const bool more = step < steps;
+                Pairs<DT, G> pair[2];
+                pair[0].set(x.sb[0]);
+                pair[1].set(x.sb[1]);
+                const bool was0 = there0, was1 = there1;
+                if (more) {
+                    there0 = pages.there(c, 0);
+                    there1 = pages.there(c, 1);
+                    pages.place(c, head, step, at);
+                    pages.read(c, step + WK);
+                    x.load_pairs(c, at);
+                }
+                x.scores(pair);
+                if (more) x.load_codes(x.k, c.kc, at);
+                const uint32_t seen = all ? 0xffu : x.hide(key, was0, was1);
+                x.probabilities(scale);
+                x.values(pair, all, seen);
+                if (!more) break;
+                x.load_codes(x.v, c.vc, at);
+            }
         }
         x.join();
-    }
 
+        const bool seen = x.top > -INFINITY || x.l != x.l;
+        if (h == 0) {
+            s_m[wave][n] = seen ? x.m : -INFINITY;
+            s_l[wave][n] = x.l;
+        }
+        __syncthreads();
+        float m = -INFINITY, l = 0.0f;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        float m = x.m[r], l = x.l[r];
-        bool seen = x.top[r] > -INFINITY || l != l;
-        const bool row_there = mine && row0 + 16 * r + n <= last_row;
-        if constexpr (WK > 1) {
-            if (r) __syncthreads();
-            if (h == 0) {
-                s_m[wave][n] = seen ? m : -INFINITY;
-                s_l[wave][n] = l;
-            }
-            __syncthreads();
-            float all = -INFINITY, sum = 0.0f;
+        for (int w = 0; w < WK; ++w) m = fmaxf(m, s_m[w][n]);
+        const float safe = m > -INFINITY ? m : 0.0f;
 #pragma unroll
-            for (int w = 0; w < WK; ++w) all = fmaxf(all, s_m[w][n]);
-            const float safe = all > -INFINITY ? all : 0.0f;
-#pragma unroll
-            for (int w = 0; w < WK; ++w) sum += s_l[w][n] * __builtin_amdgcn_exp2f(s_m[w][n] - safe);
-            const float f = seen ? __builtin_amdgcn_exp2f(m - safe) : 0.0f;
+        for (int w = 0; w < WK; ++w) l += s_l[w][n] * __builtin_amdgcn_exp2f(s_m[w][n] - safe);
+        const float f = seen ? __builtin_amdgcn_exp2f(x.m - safe) : 0.0f;
+        if (n <= last) {
 #pragma unroll
             for (int b = 0; b < NB; ++b)
-                *reinterpret_cast<f32x4*>(&s_o[wave][n * PITCH + 16 * b + 4 * h]) = x.o[r][b] * f;
-            __syncthreads();
-            m = safe;
-            l = sum;
-            seen = all > -INFINITY || l != l;
+                *reinterpret_cast<f32x4*>(&s_o[wave][n * PITCH + 16 * b + 4 * h]) = x.o[b] * f;
         }
-        const long long at = token[r] * a.heads + qhead[r];
-        const float inv = a.splits > 1 ? 1.0f : l != 0.0f ? 1.0f / l : 0.0f;
-        auto store = [&](int b, f32x4 v) {
-            v *= inv;
-            if (a.splits > 1)
-                *reinterpret_cast<f32x4*>(a.part + ((long long)split * a.tokens * a.heads + at) * D + 16 * b + 4 * h) = v;
-            else
-                *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at * D + 16 * b + 4 * h) =
-                    u32x2{R::H::pack(v[0], v[1]), R::H::pack(v[2], v[3])};
-        };
-        if (!row_there) continue;
-        if constexpr (WK > 1) {
+        __syncthreads();
+        if (n <= last) {
+            const long long at = token * a.heads + qhead;
+            const long long place = ((long long)u.place * c.heads + head) * 16 + n;
+            const float inv = u.place >= 0 ? 1.0f : l != 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
             for (int b0 = 0; b0 < NB; b0 += WK) {
                 const int b = b0 + wave;
@@ -471,104 +449,23 @@ __global__ __launch_bounds__(64 * WM * WK) void kv4_attn_kernel(Kv4AttnArgs a) {
                 f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int w = 0; w < WK; ++w) v += *reinterpret_cast<const f32x4*>(&s_o[w][n * PITCH + 16 * b + 4 * h]);
-                store(b, v);
+                v *= inv;
+                if (u.place >= 0)
+                    *reinterpret_cast<f32x4*>(a.part + place * D + 16 * b + 4 * h) = v;
+                else
+                    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at * D + 16 * b + 4 * h) =
+                        u32x2{R::H::pack(v[0], v[1]), R::H::pack(v[2], v[3])};
             }
-        } else {
-#pragma unroll
-            for (int b = 0; b < NB; ++b) store(b, x.o[r][b]);
-        }
-        if (h == 0 && (WM > 1 || wave == 0)) {
-            if (a.splits > 1) {
-                float* stat = a.part + (long long)a.splits * a.tokens * a.heads * D;
-                f32x2* to = reinterpret_cast<f32x2*>(stat) + (long long)split * a.tokens * a.heads + at;
-                *to = f32x2{seen ? m : -INFINITY, l};
-            } else if (a.lse) {
-                a.lse[at] = seen ? (m + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f : -INFINITY;
+            if (lane == n && wave == 0) {
+                if (u.place >= 0)
+                    *reinterpret_cast<f32x2*>(a.stat + 2 * place) = f32x2{m, l};
+                else if (a.lse)
+                    a.lse[at] = l != 0.0f ? (safe + __builtin_amdgcn_logf(l)) * LN2 : -INFINITY;
             }
         }
+        __syncthreads();
     }
 }
-
-// Joins the splits: a wave takes one (query, head).
-template <int D, int DT>
-__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs a) {
-    constexpr int E = D / 64;
-    const int lane = threadIdx.x & 63;
-    long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int head = (int)(id % a.heads);
-    id /= a.heads;
-    const int i = (int)(id % a.max_query), req = (int)(id / a.max_query);
-    if (req > a.requests) return;
-    uint16_t* out = static_cast<uint16_t*>(a.out);
-    const int start = max(a.offsets[req], 0);
-    if (req == a.requests) {
-        for (long long t = (long long)start + i; t < a.tokens; t += a.max_query) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) out[(t * a.heads + head) * D + e * 64 + lane] = 0;
-            if (a.lse && lane == 0) a.lse[t * a.heads + head] = -INFINITY;
-        }
-        return;
-    }
-    const int count = a.offsets[req + 1] - start;
-    if (i >= count || start + i >= a.tokens) return;
-    int begin, end;
-    key_span(a, a.kv_lens[req], count, begin, end);
-    const int splits = end > begin ? (end - begin + a.chunk - 1) / a.chunk : 0;
-    const long long at = ((long long)start + i) * a.heads + head, all = (long long)a.tokens * a.heads;
-    const f32x2* stat = reinterpret_cast<const f32x2*>(a.part + (long long)a.splits * all * D);
-    float m = -INFINITY;
-    for (int s = lane; s < splits; s += 64) m = fmaxf(m, stat[s * all + at][0]);
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-    const float safe = m > -INFINITY ? m : 0.0f;
-    float l = 0.0f, o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.0f;
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-        const f32x2 st = stat[s * all + at];
-        const float f = __builtin_amdgcn_exp2f(st[0] - safe);
-        l += st[1] * f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += f * a.part[(s * all + at) * D + e * 64 + lane];
-    }
-    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) store_elem<DT>(out, at * D + e * 64 + lane, o[e] * inv);
-    if (a.lse && lane == 0)
-        a.lse[at] = l != 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f : -INFINITY;
-}
-
-template <int D, int GS, int DT>
-hipError_t launch_format(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t st) {
-    const dim3 grid((unsigned)((long long)p.splits * (a.requests + 1) * p.tiles * a.c.heads));
-    if (p.wk == 8) kv4_attn_kernel<D, GS, DT, 1, 1, 8><<<grid, dim3(512), 0, st>>>(a);
-    else if (p.wk == 4) kv4_attn_kernel<D, GS, DT, 1, 1, 4><<<grid, dim3(256), 0, st>>>(a);
-    else kv4_attn_kernel<D, GS, DT, 2, 4, 1><<<grid, dim3(256), 0, st>>>(a);
-    hipError_t err = hipGetLastError();
-    if (err == hipSuccess && p.splits > 1) {
-        const long long rows = (long long)(a.requests + 1) * a.max_query * a.heads;
-        kv4_join_kernel<D, DT><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st>>>(a);
-        err = hipGetLastError();
-    }
-    return err;
-}
-
-// One source for each head size and type.
-template <int D, int DT>
-hipError_t launch_dim(const Kv4AttnArgs& a, const Kv4AttnPlan& p, hipStream_t st) {
-    if (a.c.group == 32) return launch_format<D, 32, DT>(a, p, st);
-    if constexpr (D >= 128)
-        if (a.c.group == 128) return launch_format<D, 128, DT>(a, p, st);
-    return launch_format<D, 64, DT>(a, p, st);
-}
-
-extern template hipError_t launch_dim<64, DT_F16>(const Kv4AttnArgs&, const Kv4AttnPlan&, hipStream_t);
-extern template hipError_t launch_dim<128, DT_F16>(const Kv4AttnArgs&, const Kv4AttnPlan&, hipStream_t);
-extern template hipError_t launch_dim<256, DT_F16>(const Kv4AttnArgs&, const Kv4AttnPlan&, hipStream_t);
-extern template hipError_t launch_dim<64, DT_BF16>(const Kv4AttnArgs&, const Kv4AttnPlan&, hipStream_t);
-extern template hipError_t launch_dim<128, DT_BF16>(const Kv4AttnArgs&, const Kv4AttnPlan&, hipStream_t);
-extern template hipError_t launch_dim<256, DT_BF16>(const Kv4AttnArgs&, const Kv4AttnPlan&, hipStream_t);
 
 }  // namespace kv4
 }  // namespace qmx

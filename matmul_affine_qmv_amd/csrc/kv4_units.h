@@ -1,0 +1,205 @@
+// kv4_units.h -- which rows and keys a work-group of an attention call takes,
+// and the kernel that joins what was cut (kv4.h describes the cut).
+#pragma once
+
+#include "kv4.h"
+#include "kv_scan.h"
+#include "qmx_device.h"
+
+namespace qmx {
+namespace kv4 {
+
+constexpr float LN2 = 0.69314718055994530942f;
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// Rows and keys of one unit, or of the part of it that a work-group takes.
+struct Unit {
+    int req;
+    int start, back;          // the request's first token, and that token's position
+    int row0, rows;           // of the request's rows
+    int end;                  // keys from here on are not there
+    int step, steps;          // the keys, 32 a step
+    int full_lo, full_hi;     // keys that every row sees
+    int place;                // of the partial sums, or -1: the unit is whole
+};
+
+// Unit `v` of a head, from what memory holds: steps is 0 where no key is seen.
+__device__ __forceinline__ Unit unit_of(const Kv4AttnArgs& a, int v) {
+    Unit u;
+    u.req = v / a.p.tiles;
+    const int tile = a.p.tiles - 1 - (v - u.req * a.p.tiles);   // the tiles that see most keys first
+    u.start = max(a.offsets[u.req], 0);
+    const int stop = a.offsets[u.req + 1], kv = a.kv_lens[u.req];
+    const int count = min(min(stop, a.tokens) - u.start, a.max_query);
+    u.back = kv - (stop - u.start);
+    u.row0 = tile * a.p.rows;
+    u.rows = min(count * a.each - u.row0, a.p.rows);
+    u.place = -1;
+    u.step = u.steps = 0;
+    u.end = u.full_lo = u.full_hi = 0;
+    if (u.rows > 0) {
+        const int pos0 = u.back + u.row0 / a.each, pos1 = u.back + (u.row0 + u.rows - 1) / a.each;
+        u.end = min(min(kv, a.max_kv), pos1 + 1);
+        const int first = a.window ? max(0, pos0 - a.window + 1) : 0;
+        u.step = first >> 5;
+        u.steps = max(0, ((u.end + 31) >> 5) - u.step);
+        u.full_lo = a.window ? pos1 - a.window + 1 : 0;
+        u.full_hi = min(pos0, u.end - 1);
+    }
+    return u;
+}
+
+// Zeros for the tokens of no request: group `id` of `of`, THREADS threads.
+__device__ __forceinline__ void clear_rest(const Kv4AttnArgs& a, int id, int of) {
+    const int begin = max(a.offsets[a.requests], 0);
+    const int per = a.heads * (a.c.dim / 8);
+    const long long all = max(0, a.tokens - begin) * (long long)per;
+    for (long long i = (long long)id * blockDim.x + threadIdx.x; i < all; i += (long long)of * blockDim.x)
+        reinterpret_cast<u32x4*>(a.out)[(long long)begin * per + i] = u32x4{0, 0, 0, 0};
+    if (a.lse)
+        for (long long i = (long long)begin * a.heads + (long long)id * blockDim.x + threadIdx.x;
+             i < (long long)a.tokens * a.heads; i += (long long)of * blockDim.x)
+            a.lse[i] = -INFINITY;
+}
+
+// The units of work-group `id` of a head, one after the other.
+template <int THREADS>
+class Units {
+    int id_, count_, at_, stop_;
+    int *begin_, *end_;   // LDS: a unit's steps on the line
+
+  public:
+    __device__ __forceinline__ Units(const Kv4AttnArgs& a, int id, int head) : id_(id), count_(a.requests * a.p.tiles) {
+        __shared__ int s_begin[KV4_LINE_UNITS], s_end[KV4_LINE_UNITS];
+        __shared__ int s_waves[THREADS / 64];
+        begin_ = s_begin;
+        end_ = s_end;
+        at_ = 0;
+        stop_ = 1;
+        if (!a.p.lines) return;
+        constexpr int EACH = KV4_LINE_UNITS / THREADS;
+        int n[EACH], sum = 0, total;
+        const int per = (count_ + THREADS - 1) / THREADS;   // units a thread, at most EACH
+        const int v0 = (int)threadIdx.x * per;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const bool there = i < per && v0 + i < count_;
+            n[i] = there ? unit_of(a, v0 + i).steps : 0;
+            sum += n[i] ? n[i] + a.p.cost : 0;
+        }
+        int upto = scan_group<THREADS / 64>(sum, s_waves, total) - sum;
+        const int length = max(a.p.least, (total + a.p.lines - 1) / a.p.lines);
+        const bool tell = id == 0 && head == 0;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            if (i < per && v0 + i < count_) {
+                const int begin = upto + (n[i] ? a.p.cost : 0);
+                upto = begin + n[i];
+                s_begin[v0 + i] = begin;
+                s_end[v0 + i] = upto;
+                if (tell) {
+                    a.pos[1 + 2 * (v0 + i)] = begin;
+                    a.pos[2 + 2 * (v0 + i)] = upto;
+                }
+            }
+        }
+        if (tell && threadIdx.x == 0) a.pos[0] = length;
+        __syncthreads();
+        at_ = (int)min((long long)id * length, (long long)total);
+        stop_ = (int)min((long long)at_ + length, (long long)total);
+    }
+
+    // Whether there is another; uniform over the work-group.
+    __device__ __forceinline__ bool next(const Kv4AttnArgs& a, Unit& u) {
+        if (at_ >= stop_) return false;
+        if (!a.p.lines) {
+            at_ = stop_;
+            if (id_ >= count_) {
+                clear_rest(a, id_ - count_ + (int)(blockIdx.x % a.c.heads), a.c.heads);
+                return false;
+            }
+            u = unit_of(a, id_);
+            return u.rows > 0;
+        }
+        const int v = __builtin_amdgcn_readfirstlane(first_after(end_, count_, at_));
+        const int begin = __builtin_amdgcn_readfirstlane(begin_[v]), end = __builtin_amdgcn_readfirstlane(end_[v]);
+        if (stop_ <= begin) return false;   // only the gap before the unit
+        u = unit_of(a, v);
+        const int first = max(at_, begin), last = min(end, stop_);
+        u.step += first - begin;
+        u.steps = last - first;
+        if (first > begin) u.place = 2 * id_;
+        else if (last < end) u.place = 2 * id_ + 1;
+        at_ = last;
+        return true;
+    }
+};
+
+// Work-groups of a call: the units of a head and one for the rest, or the lines.
+inline long long kv4_groups(const Kv4AttnArgs& a) {
+    return (long long)a.c.heads * (a.p.lines ? a.p.lines : (long long)a.requests * a.p.tiles + 1);
+}
+
+// One wave a (token of a request, head): joins the parts of its unit, writes
+// zeros where no key is seen, and leaves alone what is whole.
+template <int D, int DT>
+__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs a) {
+    constexpr int E = D / 64;
+    const int lane = threadIdx.x & 63;
+    const long long waves = (long long)a.requests * a.max_query * a.heads;
+    const int own = (int)((waves + 3) / 4);   // the groups behind these take the tokens of no request
+    if ((int)blockIdx.x >= own) {
+        clear_rest(a, blockIdx.x - own, gridDim.x - own);
+        return;
+    }
+    long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (id >= waves) return;
+    const int head = (int)(id % a.heads);
+    id /= a.heads;
+    const int i = (int)(id % a.max_query), req = (int)(id / a.max_query);
+    const int start = max(a.offsets[req], 0);
+    if (i >= a.offsets[req + 1] - start || start + i >= a.tokens) return;
+    const int row = i * a.each + head % a.each, tile = row / a.p.rows;
+    const int v = req * a.p.tiles + a.p.tiles - 1 - tile;
+    const int length = a.pos[0], p0 = a.pos[1 + 2 * v], p1 = a.pos[2 + 2 * v];
+    const int w0 = p0 / length, w1 = p1 > p0 ? (p1 - 1) / length : w0 - 1;
+    if (w0 == w1) return;
+    const long long at = ((long long)start + i) * a.heads + head;
+    const int kv_head = head / a.each;
+    const long long r = (long long)kv_head * a.p.rows + row - tile * a.p.rows, all = (long long)a.c.heads * a.p.rows;
+    auto place = [&](int w) { return (2ll * w + (w == w0 ? 1 : 0)) * all + r; };
+    const f32x2* stat = reinterpret_cast<const f32x2*>(a.stat);
+    float m = -INFINITY;
+    for (int w = w0 + lane; w <= w1; w += 64) m = fmaxf(m, stat[place(w)][0]);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    const float safe = m > -INFINITY ? m : 0.0f;
+    float l = 0.0f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll 8
+    for (int w = w0; w <= w1; ++w) {
+        const long long p = place(w);
+        const f32x2 st = stat[p];
+        const float f = __builtin_amdgcn_exp2f(st[0] - safe);
+        l += st[1] * f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += f * a.part[p * D + e * 64 + lane];
+    }
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) store_elem<DT>(a.out, at * D + e * 64 + lane, o[e] * inv);
+    if (a.lse && lane == 0) a.lse[at] = l != 0.0f ? (safe + __builtin_amdgcn_logf(l)) * LN2 : -INFINITY;
+}
+
+template <int D, int DT>
+hipError_t launch_join(const Kv4AttnArgs& a, hipStream_t st) {
+    const long long waves = (long long)a.requests * a.max_query * a.heads;
+    const long long rest = 1 + ((long long)a.tokens * a.heads * (D / 8) >> 12);   // 16 stores a thread
+    kv4_join_kernel<D, DT><<<dim3((unsigned)((waves + 3) / 4 + (rest < 64 ? rest : 64))), dim3(256), 0, st>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace kv4
+}  // namespace qmx

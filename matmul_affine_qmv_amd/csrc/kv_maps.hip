@@ -7,6 +7,7 @@
 // A work-group then writes its own range of tokens, and its share of the new
 // table entries.
 #include "kv4.h"
+#include "kv_scan.h"
 
 namespace qmx {
 namespace {
@@ -14,47 +15,6 @@ namespace {
 constexpr int THREADS = 512;
 constexpr int CHUNK = 2 * THREADS;   // requests scanned at a time, two a thread
 constexpr int WAVES = THREADS / 64;
-
-template <class T>
-__device__ __forceinline__ T scan_wave(T v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const T up = __shfl_up(v, off, 64);
-        if (lane >= off) v += up;
-    }
-    return v;
-}
-
-// Inclusive sum over the work-group's threads; `total` is the sum of all.
-template <class T>
-__device__ __forceinline__ T scan_group(T v, T* waves, T& total) {
-    v = scan_wave(v);
-    const int wave = threadIdx.x >> 6;
-    __syncthreads();
-    if ((threadIdx.x & 63) == 63) waves[wave] = v;
-    __syncthreads();
-    T before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-        const T x = waves[w];
-        before += w < wave ? x : 0;
-        total += x;
-    }
-    return v + before;
-}
-
-// First index whose end is greater than x, of `count` ends in order.
-__device__ __forceinline__ int first_after(const int* ends, int count, int x) {
-    int lo = 0, hi = count;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (ends[mid] <= x) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo;
-}
 
 __global__ __launch_bounds__(THREADS) void kv_maps_kernel(KvMapsArgs a, int per_group) {
     __shared__ int s_end[CHUNK], s_page_end[CHUNK], s_past[CHUNK], s_held[CHUNK];
@@ -79,7 +39,7 @@ __global__ __launch_bounds__(THREADS) void kv_maps_kernel(KvMapsArgs a, int per_
             past[i] = r < count ? max(a.past[r0 + r], 0) : 0;
         }
         long long chunk_sum;
-        const long long upto = sum + scan_group(n[0] + n[1], s_waves64, chunk_sum);
+        const long long upto = sum + scan_group<WAVES>(n[0] + n[1], s_waves64, chunk_sum);
         int take[2], held[2], end[2];
         long long e = upto - n[1] - n[0];
 #pragma unroll
@@ -99,7 +59,7 @@ __global__ __launch_bounds__(THREADS) void kv_maps_kernel(KvMapsArgs a, int per_
             }
         }
         int chunk_pages;
-        const int page_upto = pages + scan_group(take[0] + take[1], s_waves32, chunk_pages);
+        const int page_upto = pages + scan_group<WAVES>(take[0] + take[1], s_waves32, chunk_pages);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = 2 * tid + i;

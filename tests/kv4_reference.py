@@ -13,6 +13,11 @@ roundings alone (``u`` is half a step of the type, 2^-24 that of float32):
 * the scores' 32-bit error E_t (the same count on q's side, and the exponent's
   argument): p_t moves by a factor of at most exp(2 max E), so the output by
   expm1(2 max E) sum_t p_t |v_t - out|.
+
+``prompt``: the kernel of many rows rounds other things.  Values and
+probabilities to the type, 2 u sum_t p_t |v_td|, in place of p_t s_tg; keys and
+queries to float16 after a power of two each, 2^-11 of a number or 2^-25 of the
+largest (twice the power of two at most), which enters E_t.
 """
 import numpy as np
 import torch
@@ -105,7 +110,7 @@ def maps(past, new, table, free, page, T):
     return offsets, kv, slots, at_, ids, [sum(max(x, 0) for x in new), used]
 
 
-def attention(cache, q, table, kv_lens, offsets, window=0, scale=None):
+def attention(cache, q, table, kv_lens, offsets, window=0, scale=None, prompt=False):
     """(out, lse, bound of out, bound of lse), float64, q [T, heads, D] torch on the CPU."""
     T, heads, D = q.shape
     each = heads // cache.heads
@@ -113,7 +118,7 @@ def attention(cache, q, table, kv_lens, offsets, window=0, scale=None):
     q = q.double().numpy()
     out, lse = np.zeros((T, heads, D)), np.full((T, heads), -np.inf)
     tol, lse_tol = np.zeros((T, heads, D)), np.zeros((T, heads))
-    u = HALF[cache.type] / 1
+    u = HALF[cache.type]
     for r in range(len(kv_lens)):
         n, kv = offsets[r + 1] - offsets[r], kv_lens[r]
         for h in range(cache.heads):
@@ -144,9 +149,15 @@ def attention(cache, q, table, kv_lens, offsets, window=0, scale=None):
                     lse[t, a] = m + np.log(total)
                     size = ((OFF + 15) * ks[see] + np.abs(kb[see]) + OFF * ks[see]) @ np.abs(x) * abs(scale)
                     err = (D + 8) * U32 * size.max() + 8 * U32 * (np.abs(s).max() + 1)
+                    if prompt:
+                        off = 2.0 ** -11 * np.abs(k) + 2.0 ** -24 * np.abs(k).max(-1, keepdims=True)
+                        size = off @ np.abs(x) + (np.abs(k) + off) @ np.maximum(
+                            2.0 ** -11 * np.abs(x) * (cache.type == "f16"), 2.0 ** -24 * np.abs(x).max())
+                        err += size.max() * scale
                     steps = see.sum() / 32 + 64
                     spread = p @ np.abs(v - out[t, a])
-                    tol[t, a] = (u * np.abs(out[t, a]) + u * (p @ (vs[see] * np.abs(vc[see] - 8)))
+                    held = 2 * np.abs(v) if prompt else vs[see] * np.abs(vc[see] - 8)
+                    tol[t, a] = (u * np.abs(out[t, a]) + u * (p @ held)
                                  + steps * U32 * (p @ (vs[see] * (OFF + 23) + np.abs(vb[see])))
                                  + np.expm1(2 * err) * spread)
                     if cache.type == "f16":

@@ -309,7 +309,8 @@ def attention_case(dtype, D, group, page, each, H, lens, window=0, pad=0, holes=
     kw = dict(max_query_len=max([n for _, n in lens] + [0]), max_kv_len=max(kv + [0]), window=window, scale=scale)
     args = (cache, qd, torch.from_numpy(table).to(DEV), ints(kv), ints(offsets))
     out, lse = qmx.kv4_attention(*args, return_lse=True, **kw)
-    o, l, tol, ltol = ref.attention(c, q, table, kv, offsets, window, scale)
+    prompt = kw["max_query_len"] * each > 64   # the kernel of many rows
+    o, l, tol, ltol = ref.attention(c, q, table, kv, offsets, window, scale, prompt)
     out_, lse_ = out.double().cpu().numpy(), lse.double().cpu().numpy()
     assert np.isfinite(out_).all()
     over = np.abs(out_ - o) - tol
@@ -338,6 +339,13 @@ def test_attention_single_tokens(dtype, D, group):
 def test_attention_prompts(dtype, D, group):
     """Rows of several waves and tiles; prompts beside chunks behind a cached prefix."""
     attention_case(dtype, D, group, 32, 2, 1, [(0, 70), (45, 33), (3, 0), (200, 1)], pad=1, seed=2, spoil=True)
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype,D,group", FORMATS)
+def test_attention_prompts_of_many_tiles(dtype, D, group):
+    """Several work-groups' rows, keys shared among work-groups, an odd number of query heads a key head."""
+    attention_case(dtype, D, group, 64, 5, 1, [(1200, 61), (0, 0), (7, 110), (30, 1)], pad=5, seed=12, spoil=True)
 
 
 @on_gpu
@@ -403,6 +411,15 @@ def test_attention_nan_stays_with_its_rows():
     bad = torch.isnan(out.float()).cpu()
     assert bad[10:20, :, 32:].all()            # positions 20..29
     assert not bad[:10].any() and not bad[20:].any() and not bad[:, :, :32].any()
+    # the same through the kernel of many rows, and an infinite bias
+    packed[3][2, 0, 4, 1] = torch.tensor([0.0, math.inf])
+    cache = qmx.Kv4Cache(*(x.to(DEV) for x in packed))
+    q = torch.randn(25, 4, 64, dtype=torch.bfloat16, device=DEV)
+    out = qmx.kv4_attention(cache, q, table, ints([30, 20]), ints([0, 20, 25]), max_query_len=20, max_kv_len=30)
+    bad = torch.isinf(out.float()).cpu()
+    assert bad[10:20, :, 32:].all()
+    assert torch.isfinite(out[:10].float()).all() and torch.isfinite(out[20:].float()).all()
+    assert torch.isfinite(out[:, :, :32].float()).all()
 
 
 @on_gpu
