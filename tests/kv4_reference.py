@@ -15,9 +15,10 @@ roundings alone (``u`` is half a step of the type, 2^-24 that of float32):
   expm1(2 max E) sum_t p_t |v_t - out|.
 
 ``prompt``: the kernel of many rows rounds other things.  Values and
-probabilities to the type, 2 u sum_t p_t |v_td|, in place of p_t s_tg; keys and
-queries to float16 after a power of two each, 2^-11 of a number or 2^-25 of the
-largest (twice the power of two at most), which enters E_t.
+probabilities to float16, 2 * 2^-11 sum_t p_t |v_td|, in place of p_t s_tg, or
+2^-24 of the largest value each (a power of two above it at most twice it;
+probabilities down to 2^-25 a key, and those scaled with it); queries to
+float16, 2^-24 of the row's largest, which enters E_t.
 """
 import numpy as np
 import torch
@@ -150,14 +151,13 @@ def attention(cache, q, table, kv_lens, offsets, window=0, scale=None, prompt=Fa
                     size = ((OFF + 15) * ks[see] + np.abs(kb[see]) + OFF * ks[see]) @ np.abs(x) * abs(scale)
                     err = (D + 8) * U32 * size.max() + 8 * U32 * (np.abs(s).max() + 1)
                     if prompt:
-                        off = 2.0 ** -11 * np.abs(k) + 2.0 ** -24 * np.abs(k).max(-1, keepdims=True)
-                        size = off @ np.abs(x) + (np.abs(k) + off) @ np.maximum(
-                            2.0 ** -11 * np.abs(x) * (cache.type == "f16"), 2.0 ** -24 * np.abs(x).max())
-                        err += size.max() * scale
+                        err += 2.0 ** -24 * np.abs(x).max() * np.abs(k).sum(-1).max() * scale
                     steps = see.sum() / 32 + 64
                     spread = p @ np.abs(v - out[t, a])
-                    held = 2 * np.abs(v) if prompt else vs[see] * np.abs(vc[see] - 8)
-                    tol[t, a] = (u * np.abs(out[t, a]) + u * (p @ held)
+                    held = u * (p @ (vs[see] * np.abs(vc[see] - 8)))
+                    if prompt:
+                        held = 2.0 ** -10 * (p @ np.abs(v)) + 2.0 ** -24 * np.abs(v).max() * (1 + see.sum() / total)
+                    tol[t, a] = (u * np.abs(out[t, a]) + held
                                  + steps * U32 * (p @ (vs[see] * (OFF + 23) + np.abs(vb[see])))
                                  + np.expm1(2 * err) * spread)
                     if cache.type == "f16":
