@@ -3,12 +3,13 @@
 // ALU beside them, where kv4_attn_impl.h is bound by what it reads.
 //
 // A work-group of 8 waves takes 256 rows, a wave 32 of them, and walks the keys
-// 64 at a time.  Four waves turn the keys' codes into numbers and four the
-// values', once for all 256 rows, into LDS (two buffers, one barrier a tile) in
-// the order in which the products read them: 16 bytes a lane, lane after lane.
-// The first four do so before their own products of a tile and the others
-// after, so that of the two waves on a SIMD one has the vector ALU's work when
-// the other has the matrix cores'.
+// 64 at a time (32 where the head has 256 dimensions).  Four waves turn the keys'
+// codes into operands and four the values', once for all 256 rows, into LDS (one
+// barrier a tile) in the order in which the products read them: 16 bytes a lane,
+// lane after lane.  The second four run half a tile behind: their barrier stands
+// between a tile's two products (so values have three buffers, keys two), and of
+// the two waves on a SIMD one has the first product, which is the matrix cores'
+// work, while the other has the exponentials, which are the vector ALU's.
 //
 //   S^T[key, row] = K Q^T,  O^T[dim, row] += V^T P:  v_mfma_32x32x16, where the
 //   probabilities that a lane computes are the operand it needs (as in
@@ -17,7 +18,7 @@
 // A code c enters both products as the bits of the float16 number c 2^-18, which
 // is exact.  Keys stay codes: a group's product is multiplied by the token's
 // scale in 32 bits, and the biases times the queries' sums (each in three
-// pieces of the type, which hold 24 bits) are one more step of the product; so
+// pieces of the type, which hold 24 bits) are a first step of the product; so
 // scores are as exact as their 32-bit sums.  Queries are float16, brought to at
 // most 1 by a power of two a row (what is under 2^-14 of the largest keeps
 // 2^-25 of it).  A value becomes c s + b in one multiply-add, a block of 16
@@ -61,78 +62,96 @@ __device__ __forceinline__ uint32_t tiny_codes(uint32_t w, int f) {
     return (f < 2 ? w << (6 - 4 * f) : w >> (4 * f - 6)) & 0x03c003c0u;
 }
 
-constexpr int PROMPT_WAVES = 8, PROMPT_ROWS = 256, PROMPT_KEYS = 64;
+constexpr int PROMPT_WAVES = 8, PROMPT_ROWS = 256;
 
-// The codes and pairs of one block of 16 tokens, as a lane takes them to turn
-// them into operands.  Keys: the lane's token n = lane % 16 with all its pairs;
-// values: the tokens 4h .. 4h + 3, h = lane / 16, their pairs spread over the
-// row's 16 lanes as in kv4_attn_impl.h.
+// Products and reads of LDS stay in the order of the source, so that operands
+// are read a few products ahead; everything else may move.
+#ifdef QV_FREE
+__device__ __forceinline__ void keep_order() {}
+#else
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0x676); }
+#endif
+
+// The largest of the wave's numbers, none below 0, without a trip through LDS:
+// over rows of 16 lanes, then the four rows as integers, which order alike.
+__device__ __forceinline__ float wave_max(float v) {
+    int x = __float_as_int(v);
+#define QMX_ROW_TURN(K) x = max(x, __builtin_amdgcn_mov_dpp(x, 0x120 + K, 0xf, 0xf, true))
+    QMX_ROW_TURN(8);
+    QMX_ROW_TURN(4);
+    QMX_ROW_TURN(2);
+    QMX_ROW_TURN(1);
+#undef QMX_ROW_TURN
+    return __int_as_float(max(max(__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16)),
+                              max(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48))));
+}
+
+// What a lane takes of one block of 16 tokens to turn it into operands: codes,
+// and pairs of the D / SPLIT dimensions that fall to its wave.  Keys: the lane's
+// token n = lane % 16; values: the tokens 4h .. 4h + 3, h = lane / 16, their pairs
+// spread over the row's 16 lanes as in kv4_attn_impl.h.
 template <int D, int GS, int DT>
 struct Raw {
+    static constexpr int KEYS = 64 * 128 / (D < 128 ? 128 : D);   // of a tile
+    static constexpr int SPLIT = 64 / KEYS;                       // waves that share a block
     static constexpr int NJ = D / 32, G = D / GS, KS = D / 16, DB = D / 32;
-    static constexpr int BK = (3 * G + 15) / 16;          // steps of the product of biases
-    static constexpr int SHARE = (4 * G + 15) / 16;       // registers of a lane's share of the values' pairs
-    static constexpr int EMPTY = -120;                    // exponent of a block of zeros
-    uint32_t w[NJ], sb[G > SHARE ? G : SHARE];
+    static constexpr int NW = NJ / SPLIT, GW = G / SPLIT;         // words and groups of a wave
+    static constexpr int BK = (4 * G + 15) / 16;                  // steps of the product of biases
+    static constexpr int SHARE = (4 * G + 15) / 16;               // a lane's share of the values' pairs
+    static constexpr int EMPTY = -120, MISSING = -1000;           // exponents of no values, and of no page
+    uint32_t w[NW], sb[GW > SHARE ? GW : SHARE];
     bool there;
     int tokens;   // of the block, from its first on, that are there
 
-    __device__ __forceinline__ void load(const Kv4View& c, int page, int head, int blk, int end, bool value) {
+    __device__ __forceinline__ void load(const Kv4View& c, int page, int head, int blk, int part, int end,
+                                         bool value) {
         const int lane = threadIdx.x & 63;
         tokens = end - 16 * blk;
         there = tokens > 0 && page >= 0 && page < c.num_pages;
         if (!there) return;
         const size_t at = (((size_t)page * c.heads + head) << c.page_shift) + (blk & ((1 << c.page_shift) - 1));
-        load_words(w, (value ? c.vc : c.kc) + at * (64 * NJ) + lane * NJ);
+        load_words(w, (value ? c.vc : c.kc) + at * (64 * NJ) + lane * NJ + part * NW);
         if (value) {
             const uint32_t* from = c.vs + at * (16 * G) + (lane >> 4) * (4 * G);
 #pragma unroll
             for (int r = 0; r < SHARE; ++r) sb[r] = from[(16 * r + (lane & 15)) & (4 * G - 1)];
         } else {
-            const uint32_t* from = c.ks + at * (16 * G) + (lane & 15) * G;
+            const uint32_t* from = c.ks + at * (16 * G) + (lane & 15) * G + part * GW;
 #pragma unroll
-            for (int g = 0; g < G; ++g) sb[g] = from[g];
+            for (int g = 0; g < GW; ++g) sb[g] = from[g];
         }
     }
 
-    // Keys to `k` [2 blocks of 32][KS + BK][2][32] of 16 bytes, the scales times
-    // 2^18 to `factor` [G][64]; `blk` counts in the tile.
-    __device__ __forceinline__ void keys(u32x4* k, float* factor, int blk) const {
+    // Keys to `k` [blocks of 32][BK + KS][2][32] of 16 bytes, the scales times
+    // 2^18 to `factor` [G][KEYS]; `blk` counts in the tile.
+    __device__ __forceinline__ void keys(u32x4* k, float* factor, int blk, int part) const {
         const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
-        u32x4* to = k + (blk >> 1) * (KS + BK) * 64 + (blk & 1) * 16 + n;
+        u32x4* to = k + (blk >> 1) * (BK + KS) * 64 + (blk & 1) * 16 + n;
         const bool live = there && n < tokens;
-        if (h == 0) {
 #pragma unroll
-            for (int g = 0; g < G; ++g) factor[64 * g + 16 * blk + n] = live ? half_lo<DT>(sb[g]) * 0x1p18f : 0.0f;
+        for (int g = 0; g < GW; ++g) {
+            const int group = part * GW + g;
+            if (h == g % 4) {   // slots 4 * group .. + 2 take the group's bias
+                const uint32_t b = live ? sb[g] >> 16 : 0u;
+                reinterpret_cast<u32x2*>(to + (group / 4) * 64 + (group / 2 % 2) * 32)[group % 2] =
+                    u32x2{b | (b << 16), b};
+                factor[KEYS * group + 16 * blk + n] = live ? half_lo<DT>(sb[g]) * 0x1p18f : 0.0f;
+            }
         }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
+        for (int j = 0; j < NW; ++j) {
             u32x4 x;
 #pragma unroll
             for (int f = 0; f < 4; ++f) x[f] = tiny_codes(w[j], f);
-            to[(2 * j + (h >> 1)) * 64 + (h & 1) * 32] = x;
-        }
-#pragma unroll
-        for (int y = 0; y < 2 * BK; ++y) {
-            if (h == y) {   // eight slots: slot 3g + i takes group g's bias
-                u32x4 x;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int g0 = (8 * y + 2 * i) / 3, g1 = (8 * y + 2 * i + 1) / 3;
-                    const uint32_t b0 = g0 < G && live ? sb[g0 < G ? g0 : 0] >> 16 : 0u;
-                    const uint32_t b1 = g1 < G && live ? sb[g1 < G ? g1 : 0] & 0xffff0000u : 0u;
-                    x[i] = b0 | b1;
-                }
-                to[(KS + (y >> 1)) * 64 + (y & 1) * 32] = x;
-            }
+            to[(BK + 2 * (part * NW + j) + (h >> 1)) * 64 + (h & 1) * 32] = x;
         }
     }
 
-    // Values to `v` [4 blocks of 16][DB][2][32] of 16 bytes, all of the block's
+    // Values to `v` [blocks of 16][DB][2][32] of 16 bytes, all of the block's
     // divided by 2^exponent.  Whether they are finite.
-    __device__ __forceinline__ bool values(u32x4* v, int& exponent, int blk) const {
+    __device__ __forceinline__ bool values(u32x4* v, int& exponent, int blk, int part) const {
         const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
-        u32x2* to = reinterpret_cast<u32x2*>(v + (blk * DB * 2 + (h & 1)) * 32 + n) + (h >> 1);
+        u32x2* to = reinterpret_cast<u32x2*>(v + ((blk * DB + part * (DB / SPLIT)) * 2 + (h & 1)) * 32 + n) + (h >> 1);
         float s[SHARE], b[SHARE], most = 0.0f;
         bool good = true;
 #pragma unroll
@@ -145,16 +164,15 @@ struct Raw {
             b[r] = live && finite ? y : 0.0f;
             most = fmaxf(most, fmaxf(fabsf(b[r]), fabsf(fmaf(15.0f, s[r], b[r]))));
         }
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) most = fmaxf(most, __shfl_xor(most, off, 64));
+        most = wave_max(most);
         const int e = most > 0.0f ? __builtin_amdgcn_frexp_expf(fminf(most, 0x1.fffffep127f)) : EMPTY;
-        exponent = e;
+        exponent = there ? e : MISSING;
         uint32_t pair[SHARE];   // scale 2^18 and bias, float16
 #pragma unroll
         for (int r = 0; r < SHARE; ++r)
             pair[r] = __builtin_bit_cast(uint32_t, half2_of(ldexpf(s[r], 18 - e), ldexpf(b[r], -e)));
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
+        for (int g = 0; g < GW; ++g) {
             f16x2 s2[2], b2[2];   // of two tokens
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
@@ -162,7 +180,8 @@ struct Raw {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int at = (2 * p + i) * G + g;
-                    x[i] = (uint32_t)__float_as_int(row_lane(__int_as_float((int)pair[at / 16]), at % 16));
+                    x[i] = pair_at(pair, at);
+                    if constexpr (SPLIT == 2) x[i] = part ? pair_at(pair, at + GW) : x[i];
                 }
                 s2[p] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(x[1], x[0], 0x05040100u));
                 b2[p] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(x[1], x[0], 0x07060302u));
@@ -181,23 +200,35 @@ struct Raw {
         }
         return good;
     }
+    static __device__ __forceinline__ uint32_t pair_at(const uint32_t (&pair)[SHARE], int at) {
+        return (uint32_t)__float_as_int(row_lane(__int_as_float((int)pair[at / 16]), at % 16));
+    }
 };
 
 template <int D, int GS, int DT>
 __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4AttnArgs a) {
     using W = Raw<D, GS, DT>;
-    constexpr int KS = D / 16, DB = D / 32, G = D / GS, BK = W::BK, NT = D == 256 ? 1 : 2;
-    constexpr float kSlack = 8.0f;
     using H = Half<DT>;
-    __shared__ u32x4 s_k[2][2 * (KS + BK) * 64], s_v[2][4 * DB * 64];
-    __shared__ float s_factor[2][G * PROMPT_KEYS];
-    __shared__ int s_bad[2], s_there[2][4], s_exponent[2][4];
+    constexpr int KS = D / 16, DB = D / 32, G = D / GS, BK = W::BK, KEYS = W::KEYS, NT = KEYS / 32;
+    constexpr int KQ = D == 256 ? KS / 2 : KS;   // steps whose queries stay in registers; the others' in LDS
+    #ifndef QV_AHEAD
+#define QV_AHEAD 4
+#endif
+    constexpr int AHEAD = QV_AHEAD;                   // operands read ahead
+    constexpr float kSlack = 8.0f;
+    __shared__ u32x4 s_k[2][NT * (BK + KS) * 64], s_v[3][2 * NT * DB * 64];
+    __shared__ u32x4 s_q[PROMPT_WAVES][KS > KQ ? (KS - KQ) * 64 : 1];
+    __shared__ float s_factor[2][G * KEYS];
+    __shared__ int s_bad[3], s_exponent[3][4];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, n = lane & 31, hh = lane >> 5;
     const Kv4View& c = a.c;
     const int head = blockIdx.x % c.heads;
-    const bool value = wave >= 4;   // which codes this wave turns into numbers
-    const int my_blk = wave & 3;
+    const bool value = wave >= 4;   // which codes this wave turns into operands
+    const int my_blk = (wave & 3) / W::SPLIT, my_part = (wave & 3) % W::SPLIT;
+
+    for (int i = threadIdx.x; i < 2 * NT * BK * 64; i += 64 * PROMPT_WAVES)   // slots that no group has
+        s_k[i / (NT * BK * 64)][i / (BK * 64) % NT * (BK + KS) * 64 + i % (BK * 64)] = u32x4{0, 0, 0, 0};
 
     Units<64 * PROMPT_WAVES> units(a, blockIdx.x / c.heads, head);
     for (Unit u; units.next(a, u);) {
@@ -210,48 +241,58 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
         const long long token = (long long)u.start + i;
         const int qhead = head * a.each + (mine ? row - i * a.each : 0);
         const int key0 = u.step * 32, part_end = min(u.end, (u.step + u.steps) * 32);
-        const int lo = a.window ? u.back + i - a.window + 1 : 0, hi = min(u.back + i, part_end - 1);
+        int lo = a.window ? u.back + i - a.window + 1 : 0, reach = min(u.back + i, part_end - 1) - lo;
+        if (reach < 0) {   // none: no key is that far
+            lo = 0x7fffffff;
+            reach = 0;
+        }
         const int pos0 = u.back + row0 / a.each, pos1 = mine ? u.back + (row0 + rows - 1) / a.each : 0;
         const int full_lo = a.window ? pos1 - a.window + 1 : 0, full_hi = min(pos0, part_end - 1);
         const int any_lo = a.window ? pos0 - a.window + 1 : 0, any_hi = mine ? min(pos1, part_end - 1) : -1;
 
-        u32x4 q[KS], qb[BK];
+        u32x4 q[KQ], qb[BK];
         float rf;
         {
             const uint16_t* from = static_cast<const uint16_t*>(a.q) + token * a.q_ts + qhead * a.q_hs + 8 * hh;
             const bool vec = (((uintptr_t)a.q & 15) | ((a.q_ts | a.q_hs) & 7)) == 0;
-            float most = 0.0f;
-#pragma unroll
-            for (int j = 0; j < KS; ++j) {
+            auto load = [&](int j) {
+                u32x4 x;
                 if (vec) {
-                    q[j] = *reinterpret_cast<const u32x4*>(from + 16 * j);
+                    x = *reinterpret_cast<const u32x4*>(from + 16 * j);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        q[j][e] = (uint32_t)from[16 * j + 2 * e] | ((uint32_t)from[16 * j + 2 * e + 1] << 16);
+                        x[e] = (uint32_t)from[16 * j + 2 * e] | ((uint32_t)from[16 * j + 2 * e + 1] << 16);
                 }
+                return x;
+            };
+            float most = 0.0f, sum[G];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    most = fmaxf(most, fmaxf(fabsf(half_lo<DT>(q[j][e])), fabsf(half_hi<DT>(q[j][e]))));
+            for (int g = 0; g < G; ++g) {
+                sum[g] = 0.0f;
+#pragma unroll
+                for (int j = g * (GS / 16); j < (g + 1) * (GS / 16); ++j) {
+                    const u32x4 x = load(j);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float y = half_lo<DT>(x[e]), z = half_hi<DT>(x[e]);
+                        most = fmaxf(most, fmaxf(fabsf(y), fabsf(z)));
+                        sum[g] += y + z;
+                    }
+                }
             }
             most = fmaxf(most, __shfl_xor(most, 32, 64));
             const int e = min(__builtin_amdgcn_frexp_expf(most), 127);
             rf = ldexpf(a.scale_log2, e);
-            u32x4 sums[4] = {};   // slot 3g + i: piece i of group g's sum
+            u32x4 sums[2 * BK] = {};   // slot 4g + i: piece i of group g's sum
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                float sum = 0.0f;
-#pragma unroll
-                for (int j = g * (GS / 16); j < (g + 1) * (GS / 16); ++j)
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) sum += half_lo<DT>(q[j][w]) + half_hi<DT>(q[j][w]);
-                sum = ldexpf(sum + __shfl_xor(sum, 32, 64), -e);
+                float rest = ldexpf(sum[g] + __shfl_xor(sum[g], 32, 64), -e);
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
-                    const int slot = 3 * g + i;
-                    const uint32_t piece = H::pack(sum, 0.0f) & 0xffffu;
-                    sum -= half_lo<DT>(piece);
-                    sums[slot / 8][slot % 8 / 2] |= piece << (16 * (slot % 2));
+                    const uint32_t piece = H::pack(rest, 0.0f) & 0xffffu;
+                    rest -= half_lo<DT>(piece);
+                    sums[g / 2][(4 * g + i) % 8 / 2] |= piece << (16 * (i % 2));
                 }
             }
 #pragma unroll
@@ -259,11 +300,15 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
 #pragma unroll
                 for (int w = 0; w < 4; ++w) qb[y][w] = hh ? sums[2 * y + 1][w] : sums[2 * y][w];
 #pragma unroll
-            for (int j = 0; j < KS; ++j)
+            for (int j = 0; j < KS; ++j) {
+                u32x4 x = load(j);
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
-                    q[j][w] = __builtin_bit_cast(uint32_t, half2_of(ldexpf(half_lo<DT>(q[j][w]), -e),
-                                                                    ldexpf(half_hi<DT>(q[j][w]), -e)));
+                    x[w] = __builtin_bit_cast(uint32_t,
+                                              half2_of(ldexpf(half_lo<DT>(x[w]), -e), ldexpf(half_hi<DT>(x[w]), -e)));
+                if (j < KQ) q[j < KQ ? j : 0] = x;
+                else s_q[wave][(j - KQ) * 64 + lane] = x;   // read by the same lane
+            }
         }
 
         float m = 0.0f, top = -INFINITY, l = 0.0f;
@@ -276,128 +321,143 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
 
         const int* table = a.table + u.req * a.table_stride;
         const int blocks = min((part_end + 15) >> 4, a.columns << c.page_shift);
-        const int tiles = (part_end - key0 + PROMPT_KEYS - 1) / PROMPT_KEYS;
+        const int tiles = (part_end - key0 + KEYS - 1) / KEYS;
+        auto block_of = [&](int tile) { return ((key0 + KEYS * tile) >> 4) + my_blk; };
+        // The wave's block table entries of 64 tiles, one a lane: read by the scalar
+        // unit, each would hold up the next read of LDS.
+        int pages = -1;
         auto page_of = [&](int tile) {
-            const int blk = (key0 >> 4) + 4 * tile + my_blk;
-            return blk < blocks ? table[blk >> c.page_shift] : -1;
+            if (tile % 64 == 0) {
+                const int blk = block_of(tile + lane);
+                pages = blk < blocks ? table[blk >> c.page_shift] : -1;
+            }
+            return __builtin_amdgcn_readlane(pages, tile % 64);
         };
         W raw;
-        auto load = [&](int page, int tile) {
-            raw.load(c, page, head, (key0 >> 4) + 4 * tile + my_blk, part_end, value);
+        f32x16 s[NT];
+        auto skip = [&](int tile) {   // no row of the wave sees a key of the tile
+            const int key = key0 + KEYS * tile;
+            return key > any_hi || key + KEYS - 1 < any_lo;
         };
-        auto turn = [&](int tile) {   // this wave's block of the tile into LDS
-            if (value) {
-                int e;
-                if (!raw.values(s_v[tile & 1], e, my_blk)) s_bad[tile & 1] = tile + 1;
-                s_exponent[tile & 1][my_blk] = e;
-            } else {
-                raw.keys(s_k[tile & 1], s_factor[tile & 1], my_blk);
-                s_there[tile & 1][my_blk] = raw.there ? 1 : 0;
-            }
-        };
-        auto work = [&](int tile) {
-            const int tile_key = key0 + PROMPT_KEYS * tile;
-            if (tile_key > any_hi || tile_key + PROMPT_KEYS - 1 < any_lo) return;
-            // NT blocks of 32 keys at a time (one where the sums leave no registers for two)
-#pragma unroll 1
-            for (int t0 = 0; t0 < 2; t0 += NT) {
-                const int key = tile_key + 32 * t0;
-                const u32x4* sk = s_k[tile & 1] + t0 * (KS + BK) * 64 + lane;
-                const u32x4* sv = s_v[tile & 1] + 2 * t0 * DB * 64 + lane;
-                f32x16 s[NT];
+        auto scores = [&](int tile) {
+            if (skip(tile)) return;
+            const u32x4* sk = s_k[tile & 1] + lane;
+            u32x4 next[AHEAD];
+#ifdef QV_PRIO
+            __builtin_amdgcn_s_setprio(1);
+#endif
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
+            for (int y = 0; y < AHEAD; ++y) next[y] = sk[y * 64];
+            keep_order();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
+            for (int t = 0; t < NT; ++t) {
+                f32x16 part;
+                f32x4 f[4];
 #pragma unroll
-                    for (int y = 0; y < BK; ++y)
-                        s[t] = mfma32_type<DT>(sk[(t * (KS + BK) + KS + y) * 64], qb[y], s[t]);
+                for (int y = 0; y < BK + KS; ++y) {
+                    const int at = t * (BK + KS) + y, j = y - BK;
+                    if (j >= 0 && j % (GS / 16) == 0) {
 #pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        f32x16 part;
+                        for (int x = 0; x < 4; ++x)
+                            f[x] = *reinterpret_cast<const f32x4*>(
+                                &s_factor[tile & 1][KEYS * (j / (GS / 16)) + 32 * t + 8 * x + 4 * hh]);
+                    }
+                    u32x4 mine_q = y < BK ? qb[y < BK ? y : 0] : q[j >= 0 && j < KQ ? j : 0];
+                    if (j >= KQ) mine_q = s_q[wave][(j - KQ) * 64 + lane];
+                    const u32x4 operand = next[at % AHEAD];
+                    if (at + AHEAD < NT * (BK + KS)) next[at % AHEAD] = sk[(at + AHEAD) * 64];
+                    const f32x16 zero = {};
+                    if (y < BK) s[t] = mfma32_type<DT>(operand, mine_q, y == 0 ? zero : s[t]);
+                    else part = mfma32(operand, mine_q, j % (GS / 16) == 0 ? zero : part);
+                    keep_order();
+                    if (j >= 0 && j % (GS / 16) == GS / 16 - 1) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) part[e] = 0.0f;
-#pragma unroll
-                        for (int j = g * (GS / 16); j < (g + 1) * (GS / 16); ++j)
-                            part = mfma32(sk[(t * (KS + BK) + j) * 64], q[j], part);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const f32x4 f = *reinterpret_cast<const f32x4*>(
-                                &s_factor[tile & 1][64 * g + 32 * (t0 + t) + 8 * x + 4 * hh]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) s[t][4 * x + e] = fmaf(f[e], part[4 * x + e], s[t][4 * x + e]);
-                        }
+                        for (int e = 0; e < 16; ++e) s[t][e] = fmaf(f[e / 4][e % 4], part[e], s[t][e]);
                     }
                 }
-                bool all = key >= full_lo && key + 32 * NT - 1 <= full_hi;
-                uint32_t there = 0;   // a bit for each block of 16 keys
+            }
+#ifdef QV_PRIO
+            __builtin_amdgcn_s_setprio(0);
+#endif
+        };
+        auto sums = [&](int tile, int buffer) {
+            if (skip(tile)) return;
+            const int key = key0 + KEYS * tile;
+            const u32x4* sv = s_v[buffer] + lane;
+            u32x4 next[AHEAD];
 #pragma unroll
-                for (int x = 0; x < 2 * NT; ++x)
-                    there |= (uint32_t)__builtin_amdgcn_readfirstlane(s_there[tile & 1][2 * t0 + x]) << x;
-                if (!all || there != (1u << (2 * NT)) - 1) {
+            for (int y = 0; y < AHEAD; ++y) next[y] = sv[y * 64];
+            int exponent[2 * NT], now = most;
+            bool all = key >= full_lo && key + KEYS - 1 <= full_hi;
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int at = key + 32 * t + 8 * (e / 4) + 4 * hh + e % 4;
-                            const bool see = at >= lo && at <= hi && ((there >> (2 * t + e / 8)) & 1u);
-                            s[t][e] = see ? s[t][e] : -INFINITY;
-                        }
-                }
-                float mx = s[0][0];
+            for (int x = 0; x < 2 * NT; ++x) {
+                exponent[x] = __builtin_amdgcn_readfirstlane(s_exponent[buffer][x]);
+                now = max(now, exponent[x]);
+                all = all && exponent[x] != W::MISSING;
+            }
+            keep_order();
+            if (!all) {
+                const int first = key + 4 * hh - lo;
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[t][e]);
-                mx *= rf;
-                if (__any(mx > top)) {
-                    float now = fmaxf(mx, top - kSlack);
-                    now = fmaxf(now, __shfl_xor(now, 32, 64));
-                    const float safe = now > -INFINITY ? now : 0.0f;
-                    const float fade = top > -INFINITY ? __builtin_amdgcn_exp2f(m - safe) : 0.0f;
-                    top = now + kSlack;
-                    m = safe;
-                    l *= fade;
-#pragma unroll
-                    for (int d = 0; d < DB; ++d) o[d] *= fade;
-                }
-                int exponent[2 * NT], now = most;
-#pragma unroll
-                for (int x = 0; x < 2 * NT; ++x) {
-                    exponent[x] = __builtin_amdgcn_readfirstlane(s_exponent[tile & 1][2 * t0 + x]);
-                    now = max(now, exponent[x]);
-                }
-                if (now > most) {
-#pragma unroll
-                    for (int d = 0; d < DB; ++d) o[d] *= ldexpf(1.0f, most - now);
-                    most = now;
-                }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        // what is 2^-60 of the largest need not be told from 0
-                        const int less = max(exponent[2 * t + x] - most, -60);
-                        const float off = (float)less - m;
-                        float sum = 0.0f;
-#pragma unroll
-                        for (int e = 8 * x; e < 8 * x + 8; ++e) {
-                            s[t][e] = __builtin_amdgcn_exp2f(fmaf(s[t][e], rf, off));
-                            sum += s[t][e];
-                        }
-                        l = fmaf(sum, ldexpf(1.0f, -less), l);
-                        u32x4 p;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            p[e] = __builtin_bit_cast(uint32_t, half2_of(s[t][8 * x + 2 * e], s[t][8 * x + 2 * e + 1]));
-#pragma unroll
-                        for (int d = 0; d < DB; ++d) o[d] = mfma32(sv[((2 * t + x) * DB + d) * 64], p, o[d]);
+                    for (int e = 0; e < 16; ++e) {
+                        const bool see = (uint32_t)(first + 32 * t + 8 * (e / 4) + e % 4) <= (uint32_t)reach;
+                        s[t][e] = see && exponent[2 * t + e / 8] != W::MISSING ? s[t][e] : -INFINITY;
                     }
+            }
+            float mx = s[0][0];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[t][e]);
+            mx *= rf;
+            if (__any(mx > top)) {
+                float higher = fmaxf(mx, top - kSlack);
+                higher = fmaxf(higher, __shfl_xor(higher, 32, 64));
+                const float safe = higher > -INFINITY ? higher : 0.0f;
+                const float fade = top > -INFINITY ? __builtin_amdgcn_exp2f(m - safe) : 0.0f;
+                top = higher + kSlack;
+                m = safe;
+                l *= fade;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) o[d] *= fade;
+            }
+            if (now > most) {
+                const float fade = ldexpf(1.0f, most - now);
+#pragma unroll
+                for (int d = 0; d < DB; ++d) o[d] *= fade;
+                most = now;
+            }
+#pragma unroll
+            for (int x = 0; x < 2 * NT; ++x) {
+                // what is 2^-60 of the largest need not be told from 0
+                const int less = max(exponent[x] - most, -60);
+                const float off = (float)less - m;
+                f32x16& y = s[x / 2];
+                float sum = 0.0f;
+                u32x4 p;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int z = 8 * (x % 2) + 2 * e;
+                    const float p0 = __builtin_amdgcn_exp2f(fmaf(y[z], rf, off));
+                    const float p1 = __builtin_amdgcn_exp2f(fmaf(y[z + 1], rf, off));
+                    p[e] = __builtin_bit_cast(uint32_t, half2_of(p0, p1));
+                    sum += p0 + p1;
+                }
+                l = fmaf(sum, ldexpf(1.0f, -less), l);
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    const int at = x * DB + d;
+                    const u32x4 operand = next[at % AHEAD];
+                    if (at + AHEAD < 2 * NT * DB) next[at % AHEAD] = sv[(at + AHEAD) * 64];
+                    o[d] = mfma32(operand, p, o[d]);
+                    keep_order();
                 }
             }
-            if (s_bad[tile & 1] == tile + 1) {   // values that are not finite, to the rows that see them
-                for (int t = 0; t < PROMPT_KEYS; ++t) {
-                    const int at = tile_key + t;
+            if (s_bad[buffer] == tile + 1) {   // values that are not finite, to the rows that see them
+                for (int t = 0; t < KEYS; ++t) {
+                    const int at = key + t;
                     const int page = (at >> 4) < blocks ? table[at >> 4 >> c.page_shift] : -1;
                     if (at >= part_end || page < 0 || page >= c.num_pages) continue;
                     const size_t tok = (((size_t)page * c.heads + head) << (c.page_shift + 4)) +
@@ -407,7 +467,7 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                         const uint32_t p = c.vs[tok * G + g];
                         const float x = half_lo<DT>(p), y = half_hi<DT>(p);
                         if ((x - x) + (y - y) == 0.0f) continue;
-                        const float add = at >= lo && at <= hi ? fmaf(0.0f, x, y) : 0.0f;
+                        const float add = (uint32_t)(at - lo) <= (uint32_t)reach ? fmaf(0.0f, x, y) : 0.0f;
 #pragma unroll
                         for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -418,25 +478,30 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
             }
         };
 
-        if (threadIdx.x < 2) s_bad[threadIdx.x] = 0;
+        if (threadIdx.x < 3) s_bad[threadIdx.x] = 0;
+        if (tiles > 0) raw.load(c, page_of(0), head, block_of(0), my_part, part_end, value);
+        int page = page_of(1);
         __syncthreads();
-        if (tiles > 0) {
-            load(page_of(0), 0);
-            int page = page_of(1);
-            turn(0);
-            load(page, 1);
-            page = page_of(2);
-            __syncthreads();
-            for (int t = 0; t < tiles; ++t) {
-                if (value) work(t);
-                if (t + 1 < tiles) {
-                    turn(t + 1);
-                    load(page, t + 2);
-                    page = page_of(t + 3);
+        int buffer = 2;   // of tile t's values
+        for (int t = -1; t < tiles; ++t) {
+            const int after = buffer == 2 ? 0 : buffer + 1;
+            if (t + 1 < tiles) {   // tile t + 1 to LDS, the next one's codes to registers
+                if (value) {
+                    int e;
+                    if (!raw.values(s_v[after], e, my_blk, my_part)) s_bad[after] = t + 2;
+                    if (my_part == 0) s_exponent[after][my_blk] = e;
+                } else {
+                    raw.keys(s_k[(t + 1) & 1], s_factor[(t + 1) & 1], my_blk, my_part);
                 }
-                if (!value) work(t);
-                __syncthreads();
+                const int next_page = page_of(t + 3);   // what waits for it must not wait for the codes
+                raw.load(c, page, head, block_of(t + 2), my_part, part_end, value);
+                page = next_page;
             }
+            if (t >= 0) scores(t);
+            if (value) __syncthreads();
+            if (t >= 0) sums(t, buffer);
+            if (!value) __syncthreads();
+            buffer = after;
         }
 
         l += __shfl_xor(l, 32, 64);
