@@ -44,7 +44,8 @@ struct Kv4AttnPlan {
     int lines, least;
     int cost;     // what a unit costs beside its steps, in steps: on a line, units stand this far apart
 };
-constexpr int KV4_LINE_UNITS = 1024;   // most units of a head that can be laid end to end
+// Most units of a head that can be laid end to end, by a work-group's waves.
+constexpr int kv4_line_units(int waves) { return waves == 4 ? 1024 : 512; }
 
 struct Kv4AttnArgs {
     Kv4View c;

@@ -68,7 +68,7 @@ Kv4AttnPlan kv4_attn_plan(int requests, int heads, int kv_heads, int dim, int ma
     p.tiles = (int)((rows + p.rows - 1) / p.rows);
     const long long units = (long long)requests * p.tiles;
     const bool line = keys > 1024 && (!prompt || units * kv_heads < 4 * cus) && units > 0 &&
-                      units <= KV4_LINE_UNITS && units * (keys / 32 + 32) <= INT_MAX;
+                      units <= kv4_line_units(prompt ? kv4::PROMPT_WAVES : 4) && units * (keys / 32 + 32) <= INT_MAX;
     p.waves = prompt ? kv4::PROMPT_WAVES : line || dim == 256 ? 4 : 8;
     p.lines = line ? std::max(1, (prompt ? 1 : 2) * cus / kv_heads) : 0;
     // A unit's queries, first loads and joining waves wait on memory about four

@@ -15,17 +15,22 @@
 //   probabilities that a lane computes are the operand it needs (as in
 //   kv4_attn_impl.h), the values' tokens being put into that order.
 //
-// A code c enters both products as the bits of the float16 number c 2^-18, which
-// is exact.  Keys stay codes: a group's product is multiplied by the token's
-// scale in 32 bits, and the biases times the queries' sums (each in three
-// pieces of the type, which hold 24 bits) are a first step of the product; so
-// scores are as exact as their 32-bit sums.  Queries are float16, brought to at
-// most 1 by a power of two a row (what is under 2^-14 of the largest keeps
-// 2^-25 of it).  A value becomes c s + b in one multiply-add, a block of 16
-// tokens brought to at most 1 by a power of two that goes into the
-// probabilities' exponent, relative to the largest met so far; values and
-// probabilities are rounded to float16, half a step 2^-11, as the matrix cores
-// need (bfloat16 would cost eight times that).  All sums are float32.
+// A code c becomes an operand from the bits of the float16 number c 2^-18, which
+// is exact, in one multiply-add.  Queries are float16, brought to at most 1 by a
+// power of two a row (what is under 2^-14 of the largest keeps 2^-25 of it).
+//
+// Keys of bfloat16 scales: s (c - 8) has 8 + 3 bits, so float16 holds it exactly,
+// the block of 16 tokens brought to at most 1 by a power of two that goes into
+// the softmax scale.  What is left, b + 8 s, times the sums of the queries is a
+// first step of the product: b and s by the sums in three bfloat16 pieces each,
+// which hold 24 bits.  Keys of float16 scales (11 bits) stay codes, and a group's
+// product is multiplied by the token's scale in 32 bits.  Either way scores are
+// as exact as their 32-bit sums.
+//
+// Values become c s + b divided by a power of two, the largest of the unit so
+// far; when it rises, the sums are divided too.  Values and probabilities are
+// rounded to float16, half a step 2^-11, as the matrix cores need (bfloat16
+// would cost eight times that).  All sums are float32.
 //
 // 0 * NaN is NaN in a product, so values that are not finite are entered as 0
 // and added afterwards to the rows that see them (a tile that holds one is rare
@@ -86,91 +91,141 @@ __device__ __forceinline__ float wave_max(float v) {
                               max(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48))));
 }
 
-// What a lane takes of one block of 16 tokens to turn it into operands: codes,
-// and pairs of the D / SPLIT dimensions that fall to its wave.  Keys: the lane's
+// What a lane takes of one block of 16 tokens to turn it into operands: codes of
+// the D / SPLIT dimensions that fall to its wave, and pairs.  Keys: the lane's
 // token n = lane % 16; values: the tokens 4h .. 4h + 3, h = lane / 16, their pairs
-// spread over the row's 16 lanes as in kv4_attn_impl.h.
+// spread over the row's 16 lanes as in kv4_attn_impl.h, and all pairs of the
+// tile, spread over the wave, for their largest.
 template <int D, int GS, int DT>
 struct Raw {
     static constexpr int KEYS = 64 * 128 / (D < 128 ? 128 : D);   // of a tile
     static constexpr int SPLIT = 64 / KEYS;                       // waves that share a block
     static constexpr int NJ = D / 32, G = D / GS, KS = D / 16, DB = D / 32;
     static constexpr int NW = NJ / SPLIT, GW = G / SPLIT;         // words and groups of a wave
-    static constexpr int BK = (4 * G + 15) / 16;                  // steps of the product of biases
-    static constexpr int SHARE = (4 * G + 15) / 16;               // a lane's share of the values' pairs
-    static constexpr int EMPTY = -120, MISSING = -1000;           // exponents of no values, and of no page
-    uint32_t w[NW], sb[GW > SHARE ? GW : SHARE];
-    bool there;
-    int tokens;   // of the block, from its first on, that are there
+    static constexpr bool SCALED = DT == DT_BF16;                 // keys enter the product with their scales
+    static constexpr int SLOTS = SCALED ? 8 : 4;                  // of a group in the product of biases
+    static constexpr int BK = (SLOTS * G + 15) / 16;              // its steps
+    static constexpr int SHARE = (4 * G + 15) / 16;               // a lane's share of a block's pairs
+    static constexpr int ALL = G / SPLIT;                         // a lane's share of the tile's pairs
+    static constexpr int EMPTY = -120;                            // exponent of nothing but zeros
+    uint32_t w[NW], sb[G > SHARE + ALL ? G : SHARE + ALL];
+    bool there;    // the block's page is in the cache
+    int tokens;    // of the block, from its first on, that are there
+    bool live;     // values: the lane's token of the tile is there
 
-    __device__ __forceinline__ void load(const Kv4View& c, int page, int head, int blk, int part, int end,
-                                         bool value) {
+    // `pages`: entries of 64 blocks of 16 tokens, one a lane, from a tile's start
+    // on; the tile's are from `first` on, `key` its first key.
+    __device__ __forceinline__ void load(const Kv4View& c, int pages, int first, int head, int key, int my_blk,
+                                         int part, int end, bool value) {
         const int lane = threadIdx.x & 63;
+        const int page = __builtin_amdgcn_readlane(pages, first + my_blk), blk = (key >> 4) + my_blk;
+        const int mask = (1 << c.page_shift) - 1;
+        if (value) {
+            const int at = key + lane % KEYS;
+            const int its = __shfl(pages, first + lane % KEYS / 16, 64);
+            live = at < end && its >= 0 && its < c.num_pages;
+            if (live) {
+                const size_t row = (((size_t)its * c.heads + head) << c.page_shift) + ((at >> 4) & mask);
+                const uint32_t* from = c.vs + (row * 16 + (at & 15)) * G + lane / KEYS * ALL;
+#pragma unroll
+                for (int g = 0; g < ALL; ++g) sb[SHARE + g] = from[g];
+            }
+        }
         tokens = end - 16 * blk;
         there = tokens > 0 && page >= 0 && page < c.num_pages;
         if (!there) return;
-        const size_t at = (((size_t)page * c.heads + head) << c.page_shift) + (blk & ((1 << c.page_shift) - 1));
+        const size_t at = (((size_t)page * c.heads + head) << c.page_shift) + (blk & mask);
         load_words(w, (value ? c.vc : c.kc) + at * (64 * NJ) + lane * NJ + part * NW);
         if (value) {
             const uint32_t* from = c.vs + at * (16 * G) + (lane >> 4) * (4 * G);
 #pragma unroll
             for (int r = 0; r < SHARE; ++r) sb[r] = from[(16 * r + (lane & 15)) & (4 * G - 1)];
         } else {
-            const uint32_t* from = c.ks + at * (16 * G) + (lane & 15) * G + part * GW;
+            const uint32_t* from = c.ks + at * (16 * G) + (lane & 15) * G;
 #pragma unroll
-            for (int g = 0; g < GW; ++g) sb[g] = from[g];
+            for (int g = 0; g < G; ++g) sb[g] = from[g];
         }
     }
 
-    // Keys to `k` [blocks of 32][BK + KS][2][32] of 16 bytes, the scales times
-    // 2^18 to `factor` [G][KEYS]; `blk` counts in the tile.
-    __device__ __forceinline__ void keys(u32x4* k, float* factor, int blk, int part) const {
+    // Keys to `k` [blocks of 32][BK + KS][2][32] of 16 bytes; `blk` counts in the
+    // tile.  SCALED: divided by 2^(what is returned).  Else: the scales times
+    // 2^18 to `factor` [G][KEYS].
+    __device__ __forceinline__ int keys(u32x4* k, float* factor, int blk, int part) const {
         const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
         u32x4* to = k + (blk >> 1) * (BK + KS) * 64 + (blk & 1) * 16 + n;
         const bool live = there && n < tokens;
+        int e = 0;
+        if constexpr (SCALED) {
+            float most = 0.0f;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const float x = fmaxf(fabsf(8.0f * half_lo<DT>(sb[g])), fabsf(half_hi<DT>(sb[g])));
+                most = x < INFINITY ? fmaxf(most, x) : most;
+            }
+            most = wave_max(live ? most : 0.0f);
+            e = most > 0.0f ? __builtin_amdgcn_frexp_expf(most) : EMPTY;
+        }
 #pragma unroll
         for (int g = 0; g < GW; ++g) {
             const int group = part * GW + g;
-            if (h == g % 4) {   // slots 4 * group .. + 2 take the group's bias
-                const uint32_t b = live ? sb[g] >> 16 : 0u;
+            const uint32_t pair = live ? (SPLIT == 2 && part ? sb[GW + g < G ? GW + g : 0] : sb[g]) : 0u;
+            const float s = half_lo<DT>(pair);
+            f16x2 s2, b2;
+            if constexpr (SCALED) {
+                s2 = half2_of(ldexpf(s, 18 - e), ldexpf(s, 18 - e));
+                b2 = half2_of(-ldexpf(s, 3 - e), -ldexpf(s, 3 - e));
+                if (h == g % 4) {   // 8 slots: three times b, and three times s for 8 s
+                    const uint32_t x = Half<DT>::pack(ldexpf(half_hi<DT>(pair), -e), ldexpf(s, -e));
+                    const uint32_t b = x & 0xffffu, y = x >> 16;
+                    to[(group / 2) * 64 + (group % 2) * 32] = u32x4{b | (b << 16), b, y | (y << 16), y};
+                }
+            } else if (h == g % 4) {   // 4 slots: three times b
+                const uint32_t b = pair >> 16;
                 reinterpret_cast<u32x2*>(to + (group / 4) * 64 + (group / 2 % 2) * 32)[group % 2] =
                     u32x2{b | (b << 16), b};
-                factor[KEYS * group + 16 * blk + n] = live ? half_lo<DT>(sb[g]) * 0x1p18f : 0.0f;
+                factor[KEYS * group + 16 * blk + n] = s * 0x1p18f;
+            }
+#pragma unroll
+            for (int j = g * (GS / 32); j < (g + 1) * (GS / 32); ++j) {
+                u32x4 x;
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const uint32_t y = tiny_codes(w[j], f);
+                    x[f] = SCALED ? __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(
+                                                                     __builtin_bit_cast(f16x2, y), s2, b2))
+                                  : y;
+                }
+                to[(BK + 2 * (part * NW + j) + (h >> 1)) * 64 + (h & 1) * 32] = x;
             }
         }
-#pragma unroll
-        for (int j = 0; j < NW; ++j) {
-            u32x4 x;
-#pragma unroll
-            for (int f = 0; f < 4; ++f) x[f] = tiny_codes(w[j], f);
-            to[(BK + 2 * (part * NW + j) + (h >> 1)) * 64 + (h & 1) * 32] = x;
-        }
+        return e;
     }
 
-    // Values to `v` [blocks of 16][DB][2][32] of 16 bytes, all of the block's
-    // divided by 2^exponent.  Whether they are finite.
+    // Values to `v` [blocks of 16][DB][2][32] of 16 bytes, divided by 2^exponent,
+    // which rises to the tile's largest.  Whether the tile is finite.
     __device__ __forceinline__ bool values(u32x4* v, int& exponent, int blk, int part) const {
         const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
         u32x2* to = reinterpret_cast<u32x2*>(v + ((blk * DB + part * (DB / SPLIT)) * 2 + (h & 1)) * 32 + n) + (h >> 1);
-        float s[SHARE], b[SHARE], most = 0.0f;
+        float most = 0.0f;
         bool good = true;
 #pragma unroll
-        for (int r = 0; r < SHARE; ++r) {
-            const bool live = there && 4 * h + ((16 * r + n) & (4 * G - 1)) / G < tokens;
-            const float x = half_lo<DT>(sb[r]), y = half_hi<DT>(sb[r]);
+        for (int g = 0; g < ALL; ++g) {
+            const float x = half_lo<DT>(sb[SHARE + g]), y = half_hi<DT>(sb[SHARE + g]);
             const bool finite = (x - x) + (y - y) == 0.0f;
             good = good && (finite || !live);
-            s[r] = live && finite ? x : 0.0f;
-            b[r] = live && finite ? y : 0.0f;
-            most = fmaxf(most, fmaxf(fabsf(b[r]), fabsf(fmaf(15.0f, s[r], b[r]))));
+            const float z = fmaxf(fabsf(y), fabsf(fmaf(15.0f, x, y)));
+            most = live && finite ? fmaxf(most, z) : most;
         }
         most = wave_max(most);
-        const int e = most > 0.0f ? __builtin_amdgcn_frexp_expf(fminf(most, 0x1.fffffep127f)) : EMPTY;
-        exponent = there ? e : MISSING;
+        if (most > 0.0f) exponent = max(exponent, __builtin_amdgcn_frexp_expf(fminf(most, 0x1.fffffep127f)));
+        const int e = exponent;
         uint32_t pair[SHARE];   // scale 2^18 and bias, float16
 #pragma unroll
-        for (int r = 0; r < SHARE; ++r)
-            pair[r] = __builtin_bit_cast(uint32_t, half2_of(ldexpf(s[r], 18 - e), ldexpf(b[r], -e)));
+        for (int r = 0; r < SHARE; ++r) {
+            const float x = half_lo<DT>(sb[r]), y = half_hi<DT>(sb[r]);
+            const bool use = there && 4 * h + ((16 * r + n) & (4 * G - 1)) / G < tokens && (x - x) + (y - y) == 0.0f;
+            pair[r] = use ? __builtin_bit_cast(uint32_t, half2_of(ldexpf(x, 18 - e), ldexpf(y, -e))) : 0u;
+        }
 #pragma unroll
         for (int g = 0; g < GW; ++g) {
             f16x2 s2[2], b2[2];   // of two tokens
@@ -212,14 +267,14 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
     constexpr int KS = D / 16, DB = D / 32, G = D / GS, BK = W::BK, KEYS = W::KEYS, NT = KEYS / 32;
     constexpr int KQ = D == 256 ? KS / 2 : KS;   // steps whose queries stay in registers; the others' in LDS
     #ifndef QV_AHEAD
-#define QV_AHEAD 4
+#define QV_AHEAD (D == 256 ? 2 : 4)
 #endif
     constexpr int AHEAD = QV_AHEAD;                   // operands read ahead
     constexpr float kSlack = 8.0f;
     __shared__ u32x4 s_k[2][NT * (BK + KS) * 64], s_v[3][2 * NT * DB * 64];
     __shared__ u32x4 s_q[PROMPT_WAVES][KS > KQ ? (KS - KQ) * 64 : 1];
-    __shared__ float s_factor[2][G * KEYS];
-    __shared__ int s_bad[3], s_exponent[3][4];
+    __shared__ float s_factor[2][W::SCALED ? 1 : G * KEYS];
+    __shared__ int s_bad[3], s_there[3][4], s_key_exponent[3][4], s_value_exponent[3];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, n = lane & 31, hh = lane >> 5;
     const Kv4View& c = a.c;
@@ -284,7 +339,7 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
             most = fmaxf(most, __shfl_xor(most, 32, 64));
             const int e = min(__builtin_amdgcn_frexp_expf(most), 127);
             rf = ldexpf(a.scale_log2, e);
-            u32x4 sums[2 * BK] = {};   // slot 4g + i: piece i of group g's sum
+            u32x4 sums[2 * BK] = {};   // a group's slots: the sum's pieces, and those of 8 times it
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 float rest = ldexpf(sum[g] + __shfl_xor(sum[g], 32, 64), -e);
@@ -292,7 +347,11 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                 for (int i = 0; i < 3; ++i) {
                     const uint32_t piece = H::pack(rest, 0.0f) & 0xffffu;
                     rest -= half_lo<DT>(piece);
-                    sums[g / 2][(4 * g + i) % 8 / 2] |= piece << (16 * (i % 2));
+                    const int slot = W::SLOTS * g + i;
+                    sums[slot / 8][slot % 8 / 2] |= piece << (16 * (slot % 2));
+                    if constexpr (W::SCALED)
+                        sums[slot / 8][2 + i / 2] |= (H::pack(8.0f * half_lo<DT>(piece), 0.0f) & 0xffffu)
+                                                     << (16 * (i % 2));
                 }
             }
 #pragma unroll
@@ -322,18 +381,21 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
         const int* table = a.table + u.req * a.table_stride;
         const int blocks = min((part_end + 15) >> 4, a.columns << c.page_shift);
         const int tiles = (part_end - key0 + KEYS - 1) / KEYS;
-        auto block_of = [&](int tile) { return ((key0 + KEYS * tile) >> 4) + my_blk; };
-        // The wave's block table entries of 64 tiles, one a lane: read by the scalar
-        // unit, each would hold up the next read of LDS.
+        // Block table entries of 64 blocks, one a lane: read by the scalar unit, each
+        // would hold up the next read of LDS.
+        constexpr int BLOCKS = KEYS / 16, FETCH = 64 / BLOCKS;   // of a tile; tiles an entry read goes for
         int pages = -1;
-        auto page_of = [&](int tile) {
-            if (tile % 64 == 0) {
-                const int blk = block_of(tile + lane);
+        auto fetch = [&](int tile) {   // for the tile that is loaded next
+            if (tile % FETCH == 0) {
+                const int blk = ((key0 + KEYS * tile) >> 4) + lane;
                 pages = blk < blocks ? table[blk >> c.page_shift] : -1;
             }
-            return __builtin_amdgcn_readlane(pages, tile % 64);
         };
         W raw;
+        int exponent = W::EMPTY;   // of the values so far (the waves that turn them)
+        auto load = [&](int tile) {
+            raw.load(c, pages, tile % FETCH * BLOCKS, head, key0 + KEYS * tile, my_blk, my_part, part_end, value);
+        };
         f32x16 s[NT];
         auto skip = [&](int tile) {   // no row of the wave sees a key of the tile
             const int key = key0 + KEYS * tile;
@@ -356,7 +418,7 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
 #pragma unroll
                 for (int y = 0; y < BK + KS; ++y) {
                     const int at = t * (BK + KS) + y, j = y - BK;
-                    if (j >= 0 && j % (GS / 16) == 0) {
+                    if (!W::SCALED && j >= 0 && j % (GS / 16) == 0) {
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
                             f[x] = *reinterpret_cast<const f32x4*>(
@@ -368,9 +430,10 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                     if (at + AHEAD < NT * (BK + KS)) next[at % AHEAD] = sk[(at + AHEAD) * 64];
                     const f32x16 zero = {};
                     if (y < BK) s[t] = mfma32_type<DT>(operand, mine_q, y == 0 ? zero : s[t]);
+                    else if (W::SCALED) s[t] = mfma32(operand, mine_q, s[t]);
                     else part = mfma32(operand, mine_q, j % (GS / 16) == 0 ? zero : part);
                     keep_order();
-                    if (j >= 0 && j % (GS / 16) == GS / 16 - 1) {
+                    if (!W::SCALED && j >= 0 && j % (GS / 16) == GS / 16 - 1) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) s[t][e] = fmaf(f[e / 4][e % 4], part[e], s[t][e]);
                     }
@@ -387,13 +450,14 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
             u32x4 next[AHEAD];
 #pragma unroll
             for (int y = 0; y < AHEAD; ++y) next[y] = sv[y * 64];
-            int exponent[2 * NT], now = most;
-            bool all = key >= full_lo && key + KEYS - 1 <= full_hi;
+            const int now = __builtin_amdgcn_readfirstlane(s_value_exponent[buffer]);
+            bool all = key >= full_lo && key + KEYS - 1 <= full_hi, there[BLOCKS];
+            float by[BLOCKS];   // what takes a block's scores to powers of two
 #pragma unroll
-            for (int x = 0; x < 2 * NT; ++x) {
-                exponent[x] = __builtin_amdgcn_readfirstlane(s_exponent[buffer][x]);
-                now = max(now, exponent[x]);
-                all = all && exponent[x] != W::MISSING;
+            for (int x = 0; x < BLOCKS; ++x) {
+                there[x] = __builtin_amdgcn_readfirstlane(s_there[buffer][x]);
+                all = all && there[x];
+                by[x] = W::SCALED ? ldexpf(rf, __builtin_amdgcn_readfirstlane(s_key_exponent[buffer][x])) : rf;
             }
             keep_order();
             if (!all) {
@@ -403,15 +467,17 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const bool see = (uint32_t)(first + 32 * t + 8 * (e / 4) + e % 4) <= (uint32_t)reach;
-                        s[t][e] = see && exponent[2 * t + e / 8] != W::MISSING ? s[t][e] : -INFINITY;
+                        s[t][e] = see && there[2 * t + e / 8] ? s[t][e] : -INFINITY;
                     }
             }
-            float mx = s[0][0];
+            float mx = -INFINITY;
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int x = 0; x < BLOCKS; ++x) {
+                float z = s[x / 2][8 * (x % 2)];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[t][e]);
-            mx *= rf;
+                for (int e = 1; e < 8; ++e) z = fmaxf(z, s[x / 2][8 * (x % 2) + e]);
+                mx = fmaxf(mx, z * by[x]);
+            }
             if (__any(mx > top)) {
                 float higher = fmaxf(mx, top - kSlack);
                 higher = fmaxf(higher, __shfl_xor(higher, 32, 64));
@@ -430,27 +496,22 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                 most = now;
             }
 #pragma unroll
-            for (int x = 0; x < 2 * NT; ++x) {
-                // what is 2^-60 of the largest need not be told from 0
-                const int less = max(exponent[x] - most, -60);
-                const float off = (float)less - m;
-                f32x16& y = s[x / 2];
-                float sum = 0.0f;
+            for (int x = 0; x < BLOCKS; ++x) {
+                const f32x16& y = s[x / 2];
                 u32x4 p;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int z = 8 * (x % 2) + 2 * e;
-                    const float p0 = __builtin_amdgcn_exp2f(fmaf(y[z], rf, off));
-                    const float p1 = __builtin_amdgcn_exp2f(fmaf(y[z + 1], rf, off));
+                    const float p0 = __builtin_amdgcn_exp2f(fmaf(y[z], by[x], -m));
+                    const float p1 = __builtin_amdgcn_exp2f(fmaf(y[z + 1], by[x], -m));
+                    l += p0 + p1;
                     p[e] = __builtin_bit_cast(uint32_t, half2_of(p0, p1));
-                    sum += p0 + p1;
                 }
-                l = fmaf(sum, ldexpf(1.0f, -less), l);
 #pragma unroll
                 for (int d = 0; d < DB; ++d) {
                     const int at = x * DB + d;
                     const u32x4 operand = next[at % AHEAD];
-                    if (at + AHEAD < 2 * NT * DB) next[at % AHEAD] = sv[(at + AHEAD) * 64];
+                    if (at + AHEAD < BLOCKS * DB) next[at % AHEAD] = sv[(at + AHEAD) * 64];
                     o[d] = mfma32(operand, p, o[d]);
                     keep_order();
                 }
@@ -479,23 +540,30 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
         };
 
         if (threadIdx.x < 3) s_bad[threadIdx.x] = 0;
-        if (tiles > 0) raw.load(c, page_of(0), head, block_of(0), my_part, part_end, value);
-        int page = page_of(1);
+        if (tiles > 0) {
+            fetch(0);
+            load(0);
+        }
         __syncthreads();
-        int buffer = 2;   // of tile t's values
+        int buffer = 2;   // of tile t
         for (int t = -1; t < tiles; ++t) {
             const int after = buffer == 2 ? 0 : buffer + 1;
             if (t + 1 < tiles) {   // tile t + 1 to LDS, the next one's codes to registers
                 if (value) {
-                    int e;
-                    if (!raw.values(s_v[after], e, my_blk, my_part)) s_bad[after] = t + 2;
-                    if (my_part == 0) s_exponent[after][my_blk] = e;
+                    const bool good = raw.values(s_v[after], exponent, my_blk, my_part);
+                    if (wave == 4) {
+                        if (!good) s_bad[after] = t + 2;
+                        s_value_exponent[after] = exponent;
+                    }
                 } else {
-                    raw.keys(s_k[(t + 1) & 1], s_factor[(t + 1) & 1], my_blk, my_part);
+                    const int e = raw.keys(s_k[(t + 1) & 1], s_factor[(t + 1) & 1], my_blk, my_part);
+                    if (my_part == 0) {
+                        s_key_exponent[after][my_blk] = e;
+                        s_there[after][my_blk] = raw.there ? 1 : 0;
+                    }
                 }
-                const int next_page = page_of(t + 3);   // what waits for it must not wait for the codes
-                raw.load(c, page, head, block_of(t + 2), my_part, part_end, value);
-                page = next_page;
+                fetch(t + 2);
+                load(t + 2);
             }
             if (t >= 0) scores(t);
             if (value) __syncthreads();

@@ -71,14 +71,15 @@ class Units {
 
   public:
     __device__ __forceinline__ Units(const Kv4AttnArgs& a, int id, int head) : id_(id), count_(a.requests * a.p.tiles) {
-        __shared__ int s_begin[KV4_LINE_UNITS], s_end[KV4_LINE_UNITS];
+        constexpr int MOST = kv4_line_units(THREADS / 64);
+        __shared__ int s_begin[MOST], s_end[MOST];
         __shared__ int s_waves[THREADS / 64];
         begin_ = s_begin;
         end_ = s_end;
         at_ = 0;
         stop_ = 1;
         if (!a.p.lines) return;
-        constexpr int EACH = KV4_LINE_UNITS / THREADS;
+        constexpr int EACH = MOST / THREADS;
         int n[EACH], sum = 0, total;
         const int per = (count_ + THREADS - 1) / THREADS;   // units a thread, at most EACH
         const int v0 = (int)threadIdx.x * per;
