@@ -77,8 +77,25 @@ __device__ __forceinline__ u32x4 load8(const uint16_t* p) {
     return w;
 }
 
-// Codes of the lane's eight elements, and the (scale, bias) pair of its group,
-// whose elements lie in GS / 8 neighbouring lanes.
+// The value of the lane whose number differs in the bits of MASK (1, 2, 4 or 8),
+// without a trip through LDS.
+template <int MASK>
+__device__ __forceinline__ uint32_t across(uint32_t v) {
+    const int x = (int)v;
+    if constexpr (MASK == 1) return (uint32_t)__builtin_amdgcn_mov_dpp(x, 0xb1, 0xf, 0xf, true);    // quad 1 0 3 2
+    if constexpr (MASK == 2) return (uint32_t)__builtin_amdgcn_mov_dpp(x, 0x4e, 0xf, 0xf, true);    // quad 2 3 0 1
+    if constexpr (MASK == 8) return (uint32_t)__builtin_amdgcn_mov_dpp(x, 0x128, 0xf, 0xf, true);   // row turned by 8
+    const int y = __builtin_amdgcn_mov_dpp(x, 0x141, 0xf, 0xf, true);                               // halves mirrored
+    return (uint32_t)__builtin_amdgcn_mov_dpp(y, 0x1b, 0xf, 0xf, true);                             // quad 3 2 1 0
+}
+
+// A row (token, head) is cut among D / 8 lanes: lane u has the eight elements
+// from elements_of(u) on.  The four lanes of a quad have those 16 apart, which
+// share the 16-bit halves of the value codes; a group of GS elements lies in the
+// lanes that differ in bits 0 and 2 (GS = 32), 0..2 (64) or 0..3 (128).
+__device__ __forceinline__ int elements_of(int u) { return 64 * (u >> 3) + 16 * (u & 3) + 8 * ((u >> 2) & 1); }
+
+// Codes of the lane's eight elements, and the (scale, bias) pair of its group.
 template <int DT, int GS>
 __device__ __forceinline__ uint32_t quantise8(u32x4 w, uint32_t (&c)[8]) {
     uint32_t lo = sortable(w[0]), hi = lo;
@@ -88,11 +105,14 @@ __device__ __forceinline__ uint32_t quantise8(u32x4 w, uint32_t (&c)[8]) {
         lo = min2(lo, k);
         hi = max2(hi, k);
     }
-#pragma unroll
-    for (int off = 1; off < GS / 8; off <<= 1) {
-        lo = min2(lo, __shfl_xor(lo, off, 64));
-        hi = max2(hi, __shfl_xor(hi, off, 64));
-    }
+    auto join = [&](auto mask) {
+        lo = min2(lo, across<decltype(mask)::value>(lo));
+        hi = max2(hi, across<decltype(mask)::value>(hi));
+    };
+    join(std::integral_constant<int, 1>());
+    join(std::integral_constant<int, 4>());
+    if constexpr (GS >= 64) join(std::integral_constant<int, 2>());
+    if constexpr (GS >= 128) join(std::integral_constant<int, 8>());
     lo = min2(lo, (lo >> 16) | (lo << 16));
     hi = max2(hi, (hi >> 16) | (hi << 16));
     const uint32_t lob = sortable(lo) & 0xffffu, hib = sortable(hi) & 0xffffu;
@@ -108,95 +128,114 @@ __device__ __forceinline__ uint32_t quantise8(u32x4 w, uint32_t (&c)[8]) {
     return sb | (lob << 16);
 }
 
-// D / 8 lanes take one row (token, head): a lane its eight neighbouring
-// elements.  Keys: the lane's codes are one word.  Values: a half holds the
-// codes of elements 16 apart, which lie in four lanes; two exchanges leave
-// each of the four with two whole halves.
+// Rows in the order in which the cache keeps them: 16 tokens of a head, then
+// the next head, so that a work-group's rows share the cache's lines.
+struct Row {
+    long long token;
+    int head, u;
+};
+template <int D>
+__device__ __forceinline__ Row row_of(int heads, int tokens) {
+    constexpr uint32_t LANES = D / 8;
+    const uint32_t unit = blockIdx.x * (THREADS / LANES) + threadIdx.x / LANES;   // at most tokens * heads and a group
+    const uint32_t block = unit / (16u * heads), in = unit - block * (16u * heads);
+    const int u = (int)(threadIdx.x % LANES);
+    const long long first = 16ll * block;
+    if (first + 16 <= tokens) return {first + (in & 15), (int)(in >> 4), u};
+    const uint32_t left = first < tokens ? (uint32_t)(tokens - first) : 1;   // the last block is short
+    return {first + in % left, (int)(in / left), u};
+}
+
+// Where a token's codes and pairs are.
+struct Place {
+    bool there;
+    long long block, pair;   // pair: of the row's first group
+    int t;
+};
+template <int D, int GS>
+__device__ __forceinline__ Place place_of(const Kv4View& c, int slot, int head) {
+    Place p;
+    const int page_tokens = 16 << c.page_shift;
+    const int page = slot >= 0 ? slot / page_tokens : -1;
+    p.there = page >= 0 && page < c.num_pages;
+    const int at = slot % page_tokens;
+    const long long row = (long long)page * c.heads + head;
+    p.block = (row << c.page_shift) + (at >> 4);
+    p.pair = (row * page_tokens + at) * (D / GS);
+    p.t = at & 15;
+    return p;
+}
+
+// Keys: the lane's codes are one word.  Values: a quad's codes are eight halves,
+// two of which each lane is left with after two exchanges.
 template <int D, int GS, int DT, bool VEC>
 __global__ __launch_bounds__(THREADS) void kv4_write_kernel(Kv4View c, const uint16_t* k, const uint16_t* v,
                                                             long long k_ts, long long k_hs, long long v_ts,
                                                             long long v_hs, const int* slots, int tokens) {
-    constexpr int LANES = D / 8;
-    const long long unit = ((long long)blockIdx.x * THREADS + threadIdx.x) / LANES;
-    const int u = threadIdx.x % LANES;
-    const long long token = unit / c.heads;
-    const int head = (int)(unit % c.heads);
-    const int slot = token < tokens ? slots[token] : -1;
-    const int page_tokens = 16 << c.page_shift;
-    const int page = slot >= 0 ? slot / page_tokens : -1;
-    if (page < 0 || page >= c.num_pages) return;   // whole rows leave together
-    const int at = slot % page_tokens;
-    const long long row = (long long)page * c.heads + head;
-    const long long block = (row << c.page_shift) + (at >> 4);
-    const long long pair = (row * page_tokens + at) * (D / GS) + u / (GS / 8);
-    const int t = at & 15;
+    const Row row = row_of<D>(c.heads, tokens);
+    if (row.token >= tokens || row.head >= c.heads) return;   // whole rows leave together
+    const Place at = place_of<D, GS>(c, slots[row.token], row.head);
+    if (!at.there) return;
+    const int e0 = elements_of(row.u), g = e0 / GS;
+    const bool tells = (e0 & (GS - 1)) == 0;   // the group's first lane
     uint32_t x[8];
 
-    const u32x4 kw = load8<VEC>(k + token * k_ts + head * k_hs + 8 * u);
-    const u32x4 vw = load8<VEC>(v + token * v_ts + head * v_hs + 8 * u);
+    const u32x4 kw = load8<VEC>(k + row.token * k_ts + row.head * k_hs + e0);
+    const u32x4 vw = load8<VEC>(v + row.token * v_ts + row.head * v_hs + e0);
     uint32_t sb = quantise8<DT, GS>(kw, x);
     uint32_t word = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) word |= x[e] << (4 * (e / 2) + 16 * (e % 2));
-    c.kc[block * (2 * D) + ((u & 3) * 16 + t) * (D / 32) + u / 4] = word;
-    if (u % (GS / 8) == 0) c.ks[pair] = sb;
+    c.kc[at.block * (2 * D) + ((e0 / 8 & 3) * 16 + at.t) * (D / 32) + e0 / 32] = word;
+    if (tells) c.ks[at.pair + g] = sb;
 
     sb = quantise8<DT, GS>(vw, x);
-    const int f = (u >> 1) & 3;
+    const int f = row.u & 3;
     uint32_t p[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = (x[2 * i] | (x[2 * i + 1] << 16)) << (4 * f);
-    const bool up = f & 2;
-    uint32_t a0 = up ? p[2] : p[0], a1 = up ? p[3] : p[1];
-    a0 |= __shfl_xor(up ? p[0] : p[2], 4, 64);
-    a1 |= __shfl_xor(up ? p[1] : p[3], 4, 64);
-    const bool odd = f & 1;
-    uint32_t h = odd ? a1 : a0;
-    h |= __shfl_xor(odd ? a0 : a1, 2, 64);
-    const int n = 8 * (u & 1) + 2 * f;
-    uint16_t* to = reinterpret_cast<uint16_t*>(c.vc) + block * (4 * D) +
-                   ((((t >> 2) * 16 + n) * (D / 64) + u / 8) * 4 + (t & 3));
+    const bool up = f & 2, odd = f & 1;
+    const uint32_t a0 = (up ? p[2] : p[0]) | across<2>(up ? p[0] : p[2]);
+    const uint32_t a1 = (up ? p[3] : p[1]) | across<2>(up ? p[1] : p[3]);
+    const uint32_t h = (odd ? a1 : a0) | across<1>(odd ? a0 : a1);
+    const int n = (e0 & 8) + 2 * f;
+    uint16_t* to = reinterpret_cast<uint16_t*>(c.vc) + at.block * (4 * D) +
+                   ((((at.t >> 2) * 16 + n) * (D / 64) + e0 / 64) * 4 + (at.t & 3));
     to[0] = (uint16_t)h;
     to[D / 16] = (uint16_t)(h >> 16);
-    if (u % (GS / 8) == 0) c.vs[pair] = sb;
+    if (tells) c.vs[at.pair + g] = sb;
 }
 
-// The same cut of the work: a lane gives eight neighbouring elements.
+// The same cut of the work; a lane reads two halves of the value codes and has
+// the quad's other six from its neighbours.
 template <int D, int GS, int DT>
 __global__ __launch_bounds__(THREADS) void kv4_read_kernel(Kv4View c, uint16_t* k, uint16_t* v, const int* slots,
                                                            int tokens) {
-    constexpr int LANES = D / 8;
-    const long long unit = ((long long)blockIdx.x * THREADS + threadIdx.x) / LANES;
-    const int u = threadIdx.x % LANES;
-    const long long token = unit / c.heads;
-    const int head = (int)(unit % c.heads);
-    if (token >= tokens) return;
-    const int slot = slots[token];
-    const int page_tokens = 16 << c.page_shift;
-    const int page = slot >= 0 ? slot / page_tokens : -1;
+    const Row row = row_of<D>(c.heads, tokens);
+    if (row.token >= tokens || row.head >= c.heads) return;
+    const Place at = place_of<D, GS>(c, slots[row.token], row.head);
+    const int e0 = elements_of(row.u), f = row.u & 3;
     u32x4 ko = {0, 0, 0, 0}, vo = {0, 0, 0, 0};
-    if (page >= 0 && page < c.num_pages) {
-        const int at = slot % page_tokens;
-        const long long row = (long long)page * c.heads + head;
-        const long long block = (row << c.page_shift) + (at >> 4);
-        const long long pair = (row * page_tokens + at) * (D / GS) + u / (GS / 8);
-        const int t = at & 15, f = (u >> 1) & 3;
-        const uint32_t word = c.kc[block * (2 * D) + ((u & 3) * 16 + t) * (D / 32) + u / 4];
-        const uint32_t ksb = c.ks[pair], vsb = c.vs[pair];
-        const uint16_t* from = reinterpret_cast<const uint16_t*>(c.vc) + block * (4 * D) +
-                               ((((t >> 2) * 16 + 8 * (u & 1)) * (D / 64) + u / 8) * 4 + (t & 3));
-        uint32_t h[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = from[i * (D / 16)];
+    if (at.there) {
+        const uint32_t word = c.kc[at.block * (2 * D) + ((e0 / 8 & 3) * 16 + at.t) * (D / 32) + e0 / 32];
+        const uint32_t ksb = c.ks[at.pair + e0 / GS], vsb = c.vs[at.pair + e0 / GS];
+        const uint16_t* from = reinterpret_cast<const uint16_t*>(c.vc) + at.block * (4 * D) +
+                               ((((at.t >> 2) * 16 + (e0 & 8) + 2 * f) * (D / 64) + e0 / 64) * 4 + (at.t & 3));
+        const int own = (int)((uint32_t)from[0] | ((uint32_t)from[D / 16] << 16));
+        const uint32_t h[4] = {(uint32_t)__builtin_amdgcn_mov_dpp(own, 0x00, 0xf, 0xf, true),    // quad's lane 0
+                               (uint32_t)__builtin_amdgcn_mov_dpp(own, 0x55, 0xf, 0xf, true),
+                               (uint32_t)__builtin_amdgcn_mov_dpp(own, 0xaa, 0xf, 0xf, true),
+                               (uint32_t)__builtin_amdgcn_mov_dpp(own, 0xff, 0xf, 0xf, true)};
         const float s = half_lo<DT>(ksb), b = half_hi<DT>(ksb);
         const float s2 = half_lo<DT>(vsb), b2 = half_hi<DT>(vsb);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t w[2], w2[2];
+            const uint32_t codes = h[i] >> (4 * f);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float x = fmaf((float)((word >> (4 * i + 16 * j)) & 15u), s, b);
-                const float y = fmaf((float)((h[2 * i + j] >> (4 * f)) & 15u), s2, b2);
+                const float y = fmaf((float)((codes >> (16 * j)) & 15u), s2, b2);
                 w[j] = DT == DT_F16 ? f32_to_f16_bits(x) : f32_to_bf16_bits(x);
                 w2[j] = DT == DT_F16 ? f32_to_f16_bits(y) : f32_to_bf16_bits(y);
             }
@@ -204,8 +243,9 @@ __global__ __launch_bounds__(THREADS) void kv4_read_kernel(Kv4View c, uint16_t* 
             vo[i] = w2[0] | (w2[1] << 16);
         }
     }
-    *reinterpret_cast<u32x4*>(k + unit * D + 8 * u) = ko;
-    *reinterpret_cast<u32x4*>(v + unit * D + 8 * u) = vo;
+    const long long to = (row.token * c.heads + row.head) * D + e0;
+    *reinterpret_cast<u32x4*>(k + to) = ko;
+    *reinterpret_cast<u32x4*>(v + to) = vo;
 }
 
 // Calls f with the cache's head size, group size and type as constants.

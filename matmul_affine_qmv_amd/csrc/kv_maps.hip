@@ -13,101 +13,122 @@ namespace qmx {
 namespace {
 
 constexpr int THREADS = 512;
-constexpr int CHUNK = 2 * THREADS;   // requests scanned at a time, two a thread
+constexpr int EACH = 4;                // requests of a thread at a time
+constexpr int CHUNK = EACH * THREADS;
 constexpr int WAVES = THREADS / 64;
 
-__global__ __launch_bounds__(THREADS) void kv_maps_kernel(KvMapsArgs a, int per_group) {
+// Numbers up to 2^32 - 1 by the page size: a shift where that is a power of two.
+struct Pages {
+    uint32_t size;
+    int shift;   // or -1
+    __device__ __forceinline__ uint32_t whole(uint32_t x) const { return shift >= 0 ? x >> shift : x / size; }
+    __device__ __forceinline__ uint32_t count(uint32_t x) const { return whole(x) + (whole(x) * size != x ? 1 : 0); }
+};
+
+__global__ __launch_bounds__(THREADS) void kv_maps_kernel(KvMapsArgs a, int per_group, int shift) {
     __shared__ int s_end[CHUNK], s_page_end[CHUNK], s_past[CHUNK], s_held[CHUNK];
-    __shared__ long long s_waves64[WAVES];
-    __shared__ int s_waves32[WAVES];
+    __shared__ int s_waves[2][WAVES];
+    const Pages page{(uint32_t)a.page_size, shift};
     const int tid = threadIdx.x;
     const bool first = blockIdx.x == 0;
     const int t0 = (int)min((long long)blockIdx.x * per_group, (long long)a.tokens);
     const int t1 = (int)min((long long)t0 + per_group, (long long)a.tokens);
-    long long sum = 0;   // new tokens of the chunks before, not held to the room for them
-    int pages = 0;       // pages handed out before
+    int sum = 0;     // new tokens of the chunks before, held to 2^31 - 1
+    int pages = 0;   // pages handed out before
     if (first && tid == 0) a.offsets[0] = 0;
+    int n[EACH], past[EACH];
+    auto read = [&](int r0) {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int r = r0 + EACH * tid + i;
+            n[i] = r < a.requests ? max(a.fresh[r], 0) : 0;
+            past[i] = r < a.requests ? max(a.past[r], 0) : 0;
+        }
+    };
+    read(0);
     for (int r0 = 0; r0 < a.requests; r0 += CHUNK) {
         const int count = min(CHUNK, a.requests - r0);
-        const int begin = (int)min(sum, (long long)a.tokens);
-        long long n[2];
-        int past[2];
+        const int begin = min(sum, a.tokens);
+        int mine = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = 2 * tid + i;
-            n[i] = r < count ? max(a.fresh[r0 + r], 0) : 0;
-            past[i] = r < count ? max(a.past[r0 + r], 0) : 0;
+        for (int i = 0; i < EACH; ++i) mine = add_held(mine, n[i]);
+        int chunk_sum;
+        const int upto = scan_group<WAVES>(mine, s_waves[0], chunk_sum);
+        // exclusive, from the inclusive sum of the thread before (a difference of held sums would not do)
+        int e = __shfl_up(upto, 1, 64);
+        if ((tid & 63) == 0) {
+            e = 0;
+            for (int w = 0; w < tid >> 6; ++w) e = add_held(e, s_waves[0][w]);
         }
-        long long chunk_sum;
-        const long long upto = sum + scan_group<WAVES>(n[0] + n[1], s_waves64, chunk_sum);
-        int take[2], held[2], end[2];
-        long long e = upto - n[1] - n[0];
+        e = add_held(e, sum);
+        int take[EACH], takes = 0, end[EACH], held[EACH];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int start = (int)min(e, (long long)a.tokens);
-            e += n[i];
-            end[i] = (int)min(e, (long long)a.tokens);
-            const long long kv = (long long)past[i] + (end[i] - start);
-            const long long h = ((long long)past[i] + a.page_size - 1) / a.page_size;
-            const long long h2 = (kv + a.page_size - 1) / a.page_size;
-            held[i] = (int)min(h, (long long)a.columns);
-            take[i] = (int)min(h2, (long long)a.columns) - held[i];
-            const int r = 2 * tid + i;
+        for (int i = 0; i < EACH; ++i) {
+            const int start = min(e, a.tokens);
+            e = add_held(e, n[i]);
+            end[i] = min(e, a.tokens);
+            const uint32_t kv = (uint32_t)past[i] + (uint32_t)(end[i] - start);
+            held[i] = (int)min(page.count((uint32_t)past[i]), (uint32_t)a.columns);
+            take[i] = (int)min(page.count(kv), (uint32_t)a.columns) - held[i];
+            takes += take[i];
+            const int r = EACH * tid + i;
             if (first && r < count) {
                 a.offsets[r0 + r + 1] = end[i];
-                a.kv_lens[r0 + r] = (int)min(kv, 0x7fffffffll);
+                a.kv_lens[r0 + r] = (int)min(kv, 0x7fffffffu);
             }
         }
         int chunk_pages;
-        const int page_upto = pages + scan_group<WAVES>(take[0] + take[1], s_waves32, chunk_pages);
+        int page_end = pages + scan_group<WAVES>(takes, s_waves[1], chunk_pages) - takes;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = 2 * tid + i;
+        for (int i = 0; i < EACH; ++i) {
+            const int r = EACH * tid + i;
+            page_end += take[i];
             s_end[r] = end[i];
-            s_page_end[r] = page_upto - (i == 0 ? take[1] : 0);
+            s_page_end[r] = page_end;
             s_past[r] = past[i];
             s_held[r] = held[i];
         }
+        if (r0 + CHUNK < a.requests) read(r0 + CHUNK);
         __syncthreads();
         const int stop = s_end[count - 1];
         for (int t = max(t0, begin) + tid; t < min(t1, stop); t += THREADS) {
             const int r = first_after(s_end, count, t);
             const int start = r ? s_end[r - 1] : begin;
-            const long long at = (long long)s_past[r] + (t - start);
-            const long long col = at / a.page_size;
+            const uint32_t at = (uint32_t)s_past[r] + (uint32_t)(t - start);
+            const uint32_t col = page.whole(at);
             long long slot = -1;
-            if (col < a.columns) {
-                long long page;
-                if (col < s_held[r]) {
-                    page = a.table[(r0 + r) * a.table_stride + col];
+            if (col < (uint32_t)a.columns) {
+                long long p;
+                if ((int)col < s_held[r]) {
+                    p = a.table[(r0 + r) * a.table_stride + col];
                 } else {
-                    const long long p = (r ? s_page_end[r - 1] : pages) + col - s_held[r];
-                    page = p < a.num_free ? a.free_pages[p] : -1;
+                    const long long place = (long long)(r ? s_page_end[r - 1] : pages) + ((int)col - s_held[r]);
+                    p = place < a.num_free ? a.free_pages[place] : -1;
                 }
-                if (page >= 0) slot = page * a.page_size + at % a.page_size;
+                if (p >= 0) slot = p * a.page_size + (at - col * page.size);
                 if (slot > 0x7fffffffll) slot = -1;
             }
             a.slots[t] = (int)slot;
-            a.positions[t] = (int)min(at, 0x7fffffffll);
+            a.positions[t] = (int)min(at, 0x7fffffffu);
             a.request_ids[t] = r0 + r;
         }
-        for (int p = pages + blockIdx.x * THREADS + tid; p < pages + chunk_pages; p += gridDim.x * THREADS) {
-            const int r = first_after(s_page_end, count, p);
-            const int j = p - (r ? s_page_end[r - 1] : pages);
+        for (long long p = (long long)pages + blockIdx.x * THREADS + tid; p < (long long)pages + chunk_pages;
+             p += gridDim.x * THREADS) {
+            const int r = first_after(s_page_end, count, (int)p);
+            const int j = (int)p - (r ? s_page_end[r - 1] : pages);
             a.table[(r0 + r) * a.table_stride + s_held[r] + j] = p < a.num_free ? a.free_pages[p] : -1;
         }
-        sum += chunk_sum;
+        sum = add_held(sum, chunk_sum);
         pages += chunk_pages;
         __syncthreads();
     }
-    const int end = (int)min(sum, (long long)a.tokens);
-    for (int t = max(t0, end) + tid; t < t1; t += THREADS) {
+    for (int t = max(t0, min(sum, a.tokens)) + tid; t < t1; t += THREADS) {
         a.slots[t] = -1;
         a.positions[t] = -1;
         a.request_ids[t] = -1;
     }
     if (first && tid == 0) {
-        a.counts[0] = (int)min(sum, 0x7fffffffll);
+        a.counts[0] = sum;
         a.counts[1] = pages;
     }
 }
@@ -117,8 +138,11 @@ __global__ __launch_bounds__(THREADS) void kv_maps_kernel(KvMapsArgs a, int per_
 hipError_t launch_kv_maps(const KvMapsArgs& a, hipStream_t st) {
     long long groups = ((long long)a.tokens + 2 * THREADS - 1) / (2 * THREADS);
     groups = groups < 1 ? 1 : groups > 512 ? 512 : groups;
+    int shift = -1;
+    if ((a.page_size & (a.page_size - 1)) == 0)
+        for (shift = 0; (1 << shift) < a.page_size;) ++shift;
     const int per_group = (int)(((long long)a.tokens + groups - 1) / groups);
-    kv_maps_kernel<<<dim3((unsigned)groups), dim3(THREADS), 0, st>>>(a, per_group);
+    kv_maps_kernel<<<dim3((unsigned)groups), dim3(THREADS), 0, st>>>(a, per_group, shift);
     return hipGetLastError();
 }
 

@@ -5,34 +5,41 @@
 
 namespace qmx {
 
-template <class T>
-__device__ __forceinline__ T scan_wave(T v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const T up = __shfl_up(v, off, 64);
-        if (lane >= off) v += up;
-    }
+// a + b of numbers from 0 on, held to 2^31 - 1 (which keeps it associative).
+__device__ __forceinline__ int add_held(int a, int b) {
+    return (int)min((uint32_t)a + (uint32_t)b, 0x7fffffffu);
+}
+
+// Inclusive sums over a wave, held: in rows of 16 lanes, then from row to row.
+__device__ __forceinline__ int scan_wave(int v) {
+#define QMX_SCAN_STEP(CTRL, ROWS) v = add_held(v, __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false))
+    QMX_SCAN_STEP(0x111, 0xf);   // from 1, 2, 4 and 8 lanes below in the row
+    QMX_SCAN_STEP(0x112, 0xf);
+    QMX_SCAN_STEP(0x114, 0xf);
+    QMX_SCAN_STEP(0x118, 0xf);
+    QMX_SCAN_STEP(0x142, 0xa);   // row 0's last lane to row 1, row 2's to row 3
+    QMX_SCAN_STEP(0x143, 0xc);   // lane 31 to rows 2 and 3
+#undef QMX_SCAN_STEP
     return v;
 }
 
-// Inclusive sum over the work-group's threads; `total` is the sum of all.
-template <int WAVES, class T>
-__device__ __forceinline__ T scan_group(T v, T* waves, T& total) {
+// Inclusive sums over the work-group's threads, held; `total` is the sum of all.
+template <int WAVES>
+__device__ __forceinline__ int scan_group(int v, int* waves, int& total) {
     v = scan_wave(v);
     const int wave = threadIdx.x >> 6;
     __syncthreads();
     if ((threadIdx.x & 63) == 63) waves[wave] = v;
     __syncthreads();
-    T before = 0;
+    int before = 0;
     total = 0;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
-        const T x = waves[w];
-        before += w < wave ? x : 0;
-        total += x;
+        const int x = waves[w];
+        before = w < wave ? add_held(before, x) : before;
+        total = add_held(total, x);
     }
-    return v + before;
+    return add_held(v, before);
 }
 
 // First index whose end is greater than x, of `count` ends in order.
