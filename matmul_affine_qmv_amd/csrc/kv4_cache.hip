@@ -39,32 +39,44 @@ __device__ __forceinline__ uint32_t group_scale(float lo, float hi) {
     return DT == DT_F16 ? f32_to_f16_bits(f) : f32_to_bf16_bits(f);
 }
 
-// Eight codes.  rint of a product with the reciprocal, set right against the
-// middles between codes by an exact remainder; where x - b itself was rounded
-// the group's eight are done in 64 bits.
-__device__ __forceinline__ void codes_of(const float (&x)[8], float b, float s, uint32_t (&c)[8]) {
+// Eight codes.  With 1.5 * 2^23 added, the nearest whole number to (x - b) / s
+// stands in a float's low bits; the reciprocal may put it off by one next to a
+// middle, so the remainder, which is exact, is held against s / 2 (just under it
+// where the number is odd: middles go to even).  x - b is exact in 32 bits unless
+// x, or b, has digits more than 24 places below the group's span: then the
+// lane's eight are done with remainders in 64 bits.
+template <int DT>
+__device__ __forceinline__ void codes_of(u32x4 w, float b, float hi, float s, uint32_t (&c)[8]) {
+    constexpr int MAGIC = 0x4b400000;
     if (!(s > 0.0f) || !(s < INFINITY)) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) c[e] = 0;
         return;
     }
+    // the least magnitude but 0, less one step (so that 0 wraps to the top)
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 least = {0xffff, 0xffff};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t magnitudes = w[i] & 0x7fff7fffu;
+        least = __builtin_elementwise_min(least, (u16x2)(__builtin_bit_cast(u16x2, magnitudes) - u16x2{1, 1}));
+    }
+    const uint32_t small = min((uint32_t)least[0], (uint32_t)least[1]);
+    const float span = (hi - b) * (DT == DT_F16 ? 0x1p-13f : 0x1p-16f);
+    const bool deep = (small < 0x8000u && as_float<DT>(small + 1) <= span) || (b != 0.0f && fabsf(b) <= span);
     const float inv = __builtin_amdgcn_rcpf(s), half = 0.5f * s;
-    bool rounded = !(inv < INFINITY);
+    const float magic = __int_as_float(MAGIC);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float t = x[e] - b;
-        rounded |= (t + b != x[e]) | (x[e] - t != b);
-        float c0 = fminf(rintf(t * inv), 15.0f);
-        const float r = fmaf(-c0, s, t);
-        const bool odd = ((int)c0 & 1) != 0;
-        c0 += (odd ? r >= half : r > half) ? 1.0f : 0.0f;
-        c0 -= (odd ? r <= -half : r < -half) ? 1.0f : 0.0f;
-        c[e] = (uint32_t)(int)fminf(fmaxf(c0, 0.0f), 15.0f);
-    }
-    if (rounded) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            c[e] = (uint32_t)(int)fmin(fmax(rint(((double)x[e] - (double)b) / (double)s), 0.0), 15.0);
+        const float x = e % 2 ? half_hi<DT>(w[e / 2]) : half_lo<DT>(w[e / 2]);
+        const float t = x - b, y = fmaf(t, inv, magic);
+        const int k = __float_as_int(y);
+        const float r = fmaf(magic - y, s, t), most = __int_as_float(__float_as_int(half) - (k & 1));
+        c[e] = (uint32_t)min(max(k + (r > most ? 1 : 0) - (r < -most ? 1 : 0), MAGIC), MAGIC + 15) & 15u;
+        if (deep) {
+            const double rd = fma((double)(magic - y), (double)s, (double)x - (double)b), md = (double)most;
+            c[e] = (uint32_t)min(max(k + (rd > md ? 1 : 0) - (rd < -md ? 1 : 0), MAGIC), MAGIC + 15) & 15u;
+        }
     }
 }
 
@@ -118,13 +130,7 @@ __device__ __forceinline__ uint32_t quantise8(u32x4 w, uint32_t (&c)[8]) {
     const uint32_t lob = sortable(lo) & 0xffffu, hib = sortable(hi) & 0xffffu;
     const float b = as_float<DT>(lob);
     const uint32_t sb = group_scale<DT>(b, as_float<DT>(hib));
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = half_lo<DT>(w[i]);
-        x[2 * i + 1] = half_hi<DT>(w[i]);
-    }
-    codes_of(x, b, as_float<DT>(sb), c);
+    codes_of<DT>(w, b, as_float<DT>(hib), as_float<DT>(sb), c);
     return sb | (lob << 16);
 }
 
@@ -244,8 +250,8 @@ __global__ __launch_bounds__(THREADS) void kv4_read_kernel(Kv4View c, uint16_t* 
         }
     }
     const long long to = (row.token * c.heads + row.head) * D + e0;
-    *reinterpret_cast<u32x4*>(k + to) = ko;
-    *reinterpret_cast<u32x4*>(v + to) = vo;
+    __builtin_nontemporal_store(ko, reinterpret_cast<u32x4*>(k + to));
+    __builtin_nontemporal_store(vo, reinterpret_cast<u32x4*>(v + to));
 }
 
 // Calls f with the cache's head size, group size and type as constants.

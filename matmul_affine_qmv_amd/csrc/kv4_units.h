@@ -73,14 +73,14 @@ class Units {
     __device__ __forceinline__ Units(const Kv4AttnArgs& a, int id, int head) : id_(id), count_(a.requests * a.p.tiles) {
         constexpr int MOST = kv4_line_units(THREADS / 64);
         __shared__ int s_begin[MOST], s_end[MOST];
-        __shared__ int s_waves[THREADS / 64];
+        __shared__ int s_waves[1][THREADS / 64];
         begin_ = s_begin;
         end_ = s_end;
         at_ = 0;
         stop_ = 1;
         if (!a.p.lines) return;
         constexpr int EACH = MOST / THREADS;
-        int n[EACH], sum = 0, total;
+        int n[EACH], sum = 0;
         const int per = (count_ + THREADS - 1) / THREADS;   // units a thread, at most EACH
         const int v0 = (int)threadIdx.x * per;
 #pragma unroll
@@ -89,7 +89,10 @@ class Units {
             n[i] = there ? unit_of(a, v0 + i).steps : 0;
             sum += n[i] ? n[i] + a.p.cost : 0;
         }
-        int upto = scan_group<THREADS / 64>(sum, s_waves, total) - sum;
+        int ends[1] = {sum}, totals[1];
+        scan_group<THREADS / 64>(ends, s_waves, totals);
+        int upto = ends[0];
+        const int total = totals[0];
         const int length = max(a.p.least, (total + a.p.lines - 1) / a.p.lines);
         const bool tell = id == 0 && head == 0;
 #pragma unroll

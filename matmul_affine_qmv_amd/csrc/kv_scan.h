@@ -23,23 +23,32 @@ __device__ __forceinline__ int scan_wave(int v) {
     return v;
 }
 
-// Inclusive sums over the work-group's threads, held; `total` is the sum of all.
-template <int WAVES>
-__device__ __forceinline__ int scan_group(int v, int* waves, int& total) {
-    v = scan_wave(v);
+// Sums over the work-group's threads before this one, held, of N numbers at a
+// time (a difference of held sums would not do); `total` is the sum of all.
+// `waves`: N rows of WAVES in LDS.
+template <int WAVES, int N>
+__device__ __forceinline__ void scan_group(int (&v)[N], int (*waves)[WAVES], int (&total)[N]) {
     const int wave = threadIdx.x >> 6;
-    __syncthreads();
-    if ((threadIdx.x & 63) == 63) waves[wave] = v;
-    __syncthreads();
-    int before = 0;
-    total = 0;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-        const int x = waves[w];
-        before = w < wave ? add_held(before, x) : before;
-        total = add_held(total, x);
+    for (int i = 0; i < N; ++i) v[i] = scan_wave(v[i]);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if ((threadIdx.x & 63) == 63) waves[i][wave] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        int before = 0;
+        total[i] = 0;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const int x = waves[i][w];
+            before = w < wave ? add_held(before, x) : before;
+            total[i] = add_held(total[i], x);
+        }
+        const int up = __shfl_up(v[i], 1, 64);
+        v[i] = (threadIdx.x & 63) ? add_held(before, up) : before;
     }
-    return add_held(v, before);
 }
 
 // First index whose end is greater than x, of `count` ends in order.
