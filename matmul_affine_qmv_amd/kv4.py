@@ -8,13 +8,24 @@ synchronises or copies to the host, so a step can be captured into a graph.
 from __future__ import annotations
 
 import ctypes
-from typing import NamedTuple
+from collections import namedtuple
+from functools import lru_cache
 
 import torch
 
-from . import _WORD_DTYPES, QMX_BF16, QMX_F16, _check, _ptr, _stream, lib
+from . import _WORD_DTYPES, QMX_BF16, QMX_F16, QmxError, lib
 
 _HALVES = {torch.float16: QMX_F16, torch.bfloat16: QMX_BF16}
+_INT = torch.int32
+
+# A call's own cost on the host counts beside kernels of a few microseconds: the
+# stream is asked for as a number, and pointers go to the library as numbers.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _check(status: int, func: str) -> None:
+    if status:
+        raise QmxError(status, func)
 
 
 class _CCache(ctypes.Structure):
@@ -24,19 +35,27 @@ class _CCache(ctypes.Structure):
                 ("dtype", ctypes.c_int)]
 
 
-class KvMaps(NamedTuple):
-    """What kv_maps writes, int32 tensors: query_offsets [R + 1], kv_lens [R],
-    slots, positions and request_ids [tokens], counts [2]."""
-    query_offsets: torch.Tensor
-    kv_lens: torch.Tensor
-    slots: torch.Tensor
-    positions: torch.Tensor
-    request_ids: torch.Tensor
-    counts: torch.Tensor
+_MAPS = ("query_offsets", "kv_lens", "slots", "positions", "request_ids", "counts")
+
+
+class KvMaps(namedtuple("KvMaps", _MAPS)):
+    """What kv_maps writes, int32 tensors on one device: query_offsets [R + 1],
+    kv_lens [R], slots, positions and request_ids [tokens], counts [2]."""
+
+    def __new__(cls, *args, **kwargs):
+        self = super().__new__(cls, *args, **kwargs)
+        if not self.slots.is_cuda:
+            raise ValueError("all tensors must be on a HIP device")
+        _ints(self.slots.get_device(), **self._asdict())
+        R, T = self.kv_lens.numel(), self.slots.numel()
+        if [t.numel() for t in self] != [R + 1, R, T, T, T, 2]:
+            raise ValueError("the tensors must have R + 1, R, tokens, tokens, tokens and 2 elements")
+        self.requests, self.tokens, self.device_index = R, T, self.slots.get_device()
+        return self
 
     @classmethod
     def empty(cls, requests: int, tokens: int, device) -> "KvMaps":
-        return cls(*(torch.empty(n, dtype=torch.int32, device=device)
+        return cls(*(torch.empty(n, dtype=_INT, device=device)
                      for n in (requests + 1, requests, tokens, tokens, tokens, 2)))
 
 
@@ -73,7 +92,7 @@ class Kv4Cache:
         self.k_codes, self.k_sb, self.v_codes, self.v_sb = k_codes, k_sb, v_codes, v_sb
         self.num_pages, self.kv_heads, self.page_size = pages, heads, page
         self.head_dim, self.group_size = dim, dim // groups
-        self.dtype, self.device = k_sb.dtype, k_codes.device
+        self.dtype, self.device, self.device_index = k_sb.dtype, k_codes.device, k_codes.get_device()
         self._c = _CCache(k_codes.data_ptr(), k_sb.data_ptr(), v_codes.data_ptr(), v_sb.data_ptr(), pages, heads,
                           dim, page, self.group_size, _HALVES[k_sb.dtype])
         self._ref = ctypes.byref(self._c)
@@ -88,22 +107,27 @@ class Kv4Cache:
                                                    torch.zeros(pairs, dtype=dtype, device=device))))
 
 
-def _ints(device, **tensors):
+def _ints(index, **tensors):
     for name, t in tensors.items():
-        if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        if t.dtype is not _INT or t.dim() != 1 or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 vector")
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}")
+        if t.get_device() != index:
+            raise ValueError(f"{name} must be on HIP device {index}")
 
 
-def _table(t, requests, device):
-    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != requests or (t.numel() > 1 and t.shape[1] > 1
-                                                                            and t.stride(1) != 1):
+def _table(t, requests, index):
+    """Columns and row stride of a block table."""
+    if t.dtype is not _INT or t.dim() != 2:
+        raise ValueError("block_table must be int32 [requests, columns]")
+    rows, columns = t.shape
+    stride, last = t.stride()
+    if rows != requests or (last != 1 and rows and columns > 1):
         raise ValueError(f"block_table must be int32 [{requests}, columns] with a unit last stride")
-    if t.device != device:
-        raise ValueError(f"block_table must be on {device}")
-    if requests > 1 and t.numel() and t.stride(0) < t.shape[1]:
+    if t.get_device() != index:
+        raise ValueError(f"block_table must be on HIP device {index}")
+    if rows > 1 and columns and stride < columns:
         raise ValueError("block_table's rows must not overlap")
+    return columns, stride
 
 
 def kv_maps(past, new, block_table, free_pages, *, page_size, tokens=None, out=None) -> KvMaps:
@@ -116,68 +140,81 @@ def kv_maps(past, new, block_table, free_pages, *, page_size, tokens=None, out=N
     many of free_pages were wanted."""
     if not past.is_cuda:
         raise ValueError("all tensors must be on a HIP device")
-    dev, R = past.device, past.numel()
-    _ints(dev, past=past, new=new, free_pages=free_pages)
+    index, R = past.get_device(), past.numel()
+    _ints(index, past=past, new=new, free_pages=free_pages)
     if new.numel() != R:
         raise ValueError("past and new must have one length")
-    _table(block_table, R, dev)
+    columns, stride = _table(block_table, R, index)
     if out is None:
         if tokens is None:
             raise ValueError("kv_maps needs tokens or out")
-        out = KvMaps.empty(R, tokens, dev)
-    else:
-        _ints(dev, **out._asdict())
-        T = out.slots.numel()
-        if [t.numel() for t in out] != [R + 1, R, T, T, T, 2] or (tokens is not None and tokens != T):
-            raise ValueError("out's tensors must have R + 1, R, tokens, tokens, tokens and 2 elements")
-    _check(lib().qmx_kv_maps(_ptr(past), _ptr(new), _ptr(block_table), _ptr(free_pages), R, block_table.shape[1],
-                             block_table.stride(0), free_pages.numel(), page_size, out.slots.numel(),
-                             *map(_ptr, out), _stream(past)), "qmx_kv_maps")
+        out = KvMaps.empty(R, tokens, past.device)
+    elif out.requests != R or (tokens is not None and tokens != out.tokens):
+        raise ValueError("out's tensors must have R + 1, R, tokens, tokens, tokens and 2 elements")
+    elif out.device_index != index:
+        raise ValueError(f"out must be on HIP device {index}")
+    _check(lib().qmx_kv_maps(past.data_ptr(), new.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), R,
+                             columns, stride, free_pages.numel(), page_size, out.tokens,
+                             *[t.data_ptr() for t in out], _raw_stream(index)), "qmx_kv_maps")
     return out
 
 
 def _new_tokens(cache, x, name):
-    if x.dim() != 3 or tuple(x.shape[1:]) != (cache.kv_heads, cache.head_dim):
+    """Token and head strides of new keys or values."""
+    if x.dim() != 3 or x.shape[1:] != (cache.kv_heads, cache.head_dim):
         raise ValueError(f"{name} must be [tokens, {cache.kv_heads}, {cache.head_dim}]")
-    if x.dtype != cache.dtype:
+    if x.dtype is not cache.dtype:
         raise ValueError(f"{name} must have the cache's dtype {cache.dtype}")
-    if x.device != cache.device:
+    if x.get_device() != cache.device_index:
         raise ValueError(f"{name} must be on {cache.device}")
-    if x.stride(2) != 1:
+    token, head, last = x.stride()
+    if last != 1:
         raise ValueError(f"{name} must have a unit last stride")
+    return token, head
 
 
 def kv4_write(cache: Kv4Cache, k, v, slots) -> None:
     """Quantises k and v [tokens, kv_heads, head_dim] (any strides, the last 1)
     into the cache at `slots` (int32 [tokens], distinct; below 0: skipped)."""
-    _new_tokens(cache, k, "k")
-    _new_tokens(cache, v, "v")
-    _ints(cache.device, slots=slots)
-    if not k.shape[0] == v.shape[0] == slots.numel():
+    kt, kh = _new_tokens(cache, k, "k")
+    vt, vh = _new_tokens(cache, v, "v")
+    _ints(cache.device_index, slots=slots)
+    T = slots.numel()
+    if k.shape[0] != T or v.shape[0] != T:
         raise ValueError("k, v and slots must have one length")
-    _check(lib().qmx_kv4_write(cache._ref, _ptr(k), _ptr(v), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-                               _ptr(slots), slots.numel(), _stream(k)), "qmx_kv4_write")
+    _check(lib().qmx_kv4_write(cache._ref, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, slots.data_ptr(), T,
+                               _raw_stream(cache.device_index)), "qmx_kv4_write")
 
 
 def kv4_read(cache: Kv4Cache, slots, out=None):
     """(k, v) [tokens, kv_heads, head_dim]: what the cache holds at `slots`
     (zeros where a slot is below 0)."""
-    _ints(cache.device, slots=slots)
+    _ints(cache.device_index, slots=slots)
     shape = (slots.numel(), cache.kv_heads, cache.head_dim)
     if out is None:
-        out = tuple(torch.empty(shape, dtype=cache.dtype, device=cache.device) for _ in range(2))
-    for t in out:
-        if tuple(t.shape) != shape or t.dtype != cache.dtype or t.device != cache.device or not t.is_contiguous():
-            raise ValueError(f"out must be two contiguous {shape} tensors of dtype {cache.dtype}")
-    _check(lib().qmx_kv4_read(cache._ref, _ptr(out[0]), _ptr(out[1]), _ptr(slots), slots.numel(), _stream(slots)),
-           "qmx_kv4_read")
-    return out
+        k = torch.empty(shape, dtype=cache.dtype, device=cache.device)
+        v = torch.empty_like(k)
+    else:
+        k, v = out
+        for t in out:
+            if t.shape != shape or t.dtype is not cache.dtype or t.get_device() != cache.device_index \
+                    or not t.is_contiguous():
+                raise ValueError(f"out must be two contiguous {shape} tensors of dtype {cache.dtype}")
+    _check(lib().qmx_kv4_read(cache._ref, k.data_ptr(), v.data_ptr(), slots.data_ptr(), shape[0],
+                              _raw_stream(cache.device_index)), "qmx_kv4_read")
+    return k, v
+
+
+@lru_cache(maxsize=4096)
+def _workspace_bytes(device_index, *sizes):
+    return lib().qmx_kv4_attention_workspace_bytes(*sizes)
 
 
 def kv4_attention_workspace_bytes(cache: Kv4Cache, requests, tokens, heads, max_query_len, max_kv_len,
                                   window=0) -> int:
-    return lib().qmx_kv4_attention_workspace_bytes(cache.kv_heads, cache.head_dim, requests, tokens, heads,
-                                                   max_query_len, max_kv_len, window)
+    """Bytes of workspace that kv4_attention needs for these sizes (a host rule)."""
+    return _workspace_bytes(cache.device_index, cache.kv_heads, cache.head_dim, requests, tokens, heads,
+                            max_query_len, max_kv_len, window)
 
 
 def kv4_attention(cache: Kv4Cache, q, block_table, kv_lens, query_offsets, *, max_query_len, max_kv_len, window=0,
@@ -188,40 +225,41 @@ def kv4_attention(cache: Kv4Cache, q, block_table, kv_lens, query_offsets, *, ma
     block_table: int32 [R, columns]; kv_lens: int32 [R]; query_offsets: int32
     [R + 1], request r's queries being the last of its kv_lens[r] tokens.
     max_query_len, max_kv_len: host bounds of both.  window: 0, or how many
-    tokens a query sees, itself among them.  scale: above 0, head_dim ** -0.5 by default.
-    Returns out, or (out, lse) with float32 lse [tokens, heads]."""
+    tokens a query sees, itself among them.  scale: above 0, head_dim ** -0.5 by
+    default.  Returns out, or (out, lse) with float32 lse [tokens, heads]."""
     if q.dim() != 3 or q.shape[2] != cache.head_dim or q.shape[1] % cache.kv_heads or q.shape[1] < 1:
         raise ValueError(f"q must be [tokens, a multiple of {cache.kv_heads}, {cache.head_dim}]")
-    if q.dtype != cache.dtype:
+    if q.dtype is not cache.dtype:
         raise ValueError(f"q must have the cache's dtype {cache.dtype}")
-    if q.device != cache.device:
+    index = cache.device_index
+    if q.get_device() != index:
         raise ValueError(f"q must be on {cache.device}")
-    if q.stride(2) != 1:
+    token, head, last = q.stride()
+    if last != 1:
         raise ValueError("q must have a unit last stride")
     T, heads, D = q.shape
     R = kv_lens.numel()
-    _ints(q.device, kv_lens=kv_lens, query_offsets=query_offsets)
+    _ints(index, kv_lens=kv_lens, query_offsets=query_offsets)
     if query_offsets.numel() != R + 1:
         raise ValueError("query_offsets must have one element more than kv_lens")
-    _table(block_table, R, q.device)
+    columns, stride = _table(block_table, R, index)
     if out is None:
-        out = torch.empty((T, heads, D), dtype=q.dtype, device=q.device)
-    elif tuple(out.shape) != (T, heads, D) or out.dtype != q.dtype or out.device != q.device \
+        out = torch.empty((T, heads, D), dtype=q.dtype, device=cache.device)
+    elif out.shape != (T, heads, D) or out.dtype is not q.dtype or out.get_device() != index \
             or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {(T, heads, D)} of dtype {q.dtype}")
-    lse = torch.empty((T, heads), dtype=torch.float32, device=q.device) if return_lse else None
+    lse = torch.empty((T, heads), dtype=torch.float32, device=cache.device) if return_lse else None
     max_query_len = min(max_query_len, T)
-    if workspace is None:
-        need = lib().qmx_kv4_attention_workspace_bytes(cache.kv_heads, D, R, T, heads, max_query_len, max_kv_len,
-                                                       window)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif workspace.device != q.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {q.device}")
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib().qmx_kv4_attention(cache._ref, _ptr(q), q.stride(0), q.stride(1), _ptr(out), _ptr(lse),
-                                   _ptr(block_table), block_table.shape[1], block_table.stride(0), _ptr(kv_lens),
-                                   _ptr(query_offsets), R, T, heads, max_query_len, max_kv_len, window,
-                                   D ** -0.5 if scale is None else scale, _ptr(workspace), ws_bytes, _stream(q)),
+    need = _workspace_bytes(index, cache.kv_heads, D, R, T, heads, max_query_len, max_kv_len, window)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
+    elif workspace is not None and (workspace.get_device() != index or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be contiguous on {cache.device}")
+    _check(lib().qmx_kv4_attention(cache._ref, q.data_ptr(), token, head, out.data_ptr(),
+                                   lse.data_ptr() if return_lse else None, block_table.data_ptr(), columns, stride,
+                                   kv_lens.data_ptr(), query_offsets.data_ptr(), R, T, heads, max_query_len,
+                                   max_kv_len, window, D ** -0.5 if scale is None else scale,
+                                   workspace.data_ptr() if workspace is not None else None,
+                                   workspace.nbytes if workspace is not None else 0, _raw_stream(index)),
            "qmx_kv4_attention")
     return (out, lse) if return_lse else out
