@@ -73,7 +73,7 @@ Kv4AttnPlan kv4_attn_plan(int requests, int heads, int kv_heads, int dim, int ma
     p.lines = line ? std::max(1, (prompt ? 1 : 2) * cus / kv_heads) : 0;
     // A unit's queries, first loads and joining waves wait on memory about four
     // times, as long as its work-group takes for some 16 steps of 16 rows.
-    p.cost = prompt ? 8 : 16;
+    p.cost = 8;
     p.least = 8;
     return p;
 }

@@ -5,11 +5,10 @@
 // A work-group of 8 waves takes 256 rows, a wave 32 of them, and walks the keys
 // 64 at a time (32 where the head has 256 dimensions).  Four waves turn the keys'
 // codes into operands and four the values', once for all 256 rows, into LDS (one
-// barrier a tile) in the order in which the products read them: 16 bytes a lane,
-// lane after lane.  The second four run half a tile behind: their barrier stands
-// between a tile's two products (so values have three buffers, keys two), and of
-// the two waves on a SIMD one has the first product, which is the matrix cores'
-// work, while the other has the exponentials, which are the vector ALU's.
+// barrier a tile, two buffers for keys, three for values) in the order in which
+// the products read them: 16 bytes a lane, lane after lane.  With two waves on a
+// SIMD there is little to hide one wave's waits, so the exponentials of 32 keys
+// stand among the products for the scores of the next 32.
 //
 //   S^T[key, row] = K Q^T,  O^T[dim, row] += V^T P:  v_mfma_32x32x16, where the
 //   probabilities that a lane computes are the operand it needs (as in
@@ -71,11 +70,7 @@ constexpr int PROMPT_WAVES = 8, PROMPT_ROWS = 256;
 
 // Products and reads of LDS stay in the order of the source, so that operands
 // are read a few products ahead; everything else may move.
-#ifdef QV_FREE
-__device__ __forceinline__ void keep_order() {}
-#else
 __device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0x676); }
-#endif
 
 // The largest of the wave's numbers, none below 0, without a trip through LDS:
 // over rows of 16 lanes, then the four rows as integers, which order alike.
@@ -92,10 +87,11 @@ __device__ __forceinline__ float wave_max(float v) {
 }
 
 // What a lane takes of one block of 16 tokens to turn it into operands: codes of
-// the D / SPLIT dimensions that fall to its wave, and pairs.  Keys: the lane's
-// token n = lane % 16; values: the tokens 4h .. 4h + 3, h = lane / 16, their pairs
-// spread over the row's 16 lanes as in kv4_attn_impl.h, and all pairs of the
-// tile, spread over the wave, for their largest.
+// the D / SPLIT dimensions that fall to its wave, the pairs of one token, and a
+// share of the pairs of the four tokens 4h .. 4h + 3, h = lane / 16, as in
+// kv4_attn_impl.h.  Keys: the token is the block's lane % 16, whose codes the lane
+// has.  Values: the lane has codes of the four tokens; the one token, of all the
+// tile's, is for the largest value.
 template <int D, int GS, int DT>
 struct Raw {
     static constexpr int KEYS = 64 * 128 / (D < 128 ? 128 : D);   // of a tile
@@ -106,12 +102,13 @@ struct Raw {
     static constexpr int SLOTS = SCALED ? 8 : 4;                  // of a group in the product of biases
     static constexpr int BK = (SLOTS * G + 15) / 16;              // its steps
     static constexpr int SHARE = (4 * G + 15) / 16;               // a lane's share of a block's pairs
-    static constexpr int ALL = G / SPLIT;                         // a lane's share of the tile's pairs
     static constexpr int EMPTY = -120;                            // exponent of nothing but zeros
-    uint32_t w[NW], sb[G > SHARE + ALL ? G : SHARE + ALL];
+    // The same loads for either kind of wave, and no branch about them: where two
+    // met in a register, a copy behind them would wait for memory.
+    uint32_t w[NW], token_pairs[G], share[SHARE];
     bool there;    // the block's page is in the cache
+    bool live;     // the lane's token is there
     int tokens;    // of the block, from its first on, that are there
-    bool live;     // values: the lane's token of the tile is there
 
     // `pages`: entries of 64 blocks of 16 tokens, one a lane, from a tile's start
     // on; the tile's are from `first` on, `key` its first key.
@@ -119,32 +116,23 @@ struct Raw {
                                          int part, int end, bool value) {
         const int lane = threadIdx.x & 63;
         const int page = __builtin_amdgcn_readlane(pages, first + my_blk), blk = (key >> 4) + my_blk;
+        const int own = value ? lane % KEYS : 16 * my_blk + (lane & 15);   // the lane's token of the tile
+        const int its = __shfl(pages, first + own / 16, 64);
         const int mask = (1 << c.page_shift) - 1;
-        if (value) {
-            const int at = key + lane % KEYS;
-            const int its = __shfl(pages, first + lane % KEYS / 16, 64);
-            live = at < end && its >= 0 && its < c.num_pages;
-            if (live) {
-                const size_t row = (((size_t)its * c.heads + head) << c.page_shift) + ((at >> 4) & mask);
-                const uint32_t* from = c.vs + (row * 16 + (at & 15)) * G + lane / KEYS * ALL;
-#pragma unroll
-                for (int g = 0; g < ALL; ++g) sb[SHARE + g] = from[g];
-            }
-        }
         tokens = end - 16 * blk;
         there = tokens > 0 && page >= 0 && page < c.num_pages;
-        if (!there) return;
-        const size_t at = (((size_t)page * c.heads + head) << c.page_shift) + (blk & mask);
-        load_words(w, (value ? c.vc : c.kc) + at * (64 * NJ) + lane * NJ + part * NW);
-        if (value) {
-            const uint32_t* from = c.vs + at * (16 * G) + (lane >> 4) * (4 * G);
+        live = key + own < end && its >= 0 && its < c.num_pages;
+        // what is not there is read from page 0 and not used
+        const size_t at = (((size_t)(there ? page : 0) * c.heads + head) << c.page_shift) + (blk & mask);
+        const size_t row = (((size_t)(live ? its : 0) * c.heads + head) << c.page_shift) + (((key + own) >> 4) & mask);
+        const uint32_t* codes = value ? c.vc : c.kc;
+        const uint32_t* pairs = value ? c.vs : c.ks;
+        load_words(w, codes + at * (64 * NJ) + lane * NJ + part * NW);
 #pragma unroll
-            for (int r = 0; r < SHARE; ++r) sb[r] = from[(16 * r + (lane & 15)) & (4 * G - 1)];
-        } else {
-            const uint32_t* from = c.ks + at * (16 * G) + (lane & 15) * G;
+        for (int g = 0; g < G; ++g) token_pairs[g] = pairs[(row * 16 + (own & 15)) * G + g];
 #pragma unroll
-            for (int g = 0; g < G; ++g) sb[g] = from[g];
-        }
+        for (int r = 0; r < SHARE; ++r)
+            share[r] = pairs[at * (16 * G) + (lane >> 4) * (4 * G) + ((16 * r + (lane & 15)) & (4 * G - 1))];
     }
 
     // Keys to `k` [blocks of 32][BK + KS][2][32] of 16 bytes; `blk` counts in the
@@ -153,13 +141,12 @@ struct Raw {
     __device__ __forceinline__ int keys(u32x4* k, float* factor, int blk, int part) const {
         const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
         u32x4* to = k + (blk >> 1) * (BK + KS) * 64 + (blk & 1) * 16 + n;
-        const bool live = there && n < tokens;
         int e = 0;
         if constexpr (SCALED) {
             float most = 0.0f;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                const float x = fmaxf(fabsf(8.0f * half_lo<DT>(sb[g])), fabsf(half_hi<DT>(sb[g])));
+                const float x = fmaxf(fabsf(8.0f * half_lo<DT>(token_pairs[g])), fabsf(half_hi<DT>(token_pairs[g])));
                 most = x < INFINITY ? fmaxf(most, x) : most;
             }
             most = wave_max(live ? most : 0.0f);
@@ -168,7 +155,7 @@ struct Raw {
 #pragma unroll
         for (int g = 0; g < GW; ++g) {
             const int group = part * GW + g;
-            const uint32_t pair = live ? (SPLIT == 2 && part ? sb[GW + g < G ? GW + g : 0] : sb[g]) : 0u;
+            const uint32_t pair = live ? (SPLIT == 2 && part ? token_pairs[GW + g < G ? GW + g : 0] : token_pairs[g]) : 0u;
             const float s = half_lo<DT>(pair);
             f16x2 s2, b2;
             if constexpr (SCALED) {
@@ -209,8 +196,8 @@ struct Raw {
         float most = 0.0f;
         bool good = true;
 #pragma unroll
-        for (int g = 0; g < ALL; ++g) {
-            const float x = half_lo<DT>(sb[SHARE + g]), y = half_hi<DT>(sb[SHARE + g]);
+        for (int g = 0; g < G; ++g) {
+            const float x = half_lo<DT>(token_pairs[g]), y = half_hi<DT>(token_pairs[g]);
             const bool finite = (x - x) + (y - y) == 0.0f;
             good = good && (finite || !live);
             const float z = fmaxf(fabsf(y), fabsf(fmaf(15.0f, x, y)));
@@ -222,7 +209,7 @@ struct Raw {
         uint32_t pair[SHARE];   // scale 2^18 and bias, float16
 #pragma unroll
         for (int r = 0; r < SHARE; ++r) {
-            const float x = half_lo<DT>(sb[r]), y = half_hi<DT>(sb[r]);
+            const float x = half_lo<DT>(share[r]), y = half_hi<DT>(share[r]);
             const bool use = there && 4 * h + ((16 * r + n) & (4 * G - 1)) / G < tokens && (x - x) + (y - y) == 0.0f;
             pair[r] = use ? __builtin_bit_cast(uint32_t, half2_of(ldexpf(x, 18 - e), ldexpf(y, -e))) : 0u;
         }
@@ -266,14 +253,12 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
     using H = Half<DT>;
     constexpr int KS = D / 16, DB = D / 32, G = D / GS, BK = W::BK, KEYS = W::KEYS, NT = KEYS / 32;
     constexpr int KQ = D == 256 ? KS / 2 : KS;   // steps whose queries stay in registers; the others' in LDS
-    #ifndef QV_AHEAD
-#define QV_AHEAD (D == 256 ? 2 : 4)
-#endif
-    constexpr int AHEAD = QV_AHEAD;                   // operands read ahead
+        constexpr int AHEAD = D == 256 ? 2 : 4;      // operands read ahead
+    constexpr int KB = NT == 2 ? 3 : 2;          // buffers of keys
     constexpr float kSlack = 8.0f;
-    __shared__ u32x4 s_k[2][NT * (BK + KS) * 64], s_v[3][2 * NT * DB * 64];
+    __shared__ u32x4 s_k[KB][NT * (BK + KS) * 64], s_v[3][2 * NT * DB * 64];
     __shared__ u32x4 s_q[PROMPT_WAVES][KS > KQ ? (KS - KQ) * 64 : 1];
-    __shared__ float s_factor[2][W::SCALED ? 1 : G * KEYS];
+    __shared__ float s_factor[KB][W::SCALED ? 1 : G * KEYS];
     __shared__ int s_bad[3], s_there[3][4], s_key_exponent[3][4], s_value_exponent[3];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, n = lane & 31, hh = lane >> 5;
@@ -282,7 +267,7 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
     const bool value = wave >= 4;   // which codes this wave turns into operands
     const int my_blk = (wave & 3) / W::SPLIT, my_part = (wave & 3) % W::SPLIT;
 
-    for (int i = threadIdx.x; i < 2 * NT * BK * 64; i += 64 * PROMPT_WAVES)   // slots that no group has
+    for (int i = threadIdx.x; i < KB * NT * BK * 64; i += 64 * PROMPT_WAVES)   // slots that no group has
         s_k[i / (NT * BK * 64)][i / (BK * 64) % NT * (BK + KS) * 64 + i % (BK * 64)] = u32x4{0, 0, 0, 0};
 
     Units<64 * PROMPT_WAVES> units(a, blockIdx.x / c.heads, head);
@@ -396,87 +381,74 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
         auto load = [&](int tile) {
             raw.load(c, pages, tile % FETCH * BLOCKS, head, key0 + KEYS * tile, my_blk, my_part, part_end, value);
         };
-        f32x16 s[NT];
-        auto skip = [&](int tile) {   // no row of the wave sees a key of the tile
+        f32x16 s[NT];   // scores of 32 keys, and those of the next 32
+        auto unseen = [&](int tile) {   // no row of the wave sees a key of the tile
             const int key = key0 + KEYS * tile;
             return key > any_hi || key + KEYS - 1 < any_lo;
         };
-        auto scores = [&](int tile) {
-            if (skip(tile)) return;
-            const u32x4* sk = s_k[tile & 1] + lane;
+        // Scores of 32 keys, the t-th of a tile.  slice(y) is what the vector ALU
+        // does behind the y-th product.
+        auto scores = [&](int buffer, int t, f32x16& to, auto&& slice) {
+            const u32x4* sk = s_k[buffer] + t * (BK + KS) * 64 + lane;
+            const f32x16 zero = {};
             u32x4 next[AHEAD];
-#ifdef QV_PRIO
-            __builtin_amdgcn_s_setprio(1);
-#endif
+            f32x16 part;
+            f32x4 f[4];
 #pragma unroll
             for (int y = 0; y < AHEAD; ++y) next[y] = sk[y * 64];
-            keep_order();
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                f32x16 part;
-                f32x4 f[4];
+            for (int y = 0; y < BK + KS; ++y) {
+                const int j = y - BK;
+                if (!W::SCALED && j >= 0 && j % (GS / 16) == 0) {
 #pragma unroll
-                for (int y = 0; y < BK + KS; ++y) {
-                    const int at = t * (BK + KS) + y, j = y - BK;
-                    if (!W::SCALED && j >= 0 && j % (GS / 16) == 0) {
+                    for (int x = 0; x < 4; ++x)
+                        f[x] = *reinterpret_cast<const f32x4*>(
+                            &s_factor[buffer][KEYS * (j / (GS / 16)) + 32 * t + 8 * x + 4 * hh]);
+                }
+                u32x4 mine_q = y < BK ? qb[y < BK ? y : 0] : q[j >= 0 && j < KQ ? j : 0];
+                if (j >= KQ) mine_q = s_q[wave][(j - KQ) * 64 + lane];
+                const u32x4 operand = next[y % AHEAD];
+                if (y + AHEAD < BK + KS) next[y % AHEAD] = sk[(y + AHEAD) * 64];
+                if (y < BK) to = mfma32_type<DT>(operand, mine_q, y == 0 ? zero : to);
+                else if (W::SCALED) to = mfma32(operand, mine_q, to);
+                else part = mfma32(operand, mine_q, j % (GS / 16) == 0 ? zero : part);
+                slice(y);
+                keep_order();
+                if (!W::SCALED && j >= 0 && j % (GS / 16) == GS / 16 - 1) {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            f[x] = *reinterpret_cast<const f32x4*>(
-                                &s_factor[tile & 1][KEYS * (j / (GS / 16)) + 32 * t + 8 * x + 4 * hh]);
-                    }
-                    u32x4 mine_q = y < BK ? qb[y < BK ? y : 0] : q[j >= 0 && j < KQ ? j : 0];
-                    if (j >= KQ) mine_q = s_q[wave][(j - KQ) * 64 + lane];
-                    const u32x4 operand = next[at % AHEAD];
-                    if (at + AHEAD < NT * (BK + KS)) next[at % AHEAD] = sk[(at + AHEAD) * 64];
-                    const f32x16 zero = {};
-                    if (y < BK) s[t] = mfma32_type<DT>(operand, mine_q, y == 0 ? zero : s[t]);
-                    else if (W::SCALED) s[t] = mfma32(operand, mine_q, s[t]);
-                    else part = mfma32(operand, mine_q, j % (GS / 16) == 0 ? zero : part);
-                    keep_order();
-                    if (!W::SCALED && j >= 0 && j % (GS / 16) == GS / 16 - 1) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) s[t][e] = fmaf(f[e / 4][e % 4], part[e], s[t][e]);
-                    }
+                    for (int e = 0; e < 16; ++e) to[e] = fmaf(f[e / 4][e % 4], part[e], to[e]);
                 }
             }
-#ifdef QV_PRIO
-            __builtin_amdgcn_s_setprio(0);
-#endif
         };
-        auto sums = [&](int tile, int buffer) {
-            if (skip(tile)) return;
-            const int key = key0 + KEYS * tile;
-            const u32x4* sv = s_v[buffer] + lane;
-            u32x4 next[AHEAD];
-#pragma unroll
-            for (int y = 0; y < AHEAD; ++y) next[y] = sv[y * 64];
+        // The t-th 32 keys of the tile, whose scores are in x: probabilities, among
+        // the products for the next 32's scores (`more`: there are such), then sums.
+        auto sums = [&](int tile, int buffer, int t, f32x16& x, bool more, int next_buffer, int next_t, f32x16& y) {
+            const int key = key0 + KEYS * tile + 32 * t;
+            const u32x4* sv = s_v[buffer] + 2 * t * DB * 64 + lane;
             const int now = __builtin_amdgcn_readfirstlane(s_value_exponent[buffer]);
-            bool all = key >= full_lo && key + KEYS - 1 <= full_hi, there[BLOCKS];
-            float by[BLOCKS];   // what takes a block's scores to powers of two
+            bool all = key >= full_lo && key + 31 <= full_hi, there[2];
+            float by[2];   // what takes a block's scores to powers of two
 #pragma unroll
-            for (int x = 0; x < BLOCKS; ++x) {
-                there[x] = __builtin_amdgcn_readfirstlane(s_there[buffer][x]);
-                all = all && there[x];
-                by[x] = W::SCALED ? ldexpf(rf, __builtin_amdgcn_readfirstlane(s_key_exponent[buffer][x])) : rf;
+            for (int b = 0; b < 2; ++b) {
+                there[b] = __builtin_amdgcn_readfirstlane(s_there[buffer][2 * t + b]);
+                all = all && there[b];
+                by[b] = W::SCALED ? ldexpf(rf, __builtin_amdgcn_readfirstlane(s_key_exponent[buffer][2 * t + b])) : rf;
             }
-            keep_order();
             if (!all) {
                 const int first = key + 4 * hh - lo;
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const bool see = (uint32_t)(first + 32 * t + 8 * (e / 4) + e % 4) <= (uint32_t)reach;
-                        s[t][e] = see && there[2 * t + e / 8] ? s[t][e] : -INFINITY;
-                    }
+                for (int e = 0; e < 16; ++e) {
+                    const bool see = (uint32_t)(first + 8 * (e / 4) + e % 4) <= (uint32_t)reach;
+                    x[e] = see && there[e / 8] ? x[e] : -INFINITY;
+                }
             }
             float mx = -INFINITY;
 #pragma unroll
-            for (int x = 0; x < BLOCKS; ++x) {
-                float z = s[x / 2][8 * (x % 2)];
+            for (int b = 0; b < 2; ++b) {
+                float z = x[8 * b];
 #pragma unroll
-                for (int e = 1; e < 8; ++e) z = fmaxf(z, s[x / 2][8 * (x % 2) + e]);
-                mx = fmaxf(mx, z * by[x]);
+                for (int e = 1; e < 8; ++e) z = fmaxf(z, x[8 * b + e]);
+                mx = fmaxf(mx, z * by[b]);
             }
             if (__any(mx > top)) {
                 float higher = fmaxf(mx, top - kSlack);
@@ -495,46 +467,53 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                 for (int d = 0; d < DB; ++d) o[d] *= fade;
                 most = now;
             }
+            u32x4 p[2];
+            auto pair = [&](int e) {   // two probabilities
+                const float p0 = __builtin_amdgcn_exp2f(fmaf(x[2 * e], by[e / 4], -m));
+                const float p1 = __builtin_amdgcn_exp2f(fmaf(x[2 * e + 1], by[e / 4], -m));
+                l += p0 + p1;
+                p[e / 4][e % 4] = __builtin_bit_cast(uint32_t, half2_of(p0, p1));
+            };
+            if (NT == 2 && more) {
+                scores(next_buffer, next_t, y, [&](int z) {
 #pragma unroll
-            for (int x = 0; x < BLOCKS; ++x) {
-                const f32x16& y = s[x / 2];
-                u32x4 p;
+                    for (int e = z * 8 / (BK + KS); e < (z + 1) * 8 / (BK + KS); ++e) pair(e);
+                });
+            } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int z = 8 * (x % 2) + 2 * e;
-                    const float p0 = __builtin_amdgcn_exp2f(fmaf(y[z], by[x], -m));
-                    const float p1 = __builtin_amdgcn_exp2f(fmaf(y[z + 1], by[x], -m));
-                    l += p0 + p1;
-                    p[e] = __builtin_bit_cast(uint32_t, half2_of(p0, p1));
-                }
-#pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    const int at = x * DB + d;
-                    const u32x4 operand = next[at % AHEAD];
-                    if (at + AHEAD < BLOCKS * DB) next[at % AHEAD] = sv[(at + AHEAD) * 64];
-                    o[d] = mfma32(operand, p, o[d]);
-                    keep_order();
-                }
+                for (int e = 0; e < 8; ++e) pair(e);
             }
-            if (s_bad[buffer] == tile + 1) {   // values that are not finite, to the rows that see them
-                for (int t = 0; t < KEYS; ++t) {
-                    const int at = key + t;
-                    const int page = (at >> 4) < blocks ? table[at >> 4 >> c.page_shift] : -1;
-                    if (at >= part_end || page < 0 || page >= c.num_pages) continue;
-                    const size_t tok = (((size_t)page * c.heads + head) << (c.page_shift + 4)) +
-                                       (at & ((16 << c.page_shift) - 1));
+            u32x4 next[AHEAD];
 #pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        const uint32_t p = c.vs[tok * G + g];
-                        const float x = half_lo<DT>(p), y = half_hi<DT>(p);
-                        if ((x - x) + (y - y) == 0.0f) continue;
-                        const float add = (uint32_t)(at - lo) <= (uint32_t)reach ? fmaf(0.0f, x, y) : 0.0f;
+            for (int z = 0; z < AHEAD; ++z) next[z] = sv[z * 64];
 #pragma unroll
-                        for (int d = 0; d < DB; ++d)
+            for (int z = 0; z < 2 * DB; ++z) {
+                const u32x4 operand = next[z % AHEAD];
+                if (z + AHEAD < 2 * DB) next[z % AHEAD] = sv[(z + AHEAD) * 64];
+                o[z % DB] = mfma32(operand, p[z / DB], o[z % DB]);
+                keep_order();
+            }
+        };
+        // Values that are not finite, to the rows that see them.
+        auto mend = [&](int tile) {
+            const int key = key0 + KEYS * tile;
+            for (int t = 0; t < KEYS; ++t) {
+                const int at = key + t;
+                const int page = (at >> 4) < blocks ? table[at >> 4 >> c.page_shift] : -1;
+                if (at >= part_end || page < 0 || page >= c.num_pages) continue;
+                const size_t tok = (((size_t)page * c.heads + head) << (c.page_shift + 4)) +
+                                   (at & ((16 << c.page_shift) - 1));
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if ((32 * d + 8 * (e / 4)) / GS == g) o[d][e] += add;
-                    }
+                for (int g = 0; g < G; ++g) {
+                    const uint32_t p = c.vs[tok * G + g];
+                    const float x = half_lo<DT>(p), y = half_hi<DT>(p);
+                    if ((x - x) + (y - y) == 0.0f) continue;
+                    const float add = (uint32_t)(at - lo) <= (uint32_t)reach ? fmaf(0.0f, x, y) : 0.0f;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if ((32 * d + 8 * (e / 4)) / GS == g) o[d][e] += add;
                 }
             }
         };
@@ -545,10 +524,9 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
             load(0);
         }
         __syncthreads();
-        int buffer = 2;   // of tile t
-        for (int t = -1; t < tiles; ++t) {
-            const int after = buffer == 2 ? 0 : buffer + 1;
-            if (t + 1 < tiles) {   // tile t + 1 to LDS, the next one's codes to registers
+        // Tile t + 1 to LDS, the next one's codes to registers.
+        auto turn = [&](int t, int after, int key_after) {
+            if (t + 1 < tiles) {
                 if (value) {
                     const bool good = raw.values(s_v[after], exponent, my_blk, my_part);
                     if (wave == 4) {
@@ -556,20 +534,34 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                         s_value_exponent[after] = exponent;
                     }
                 } else {
-                    const int e = raw.keys(s_k[(t + 1) & 1], s_factor[(t + 1) & 1], my_blk, my_part);
+                    const int e = raw.keys(s_k[key_after], s_factor[key_after], my_blk, my_part);
                     if (my_part == 0) {
                         s_key_exponent[after][my_blk] = e;
                         s_there[after][my_blk] = raw.there ? 1 : 0;
                     }
                 }
-                fetch(t + 2);
-                load(t + 2);
             }
-            if (t >= 0) scores(t);
-            if (value) __syncthreads();
-            if (t >= 0) sums(t, buffer);
-            if (!value) __syncthreads();
+            fetch(t + 2);
+            load(t + 2);
+        };
+        int buffer = 2, key_buffer = KB - 1;   // of tile t
+        for (int t = -1; t < tiles; ++t) {
+            const int after = buffer == 2 ? 0 : buffer + 1, key_after = key_buffer == KB - 1 ? 0 : key_buffer + 1;
+            const bool more = t + 1 < tiles, here = t >= 0 && !unseen(t);
+            turn(t, after, key_after);
+            if constexpr (NT == 2) {
+                if (!value && here) sums(t, buffer, 0, s[0], true, key_buffer, 1, s[1]);
+                __syncthreads();   // tile t + 1 is in LDS
+                if (value && here) sums(t, buffer, 0, s[0], true, key_buffer, 1, s[1]);
+                if (here) sums(t, buffer, 1, s[1], more, key_after, 0, s[0]);
+            } else {
+                __syncthreads();
+                if (here) sums(t, buffer, 0, s[0], false, 0, 0, s[0]);
+            }
+            if (here && s_bad[buffer] == t + 1) mend(t);
+            if (more && !unseen(t + 1) && (NT == 1 || !here)) scores(key_after, 0, s[0], [](int) {});
             buffer = after;
+            key_buffer = key_after;
         }
 
         l += __shfl_xor(l, 32, 64);

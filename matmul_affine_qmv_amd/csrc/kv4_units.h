@@ -145,23 +145,28 @@ inline long long kv4_groups(const Kv4AttnArgs& a) {
     return (long long)a.c.heads * (a.p.lines ? a.p.lines : (long long)a.requests * a.p.tiles + 1);
 }
 
-// One wave a (token of a request, head): joins the parts of its unit, writes
-// zeros where no key is seen, and leaves alone what is whole.
-template <int D, int DT>
+// Joins the parts of the units, writes zeros where no key is seen, and leaves
+// alone what is whole.  A row (token of a request, head) takes D / 4 threads side
+// by side, `ALONG` of which sets share its parts, every ALONG-th each: one for the
+// many rows of prompts, whose units have few parts; a work-group's worth for few
+// rows, which may have as many parts as there are lines.
+template <int D, int DT, int ALONG>
 __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs a) {
-    constexpr int E = D / 64;
-    const int lane = threadIdx.x & 63;
-    const long long waves = (long long)a.requests * a.max_query * a.heads;
-    const int own = (int)((waves + 3) / 4);   // the groups behind these take the tokens of no request
+    constexpr int LANES = D / 4, ROWS = 256 / (LANES * ALONG);
+    __shared__ f32x4 s_o[ALONG > 1 ? 256 : 1];
+    __shared__ float s_l[ALONG];
+    const long long rows = (long long)a.requests * a.max_query * a.heads;
+    const int own = (int)((rows + ROWS - 1) / ROWS);   // the groups behind these take the tokens of no request
     if ((int)blockIdx.x >= own) {
         clear_rest(a, blockIdx.x - own, gridDim.x - own);
         return;
     }
-    long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (id >= waves) return;
+    const int lane = threadIdx.x % LANES, set = threadIdx.x / LANES % ALONG;
+    const long long id = (long long)blockIdx.x * ROWS + threadIdx.x / (LANES * ALONG);
+    if (id >= rows) return;
     const int head = (int)(id % a.heads);
-    id /= a.heads;
-    const int i = (int)(id % a.max_query), req = (int)(id / a.max_query);
+    const uint32_t t = (uint32_t)(id / a.heads);   // below 2^31: rows are
+    const int req = (int)(t / (uint32_t)a.max_query), i = (int)(t - (uint32_t)req * a.max_query);
     const int start = max(a.offsets[req], 0);
     if (i >= a.offsets[req + 1] - start || start + i >= a.tokens) return;
     const int row = i * a.each + head % a.each, tile = row / a.p.rows;
@@ -170,38 +175,58 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs a) {
     const int w0 = p0 / length, w1 = p1 > p0 ? (p1 - 1) / length : w0 - 1;
     if (w0 == w1) return;
     const long long at = ((long long)start + i) * a.heads + head;
-    const int kv_head = head / a.each;
-    const long long r = (long long)kv_head * a.p.rows + row - tile * a.p.rows, all = (long long)a.c.heads * a.p.rows;
+    const long long r = (long long)(head / a.each) * a.p.rows + row - tile * a.p.rows;
+    const long long all = (long long)a.c.heads * a.p.rows;
     auto place = [&](int w) { return (2ll * w + (w == w0 ? 1 : 0)) * all + r; };
     const f32x2* stat = reinterpret_cast<const f32x2*>(a.stat);
-    float m = -INFINITY;
-    for (int w = w0 + lane; w <= w1; w += 64) m = fmaxf(m, stat[place(w)][0]);
+    float m = -INFINITY, l = 0.0f;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (ALONG > 1) {   // the largest maximum first: the sets' sums then just add
+        for (int w = w0 + (int)(threadIdx.x & 63); w <= w1; w += 64) m = fmaxf(m, stat[place(w)][0]);
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+        for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    } else {
+        for (int w = w0; w <= w1; ++w) m = fmaxf(m, stat[place(w)][0]);
+    }
     const float safe = m > -INFINITY ? m : 0.0f;
-    float l = 0.0f, o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.0f;
-#pragma unroll 8
-    for (int w = w0; w <= w1; ++w) {
+#pragma unroll 4
+    for (int w = w0 + set; w <= w1; w += ALONG) {
         const long long p = place(w);
         const f32x2 st = stat[p];
         const float f = __builtin_amdgcn_exp2f(st[0] - safe);
         l += st[1] * f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += f * a.part[p * D + e * 64 + lane];
+        o += *reinterpret_cast<const f32x4*>(a.part + p * D + 4 * lane) * f;
     }
-    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    if constexpr (ALONG > 1) {
+        s_o[threadIdx.x] = o;
+        if (lane == 0) s_l[set] = l;
+        __syncthreads();
+        if (set) return;
 #pragma unroll
-    for (int e = 0; e < E; ++e) store_elem<DT>(a.out, at * D + e * 64 + lane, o[e] * inv);
+        for (int s = 1; s < ALONG; ++s) {
+            o += s_o[s * LANES + lane];
+            l += s_l[s];
+        }
+    }
+    o *= l != 0.0f ? 1.0f / l : 0.0f;
+    uint32_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = DT == DT_F16 ? f32_to_f16_bits(o[e]) : f32_to_bf16_bits(o[e]);
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at * D + 4 * lane) =
+        u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
     if (a.lse && lane == 0) a.lse[at] = l != 0.0f ? (safe + __builtin_amdgcn_logf(l)) * LN2 : -INFINITY;
 }
 
 template <int D, int DT>
 hipError_t launch_join(const Kv4AttnArgs& a, hipStream_t st) {
-    const long long waves = (long long)a.requests * a.max_query * a.heads;
+    constexpr int ALONG = 256 / (D / 4);
+    const long long rows = (long long)a.requests * a.max_query * a.heads;
     const long long rest = 1 + ((long long)a.tokens * a.heads * (D / 8) >> 12);   // 16 stores a thread
-    kv4_join_kernel<D, DT><<<dim3((unsigned)((waves + 3) / 4 + (rest < 64 ? rest : 64))), dim3(256), 0, st>>>(a);
+    const unsigned behind = (unsigned)(rest < 64 ? rest : 64);
+    if (a.p.rows > 16)
+        kv4_join_kernel<D, DT, 1><<<(unsigned)((rows + ALONG - 1) / ALONG) + behind, 256, 0, st>>>(a);
+    else
+        kv4_join_kernel<D, DT, ALONG><<<(unsigned)rows + behind, 256, 0, st>>>(a);
     return hipGetLastError();
 }
 
