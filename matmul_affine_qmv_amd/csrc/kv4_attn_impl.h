@@ -183,7 +183,7 @@ struct Rows {
     }
 
     // `at`: the numbers of the two blocks.
-    __device__ __forceinline__ void load_pairs(const Kv4View& c, const size_t (&at)[2]) {
+    __device__ __forceinline__ void load_pairs(const Kv4View& c, const uint32_t (&at)[2]) {
         const int lane = threadIdx.x & 63;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -191,12 +191,12 @@ struct Rows {
             for (int r = 0; r < Pairs<DT, G>::PAIRS; ++r) {
                 const int w = 16 * r + (lane & 15);   // of the row's 8 * G pairs (fewer than 16: the rest repeat)
                 const uint32_t* from = (w & (4 * G)) ? c.vs : c.ks;
-                sb[i][r] = from[at[i] * (16 * G) + (lane >> 4) * (4 * G) + (w & (4 * G - 1))];
+                sb[i][r] = from[(uint64_t)at[i] * (16 * G) + (lane >> 4) * (4 * G) + (w & (4 * G - 1))];
             }
     }
-    __device__ __forceinline__ void load_codes(uint32_t (&to)[2][NJ], const uint32_t* codes, const size_t (&at)[2]) {
+    __device__ __forceinline__ void load_codes(uint32_t (&to)[2][NJ], const uint32_t* codes, const uint32_t (&at)[2]) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) load_words(to[i], codes + at[i] * (64 * NJ) + (threadIdx.x & 63) * NJ);
+        for (int i = 0; i < 2; ++i) load_words(to[i], codes + (uint64_t)at[i] * (64 * NJ) + (threadIdx.x & 63) * NJ);
     }
 
     __device__ __forceinline__ void scores(const Pairs<DT, G> (&pair)[2]) {
@@ -325,11 +325,10 @@ struct Pages {
     }
     // The two blocks' numbers in the cache (page 0's where there is none: its
     // tokens are hidden).
-    __device__ __forceinline__ void place(const Kv4View& c, int head, int step, size_t (&at)[2]) const {
+    __device__ __forceinline__ void place(const Kv4View& c, int head, int step, uint32_t (&at)[2]) const {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            at[i] = (((size_t)(there(c, i) ? page[i] : 0) * c.heads + head) << c.page_shift) +
-                    ((2 * step + i) & ((1 << c.page_shift) - 1));
+            at[i] = block_number(c, there(c, i) ? page[i] : 0, head, 2 * step + i);
     }
 };
 
@@ -384,7 +383,7 @@ __global__ __launch_bounds__(64 * WK, 2) void kv4_attn_kernel(Kv4AttnArgs a) {
         if (step < steps) {
             // A step's loads go out as soon as the step before has used the same
             // registers, its block table entries another step ahead.
-            size_t at[2];
+            uint32_t at[2];
             pages.read(c, step);
             pages.place(c, head, step, at);
             bool there0 = pages.there(c, 0), there1 = pages.there(c, 1);

@@ -118,21 +118,22 @@ struct Raw {
         const int page = __builtin_amdgcn_readlane(pages, first + my_blk), blk = (key >> 4) + my_blk;
         const int own = value ? lane % KEYS : 16 * my_blk + (lane & 15);   // the lane's token of the tile
         const int its = __shfl(pages, first + own / 16, 64);
-        const int mask = (1 << c.page_shift) - 1;
         tokens = end - 16 * blk;
         there = tokens > 0 && page >= 0 && page < c.num_pages;
         live = key + own < end && its >= 0 && its < c.num_pages;
         // what is not there is read from page 0 and not used
-        const size_t at = (((size_t)(there ? page : 0) * c.heads + head) << c.page_shift) + (blk & mask);
-        const size_t row = (((size_t)(live ? its : 0) * c.heads + head) << c.page_shift) + (((key + own) >> 4) & mask);
-        const uint32_t* codes = value ? c.vc : c.kc;
+        const uint32_t at = block_number(c, there ? page : 0, head, blk);
+        const uint32_t row = block_number(c, live ? its : 0, head, (key + own) >> 4);
+        const uint32_t* codes = (value ? c.vc : c.kc) + lane * NJ + part * NW;
         const uint32_t* pairs = value ? c.vs : c.ks;
-        load_words(w, codes + at * (64 * NJ) + lane * NJ + part * NW);
+        const uint32_t* own_pairs = pairs + (own & 15) * G;
+        const uint32_t* shared = pairs + (lane >> 4) * (4 * G);
+        load_words(w, codes + (uint64_t)at * (64 * NJ));
 #pragma unroll
-        for (int g = 0; g < G; ++g) token_pairs[g] = pairs[(row * 16 + (own & 15)) * G + g];
+        for (int g = 0; g < G; ++g) token_pairs[g] = own_pairs[(uint64_t)row * (16 * G) + g];
 #pragma unroll
         for (int r = 0; r < SHARE; ++r)
-            share[r] = pairs[at * (16 * G) + (lane >> 4) * (4 * G) + ((16 * r + (lane & 15)) & (4 * G - 1))];
+            share[r] = shared[(uint64_t)at * (16 * G) + ((16 * r + (lane & 15)) & (4 * G - 1))];
     }
 
     // Keys to `k` [blocks of 32][BK + KS][2][32] of 16 bytes; `blk` counts in the
@@ -247,6 +248,15 @@ struct Raw {
     }
 };
 
+// What the rows need to know of a tile beside its operands.
+struct alignas(16) TileInfo {
+    static constexpr int MISSING = -1000;
+    int block[4];   // the keys' exponent, or MISSING: no page
+    int value_exponent;
+    int bad;        // tile + 1, where it holds values that are not finite
+    int unused[2];
+};
+
 template <int D, int GS, int DT>
 __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4AttnArgs a) {
     using W = Raw<D, GS, DT>;
@@ -259,7 +269,7 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
     __shared__ u32x4 s_k[KB][NT * (BK + KS) * 64], s_v[3][2 * NT * DB * 64];
     __shared__ u32x4 s_q[PROMPT_WAVES][KS > KQ ? (KS - KQ) * 64 : 1];
     __shared__ float s_factor[KB][W::SCALED ? 1 : G * KEYS];
-    __shared__ int s_bad[3], s_there[3][4], s_key_exponent[3][4], s_value_exponent[3];
+    __shared__ TileInfo s_info[3];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, n = lane & 31, hh = lane >> 5;
     const Kv4View& c = a.c;
@@ -422,17 +432,19 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
         };
         // The t-th 32 keys of the tile, whose scores are in x: probabilities, among
         // the products for the next 32's scores (`more`: there are such), then sums.
+        TileInfo info;   // of the tile at hand, read one barrier ahead of its use
         auto sums = [&](int tile, int buffer, int t, f32x16& x, bool more, int next_buffer, int next_t, f32x16& y) {
             const int key = key0 + KEYS * tile + 32 * t;
             const u32x4* sv = s_v[buffer] + 2 * t * DB * 64 + lane;
-            const int now = __builtin_amdgcn_readfirstlane(s_value_exponent[buffer]);
+            const int now = __builtin_amdgcn_readfirstlane(info.value_exponent);
             bool all = key >= full_lo && key + 31 <= full_hi, there[2];
             float by[2];   // what takes a block's scores to powers of two
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                there[b] = __builtin_amdgcn_readfirstlane(s_there[buffer][2 * t + b]);
+                const int e = __builtin_amdgcn_readfirstlane(info.block[2 * t + b]);
+                there[b] = e != TileInfo::MISSING;
                 all = all && there[b];
-                by[b] = W::SCALED ? ldexpf(rf, __builtin_amdgcn_readfirstlane(s_key_exponent[buffer][2 * t + b])) : rf;
+                by[b] = W::SCALED ? ldexpf(rf, there[b] ? e : 0) : rf;
             }
             if (!all) {
                 const int first = key + 4 * hh - lo;
@@ -501,8 +513,7 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                 const int at = key + t;
                 const int page = (at >> 4) < blocks ? table[at >> 4 >> c.page_shift] : -1;
                 if (at >= part_end || page < 0 || page >= c.num_pages) continue;
-                const size_t tok = (((size_t)page * c.heads + head) << (c.page_shift + 4)) +
-                                   (at & ((16 << c.page_shift) - 1));
+                const size_t tok = (size_t)block_number(c, page, head, at >> 4) * 16 + (at & 15);
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     const uint32_t p = c.vs[tok * G + g];
@@ -518,7 +529,7 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
             }
         };
 
-        if (threadIdx.x < 3) s_bad[threadIdx.x] = 0;
+        if (threadIdx.x < 3) s_info[threadIdx.x].bad = 0;
         if (tiles > 0) {
             fetch(0);
             load(0);
@@ -530,15 +541,12 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                 if (value) {
                     const bool good = raw.values(s_v[after], exponent, my_blk, my_part);
                     if (wave == 4) {
-                        if (!good) s_bad[after] = t + 2;
-                        s_value_exponent[after] = exponent;
+                        if (!good) s_info[after].bad = t + 2;
+                        s_info[after].value_exponent = exponent;
                     }
                 } else {
                     const int e = raw.keys(s_k[key_after], s_factor[key_after], my_blk, my_part);
-                    if (my_part == 0) {
-                        s_key_exponent[after][my_blk] = e;
-                        s_there[after][my_blk] = raw.there ? 1 : 0;
-                    }
+                    if (my_part == 0) s_info[after].block[my_blk] = raw.there ? e : TileInfo::MISSING;
                 }
             }
             fetch(t + 2);
@@ -558,7 +566,8 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                 __syncthreads();
                 if (here) sums(t, buffer, 0, s[0], false, 0, 0, s[0]);
             }
-            if (here && s_bad[buffer] == t + 1) mend(t);
+            if (here && __builtin_amdgcn_readfirstlane(info.bad) == t + 1) mend(t);
+            info = s_info[after];
             if (more && !unseen(t + 1) && (NT == 1 || !here)) scores(key_after, 0, s[0], [](int) {});
             buffer = after;
             key_buffer = key_after;

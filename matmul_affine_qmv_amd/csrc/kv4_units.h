@@ -13,6 +13,12 @@ constexpr float LN2 = 0.69314718055994530942f;
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
+// The number of block `blk` of a request's tokens, which is in the page given.  32
+// bits hold it: 2^32 blocks of the smallest head would be 4 TB.
+__device__ __forceinline__ uint32_t block_number(const Kv4View& c, int page, int head, int blk) {
+    return (((uint32_t)page * c.heads + head) << c.page_shift) + (blk & ((1 << c.page_shift) - 1));
+}
+
 // Rows and keys of one unit, or of the part of it that a work-group takes.
 struct Unit {
     int req;
