@@ -451,9 +451,12 @@ int qmx_kv4_read(const qmx_kv4_cache* cache, void* k_out, void* v_out, const int
  *   scale : finite and above 0.
  *   workspace : qmx_kv4_attention_workspace_bytes bytes, 16-byte aligned (NULL
  *           where that is 0), overwritten; calls that share it are ordered.
- * Scores and sums are float32 on exact codes; what multiplies the value codes,
- * a probability times a scale, is rounded to dtype.  The split of the keys
- * depends on the host arguments only, so reruns are bit-identical. */
+ * Scores and sums are float32 on exact codes.  What the value codes are multiplied
+ * by, a probability times a scale, is rounded to dtype; with more than 64 query
+ * rows a key head (max_query_len * heads / kv_heads), values and probabilities
+ * are rounded to float16 instead, after a power of two.  How the keys are cut
+ * among work-groups follows the lengths and these arguments, so reruns with the
+ * same are bit-identical. */
 int qmx_kv4_attention(const qmx_kv4_cache* cache, const void* q, long long q_token_stride,
                       long long q_head_stride, void* out, float* lse, const int32_t* block_table,
                       int columns, long long table_stride, const int32_t* kv_lens,

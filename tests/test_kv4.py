@@ -491,6 +491,18 @@ def test_other_stream():
 
 
 @on_gpu
+def test_example_of_a_serving_loop():
+    """Prompts, then graph replays of one token each, against float64 on what the cache reads back as.  Reading back
+    rounds keys and values to bfloat16 (half a step 2^-8 each, scores of at most a few units move p by that much again),
+    the kernel's probabilities and outputs are rounded alike: 8 such roundings of the row's largest output bound them."""
+    say("example")
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import kv4_decode
+    errors = kv4_decode.main(steps=20)
+    assert len(errors) == 21 and max(errors) <= 8 * 2.0 ** -8, errors
+
+
+@on_gpu
 def test_binding_refusals():
     cache = qmx.Kv4Cache.zeros(2, 2, 64, page_size=16, group_size=32, device=DEV)
     x = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device=DEV)
