@@ -5,7 +5,7 @@
 // A work-group of 8 waves takes 256 rows, a wave 32 of them, and walks the keys
 // 64 at a time (32 where the head has 256 dimensions).  Four waves turn the keys'
 // codes into operands and four the values', once for all 256 rows, into LDS (one
-// barrier a tile, two buffers for keys, three for values) in the order in which
+// barrier a tile, three buffers, or two of keys of 256 dimensions) in the order in which
 // the products read them: 16 bytes a lane, lane after lane.  With two waves on a
 // SIMD there is little to hide one wave's waits, so the exponentials of 32 keys
 // stand among the products for the scores of the next 32.
@@ -553,13 +553,15 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
             load(t + 2);
         };
         int buffer = 2, key_buffer = KB - 1;   // of tile t
-        for (int t = -1; t < tiles; ++t) {
+        for (int t = tiles > 0 ? -1 : 0; t < tiles; ++t) {   // no key, no read: there may be no page at all
             const int after = buffer == 2 ? 0 : buffer + 1, key_after = key_buffer == KB - 1 ? 0 : key_buffer + 1;
             const bool more = t + 1 < tiles, here = t >= 0 && !unseen(t);
             turn(t, after, key_after);
             if constexpr (NT == 2) {
+                // Tile t + 1 is in LDS behind the barrier.  The values' waves take it half
+                // a tile earlier, so that a SIMD's two waves are not at the same work.
                 if (!value && here) sums(t, buffer, 0, s[0], true, key_buffer, 1, s[1]);
-                __syncthreads();   // tile t + 1 is in LDS
+                __syncthreads();
                 if (value && here) sums(t, buffer, 0, s[0], true, key_buffer, 1, s[1]);
                 if (here) sums(t, buffer, 1, s[1], more, key_after, 0, s[0]);
             } else {

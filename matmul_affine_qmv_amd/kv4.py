@@ -54,6 +54,10 @@ class KvMaps(namedtuple("KvMaps", _MAPS)):
         return self
 
     @classmethod
+    def _make(cls, tensors) -> "KvMaps":
+        return cls(*tensors)
+
+    @classmethod
     def empty(cls, requests: int, tokens: int, device) -> "KvMaps":
         return cls(*(torch.empty(n, dtype=_INT, device=device)
                      for n in (requests + 1, requests, tokens, tokens, tokens, 2)))

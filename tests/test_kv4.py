@@ -491,6 +491,46 @@ def test_other_stream():
 
 
 @on_gpu
+@pytest.mark.parametrize("new", [1, 90])
+def test_cache_without_pages(new):
+    """Nothing is there: attention and reads give zeros, writes do nothing."""
+    say("no pages", new)
+    cache = qmx.Kv4Cache.zeros(0, 2, 128, page_size=16, group_size=64, device=DEV)
+    q = torch.randn(new, 4, 128, dtype=torch.bfloat16, device=DEV)
+    out, lse = qmx.kv4_attention(cache, q, ints([[0, 1, 2, 3, 4, 5]]), ints([90]), ints([0, new]), max_query_len=new,
+                                 max_kv_len=2000, return_lse=True)
+    assert not out.any() and torch.isneginf(lse).all()
+    slots = ints(list(range(new)))
+    qmx.kv4_write(cache, q[:, :2], q[:, 2:], slots)
+    assert not any(t.any() for t in qmx.kv4_read(cache, slots))
+
+
+@on_gpu
+@pytest.mark.parametrize("new,max_kv", [(1, 50), (70, 90), (1, 5000)])
+def test_bounds_of_the_host_hold(new, max_kv):
+    """Keys past max_kv_len, or past the table's columns, are not seen whatever kv_lens says; tokens of no request,
+    and all of them where there are no requests, get zeros."""
+    say("bounds", new, max_kv)
+    rng = np.random.default_rng(20)
+    c = ref.Cache(8, 1, 64, 16, 32, "f16", rng)
+    cache = device_cache(c)
+    table = np.arange(6, dtype=np.int32)[None]
+    q = torch.from_numpy(rng.normal(0, 1, (new + 2, 2, 64))).half()
+    seen = min(max_kv, 96)
+    out = qmx.kv4_attention(cache, q.to(DEV), ints(table.tolist()), ints([300]), ints([0, new]), max_query_len=new,
+                            max_kv_len=max_kv)
+    # every query is at position 300 - new or later, so it sees all that is there
+    for t in range(new):
+        want, _, tol, _ = ref.attention(c, q[t:t + 1], table, [seen], [0, 1], prompt=2 * new > 64)
+        assert (np.abs(out[t].double().cpu().numpy() - want[0]) <= tol[0]).all()
+    assert not out[new:].any()
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    out = qmx.kv4_attention(cache, q.to(DEV), torch.zeros(0, 6, dtype=torch.int32, device=DEV), none, ints([0]),
+                            max_query_len=new, max_kv_len=max_kv)
+    assert not out.any()
+
+
+@on_gpu
 def test_example_of_a_serving_loop():
     """Prompts, then graph replays of one token each, against float64 on what the cache reads back as.  Reading back
     rounds keys and values to bfloat16 (half a step 2^-8 each, scores of at most a few units move p by that much again),
