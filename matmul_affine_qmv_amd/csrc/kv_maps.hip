@@ -6,6 +6,10 @@
 // leaves alone there) or the free page whose place in the list the scan gives.
 // A work-group then writes its own range of tokens, or its share of the new
 // table entries.
+//
+// Bound by waits, one after the other (lengths, scan, search, table, stores): 5 us
+// for 24 requests, 13 us for 3000 requests with 300000 tokens, where the 3.8 MB
+// would take 0.8 us.  Two scans, for tokens and then pages, took 15 us.
 #include "kv4.h"
 #include "kv_scan.h"
 

@@ -350,6 +350,13 @@ def test_attention_prompts_of_many_tiles(dtype, D, group):
 
 @on_gpu
 @pytest.mark.parametrize("dtype,D,group", FORMATS)
+def test_attention_prompts_cut(dtype, D, group):
+    """Prompts behind a long prefix, whose units are cut and joined."""
+    attention_case(dtype, D, group, 64, 2, 2, [(1777, 61), (0, 0), (7, 90), (700, 1)], pad=3, seed=13, spoil=True)
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype,D,group", FORMATS)
 def test_attention_split_keys(dtype, D, group):
     """Keys cut over work-groups, requests that end in the first part."""
     attention_case(dtype, D, group, 64, 3, 1, [(2500, 1), (10, 2), (0, 0), (1111, 4)], pad=2, seed=3, spoil=True)
@@ -370,7 +377,7 @@ def test_attention_shared_heads(each, H, new):
 
 
 @on_gpu
-@pytest.mark.parametrize("lens", [[(70, 1), (40, 1)], [(60, 40), (35, 50)], [(1300, 1), (600, 2)]])
+@pytest.mark.parametrize("lens", [[(70, 1), (40, 1)], [(60, 40), (35, 50)], [(1700, 1), (600, 2)]])
 def test_attention_missing_pages(lens):
     """Entries without a page inside a request; a request whose every page is missing sees nothing."""
     holes = [(0, 0), (0, 2), (1, 1)]
@@ -427,7 +434,7 @@ def test_step_under_a_graph():
     """Maps, write and attention captured once and replayed over new lengths, with eager work between."""
     say("graph")
     torch.manual_seed(0)
-    H, each, D, page, R, T, columns = 2, 3, 128, 16, 5, 8, 90
+    H, each, D, page, R, T, columns = 2, 3, 128, 16, 5, 8, 120
     cache = qmx.Kv4Cache.zeros(200, H, D, page_size=page, group_size=64, device=DEV)
     other = qmx.Kv4Cache.zeros(200, H, D, page_size=page, group_size=64, device=DEV)
     tables = [torch.full((R, columns), -1, dtype=torch.int32, device=DEV) for _ in range(2)]
