@@ -454,7 +454,8 @@ int qmx_kv4_read(const qmx_kv4_cache* cache, void* k_out, void* v_out, const int
  * Scores and sums are float32 on exact codes.  What the value codes are multiplied
  * by, a probability times a scale, is rounded to dtype; with more than 64 query
  * rows a key head (max_query_len * heads / kv_heads), values and probabilities
- * are rounded to float16 instead, after a power of two.  How the keys are cut
+ * are rounded to float16 instead after a power of two, to 2^-11 of themselves or
+ * 2^-25 of the largest finite value of the request's tokens.  How the keys are cut
  * among work-groups follows the lengths and these arguments, so reruns with the
  * same are bit-identical. */
 int qmx_kv4_attention(const qmx_kv4_cache* cache, const void* q, long long q_token_stride,

@@ -16,9 +16,10 @@ roundings alone (``u`` is half a step of the type, 2^-24 that of float32):
 
 ``prompt``: the kernel of many rows rounds other things.  Values and
 probabilities to float16, 2 * 2^-11 sum_t p_t |v_td|, in place of p_t s_tg, or
-2^-24 of the largest value each (a power of two above it at most twice it;
-probabilities down to 2^-25 a key, and those scaled with it); queries to
-float16, 2^-24 of the row's largest, which enters E_t.
+2^-24 of the request's largest value each (a power of two above it at most twice
+it; probabilities down to 2^-25 a key, and those scaled with it); queries to
+float16, 2^-24 of the row's largest, and bfloat16 keys' scaled codes, 2^-24 of
+their block's largest, which enters E_t.
 """
 import numpy as np
 import torch
@@ -151,12 +152,13 @@ def attention(cache, q, table, kv_lens, offsets, window=0, scale=None, prompt=Fa
                     size = ((OFF + 15) * ks[see] + np.abs(kb[see]) + OFF * ks[see]) @ np.abs(x) * abs(scale)
                     err = (D + 8) * U32 * size.max() + 8 * U32 * (np.abs(s).max() + 1)
                     if prompt:
-                        err += 2.0 ** -24 * np.abs(x).max() * np.abs(k).sum(-1).max() * scale
+                        err += 2.0 ** -24 * scale * (np.abs(x).max() * np.abs(k).sum(-1).max()
+                                                     + np.abs(x).sum() * (ks[see] * 8 + np.abs(kb[see])).max())
                     steps = see.sum() / 32 + 64
                     spread = p @ np.abs(v - out[t, a])
                     held = u * (p @ (vs[see] * np.abs(vc[see] - 8)))
                     if prompt:
-                        held = 2.0 ** -10 * (p @ np.abs(v)) + 2.0 ** -24 * np.abs(v).max() * (1 + see.sum() / total)
+                        held = 2.0 ** -10 * (p @ np.abs(v)) + 2.0 ** -24 * np.abs(vc * vs + vb).max() * (1 + see.sum() / total)
                     tol[t, a] = (u * np.abs(out[t, a]) + held
                                  + steps * U32 * (p @ (vs[see] * (OFF + 23) + np.abs(vb[see])))
                                  + np.expm1(2 * err) * spread)

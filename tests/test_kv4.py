@@ -269,13 +269,19 @@ def test_write_keeps_nan_and_infinity_to_their_group():
 
 
 def attention_case(dtype, D, group, page, each, H, lens, window=0, pad=0, holes=(), spoil=False, strided=False,
-                   seed=0, scale=None, table_extra=0):
+                   seed=0, scale=None, table_extra=0, uneven=False):
     """lens: (past, new) of each request.  holes: (request, column) entries without a page."""
     say("attention", dtype, D, group, page, each, H, lens, window, pad, holes, spoil, strided)
     rng = np.random.default_rng(seed)
     need = [-(-(p + n) // page) for p, n in lens]
     pages = sum(need) + 2
     c = ref.Cache(pages, H, D, page, group, dtype, rng)
+    if uneven:   # keys far above and queries far below 1, values that differ from token to token
+        for x in (c.s[0], c.b[0]):
+            x *= 2.0 ** 40
+        factor = 2.0 ** rng.integers(-6, 7, (pages, H, page, 1))
+        c.s[1] *= factor
+        c.b[1] *= factor
     R, columns = len(lens), max(1, max(need)) + table_extra
     order = rng.permutation(pages)[:sum(need)]
     table = np.full((R, columns), -1, dtype=np.int32)
@@ -290,7 +296,7 @@ def attention_case(dtype, D, group, page, each, H, lens, window=0, pad=0, holes=
     for _, n in lens:
         offsets.append(offsets[-1] + n)
     T, heads = offsets[-1] + pad, each * H
-    q = torch.from_numpy(rng.normal(0, 1.3, (T, heads, D))).to(ref.TYPES[dtype])
+    q = torch.from_numpy(rng.normal(0, 1.3, (T, heads, D)) * (2.0 ** -40 if uneven else 1)).to(ref.TYPES[dtype])
     packed = c.packed()
     if spoil:   # whatever no request sees holds NaN
         seen = np.zeros((pages, page), dtype=bool)
@@ -402,6 +408,13 @@ def test_attention_spread_scores():
     """Scores far apart: the running maximum rises often, and most probabilities vanish."""
     attention_case("bf16", 128, 32, 16, 4, 1, [(700, 1)], scale=3.0, seed=10)
     attention_case("f16", 128, 64, 16, 4, 1, [(300, 30)], scale=3.0, seed=11)
+
+
+@on_gpu
+@pytest.mark.parametrize("lens", [[(90, 1), (33, 3)], [(50, 75), (0, 40)], [(2000, 1), (1700, 2)], [(1900, 70)]])
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 128), (256, 64)])
+def test_attention_uneven_magnitudes(lens, D, group):
+    attention_case("bf16", D, group, 32, 2, 1, lens, seed=14, spoil=True, uneven=True)
 
 
 @on_gpu
