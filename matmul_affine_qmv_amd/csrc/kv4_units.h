@@ -151,69 +151,26 @@ inline long long kv4_groups(const Kv4AttnArgs& a) {
     return (long long)a.c.heads * (a.p.lines ? a.p.lines : (long long)a.requests * a.p.tiles + 1);
 }
 
-// Joins the parts of the units, writes zeros where no key is seen, and leaves
-// alone what is whole.  A row (token of a request, head) takes D / 4 threads side
-// by side, `ALONG` of which sets share its parts, every ALONG-th each: one for the
-// many rows of prompts, whose units have few parts; a work-group's worth for few
-// rows, which may have as many parts as there are lines.
-template <int D, int DT, int ALONG>
-__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs a) {
-    constexpr int LANES = D / 4, ROWS = 256 / (LANES * ALONG);
-    __shared__ f32x4 s_o[ALONG > 1 ? 256 : 1];
-    __shared__ float s_l[ALONG];
-    const long long rows = (long long)a.requests * a.max_query * a.heads;
-    const int own = (int)((rows + ROWS - 1) / ROWS);   // the groups behind these take the tokens of no request
-    if ((int)blockIdx.x >= own) {
-        clear_rest(a, blockIdx.x - own, gridDim.x - own);
-        return;
+// The parts of a unit's row, in the order of the line: their places, and what
+// they add up to.
+struct Parts {
+    int first, last;   // parts of the line; last < first: no key is seen
+    long long row;     // of all rows of a part
+    long long all;
+    __device__ __forceinline__ long long place(int w) const {
+        return (2ll * w + (w == first ? 1 : 0)) * all + row;
     }
-    const int lane = threadIdx.x % LANES, set = threadIdx.x / LANES % ALONG;
-    const long long id = (long long)blockIdx.x * ROWS + threadIdx.x / (LANES * ALONG);
-    if (id >= rows) return;
-    const int head = (int)(id % a.heads);
-    const uint32_t t = (uint32_t)(id / a.heads);   // below 2^31: rows are
-    const int req = (int)(t / (uint32_t)a.max_query), i = (int)(t - (uint32_t)req * a.max_query);
-    const int start = max(a.offsets[req], 0);
-    if (i >= a.offsets[req + 1] - start || start + i >= a.tokens) return;
-    const int row = i * a.each + head % a.each, tile = row / a.p.rows;
-    const int v = req * a.p.tiles + a.p.tiles - 1 - tile;
+};
+__device__ __forceinline__ Parts parts_of(const Kv4AttnArgs& a, int v, int kv_head, int row) {
     const int length = a.pos[0], p0 = a.pos[1 + 2 * v], p1 = a.pos[2 + 2 * v];
-    const int w0 = p0 / length, w1 = p1 > p0 ? (p1 - 1) / length : w0 - 1;
-    if (w0 == w1) return;
-    const long long at = ((long long)start + i) * a.heads + head;
-    const long long r = (long long)(head / a.each) * a.p.rows + row - tile * a.p.rows;
-    const long long all = (long long)a.c.heads * a.p.rows;
-    auto place = [&](int w) { return (2ll * w + (w == w0 ? 1 : 0)) * all + r; };
-    const f32x2* stat = reinterpret_cast<const f32x2*>(a.stat);
-    float m = -INFINITY, l = 0.0f;
-    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (ALONG > 1) {   // the largest maximum first: the sets' sums then just add
-        for (int w = w0 + (int)(threadIdx.x & 63); w <= w1; w += 64) m = fmaxf(m, stat[place(w)][0]);
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-    } else {
-        for (int w = w0; w <= w1; ++w) m = fmaxf(m, stat[place(w)][0]);
-    }
-    const float safe = m > -INFINITY ? m : 0.0f;
-#pragma unroll 4
-    for (int w = w0 + set; w <= w1; w += ALONG) {
-        const long long p = place(w);
-        const f32x2 st = stat[p];
-        const float f = __builtin_amdgcn_exp2f(st[0] - safe);
-        l += st[1] * f;
-        o += *reinterpret_cast<const f32x4*>(a.part + p * D + 4 * lane) * f;
-    }
-    if constexpr (ALONG > 1) {
-        s_o[threadIdx.x] = o;
-        if (lane == 0) s_l[set] = l;
-        __syncthreads();
-        if (set) return;
-#pragma unroll
-        for (int s = 1; s < ALONG; ++s) {
-            o += s_o[s * LANES + lane];
-            l += s_l[s];
-        }
-    }
+    const int first = p0 / length;
+    return {first, p1 > p0 ? (p1 - 1) / length : first - 1, (long long)kv_head * a.p.rows + row,
+            (long long)a.c.heads * a.p.rows};
+}
+
+// A finished row's four values of a thread, and its log-sum-exp.
+template <int D, int DT>
+__device__ __forceinline__ void store_row(const Kv4AttnArgs& a, long long at, int lane, f32x4 o, float l, float safe) {
     o *= l != 0.0f ? 1.0f / l : 0.0f;
     uint32_t h[4];
 #pragma unroll
@@ -223,16 +180,105 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs a) {
     if (a.lse && lane == 0) a.lse[at] = l != 0.0f ? (safe + __builtin_amdgcn_logf(l)) * LN2 : -INFINITY;
 }
 
+// Joins the parts of few rows' units, writes zeros where no key is seen, and
+// leaves alone what is whole.  A work-group takes a row (token of a request,
+// head), which may have as many parts as there are lines: D / 4 threads side by
+// side, and as many such sets as there are, each every so many parts.
+template <int D, int DT>
+__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs a) {
+    constexpr int LANES = D / 4, SETS = 256 / LANES;
+    __shared__ f32x4 s_o[256];
+    __shared__ float s_l[SETS];
+    const int own = a.requests * a.max_query * a.heads;   // the groups behind these take the tokens of no request
+    if ((int)blockIdx.x >= own) {
+        clear_rest(a, blockIdx.x - own, gridDim.x - own);
+        return;
+    }
+    const int lane = threadIdx.x % LANES, set = threadIdx.x / LANES;
+    const int head = blockIdx.x % a.heads, t = blockIdx.x / a.heads, req = t / a.max_query, i = t - req * a.max_query;
+    const int start = max(a.offsets[req], 0);
+    if (i >= a.offsets[req + 1] - start || start + i >= a.tokens) return;
+    const int row = i * a.each + head % a.each, tile = row / a.p.rows;
+    const Parts parts = parts_of(a, req * a.p.tiles + a.p.tiles - 1 - tile, head / a.each, row - tile * a.p.rows);
+    if (parts.first == parts.last) return;
+    const f32x2* stat = reinterpret_cast<const f32x2*>(a.stat);
+    // the largest maximum first: the sets' sums then just add
+    float m = -INFINITY, l = 0.0f;
+    for (int w = parts.first + (int)(threadIdx.x & 63); w <= parts.last; w += 64) m = fmaxf(m, stat[parts.place(w)][0]);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    const float safe = m > -INFINITY ? m : 0.0f;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int w = parts.first + set; w <= parts.last; w += SETS) {
+        const long long p = parts.place(w);
+        const f32x2 st = stat[p];
+        const float f = __builtin_amdgcn_exp2f(st[0] - safe);
+        l += st[1] * f;
+        o += *reinterpret_cast<const f32x4*>(a.part + p * D + 4 * lane) * f;
+    }
+    s_o[threadIdx.x] = o;
+    if (lane == 0) s_l[set] = l;
+    __syncthreads();
+    if (set) return;
+#pragma unroll
+    for (int s = 1; s < SETS; ++s) {
+        o += s_o[s * LANES + lane];
+        l += s_l[s];
+    }
+    store_row<D, DT>(a, ((long long)start + i) * a.heads + head, lane, o, l, safe);
+}
+
+// The same for the many rows of a prompt's units, which have few parts: a
+// work-group takes JOIN_ROWS rows of a unit, so that one look tells it that they
+// are whole.
+constexpr int JOIN_ROWS = 32;
+template <int D, int DT>
+__global__ __launch_bounds__(256) void kv4_join_prompt_kernel(Kv4AttnArgs a) {
+    constexpr int LANES = D / 4, ABREAST = 256 / LANES;
+    const int slices = a.p.rows / JOIN_ROWS, own = a.requests * a.p.tiles * a.c.heads * slices;
+    if ((int)blockIdx.x >= own) {
+        clear_rest(a, blockIdx.x - own, gridDim.x - own);
+        return;
+    }
+    const int slice = blockIdx.x % slices, kv_head = blockIdx.x / slices % a.c.heads;
+    const int v = blockIdx.x / slices / a.c.heads, req = v / a.p.tiles;
+    const int tile = a.p.tiles - 1 - (v - req * a.p.tiles), lane = threadIdx.x % LANES;
+    const int start = max(a.offsets[req], 0);
+    const int count = min(min(a.offsets[req + 1], a.tokens) - start, a.max_query);
+    const int rows = min(count * a.each - tile * a.p.rows, a.p.rows);
+    Parts parts = parts_of(a, v, kv_head, 0);
+    if (parts.first == parts.last) return;
+    const f32x2* stat = reinterpret_cast<const f32x2*>(a.stat);
+    const long long row0 = parts.row;
+#pragma unroll 4
+    for (int r = slice * JOIN_ROWS + threadIdx.x / LANES; r < min(rows, (slice + 1) * JOIN_ROWS); r += ABREAST) {
+        parts.row = row0 + r;
+        float m = -INFINITY, l = 0.0f;
+        for (int w = parts.first; w <= parts.last; ++w) m = fmaxf(m, stat[parts.place(w)][0]);
+        const float safe = m > -INFINITY ? m : 0.0f;
+        f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int w = parts.first; w <= parts.last; ++w) {
+            const long long p = parts.place(w);
+            const f32x2 st = stat[p];
+            const float f = __builtin_amdgcn_exp2f(st[0] - safe);
+            l += st[1] * f;
+            o += *reinterpret_cast<const f32x4*>(a.part + p * D + 4 * lane) * f;
+        }
+        const int row = tile * a.p.rows + r, i = row / a.each;
+        store_row<D, DT>(a, ((long long)start + i) * a.heads + kv_head * a.each + row - i * a.each, lane, o, l, safe);
+    }
+}
+
 template <int D, int DT>
 hipError_t launch_join(const Kv4AttnArgs& a, hipStream_t st) {
-    constexpr int ALONG = 256 / (D / 4);
-    const long long rows = (long long)a.requests * a.max_query * a.heads;
     const long long rest = 1 + ((long long)a.tokens * a.heads * (D / 8) >> 12);   // 16 stores a thread
     const unsigned behind = (unsigned)(rest < 64 ? rest : 64);
     if (a.p.rows > 16)
-        kv4_join_kernel<D, DT, 1><<<(unsigned)((rows + ALONG - 1) / ALONG) + behind, 256, 0, st>>>(a);
+        kv4_join_prompt_kernel<D, DT><<<(unsigned)(a.requests * a.p.tiles * a.c.heads * (a.p.rows / JOIN_ROWS)) + behind,
+                                        256, 0, st>>>(a);
     else
-        kv4_join_kernel<D, DT, ALONG><<<(unsigned)rows + behind, 256, 0, st>>>(a);
+        kv4_join_kernel<D, DT><<<(unsigned)(a.requests * a.max_query * a.heads) + behind, 256, 0, st>>>(a);
     return hipGetLastError();
 }
 
