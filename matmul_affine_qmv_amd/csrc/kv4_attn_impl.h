@@ -16,13 +16,17 @@
 //   S = sum_g s_tg (sum_{d in g} q_d c_td) + b_tg (sum_{d in g} q_d)
 //   O = sum_t (p_t s_tg) c_td + sum_t p_t b_tg
 //
-// Codes enter the products as OFF + c, an exponent set above the four bits, and
-// the offsets are taken off in 32 bits: K's through b, V's through the sum of
-// the rounded p_t s_tg, in the same step as sum_t p_t b_tg.  V's bias is moved to
-// the middle of the codes (b + 8 s), so the two sums do not cancel.  K's codes
-// are exact and S is as exact as its 32-bit sums; the one rounding to 16 bits is
-// that of p_t s_tg (half a step: 2^-8 of it in bfloat16, 2^-11 in float16), which
-// the matrix cores need.
+// K's codes enter the product as the bits of the float16 numbers c 2^-18, queries
+// as float16 brought under 2^15 by a power of two a row (exact, but for what is
+// under 2^-29 of the row's largest and keeps 2^-40 of it), so S is as exact as its
+// 32-bit sums.  With K's codes as OFF + c the offset, up to 128 times the codes'
+// share, cost the row sums 3 to 5 bits (error of the logarithm of the sum 4e-8
+// now) and the same time.  V's codes enter as OFF + c in the cache's type, an
+// exponent set above the four bits, and the offset is taken off in 32 bits
+// through the sum of the rounded p_t s_tg, in the same step as sum_t p_t b_tg; the
+// bias is moved to the middle of the codes (b + 8 s), so the two sums do not
+// cancel.  The one rounding to 16 bits is that of p_t s_tg (half a step: 2^-8 of
+// it in bfloat16, 2^-11 in float16), which the matrix cores need.
 //
 // A work-group of WK waves takes a unit (kv4.h); the waves take every WK-th step
 // and are joined in LDS.  The running maximum is raised only when a score passes
@@ -103,6 +107,16 @@ struct Half<DT_F16> {
     }
 };
 
+__device__ __forceinline__ f16x2 half2_of(float lo, float hi) {
+    const f32x2 v = {lo, hi};
+    return __builtin_convertvector(v, f16x2);
+}
+
+// Codes at bits 4f of both halves, as float16 c 2^-18.
+__device__ __forceinline__ uint32_t tiny_codes(uint32_t w, int f) {
+    return (f < 2 ? w << (6 - 4 * f) : w >> (4 * f - 6)) & 0x03c003c0u;
+}
+
 // Sum over the four lanes that hold one row.
 __device__ __forceinline__ float row_sum(float v) {
     v += __shfl_xor(v, 16, 64);
@@ -130,8 +144,8 @@ __device__ __forceinline__ float row_lane(float v, int k) {
 
 // The (scale, bias) pairs of a block's tokens.  The 16 lanes of a row all need
 // the 4 * G pairs of the row's four tokens, keys' and values': each lane holds
-// its share, as numbers, and row_lane passes them round.  The biases are set
-// right for the codes' offset: keys' b - OFF s, values' b + 8 s.
+// its share, as numbers, and row_lane passes them round.  They are set right for
+// the codes: keys' 8 s, values' b + 8 s.
 template <int DT, int G>
 struct Pairs {
     static constexpr int PAIRS = (8 * G + 15) / 16;
@@ -139,9 +153,10 @@ struct Pairs {
     __device__ __forceinline__ void set(const uint32_t (&w)[PAIRS]) {
 #pragma unroll
         for (int r = 0; r < PAIRS; ++r) {
-            const float shift = ((16 * r + (int)(threadIdx.x & 15)) & (4 * G)) ? 8.0f : -Half<DT>::OFF;
-            s[r] = half_lo<DT>(w[r]);
-            b[r] = fmaf(shift, s[r], half_hi<DT>(w[r]));
+            const bool value = (16 * r + (int)(threadIdx.x & 15)) & (4 * G);
+            const float x = half_lo<DT>(w[r]);
+            s[r] = value ? x : x * 8.0f;
+            b[r] = fmaf(value ? 8.0f : 0.0f, x, half_hi<DT>(w[r]));
         }
     }
     __device__ __forceinline__ float scale(bool value, int i, int g) const {
@@ -175,8 +190,8 @@ template <int D, int GS, int DT>
 struct Rows {
     static constexpr int NJ = D / 32, G = D / GS, NB = D / 16;
     using H = Half<DT>;
-    u32x4 q[NJ];
-    float qsum[G];
+    u32x4 q[NJ];       // float16, over the row's power of two, times 2^15
+    float qsum[G];     // over the row's power of two
     float m, top, l;   // the maximum taken off (0 at first), what a score may reach, the sum
     float fix[G];      // sum p b + the offsets of V's codes, this lane's tokens
     f32x4 o[NB];
@@ -220,8 +235,8 @@ struct Rows {
 #pragma unroll
                 for (int j = g * (GS / 32); j < (g + 1) * (GS / 32); ++j) {
                     const uint32_t w = k[blk][j];
-                    const u32x4 a = {H::codes(w, 0), H::codes(w, 1), H::codes(w, 2), H::codes(w, 3)};
-                    part = H::mfma(a, q[j], part);
+                    const u32x4 a = {tiny_codes(w, 0), tiny_codes(w, 1), tiny_codes(w, 2), tiny_codes(w, 3)};
+                    part = Half<DT_F16>::mfma(a, q[j], part);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -354,7 +369,6 @@ __global__ __launch_bounds__(64 * WK, 2) void kv4_attn_kernel(Kv4AttnArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
     const Kv4View& c = a.c;
-    const float scale = a.scale_log2;
     const int head = blockIdx.x % c.heads;
 
     Units<64 * WK> units(a, blockIdx.x / c.heads, head);
@@ -380,13 +394,27 @@ __global__ __launch_bounds__(64 * WK, 2) void kv4_attn_kernel(Kv4AttnArgs a) {
                     x.q[j][e] = (uint32_t)q[32 * j + 2 * e] | ((uint32_t)q[32 * j + 2 * e + 1] << 16);
             }
         }
+        float most = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                most = fmaxf(most, fmaxf(fabsf(half_lo<DT>(x.q[j][e])), fabsf(half_hi<DT>(x.q[j][e]))));
+        const int exponent = min(__builtin_amdgcn_frexp_expf(row_max(most)), 127);
+        const float scale = ldexpf(a.scale_log2, exponent);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             float sum = 0.0f;
 #pragma unroll
-            for (int j = g * (GS / 32); j < (g + 1) * (GS / 32); ++j)
+            for (int j = g * (GS / 32); j < (g + 1) * (GS / 32); ++j) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sum += half_lo<DT>(x.q[j][e]) + half_hi<DT>(x.q[j][e]);
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t w = x.q[j][e];
+                    const float lo = ldexpf(half_lo<DT>(w), -exponent), hi = ldexpf(half_hi<DT>(w), -exponent);
+                    sum += lo + hi;
+                    x.q[j][e] = __builtin_bit_cast(uint32_t, half2_of(lo * 0x1p15f, hi * 0x1p15f));
+                }
+            }
             x.qsum[g] = row_sum(sum);
         }
         Pages pages{a.table + u.req * a.table_stride, min((u.end + 15) >> 4, a.columns << c.page_shift), {-1, -1}};

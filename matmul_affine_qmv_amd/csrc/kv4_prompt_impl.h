@@ -65,16 +65,6 @@ __device__ __forceinline__ f32x16 mfma32_type(u32x4 a, u32x4 b, f32x16 c) {
                                                    0, 0);
 }
 
-__device__ __forceinline__ f16x2 half2_of(float lo, float hi) {
-    const f32x2 v = {lo, hi};
-    return __builtin_convertvector(v, f16x2);
-}
-
-// Codes at bits 4f of both halves, as float16 c 2^-18.
-__device__ __forceinline__ uint32_t tiny_codes(uint32_t w, int f) {
-    return (f < 2 ? w << (6 - 4 * f) : w >> (4 * f - 6)) & 0x03c003c0u;
-}
-
 constexpr int PROMPT_WAVES = 8, PROMPT_ROWS = 256;
 
 // Products and reads of LDS stay in the order of the source, so that operands
