@@ -38,7 +38,7 @@
 // groups of 128, float16) 37 us and 5 us for joining the parts, 143 MB at 3.4 TB/s
 // (a large copy: 4.9); bound by what is in flight, two waves a SIMD with 4.6 KB
 // each (three, where registers allow: 34 + 6 us).  48 tokens over up to 8000
-// (40 heads, bfloat16) 26 + 5 us for 64 MB: half of it is the wait for lengths, block
+// (40 heads, bfloat16) 27 + 5 us for 64 MB: half of it is the wait for lengths, block
 // table, queries and first codes, one after the other.  Cut by splits of one
 // length for all requests, as the host alone could do it, they took 55 + 14 and
 // 40 + 4 us.  Pairs read by every lane that needs them instead of shared by a row

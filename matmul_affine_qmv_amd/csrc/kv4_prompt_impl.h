@@ -11,7 +11,7 @@
 // stand among the products for the scores of the next 32.
 //
 // Measured: a prompt of 8192 tokens, 32 heads of 128 on 8 key heads, groups of 64,
-// bfloat16: 659 us in a warm loop, 835 TFLOP/s, where a library matrix product
+// bfloat16: 651 us in a warm loop, 845 TFLOP/s, where a library matrix product
 // reaches 1209.  The matrix cores are busy 37 % of the cycles and the vector ALU
 // 55 %, 15 % both at once: a barrier a tile holds the waves together, and they do
 // the same things at the same time.  Setting half the waves half a tile off, or a
