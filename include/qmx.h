@@ -439,7 +439,7 @@ int qmx_kv4_read(const qmx_kv4_cache* cache, void* k_out, void* v_out, const int
  * only the last `window` of them; a position whose block_table entry is
  * outside 0..num_pages - 1, or past max_kv_len, is not seen.  Head a reads key
  * head a / (heads / kv_heads).  A token that sees nothing, or belongs to no
- * request, gets zeros.  What is not seen may hold anything, NaN included.
+ * request (before the first offset or from the last on), gets zeros.  What is not seen may hold anything, NaN included.
  *   q     : [tokens, heads, head_dim], unit element stride, other strides in
  *           elements; out: contiguous, 16-byte aligned; both in the cache's
  *           dtype.

@@ -56,17 +56,20 @@ __device__ __forceinline__ Unit unit_of(const Kv4AttnArgs& a, int v) {
     return u;
 }
 
-// Zeros for the tokens of no request: group `id` of `of`, THREADS threads.
+// Zeros for the tokens of no request, before the first offset and from the last
+// on: group `id` of `of`.
 __device__ __forceinline__ void clear_rest(const Kv4AttnArgs& a, int id, int of) {
-    const int begin = max(a.offsets[a.requests], 0);
-    const int per = a.heads * (a.c.dim / 8);
-    const long long all = max(0, a.tokens - begin) * (long long)per;
-    for (long long i = (long long)id * blockDim.x + threadIdx.x; i < all; i += (long long)of * blockDim.x)
-        reinterpret_cast<u32x4*>(a.out)[(long long)begin * per + i] = u32x4{0, 0, 0, 0};
-    if (a.lse)
-        for (long long i = (long long)begin * a.heads + (long long)id * blockDim.x + threadIdx.x;
-             i < (long long)a.tokens * a.heads; i += (long long)of * blockDim.x)
-            a.lse[i] = -INFINITY;
+    const long long thread = (long long)id * blockDim.x + threadIdx.x, threads = (long long)of * blockDim.x;
+    const int first = min(max(a.offsets[0], 0), a.tokens), begin = max(a.offsets[a.requests], 0);
+    auto clear = [&](long long from, long long to) {
+        const int per = a.heads * (a.c.dim / 8);
+        for (long long i = from * per + thread; i < to * per; i += threads)
+            reinterpret_cast<u32x4*>(a.out)[i] = u32x4{0, 0, 0, 0};
+        if (a.lse)
+            for (long long i = from * a.heads + thread; i < to * a.heads; i += threads) a.lse[i] = -INFINITY;
+    };
+    clear(0, first);
+    clear(begin, a.tokens);
 }
 
 // The units of work-group `id` of a head, one after the other.

@@ -1,0 +1,144 @@
+"""The paged 4-bit key/value cache where types, lengths and arguments end: tokens of no request at either end,
+subnormal groups, long tails, magnitudes far apart, and arguments that the entries refuse.
+
+Bounds.  ``u`` is half a step of the type, 2^-24 that of float32.  For a token, with p its keys' probabilities:
+
+* the output's rounding, u |out| (and half a subnormal step);
+* few rows: p s enters the product with its code, taken about the middle of the codes, in ``pieces`` numbers of the
+  cache's type or bfloat16, so it is off by ``held`` of itself;
+* many rows: values and probabilities are float16, 2^-11 each; values also to 2^-18 of their token's largest, and a
+  probability times a value to 2^-26 of the largest value that the token sees, for each key (the sum of exponentials
+  is at least 1 of them);
+* 32-bit sums, every product rounded and added at most ``steps`` times;
+* key t's score is off by E_t, D products on 32-bit sums and the exponent's argument (many rows: and 2^-31 of the
+  largest elements), which moves the output by sum p_t expm1(2 E_t) |v_t - out| at most.
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import kv4_reference as ref
+import matmul_affine_qmv_amd as qmx
+from test_kv4 import DEV, FAKE, ccache, device_cache, fake_ptr_test, ints, on_gpu, say
+
+U32 = ref.U32
+
+
+def expected(c, q, table, kv, offsets, window=0, scale=None, prompt=False, held=2.0 ** -16):
+    """(out, lse, bound of out, bound of lse) in float64 of q [T, heads, D] (torch, on the CPU)."""
+    T, heads, D = q.shape
+    each, scale = heads // c.heads, D ** -0.5 if scale is None else scale
+    u, q = ref.HALF[c.type], q.double().numpy()
+    out, lse = np.zeros((T, heads, D)), np.full((T, heads), -np.inf)
+    tol, ltol = np.zeros((T, heads, D)), np.zeros((T, heads))
+    rep = lambda a: np.repeat(a, c.group, -1)  # noqa: E731
+    for r, length in enumerate(kv):
+        n = offsets[r + 1] - offsets[r]
+        pages = [int(x) for x in table[r]]
+        ok = np.repeat([0 <= x < c.pages for x in pages], c.page)[:length]
+        got = [x if 0 <= x < c.pages else 0 for x in pages]
+        for a in range(heads):
+            flat = lambda x: x[got, a // each].reshape(-1, x.shape[-1])[:length]  # noqa: E731
+            ks, kb, vs, vb = (rep(flat(x[i])) for i in (0, 1) for x in (c.s, c.b))
+            kc, vc = flat(c.codes[0]), flat(c.codes[1])
+            for i in range(n):
+                t, pos, key = offsets[r] + i, length - n + i, np.arange(len(ok))
+                see = ok & (key <= pos) & (key > (pos - window if window else -1))
+                if not see.any():
+                    continue
+                x, v = q[t, a], vc[see] * vs[see] + vb[see]
+                s = (kc[see] * ks[see] + kb[see]) @ x * scale
+                size = 16 * ks[see] + np.abs(kb[see])
+                p = np.exp(s - s.max())
+                total = p.sum()
+                p /= total
+                out[t, a], lse[t, a] = p @ v, s.max() + np.log(total)
+                E = (D + 8) * U32 * scale * (size @ np.abs(x)) + 8 * U32 * (np.abs(s) + np.abs(s.max()) + 1)
+                if prompt:
+                    E += 2.0 ** -31 * scale * (np.abs(x).max() * size.sum(-1) + np.abs(x).sum() * size.max(-1))
+                eps = np.where(p > 0, np.expm1(2 * np.minimum(E, 10)), 0)
+                steps = see.sum() / 32 + 64
+                if prompt:
+                    most = np.abs(vs[see] * 15 + vb[see]).max(-1, keepdims=True)
+                    most = np.maximum(most, np.abs(vb[see]).max(-1, keepdims=True))
+                    lost = 2.0 ** -10 * np.abs(v) + 2.0 ** -18 * most
+                    rounded = p @ lost + 2.0 ** -26 * most.max() * see.sum() / total
+                else:
+                    rounded = held * (p @ (vs[see] * np.abs(vc[see] - 8)))
+                tol[t, a] = (u * np.abs(out[t, a]) + (2.0 ** -25 if c.type == "f16" else 2.0 ** -134) + rounded
+                             + steps * U32 * (p @ (vs[see] * (ref.OFF + 23) + np.abs(vb[see])))
+                             + (p * eps) @ np.abs(v - out[t, a]) / max(1 - (p * eps).sum(), 0.01))
+                ltol[t, a] = (p * eps).sum() + steps * U32 + 2 * U32 * abs(lse[t, a])
+    return out, lse, tol, ltol
+
+
+def tables(lens, page):
+    """A block table that hands pages out in order, and the number of pages."""
+    need = [-(-x // page) for x in lens]
+    table, first = np.full((len(lens), max(1, max(need))), -1, dtype=np.int32), 0
+    for r, n in enumerate(need):
+        table[r, :n] = np.arange(first, first + n)
+        first += n
+    return table, first
+
+
+def held_to(c, q, table, kv, offsets, scale=None, window=0, **bound):
+    """A call's outputs against `expected`, which it has to meet and to repeat."""
+    each, n = q.shape[1] // c.heads, int(np.diff(offsets).max())
+    prompt = n * each > 64
+    for x in (*c.s, *c.b):
+        x[:] = torch.from_numpy(x).to(c.dtype).double().numpy()
+    args = (device_cache(c), q.to(DEV), torch.from_numpy(table).to(DEV), ints(kv), ints(offsets))
+    kw = dict(max_query_len=n, max_kv_len=max(kv), scale=scale, window=window)
+    out, lse = qmx.kv4_attention(*args, return_lse=True, **kw)
+    o, l, tol, ltol = expected(c, q, table, kv, offsets, window, scale, prompt, **bound)
+    got, got_lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.isfinite(got).all(), "not finite"
+    over = np.abs(got - o) - tol
+    assert (over <= 0).all(), (over.max(), tol.flat[over.argmax()], np.unravel_index(over.argmax(), over.shape))
+    none = np.isneginf(l)
+    assert np.array_equal(np.isneginf(got_lse), none)
+    assert (np.abs(got_lse[~none] - l[~none]) <= ltol[~none]).all(), np.abs(got_lse - l)[~none].max()
+    assert torch.equal(out, qmx.kv4_attention(*args, **kw)), "rerun not bit-identical"
+
+
+@on_gpu
+@pytest.mark.parametrize("new,past", [(1, 40), (2, 3000), (50, 10), (60, 3000)])
+@pytest.mark.parametrize("before,behind", [(3, 0), (2, 4)])
+def test_tokens_before_the_first_offset(new, past, before, behind):
+    """Tokens before query_offsets[0] belong to no request, as those behind the last: zeros, and -inf."""
+    say("before", new, past, before, behind)
+    rng = np.random.default_rng(30)
+    kv = [past + new, 20]
+    table, pages = tables(kv, 16)
+    cache = device_cache(ref.Cache(pages, 2, 64, 16, 32, "bf16", rng))
+    T = before + 2 * new + behind
+    q = torch.from_numpy(rng.normal(0, 1, (T, 4, 64))).bfloat16().to(DEV)
+    table = torch.from_numpy(table).to(DEV)
+    kw = dict(max_query_len=new, max_kv_len=max(kv), return_lse=True)
+    want, want_lse = qmx.kv4_attention(cache, q[before:], table, ints(kv), ints([0, new, 2 * new]), **kw)
+    left = torch.full((T, 4), 7.0, device=DEV)   # what lse's memory may hold
+    del left
+    out, lse = qmx.kv4_attention(cache, q, table, ints(kv), ints([before, before + new, before + 2 * new]),
+                                 out=torch.full_like(q, 7.0), **kw)
+    assert torch.equal(out[before:], want) and torch.equal(lse[before:], want_lse)
+    assert not out[:before].any() and torch.isneginf(lse[:before]).all()
+
+
+@on_gpu
+@pytest.mark.parametrize("first", [0, 2, 9])
+def test_no_requests_and_a_first_offset(first):
+    """No request, or a first offset behind all tokens: nothing but zeros."""
+    say("no requests", first)
+    cache = qmx.Kv4Cache.zeros(2, 1, 64, page_size=16, group_size=32, device=DEV)
+    q = torch.ones(5, 2, 64, dtype=torch.bfloat16, device=DEV)
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    out = qmx.kv4_attention(cache, q, torch.zeros(0, 1, dtype=torch.int32, device=DEV), none, ints([first]),
+                            max_query_len=1, max_kv_len=16, out=torch.full_like(q, 7.0))
+    assert not out.any()
+    out = qmx.kv4_attention(cache, q, ints([[0]]), ints([3]), ints([first + 5, first + 6]), max_query_len=1,
+                            max_kv_len=16, out=torch.full_like(q, 7.0))
+    assert not out.any()
