@@ -109,8 +109,9 @@ __global__ __launch_bounds__(THREADS) void kv_maps_kernel(KvMapsArgs a, int per_
         if (r0 + chunk < a.requests) read(r0 + chunk);
         __syncthreads();
         const int stop = s_end[count - 1];
-        for (int t = max(t0, begin) + tid; t < min(t1, stop); t += THREADS) {
-            const int r = first_after(s_end, count, t);
+        // unsigned: a step may pass 2^31 - 1
+        for (uint32_t i = (uint32_t)max(t0, begin) + tid; i < (uint32_t)min(t1, stop); i += THREADS) {
+            const int t = (int)i, r = first_after(s_end, count, t);
             const int start = r ? s_end[r - 1] : begin;
             const uint32_t before = (uint32_t)s_past[r], at = before + (uint32_t)(t - start);
             const uint32_t col = page.whole(at), held = min(page.count(before), (uint32_t)a.columns);
@@ -142,7 +143,7 @@ __global__ __launch_bounds__(THREADS) void kv_maps_kernel(KvMapsArgs a, int per_
         pages += chunk_pages;
         __syncthreads();
     }
-    for (int t = max(t0, min(sum, a.tokens)) + tid; t < t1; t += THREADS) {
+    for (uint32_t t = (uint32_t)max(t0, min(sum, a.tokens)) + tid; t < (uint32_t)t1; t += THREADS) {
         a.slots[t] = -1;
         a.positions[t] = -1;
         a.request_ids[t] = -1;

@@ -142,3 +142,27 @@ def test_no_requests_and_a_first_offset(first):
     out = qmx.kv4_attention(cache, q, ints([[0]]), ints([3]), ints([first + 5, first + 6]), max_query_len=1,
                             max_kv_len=16, out=torch.full_like(q, 7.0))
     assert not out.any()
+
+
+@on_gpu
+def test_maps_of_all_the_tokens_that_an_int_counts():
+    """Room for 2^31 - 1 tokens: the last step of a group's walk passes that number."""
+    T = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    say("maps of 2^31 - 1 tokens")
+    got = qmx.kv_maps(ints([0, 5]), ints([100, T - 150]), ints([[0, -1], [1, 2]]), ints([7]), page_size=64, tokens=T)
+    assert got.query_offsets.tolist() == [0, 100, T - 50] and got.kv_lens.tolist() == [100, T - 145]
+    assert got.counts.tolist() == [T - 50, 3]
+    step = 1 << 28
+    for begin in range(0, T, step):
+        t = torch.arange(begin, min(T, begin + step), dtype=torch.int32, device=DEV)
+        part = slice(begin, begin + t.numel())
+        behind, second = t >= T - 50, t >= 100
+        ids = second.int().masked_fill_(behind, -1)
+        assert torch.equal(got.request_ids[part], ids)
+        at = torch.where(second, t - 95, t).masked_fill_(behind, -1)
+        assert torch.equal(got.positions[part], at)
+        slot = torch.where(second, at.clamp(max=64) + 64, at.clamp(max=64) + 7 * 64)   # each request has one page
+        slot = slot.masked_fill_((at >= 64) | behind, -1)
+        assert torch.equal(got.slots[part], slot)
