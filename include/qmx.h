@@ -69,7 +69,8 @@ typedef enum qmx_status {
     QMX_ERR_SPLITS = -8,     /* split count out of range for this K                */
     QMX_ERR_LAUNCH = -9,     /* the HIP runtime rejected a launch                  */
     QMX_ERR_DEVICE = -10,    /* no usable HIP device                               */
-    QMX_ERR_SCRATCH = -11    /* partials larger than qmx_qmm_t_splitk_noalloc holds */
+    QMX_ERR_SCRATCH = -11,   /* partials larger than qmx_qmm_t_splitk_noalloc holds */
+    QMX_ERR_OVERLAP = -12    /* an output overlaps an input or another output      */
 } qmx_status;
 
 typedef enum qmx_route {
@@ -407,7 +408,11 @@ typedef struct qmx_kv4_cache {
  *       token;
  *   counts [2] : the sum of fresh, and the pages wanted (a caller sees here
  *       that `tokens` or num_free was too small).
- * page_size: any size of at least 1.  requests * columns is at most 2^31 - 1. */
+ * page_size: any size of at least 1.  requests * columns is at most 2^31 - 1.
+ * Groups of the launch read the lengths while others write: no output may
+ * overlap past, fresh, free_pages, the table's rows or another output, nor the
+ * rows an input (QMX_ERR_OVERLAP; kv_lens are not the next step's past in
+ * place). */
 int qmx_kv_maps(const int32_t* past, const int32_t* fresh, int32_t* block_table,
                 const int32_t* free_pages, int requests, int columns, long long table_stride,
                 int num_free, int page_size, int tokens, int32_t* query_offsets, int32_t* kv_lens,

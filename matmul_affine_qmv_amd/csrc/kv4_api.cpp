@@ -43,6 +43,23 @@ qmx::Kv4View view(const qmx_kv4_cache* c) {
             c->num_pages, c->kv_heads, c->head_dim, shift, c->group_size, c->dtype};
 }
 
+// Where the ints of an argument are: `n` of them, `rows` times, `stride` apart.
+struct Span {
+    const int32_t* p;
+    long long n, rows = 1, stride = 0;
+};
+
+// Whether `x`, of one row, shares an int with `y`.
+bool overlap(const Span& x, const Span& y) {
+    if (x.n <= 0 || y.n <= 0 || y.rows <= 0) return false;
+    typedef __int128 wide;   // rows may be any distance apart
+    const wide row = 4 * (wide)y.n, step = 4 * (wide)y.stride, to = 4 * (wide)x.n;
+    const wide from = (wide)reinterpret_cast<uintptr_t>(x.p) - reinterpret_cast<uintptr_t>(y.p);
+    if (from + to <= 0 || from >= (y.rows - 1) * step + row) return false;
+    if (from < row) return true;
+    return ((from - row) / step + 1) * step < from + to;   // the first row that ends behind x's start
+}
+
 bool good_heads(int heads, int kv_heads) {
     return kv_heads >= 1 && kv_heads <= 1024 && heads >= kv_heads && heads <= 65536 && heads % kv_heads == 0;
 }
@@ -119,6 +136,19 @@ int qmx_kv_maps(const int32_t* past, const int32_t* fresh, int32_t* block_table,
                           (const void*)query_offsets, (const void*)kv_lens, (const void*)slots,
                           (const void*)positions, (const void*)request_ids, (const void*)counts})
         if (!is_aligned(p, 4)) return QMX_ERR_ALIGN;
+    const Span table = {block_table, columns, requests, table_stride};
+    const Span in[] = {{past, requests}, {fresh, requests}, {free_pages, num_free}};
+    const Span out[] = {{query_offsets, requests + 1}, {kv_lens, requests}, {slots, tokens},
+                        {positions, tokens}, {request_ids, tokens}, {counts, 2}};
+    for (const Span& x : in)
+        if (overlap(x, table)) return QMX_ERR_OVERLAP;
+    for (const Span& x : out) {
+        if (overlap(x, table)) return QMX_ERR_OVERLAP;
+        for (const Span& y : in)
+            if (overlap(x, y)) return QMX_ERR_OVERLAP;
+        for (const Span& y : out)
+            if (&x != &y && overlap(x, y)) return QMX_ERR_OVERLAP;
+    }
     const qmx::KvMapsArgs a = {past, fresh, block_table, free_pages, table_stride, requests, columns, num_free,
                                page_size, tokens, query_offsets, kv_lens, slots, positions, request_ids, counts};
     return launch_status(qmx::launch_kv_maps(a, static_cast<hipStream_t>(stream)));

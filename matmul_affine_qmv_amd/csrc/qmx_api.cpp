@@ -304,6 +304,7 @@ const char* qmx_strerror(int status) {
         case QMX_ERR_LAUNCH: return "the HIP runtime rejected a kernel launch";
         case QMX_ERR_DEVICE: return "no usable HIP device";
         case QMX_ERR_SCRATCH: return "split-K partials exceed the scratch array of qmx_qmm_t_splitk_noalloc";
+        case QMX_ERR_OVERLAP: return "an output overlaps an input or another output";
         default: return "unknown status";
     }
 }

@@ -141,7 +141,8 @@ def kv_maps(past, new, block_table, free_pages, *, page_size, tokens=None, out=N
     past, new: int32 [R]; block_table: int32 [R, columns]; free_pages: int32
     [F], handed out from its front.  tokens: the room for new tokens, when no
     `out` (a KvMaps to write into) gives it.  counts[1] of the result is how
-    many of free_pages were wanted."""
+    many of free_pages were wanted.  Outputs share no memory with the inputs:
+    the next step's past is a copy of kv_lens, or past + new in place."""
     if not past.is_cuda:
         raise ValueError("all tensors must be on a HIP device")
     index, R = past.get_device(), past.numel()

@@ -166,3 +166,54 @@ def test_maps_of_all_the_tokens_that_an_int_counts():
         slot = torch.where(second, at.clamp(max=64) + 64, at.clamp(max=64) + 7 * 64)   # each request has one page
         slot = slot.masked_fill_((at >= 64) | behind, -1)
         assert torch.equal(got.slots[part], slot)
+
+
+EOVERLAP, ELAUNCH = -12, -9
+
+
+def maps_status(at, R=3, columns=4, stride=7, nfree=5, T=8):
+    """qmx_kv_maps on placeholder pointers, by the first int of each argument."""
+    place = dict(past=0, fresh=100, table=200, free=300, query_offsets=400, kv_lens=500, slots=600, positions=700,
+                 request_ids=800, counts=900)
+    place.update(at)
+    p = {k: FAKE + 4 * v for k, v in place.items()}
+    return qmx.lib().qmx_kv_maps(p["past"], p["fresh"], p["table"], p["free"], R, columns, stride, nfree, 16, T,
+                                 p["query_offsets"], p["kv_lens"], p["slots"], p["positions"], p["request_ids"],
+                                 p["counts"], None)
+
+
+@fake_ptr_test
+def test_maps_refuse_outputs_over_inputs():
+    """The launch's groups read the lengths while one of them writes: kv_lens as the next step's past, in place, gave
+    slots that depended on which came first."""
+    assert maps_status({}) != EOVERLAP                                    # no device here: the launch fails
+    for bad in (dict(past=500), dict(past=502), dict(past=498), dict(fresh=500), dict(free=402), dict(past=599),
+                dict(past=607), dict(free=901), dict(counts=304), dict(slots=701), dict(request_ids=705),
+                dict(positions=593), dict(kv_lens=403), dict(kv_lens=200), dict(kv_lens=203), dict(kv_lens=206),
+                dict(kv_lens=217), dict(slots=193), dict(past=214), dict(free=199), dict(counts=206),
+                dict(fresh=215)):
+        assert maps_status(bad) == EOVERLAP, bad
+    # inputs may share memory; what stands beside, between the table's rows, or behind its last row does not overlap
+    for good in (dict(past=100), dict(past=301), dict(kv_lens=404), dict(kv_lens=204), dict(past=211), dict(past=218),
+                 dict(past=197), dict(slots=192), dict(counts=204), dict(counts=198)):
+        assert maps_status(good) == ELAUNCH, good
+    assert maps_status(dict(kv_lens=200), columns=0) == ELAUNCH
+    assert maps_status(dict(kv_lens=201), R=1, stride=0) == EOVERLAP
+    assert maps_status(dict(kv_lens=204), R=1, stride=0) == ELAUNCH
+    assert maps_status({}, stride=2 ** 62) == ELAUNCH and maps_status(dict(past=199), stride=2 ** 62) == EOVERLAP
+    assert "overlaps" in qmx.strerror(EOVERLAP)
+
+
+@on_gpu
+def test_binding_refuses_outputs_over_inputs():
+    """The lengths that a step wrote, given back to the same KvMaps as the next step's past."""
+    say("maps over their inputs")
+    table, free, one = ints([[0, -1], [1, -1]]), ints([2, 3]), ints([1, 1])
+    maps = qmx.kv_maps(ints([15, 3]), one, table, free, page_size=16, tokens=2)
+    with pytest.raises(qmx.QmxError, match="overlaps"):
+        qmx.kv_maps(maps.kv_lens, one, table, free, page_size=16, out=maps)
+    with pytest.raises(qmx.QmxError, match="overlaps"):
+        qmx.kv_maps(one, one, maps.slots.view(2, 1), free, page_size=16, out=maps)
+    assert maps.kv_lens.tolist() == [16, 4] and table.tolist() == [[0, -1], [1, -1]]
+    maps = qmx.kv_maps(maps.kv_lens.clone(), one, table, free, page_size=16, out=maps)
+    assert maps.kv_lens.tolist() == [17, 5] and maps.slots.tolist() == [32, 20]
