@@ -452,7 +452,8 @@ int qmx_kv4_read(const qmx_kv4_cache* cache, void* k_out, void* v_out, const int
  *           scaled scores (-inf where nothing is seen).
  *   max_query_len, max_kv_len : at least the longest request's new and cached
  *           tokens (host numbers: they size the launch; queries of a request
- *           past max_query_len are left unwritten).
+ *           past max_query_len are left unwritten); max_query_len is at most
+ *           `tokens`.
  *   scale : finite and above 0.
  *   workspace : qmx_kv4_attention_workspace_bytes bytes, 16-byte aligned (NULL
  *           where that is 0), overwritten; calls that share it are ordered.
@@ -470,8 +471,9 @@ int qmx_kv4_attention(const qmx_kv4_cache* cache, const void* q, long long q_tok
                       int max_query_len, int max_kv_len, int window, float scale, void* workspace,
                       size_t workspace_bytes, void* stream);
 
-/* Workspace bytes qmx_kv4_attention needs (0 for arguments it refuses).
- * Depends on the compute units of the current device. */
+/* Workspace bytes qmx_kv4_attention needs (0 for arguments it refuses; a
+ * max_query_len above `tokens`, which the call does not take, is taken as
+ * `tokens`).  Depends on the compute units of the current device. */
 size_t qmx_kv4_attention_workspace_bytes(int kv_heads, int head_dim, int requests, int tokens,
                                          int heads, int max_query_len, int max_kv_len, int window);
 

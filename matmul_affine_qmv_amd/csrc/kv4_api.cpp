@@ -184,7 +184,8 @@ size_t qmx_kv4_attention_workspace_bytes(int kv_heads, int head_dim, int request
     if (!good_heads(heads, kv_heads) || (head_dim != 64 && head_dim != 128 && head_dim != 256) || requests < 0 ||
         tokens < 0 || max_query_len < 0 || max_kv_len < 0 || max_kv_len > INT_MAX - 64 || window < 0)
         return 0;
-    return qmx::kv4_attn_workspace(plan_for(requests, heads, kv_heads, head_dim, max_query_len, max_kv_len, window),
+    const int queries = std::min(max_query_len, tokens);
+    return qmx::kv4_attn_workspace(plan_for(requests, heads, kv_heads, head_dim, queries, max_kv_len, window),
                                    requests, kv_heads, head_dim);
 }
 

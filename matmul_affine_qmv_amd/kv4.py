@@ -217,7 +217,8 @@ def _workspace_bytes(device_index, *sizes):
 
 def kv4_attention_workspace_bytes(cache: Kv4Cache, requests, tokens, heads, max_query_len, max_kv_len,
                                   window=0) -> int:
-    """Bytes of workspace that kv4_attention needs for these sizes (a host rule)."""
+    """Bytes of workspace that kv4_attention needs for these sizes (a host rule);
+    as there, max_query_len may be above the number of tokens."""
     return _workspace_bytes(cache.device_index, cache.kv_heads, cache.head_dim, requests, tokens, heads,
                             max_query_len, max_kv_len, window)
 
@@ -229,9 +230,12 @@ def kv4_attention(cache: Kv4Cache, q, block_table, kv_lens, query_offsets, *, ma
 
     block_table: int32 [R, columns]; kv_lens: int32 [R]; query_offsets: int32
     [R + 1], request r's queries being the last of its kv_lens[r] tokens.
-    max_query_len, max_kv_len: host bounds of both.  window: 0, or how many
-    tokens a query sees, itself among them.  scale: above 0, head_dim ** -0.5 by
-    default.  Returns out, or (out, lse) with float32 lse [tokens, heads]."""
+    max_query_len, max_kv_len: host bounds of both; what a request has past them
+    is not computed: its later queries' outputs are left unwritten, its later
+    keys unseen.  window: 0, or how many tokens a query sees, itself among them.
+    scale: above 0, head_dim ** -0.5 by default.  workspace: of
+    kv4_attention_workspace_bytes bytes, where the caller keeps one.  Returns
+    out, or (out, lse) with float32 lse [tokens, heads]."""
     if q.dim() != 3 or q.shape[2] != cache.head_dim or q.shape[1] % cache.kv_heads or q.shape[1] < 1:
         raise ValueError(f"q must be [tokens, a multiple of {cache.kv_heads}, {cache.head_dim}]")
     if q.dtype is not cache.dtype:

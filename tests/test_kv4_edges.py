@@ -217,3 +217,41 @@ def test_binding_refuses_outputs_over_inputs():
     assert maps.kv_lens.tolist() == [16, 4] and table.tolist() == [[0, -1], [1, -1]]
     maps = qmx.kv_maps(maps.kv_lens.clone(), one, table, free, page_size=16, out=maps)
     assert maps.kv_lens.tolist() == [17, 5] and maps.slots.tolist() == [32, 20]
+
+
+SIZES = [(8, 128, 64, 64, 32, 4096, 8000, 0), (8, 128, 64, 64, 32, 512, 8192, 0), (2, 64, 3, 5, 4, 9, 4000, 0),
+         (4, 256, 1, 40, 16, 2048, 70000, 0), (1, 64, 20, 20, 8, 300, 9000, 2000)]
+
+
+@pytest.mark.parametrize("sizes", SIZES)
+def test_workspace_of_a_bound_above_the_tokens(sizes):
+    """kv4_attention takes no more queries a request than there are tokens; the size it is given has to be for that."""
+    bytes_ = qmx.lib().qmx_kv4_attention_workspace_bytes
+    kv_heads, dim, R, T, heads, most, kv, window = sizes
+    assert bytes_(*sizes) == bytes_(kv_heads, dim, R, T, heads, T, kv, window) > 0
+
+
+@on_gpu
+@pytest.mark.parametrize("each,D,most", [(4, 64, 512), (1, 128, 3), (2, 256, 2000)])
+@pytest.mark.parametrize("new", [1, 2, 40])
+def test_workspace_of_the_caller(each, D, most, new):
+    """A workspace of the size that kv4_attention_workspace_bytes says, with a bound of the queries above the tokens and
+    without, gives what the call's own gives; one byte less is refused."""
+    say("workspace", each, D, most, new)
+    rng = np.random.default_rng(33)
+    kv = [3000, 1700, 9]
+    table, pages = tables(kv, 64)
+    cache = device_cache(ref.Cache(pages, 2, D, 64, 64, "bf16", rng))
+    offsets = [0, new, 2 * new, 2 * new + 1]
+    T, heads = offsets[-1], 2 * each
+    q = torch.from_numpy(rng.normal(0, 1, (T, heads, D))).bfloat16().to(DEV)
+    args = (cache, q, torch.from_numpy(table).to(DEV), ints(kv), ints(offsets))
+    need = qmx.kv4_attention_workspace_bytes(cache, 3, T, heads, most, 3000)
+    assert need > 0
+    kw = dict(max_query_len=most, max_kv_len=3000)
+    want = qmx.kv4_attention(*args, **kw)
+    room = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    assert torch.equal(want, qmx.kv4_attention(*args, workspace=room, **kw))
+    assert torch.equal(want, qmx.kv4_attention(*args, workspace=room, **kw))   # over what the last call left there
+    with pytest.raises(qmx.QmxError, match="workspace"):
+        qmx.kv4_attention(*args, workspace=room[:need - 1], **kw)
