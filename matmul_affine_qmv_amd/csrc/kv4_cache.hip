@@ -51,10 +51,32 @@ __device__ __forceinline__ uint32_t group_scale(float lo, float hi) {
 // middle, so the remainder, which is exact, is held against s / 2 (just under it
 // where the number is odd: middles go to even).  x - b is exact in 32 bits unless
 // x, or b, has digits more than 24 places below the group's span: then the
-// lane's eight are done with remainders in 64 bits.
+// lane's eight are done with remainders in 64 bits.  UP: a power of two that
+// everything is multiplied by.
+template <int DT, class Up>
+__device__ __forceinline__ void codes_times(u32x4 w, float b, float s, bool deep, Up, uint32_t (&c)[8]) {
+    constexpr int MAGIC = 0x4b400000;
+    constexpr float UP = Up::value ? 0x1p100f : 1.0f;
+    b *= UP;
+    s *= UP;
+    const float inv = __builtin_amdgcn_rcpf(s), half = 0.5f * s;
+    const float magic = __int_as_float(MAGIC);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float x = UP * (e % 2 ? half_hi<DT>(w[e / 2]) : half_lo<DT>(w[e / 2]));
+        const float t = x - b, y = fmaf(t, inv, magic);
+        const int k = __float_as_int(y);
+        const float r = fmaf(magic - y, s, t), most = __int_as_float(__float_as_int(half) - (k & 1));
+        c[e] = (uint32_t)min(max(k + (r > most ? 1 : 0) - (r < -most ? 1 : 0), MAGIC), MAGIC + 15) & 15u;
+        if (deep) {
+            const double rd = fma((double)(magic - y), (double)s, (double)x - (double)b), md = (double)most;
+            c[e] = (uint32_t)min(max(k + (rd > md ? 1 : 0) - (rd < -md ? 1 : 0), MAGIC), MAGIC + 15) & 15u;
+        }
+    }
+}
+
 template <int DT>
 __device__ __forceinline__ void codes_of(u32x4 w, float b, float hi, float s, uint32_t (&c)[8]) {
-    constexpr int MAGIC = 0x4b400000;
     if (!(s > 0.0f) || !(s < INFINITY)) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) c[e] = 0;
@@ -71,20 +93,10 @@ __device__ __forceinline__ void codes_of(u32x4 w, float b, float hi, float s, ui
     const uint32_t small = min((uint32_t)least[0], (uint32_t)least[1]);
     const float span = (hi - b) * (DT == DT_F16 ? 0x1p-13f : 0x1p-16f);
     const bool deep = (small < 0x8000u && as_float<DT>(small + 1) <= span) || (b != 0.0f && fabsf(b) <= span);
-    const float inv = __builtin_amdgcn_rcpf(s), half = 0.5f * s;
-    const float magic = __int_as_float(MAGIC);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float x = e % 2 ? half_hi<DT>(w[e / 2]) : half_lo<DT>(w[e / 2]);
-        const float t = x - b, y = fmaf(t, inv, magic);
-        const int k = __float_as_int(y);
-        const float r = fmaf(magic - y, s, t), most = __int_as_float(__float_as_int(half) - (k & 1));
-        c[e] = (uint32_t)min(max(k + (r > most ? 1 : 0) - (r < -most ? 1 : 0), MAGIC), MAGIC + 15) & 15u;
-        if (deep) {
-            const double rd = fma((double)(magic - y), (double)s, (double)x - (double)b), md = (double)most;
-            c[e] = (uint32_t)min(max(k + (rd > md ? 1 : 0) - (rd < -md ? 1 : 0), MAGIC), MAGIC + 15) & 15u;
-        }
-    }
+    // The reciprocal takes a subnormal for 0.  A group of so small a scale holds
+    // nothing above 2^-98, bfloat16 having 8 digits, so its numbers stay finite.
+    if (DT == DT_BF16 && s < 0x1p-110f) codes_times<DT>(w, b, s, deep, std::true_type(), c);
+    else codes_times<DT>(w, b, s, deep, std::false_type(), c);
 }
 
 template <bool VEC>

@@ -255,3 +255,34 @@ def test_workspace_of_the_caller(each, D, most, new):
     assert torch.equal(want, qmx.kv4_attention(*args, workspace=room, **kw))   # over what the last call left there
     with pytest.raises(qmx.QmxError, match="workspace"):
         qmx.kv4_attention(*args, workspace=room[:need - 1], **kw)
+
+
+@on_gpu
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 128), (256, 64)])
+@pytest.mark.parametrize("power", range(-133, -95, 3))
+def test_write_of_tiny_groups(D, group, power):
+    """bfloat16 groups whose scale is subnormal, or just above: codes, scales and biases bit for bit, and back.  Reading
+    rounds to bfloat16, half a step of which is 2^-134 down there."""
+    say("tiny", D, group, power)
+    rng = np.random.default_rng(200 - power)
+    T, H = 40, 2
+    x = [rng.normal(0, 1, (T, H, D)) * 2.0 ** power for _ in range(2)]
+    x[0][::2] = rng.integers(0, 31, x[0][::2].shape) * 2.0 ** power    # middles between codes
+    x[1][::2] = rng.integers(-200, 200, x[1][::2].shape) * 2.0 ** power
+    x[1][1] = 2.0 ** (power + 20)                                       # one value
+    k, v = (torch.from_numpy(a).bfloat16() for a in x)
+    c = ref.Cache(3, H, D, 16, group, "bf16", rng)
+    cache = device_cache(c)
+    slots = np.arange(5, 5 + T)
+    qmx.kv4_write(cache, k.to(DEV), v.to(DEV), ints(slots.tolist()))
+    got = qmx.kv4_read(cache, ints(slots.tolist()))
+    P, at = slots // 16, slots % 16
+    for which, a in ((0, k), (1, v)):
+        c.codes[which][P, :, at], c.s[which][P, :, at], c.b[which][P, :, at] = ref.quantise(a, group, torch.bfloat16)
+    for name, g, w in zip(("k_codes", "k_sb", "v_codes", "v_sb"),
+                          (cache.k_codes, cache.k_sb, cache.v_codes, cache.v_sb), c.packed()):
+        assert torch.equal(g.cpu(), w), name
+    for which, g in enumerate(got):
+        exact = np.stack([[c.values(which, P[t], h)[at[t]] for h in range(H)] for t in range(T)])
+        size = (ref.HALF["bf16"] + 32 * U32) * np.abs(exact) + 2.0 ** -134
+        assert (np.abs(g.double().cpu().numpy() - exact) <= size + 15 * U32 * np.abs(exact).max()).all()
