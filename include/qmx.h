@@ -458,8 +458,8 @@ int qmx_kv4_read(const qmx_kv4_cache* cache, void* k_out, void* v_out, const int
  *   workspace : qmx_kv4_attention_workspace_bytes bytes, 16-byte aligned (NULL
  *           where that is 0), overwritten; calls that share it are ordered.
  * Scores and sums are float32 on exact codes.  What the value codes are multiplied
- * by, a probability times a scale, is rounded to dtype; with more than 64 query
- * rows a key head (max_query_len * heads / kv_heads), values and probabilities
+ * by, a probability times a scale, is held in two bfloat16 numbers, to 2^-16 of
+ * itself; with more than 64 query rows a key head (max_query_len * heads / kv_heads), values and probabilities
  * are rounded to float16 instead after a power of two, to 2^-11 of themselves or
  * 2^-25 of the largest finite value of the request's tokens.  How the keys are cut
  * among work-groups follows the lengths and these arguments, so reruns with the

@@ -21,12 +21,16 @@
 // under 2^-29 of the row's largest and keeps 2^-40 of it), so S is as exact as its
 // 32-bit sums.  With K's codes as OFF + c the offset, up to 128 times the codes'
 // share, cost the row sums 3 to 5 bits (error of the logarithm of the sum 4e-8
-// now) and the same time.  V's codes enter as OFF + c in the cache's type, an
-// exponent set above the four bits, and the offset is taken off in 32 bits
-// through the sum of the rounded p_t s_tg, in the same step as sum_t p_t b_tg; the
+// now) and the same time.  V's codes enter as the bfloat16 numbers OFF + c, an
+// exponent set above the four bits, and the offset is taken off in 32 bits through
+// the sum of the p_t s_tg as they enter, in the same step as sum_t p_t b_tg; the
 // bias is moved to the middle of the codes (b + 8 s), so the two sums do not
-// cancel.  The one rounding to 16 bits is that of p_t s_tg (half a step: 2^-8 of
-// it in bfloat16, 2^-11 in float16), which the matrix cores need.
+// cancel.  p_t s_tg enters in two bfloat16 pieces, to 2^-16 of itself and at any
+// size: as float16, what lay under 2^-25 was lost, and with it the tail behind a
+// key of a large score (13 % of the output over 1200 keys 9 under it, scales of
+// 2^-13); as one bfloat16 piece it was off by 2^-8.  The second piece's products and 24 vector
+// instructions a group cost 2 to 8 % (1 to 48 requests of a token or few over 641
+// to 131000 keys, heads of 64 to 256; most where a group is 32).
 //
 // A work-group of WK waves takes a unit (kv4.h); the waves take every WK-th step
 // and are joined in LDS.  The running maximum is raised only when a score passes
@@ -64,7 +68,6 @@ struct Half;
 template <>
 struct Half<DT_BF16> {
     static constexpr float OFF = 128.0f;
-    static constexpr float kSlack = 8.0f;
     static constexpr uint32_t ONES = 0x3f803f80u;
     // Codes at bits 4f of both halves, as the numbers OFF + code.
     static __device__ __forceinline__ uint32_t codes(uint32_t w, int f) {
@@ -86,14 +89,6 @@ struct Half<DT_BF16> {
 
 template <>
 struct Half<DT_F16> {
-    static constexpr float OFF = 64.0f;
-    // p s stays finite: scales are at most (2 * 65504) / 15, p at most 4.
-    static constexpr float kSlack = 2.0f;
-    static constexpr uint32_t ONES = 0x3c003c00u;
-    static __device__ __forceinline__ uint32_t codes(uint32_t w, int f) {
-        const uint32_t x = f == 0 ? w << 4 : w >> (4 * (f - 1));
-        return (x & 0x00f000f0u) | 0x54005400u;
-    }
     static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
                                                       0, 0, 0);
@@ -101,9 +96,6 @@ struct Half<DT_F16> {
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         const f32x2 v = {lo, hi};
         return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
-    }
-    static __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
-        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, a), __builtin_bit_cast(f16x2, b), c, false);
     }
 };
 
@@ -190,6 +182,7 @@ template <int D, int GS, int DT>
 struct Rows {
     static constexpr int NJ = D / 32, G = D / GS, NB = D / 16;
     using H = Half<DT>;
+    static constexpr float kSlack = 8.0f;
     u32x4 q[NJ];       // float16, over the row's power of two, times 2^15
     float qsum[G];     // over the row's power of two
     float m, top, l;   // the maximum taken off (0 at first), what a score may reach, the sum
@@ -269,10 +262,10 @@ struct Rows {
         for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[e]);
         mx *= scale;
         if (__any(mx > top)) {
-            const float now = row_max(fmaxf(mx, top - H::kSlack));
+            const float now = row_max(fmaxf(mx, top - kSlack));
             const float safe = now > -INFINITY ? now : 0.0f;
             const float fade = top > -INFINITY ? __builtin_amdgcn_exp2f(m - safe) : 0.0f;
-            top = now + H::kSlack;
+            top = now + kSlack;
             m = safe;
             l *= fade;
 #pragma unroll
@@ -290,7 +283,7 @@ struct Rows {
     // all: every row sees every token; else `seen` says.  What is not seen has a
     // probability of 0, but its scale and bias may be infinite.
     __device__ __forceinline__ void values(const Pairs<DT, G> (&pair)[2], bool all, uint32_t seen) {
-        u32x4 ps[G];
+        using B = Half<DT_BF16>;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             float w[8], y[8];
@@ -306,24 +299,32 @@ struct Rows {
                     y[e] = (seen >> e) & 1u ? y[e] : 0.0f;
                 }
             }
+            u32x4 ps[2];   // p s in two pieces
             float sum = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) fix[g] = fmaf(s[e], y[e], fix[g]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                ps[g][e] = H::pack(w[2 * e], w[2 * e + 1]);
-                sum = H::dot2(ps[g][e], H::ONES, sum);
+                const uint32_t first = B::pack(w[2 * e], w[2 * e + 1]);
+                ps[0][e] = first;
+                ps[1][e] = B::pack(w[2 * e] - half_lo<DT_BF16>(first), w[2 * e + 1] - half_hi<DT_BF16>(first));
+                sum = B::dot2(ps[0][e], B::ONES, sum);
+                sum = B::dot2(ps[1][e], B::ONES, sum);
             }
-            fix[g] = fmaf(-(H::OFF + 8.0f), sum, fix[g]);
-        }
+            fix[g] = fmaf(-(B::OFF + 8.0f), sum, fix[g]);
+            constexpr int MOST = GS < 64 ? 2 : 4;   // blocks of 16 elements at a time
 #pragma unroll
-        for (int a = 0; a < D / 64; ++a) {
+            for (int n0 = g * (GS / 16); n0 < (g + 1) * (GS / 16); n0 += MOST) {
+                u32x4 x[MOST];
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                const u32x4 x = {H::codes(v[0][2 * a], f), H::codes(v[0][2 * a + 1], f),
-                                 H::codes(v[1][2 * a], f), H::codes(v[1][2 * a + 1], f)};
-                const int nb = 4 * a + f;
-                o[nb] = H::mfma(x, ps[nb * 16 / GS], o[nb]);
+                for (int i = 0; i < MOST; ++i) {
+                    const int a = (n0 + i) / 4, f = (n0 + i) % 4;
+                    x[i] = u32x4{B::codes(v[0][2 * a], f), B::codes(v[0][2 * a + 1], f), B::codes(v[1][2 * a], f),
+                                 B::codes(v[1][2 * a + 1], f)};
+                    o[n0 + i] = B::mfma(x[i], ps[0], o[n0 + i]);
+                }
+#pragma unroll
+                for (int i = 0; i < MOST; ++i) o[n0 + i] = B::mfma(x[i], ps[1], o[n0 + i]);
             }
         }
     }

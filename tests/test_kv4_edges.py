@@ -4,8 +4,7 @@ subnormal groups, long tails, magnitudes far apart, and arguments that the entri
 Bounds.  ``u`` is half a step of the type, 2^-24 that of float32.  For a token, with p its keys' probabilities:
 
 * the output's rounding, u |out| (and half a subnormal step);
-* few rows: p s enters the product with its code, taken about the middle of the codes, in ``pieces`` numbers of the
-  cache's type or bfloat16, so it is off by ``held`` of itself;
+* few rows: p s enters the product with its code, taken about the middle of the codes, to ``held`` of itself;
 * many rows: values and probabilities are float16, 2^-11 each; values also to 2^-18 of their token's largest, and a
   probability times a value to 2^-26 of the largest value that the token sees, for each key (the sum of exponentials
   is at least 1 of them);
@@ -286,3 +285,29 @@ def test_write_of_tiny_groups(D, group, power):
         exact = np.stack([[c.values(which, P[t], h)[at[t]] for h in range(H)] for t in range(T)])
         size = (ref.HALF["bf16"] + 32 * U32) * np.abs(exact) + 2.0 ** -134
         assert (np.abs(g.double().cpu().numpy() - exact) <= size + 15 * U32 * np.abs(exact).max()).all()
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("keys,above,size", [(1200, 9.0, 2.0 ** -13), (6000, 9.0, 1e-3), (30000, 10.0, 5e-4),
+                                             (60000, 11.0, 1e-3)])
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (256, 128)])
+def test_long_tail_behind_one_key(dtype, D, group, keys, above, size):
+    """One key far above a long tail of keys, whose values are small: each of the tail's products is tiny and their sum
+    is not.  The codes are alike from token to token, so nothing that is lost cancels.  p s is held in 16 bits."""
+    say("tail", dtype, D, group, keys, above)
+    rng = np.random.default_rng(keys + D)
+    page = 64
+    table, pages = tables([keys], page)
+    c = ref.Cache(pages, 1, D, page, group, dtype, rng)
+    q = torch.from_numpy(rng.uniform(0.5, 1.5, (1, 1, D))).to(ref.TYPES[dtype])
+    round_ = lambda x: torch.from_numpy(np.asarray(x)).to(ref.TYPES[dtype]).double().numpy()  # noqa: E731
+    x = q.double().numpy()[0, 0]
+    c.s[0][:] = round_(rng.uniform(0.02, 0.06, c.s[0].shape) * 8 / D ** 0.5)
+    c.b[0][:] = round_(-7.5 * c.s[0])
+    c.s[0][0, :, 0], c.b[0][0, :, 0] = 0, round_(above / (x.sum() * D ** -0.5))
+    c.codes[1][:] = rng.choice([0, 15], D)
+    c.s[1][:] = round_(rng.uniform(0.5, 1.5, c.s[1].shape) * size)
+    c.b[1][:] = round_(-7.5 * c.s[1])
+    c.s[1][0, :, 0] = c.b[1][0, :, 0] = 0
+    held_to(c, q, table, [keys], [0, 1])
