@@ -134,6 +134,12 @@ __device__ __forceinline__ float row_lane(float v, int k) {
     return v;
 }
 
+// The softmax scale times 2^e, held to what is neither 0 nor infinite: a hidden
+// score's -inf times 0 would be NaN.
+__device__ __forceinline__ float score_scale(const Kv4AttnArgs& a, int e) {
+    return fminf(fmaxf(ldexpf(a.scale_log2, e), 0x1p-126f), 0x1.fffffep127f);
+}
+
 // The (scale, bias) pairs of a block's tokens.  The 16 lanes of a row all need
 // the 4 * G pairs of the row's four tokens, keys' and values': each lane holds
 // its share, as numbers, and row_lane passes them round.  They are set right for
@@ -401,8 +407,9 @@ __global__ __launch_bounds__(64 * WK, 2) void kv4_attn_kernel(Kv4AttnArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 most = fmaxf(most, fmaxf(fabsf(half_lo<DT>(x.q[j][e])), fabsf(half_hi<DT>(x.q[j][e]))));
-        const int exponent = min(__builtin_amdgcn_frexp_expf(row_max(most)), 127);
-        const float scale = ldexpf(a.scale_log2, exponent);
+        // bfloat16 has no digits under 2^-133, which 2^(15 + 94) takes to float16's last
+        const int exponent = max(min(__builtin_amdgcn_frexp_expf(row_max(most)), 127), -94);
+        const float scale = score_scale(a, exponent);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             float sum = 0.0f;

@@ -299,7 +299,7 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
         const int any_lo = a.window ? pos0 - a.window + 1 : 0, any_hi = mine ? min(pos1, part_end - 1) : -1;
 
         u32x4 q[KQ], qb[BK];
-        float rf;
+        int shift;   // the queries are divided by 2^shift
         {
             const uint16_t* from = static_cast<const uint16_t*>(a.q) + token * a.q_ts + qhead * a.q_hs + 8 * hh;
             const bool vec = (((uintptr_t)a.q & 15) | ((a.q_ts | a.q_hs) & 7)) == 0;
@@ -331,7 +331,7 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
             }
             most = fmaxf(most, __shfl_xor(most, 32, 64));
             const int e = min(__builtin_amdgcn_frexp_expf(most), 127);
-            rf = ldexpf(a.scale_log2, e);
+            shift = e;
             u32x4 sums[2 * BK] = {};   // a group's slots: the sum's pieces, and those of 8 times it
 #pragma unroll
             for (int g = 0; g < G; ++g) {
@@ -442,7 +442,7 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                 const int e = __builtin_amdgcn_readfirstlane(info.block[2 * t + b]);
                 there[b] = e != TileInfo::MISSING;
                 all = all && there[b];
-                by[b] = W::SCALED ? ldexpf(rf, there[b] ? e : 0) : rf;
+                by[b] = score_scale(a, W::SCALED && there[b] ? shift + e : shift);
             }
             if (!all) {
                 const int first = key + 4 * hh - lo;

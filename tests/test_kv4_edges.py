@@ -311,3 +311,38 @@ def test_long_tail_behind_one_key(dtype, D, group, keys, above, size):
     c.b[1][:] = round_(-7.5 * c.s[1])
     c.s[1][0, :, 0] = c.b[1][0, :, 0] = 0
     held_to(c, q, table, [keys], [0, 1])
+
+
+@on_gpu
+@pytest.mark.parametrize("new,past", [(40, 50), (1, 90), (60, 2000), (2, 2000)])
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 128), (256, 64)])
+@pytest.mark.parametrize("power,key_power", [(-40, None), (-120, None), (-76, -76), (-130, 0), (-100, 90), (90, -100),
+                                             (-20, -120), (120, -130)])
+def test_scores_that_vanish(new, past, D, group, power, key_power):
+    """Keys that are all zeros, or queries and keys whose powers of two together leave the range of float32: finite
+    inputs give finite outputs, and scores of nothing the mean of what is seen."""
+    say("vanish", new, past, D, group, power, key_power)
+    rng = np.random.default_rng(41)
+    kv = [past + new, 7]
+    table, pages = tables(kv, 32)
+    c = ref.Cache(pages, 1, D, 32, group, "bf16", rng)
+    for x in (c.s[0], c.b[0]):
+        x *= 0.0 if key_power is None else 2.0 ** key_power
+        x[:] = torch.from_numpy(x).bfloat16().double().numpy()
+    offsets = [0, new, new + min(new, 7)]
+    q = torch.from_numpy(rng.normal(0, 1, (offsets[-1], 2, D)) * 2.0 ** power).bfloat16()
+    held_to(c, q, table, kv, offsets)
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("scale", [1e-44, 1e-38, 1e-30])
+def test_tiny_softmax_scales(dtype, new, scale):
+    say("scale", dtype, new, scale)
+    rng = np.random.default_rng(42)
+    kv = [100 + new]
+    table, pages = tables(kv, 16)
+    c = ref.Cache(pages, 1, 64, 16, 32, dtype, rng)
+    q = torch.from_numpy(rng.normal(0, 2.0 ** -12, (new, 2, 64))).to(ref.TYPES[dtype])
+    held_to(c, q, table, kv, [0, new], scale=scale)
