@@ -23,17 +23,21 @@
 //   probabilities that a lane computes are the operand it needs (as in
 //   kv4_attn_impl.h), the values' tokens being put into that order.
 //
-// A code c becomes an operand from the bits of the float16 number c 2^-18, which
-// is exact, in one multiply-add.  Queries are float16, brought to at most 1 by a
-// power of two a row (what is under 2^-14 of the largest keeps 2^-25 of it).
+// A code c becomes an operand from the bits of the float16 number c 2^-18 or
+// 16 + c, which is exact, in one multiply-add.  Queries are float16, brought under
+// 2^15 by a power of two a row (exact, but for what is under 2^-29 of the row's
+// largest and keeps 2^-40 of it).
 //
 // Keys of bfloat16 scales: s (c - 8) has 8 + 3 bits, so float16 holds it exactly,
-// the block of 16 tokens brought to at most 1 by a power of two that goes into
-// the softmax scale.  What is left, b + 8 s, times the sums of the queries is a
-// first step of the product: b and s by the sums in three bfloat16 pieces each,
-// which hold 24 bits.  Keys of float16 scales (11 bits) stay codes, and a group's
-// product is multiplied by the token's scale in 32 bits.  Either way scores are
-// as exact as their 32-bit sums.
+// the block of 16 tokens brought under 2^14 by a power of two that goes into the
+// softmax scale (what is under 2^-28 of the block's largest keeps 2^-39 of it).  A
+// block whose tokens are more than 2^8 apart has a power a token, which the scores
+// are multiplied by: another token's keys, seen or not, cost none of a key's
+// digits.  What is left, b + 8 s, times the sums of the queries is a first step of
+// the product: b and s by the sums in three bfloat16 pieces each, which hold 24
+// bits.  Keys of float16 scales (11 bits) stay codes, and a group's product is
+// multiplied by the token's scale in 32 bits.  Either way scores are as exact as
+// their 32-bit sums.
 //
 // Values become c s + b divided by a power of two, the largest of the unit so
 // far; when it rises, the sums are divided too.  Values and probabilities are
@@ -85,6 +89,15 @@ __device__ __forceinline__ float wave_max(float v) {
                               max(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48))));
 }
 
+// What the rows need to know of a tile beside its operands.
+struct alignas(16) TileInfo {
+    static constexpr int MISSING = -1000, OWN = 1000;
+    int block[4];   // the keys' exponent; MISSING: no page; OWN: each token has one
+    int value_exponent;
+    int bad;        // tile + 1, where it holds values that are not finite
+    int unused[2];
+};
+
 // What a lane takes of one block of 16 tokens to turn it into operands: codes of
 // the D / SPLIT dimensions that fall to its wave, the pairs of one token, and a
 // share of the pairs of the four tokens 4h .. 4h + 3, h = lane / 16, as in
@@ -102,6 +115,10 @@ struct Raw {
     static constexpr int BK = (SLOTS * G + 15) / 16;              // its steps
     static constexpr int SHARE = (4 * G + 15) / 16;               // a lane's share of a block's pairs
     static constexpr int EMPTY = -120;                            // exponent of nothing but zeros
+    // Powers of two that keys, queries and the queries' sums are brought to, and
+    // what a score is multiplied by in all.
+    static constexpr int KEY_UP = 14, QUERY_UP = 15, SUM_UP = SCALED ? QUERY_UP : 8;
+    static constexpr int SCORE_UP = SCALED ? KEY_UP + QUERY_UP : SUM_UP;
     // The same loads for either kind of wave, and no branch about them: where two
     // met in a register, a copy behind them would wait for memory.
     uint32_t w[NW], token_pairs[G], share[SHARE];
@@ -136,12 +153,12 @@ struct Raw {
     }
 
     // Keys to `k` [blocks of 32][BK + KS][2][32] of 16 bytes; `blk` counts in the
-    // tile.  SCALED: divided by 2^(what is returned).  Else: the scales times
-    // 2^18 to `factor` [G][KEYS].
-    __device__ __forceinline__ int keys(u32x4* k, float* factor, int blk, int part) const {
+    // tile.  SCALED: divided by 2^(what is returned), or, where that is OWN, each
+    // token by 2^(its `powers` [KEYS]).  Else: the scales to `factor` [G][KEYS].
+    __device__ __forceinline__ int keys(u32x4* k, float* factor, int* powers, int blk, int part) const {
         const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
         u32x4* to = k + (blk >> 1) * (BK + KS) * 64 + (blk & 1) * 16 + n;
-        int e = 0;
+        int e = 0, result = 0;
         if constexpr (SCALED) {
             float most = 0.0f;
 #pragma unroll
@@ -149,8 +166,15 @@ struct Raw {
                 const float x = fmaxf(fabsf(8.0f * half_lo<DT>(token_pairs[g])), fabsf(half_hi<DT>(token_pairs[g])));
                 most = x < INFINITY ? fmaxf(most, x) : most;
             }
-            most = wave_max(live ? most : 0.0f);
-            e = most > 0.0f ? __builtin_amdgcn_frexp_expf(most) : EMPTY;
+            most = live ? most : 0.0f;
+            const float all = wave_max(most);
+            result = e = all > 0.0f ? power(all) : 0;
+            const int own = most > 0.0f ? power(most) : e;
+            if (__any(own < e - 8)) {
+                e = own;
+                result = TileInfo::OWN;
+                if (part == 0 && h == 0) powers[16 * blk + n] = own;
+            }
         }
 #pragma unroll
         for (int g = 0; g < GW; ++g) {
@@ -159,18 +183,19 @@ struct Raw {
             const float s = half_lo<DT>(pair);
             f16x2 s2, b2;
             if constexpr (SCALED) {
-                s2 = half2_of(ldexpf(s, 18 - e), ldexpf(s, 18 - e));
-                b2 = half2_of(-ldexpf(s, 3 - e), -ldexpf(s, 3 - e));
+                const float x = ldexpf(s, KEY_UP - e);
+                s2 = half2_of(x, x);
+                b2 = half2_of(-24.0f * x, -24.0f * x);
                 if (h == g % 4) {   // 8 slots: three times b, and three times s for 8 s
-                    const uint32_t x = Half<DT>::pack(ldexpf(half_hi<DT>(pair), -e), ldexpf(s, -e));
-                    const uint32_t b = x & 0xffffu, y = x >> 16;
+                    const uint32_t z = Half<DT>::pack(ldexpf(half_hi<DT>(pair), KEY_UP - e), x);
+                    const uint32_t b = z & 0xffffu, y = z >> 16;
                     to[(group / 2) * 64 + (group % 2) * 32] = u32x4{b | (b << 16), b, y | (y << 16), y};
                 }
             } else if (h == g % 4) {   // 4 slots: three times b
                 const uint32_t b = pair >> 16;
                 reinterpret_cast<u32x2*>(to + (group / 4) * 64 + (group / 2 % 2) * 32)[group % 2] =
                     u32x2{b | (b << 16), b};
-                factor[KEYS * group + 16 * blk + n] = s * 0x1p18f;
+                factor[KEYS * group + 16 * blk + n] = ldexpf(s, 18 - QUERY_UP + SUM_UP);
             }
 #pragma unroll
             for (int j = g * (GS / 32); j < (g + 1) * (GS / 32); ++j) {
@@ -179,14 +204,17 @@ struct Raw {
                 for (int f = 0; f < 4; ++f) {
                     const uint32_t y = tiny_codes(w[j], f);
                     x[f] = SCALED ? __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(
-                                                                     __builtin_bit_cast(f16x2, y), s2, b2))
+                                                                     __builtin_bit_cast(f16x2, y | 0x4c004c00u), s2, b2))
                                   : y;
                 }
                 to[(BK + 2 * (part * NW + j) + (h >> 1)) * 64 + (h & 1) * 32] = x;
             }
         }
-        return e;
+        return result;
     }
+    // The power of two above x.  Not under 2^-95: bfloat16 has no digits below
+    // 2^-133, which KEY_UP takes to float16's.
+    static __device__ __forceinline__ int power(float x) { return max(__builtin_amdgcn_frexp_expf(x), -95); }
 
     // Values to `v` [blocks of 16][DB][2][32] of 16 bytes, divided by 2^exponent,
     // which rises to the tile's largest.  Whether the tile is finite.
@@ -247,26 +275,18 @@ struct Raw {
     }
 };
 
-// What the rows need to know of a tile beside its operands.
-struct alignas(16) TileInfo {
-    static constexpr int MISSING = -1000;
-    int block[4];   // the keys' exponent, or MISSING: no page
-    int value_exponent;
-    int bad;        // tile + 1, where it holds values that are not finite
-    int unused[2];
-};
-
 template <int D, int GS, int DT>
 __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4AttnArgs a) {
     using W = Raw<D, GS, DT>;
     using H = Half<DT>;
     constexpr int KS = D / 16, DB = D / 32, G = D / GS, BK = W::BK, KEYS = W::KEYS, NT = KEYS / 32;
     constexpr int KQ = D == 256 ? KS / 2 : KS;   // steps whose queries stay in registers; the others' in LDS
-        constexpr int AHEAD = D == 256 ? 2 : 4;      // operands read ahead
+    constexpr int AHEAD = D == 256 ? 2 : 4;      // operands read ahead
     constexpr float kSlack = 8.0f;
     __shared__ u32x4 s_k[2][NT * (BK + KS) * 64], s_v[3][2 * NT * DB * 64];
     __shared__ u32x4 s_q[PROMPT_WAVES][KS > KQ ? (KS - KQ) * 64 : 1];
     __shared__ float s_factor[2][W::SCALED ? 1 : G * KEYS];
+    __shared__ int s_key_power[3][W::SCALED ? KEYS : 1];
     __shared__ TileInfo s_info[3];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, n = lane & 31, hh = lane >> 5;
@@ -299,7 +319,7 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
         const int any_lo = a.window ? pos0 - a.window + 1 : 0, any_hi = mine ? min(pos1, part_end - 1) : -1;
 
         u32x4 q[KQ], qb[BK];
-        int shift;   // the queries are divided by 2^shift
+        int shift;   // the queries' power of two, over that of the products
         {
             const uint16_t* from = static_cast<const uint16_t*>(a.q) + token * a.q_ts + qhead * a.q_hs + 8 * hh;
             const bool vec = (((uintptr_t)a.q & 15) | ((a.q_ts | a.q_hs) & 7)) == 0;
@@ -330,12 +350,12 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                 }
             }
             most = fmaxf(most, __shfl_xor(most, 32, 64));
-            const int e = min(__builtin_amdgcn_frexp_expf(most), 127);
-            shift = e;
+            const int e = max(min(__builtin_amdgcn_frexp_expf(most), 127), -94);   // as in kv4_attn_impl.h
+            shift = e - W::SCORE_UP;
             u32x4 sums[2 * BK] = {};   // a group's slots: the sum's pieces, and those of 8 times it
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                float rest = ldexpf(sum[g] + __shfl_xor(sum[g], 32, 64), -e);
+                float rest = ldexpf(sum[g] + __shfl_xor(sum[g], 32, 64), W::SUM_UP - e);
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
                     const uint32_t piece = H::pack(rest, 0.0f) & 0xffffu;
@@ -356,8 +376,8 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                 u32x4 x = load(j);
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
-                    x[w] = __builtin_bit_cast(uint32_t,
-                                              half2_of(ldexpf(half_lo<DT>(x[w]), -e), ldexpf(half_hi<DT>(x[w]), -e)));
+                    x[w] = __builtin_bit_cast(uint32_t, half2_of(ldexpf(half_lo<DT>(x[w]), W::QUERY_UP - e),
+                                                                 ldexpf(half_hi<DT>(x[w]), W::QUERY_UP - e)));
                 if (j < KQ) q[j < KQ ? j : 0] = x;
                 else s_q[wave][(j - KQ) * 64 + lane] = x;   // read by the same lane
             }
@@ -443,6 +463,13 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                 there[b] = e != TileInfo::MISSING;
                 all = all && there[b];
                 by[b] = score_scale(a, W::SCALED && there[b] ? shift + e : shift);
+                if (W::SCALED && e == TileInfo::OWN) {
+                    by[b] = 1.0f;
+#pragma unroll
+                    for (int z = 0; z < 8; ++z)
+                        x[8 * b + z] = ldexpf(x[8 * b + z] * a.scale_log2,
+                                              shift + s_key_power[buffer][32 * t + 16 * b + 8 * (z / 4) + 4 * hh + z % 4]);
+                }
             }
             if (!all) {
                 const int first = key + 4 * hh - lo;
@@ -543,7 +570,8 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                         s_info[after].value_exponent = exponent;
                     }
                 } else {
-                    const int e = raw.keys(s_k[(t + 1) & 1], s_factor[(t + 1) & 1], my_blk, my_part);
+                    const int e = raw.keys(s_k[(t + 1) & 1], s_factor[(t + 1) & 1], s_key_power[after], my_blk,
+                                           my_part);
                     if (my_part == 0) s_info[after].block[my_blk] = raw.there ? e : TileInfo::MISSING;
                 }
             }

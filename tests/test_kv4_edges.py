@@ -10,7 +10,8 @@ Bounds.  ``u`` is half a step of the type, 2^-24 that of float32.  For a token, 
   is at least 1 of them);
 * 32-bit sums, every product rounded and added at most ``steps`` times;
 * key t's score is off by E_t, D products on 32-bit sums and the exponent's argument (many rows: and 2^-31 of the
-  largest elements), which moves the output by sum p_t expm1(2 E_t) |v_t - out| at most.
+  largest elements), which moves the output by sum p_t expm1(2 E_t) |v_t - out| and the logarithm of the sum by
+  log sum p_t exp(E_t) at most.
 """
 import ctypes
 import math
@@ -70,7 +71,8 @@ def expected(c, q, table, kv, offsets, window=0, scale=None, prompt=False, held=
                 tol[t, a] = (u * np.abs(out[t, a]) + (2.0 ** -25 if c.type == "f16" else 2.0 ** -134) + rounded
                              + steps * U32 * (p @ (vs[see] * (ref.OFF + 23) + np.abs(vb[see])))
                              + (p * eps) @ np.abs(v - out[t, a]) / max(1 - (p * eps).sum(), 0.01))
-                ltol[t, a] = (p * eps).sum() + steps * U32 + 2 * U32 * abs(lse[t, a])
+                up = s - lse[t, a] + E
+                ltol[t, a] = up.max() + np.log(np.exp(up - up.max()).sum()) + steps * U32 + 2 * U32 * abs(lse[t, a])
     return out, lse, tol, ltol
 
 
@@ -346,3 +348,67 @@ def test_tiny_softmax_scales(dtype, new, scale):
     c = ref.Cache(pages, 1, 64, 16, 32, dtype, rng)
     q = torch.from_numpy(rng.normal(0, 2.0 ** -12, (new, 2, 64))).to(ref.TYPES[dtype])
     held_to(c, q, table, kv, [0, new], scale=scale)
+
+
+def spread_case(dtype, D, group, lens, seed, page=32, heads=1):
+    rng = np.random.default_rng(seed)
+    kv = [p + n for p, n in lens]
+    table, pages = tables(kv, page)
+    c = ref.Cache(pages, heads, D, page, group, dtype, rng)
+    offsets = [0] + np.cumsum([n for _, n in lens]).tolist()
+    q = torch.from_numpy(rng.normal(0, 1, (offsets[-1], 2 * heads, D))).to(ref.TYPES[dtype])
+    return rng, c, q, table, kv, offsets
+
+
+def at(table, page, r, t):
+    return table[r, t // page], slice(None), t % page
+
+
+FAR = {"bf16": 2.0 ** 60, "f16": 2.0 ** 12}
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,group", [(64, 32), (64, 64), (128, 32), (128, 128), (256, 32), (256, 64)])
+@pytest.mark.parametrize("lens", [[(0, 50), (70, 33)], [(1900, 40)]])
+@pytest.mark.parametrize("what", ["keys"])
+def test_hidden_tokens_cost_nothing(dtype, D, group, lens, what):
+    """Tokens of huge keys or values that only the last queries see leave the others' digits alone."""
+    say("hidden", dtype, D, group, lens, what)
+    rng, c, q, table, kv, offsets = spread_case(dtype, D, group, lens, 50)
+    for x in (c.s[0], c.b[0], c.s[1], c.b[1]):
+        x *= 2.0 ** -6
+    for r, length in enumerate(kv):
+        for t in (length - 1, length - 7, length - 12):
+            for i in ((0,), (1,), (0, 1))[("keys", "values", "both").index(what)]:
+                c.s[i][at(table, 32, r, t)] *= FAR[dtype]
+                c.b[i][at(table, 32, r, t)] *= FAR[dtype]
+    held_to(c, q, table, kv, offsets)
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (256, 64)])
+@pytest.mark.parametrize("new", [1, 50])
+def test_keys_far_above_their_neighbours(dtype, D, group, new):
+    """Keys of huge elements whose scores are far below the others': they take part in no output and in no rounding."""
+    say("neighbours", dtype, D, group, new)
+    rng, c, q, table, kv, offsets = spread_case(dtype, D, group, [(90, new)], 53)
+    q = q.abs() + 0.25
+    big = {"bf16": 2.0 ** 30, "f16": 2.0 ** 11}[dtype]
+    for t in (3, 17, 40, 41):
+        c.s[0][at(table, 32, 0, t)], c.b[0][at(table, 32, 0, t)] = big, -16 * big
+    held_to(c, q, table, kv, offsets)
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (256, 64)])
+@pytest.mark.parametrize("new", [1, 50])
+def test_queries_with_elements_that_meet_zeros(dtype, D, group, new):
+    """A group of large query elements on keys that are zeros there: the others' products keep their digits."""
+    say("queries", dtype, D, group, new)
+    rng, c, q, table, kv, offsets = spread_case(dtype, D, group, [(90, new)], 54)
+    c.s[0][..., 0] = c.b[0][..., 0] = 0
+    q[..., :group] *= 2.0 ** 13
+    held_to(c, q, table, kv, offsets)
