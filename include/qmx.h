@@ -459,11 +459,12 @@ int qmx_kv4_read(const qmx_kv4_cache* cache, void* k_out, void* v_out, const int
  *           where that is 0), overwritten; calls that share it are ordered.
  * Scores and sums are float32 on exact codes.  What the value codes are multiplied
  * by, a probability times a scale, is held in two bfloat16 numbers, to 2^-16 of
- * itself; with more than 64 query rows a key head (max_query_len * heads / kv_heads), values and probabilities
- * are rounded to float16 instead after a power of two, to 2^-11 of themselves or
- * 2^-25 of the largest finite value of the request's tokens.  How the keys are cut
- * among work-groups follows the lengths and these arguments, so reruns with the
- * same are bit-identical. */
+ * itself; with more than 64 query rows a key head (max_query_len * heads /
+ * kv_heads), values and probabilities are rounded to float16 instead, to 2^-11 of
+ * themselves, values also to 2^-18 of their token's largest, and the product of
+ * both to 2^-26 of the largest finite value that the query sees.  How the keys are
+ * cut among work-groups follows the lengths and these arguments, so reruns with
+ * the same are bit-identical. */
 int qmx_kv4_attention(const qmx_kv4_cache* cache, const void* q, long long q_token_stride,
                       long long q_head_stride, void* out, float* lse, const int32_t* block_table,
                       int columns, long long table_stride, const int32_t* kv_lens,

@@ -61,7 +61,7 @@ struct Kv4AttnArgs {
     Kv4AttnPlan p;
     // Workspace, with lines > 0.  A part has two places: 2w + 1 for the unit that
     // starts in it and goes on, 2w for one that came from before.
-    float* part;   // [2 * lines][kv heads][rows][dim]
+    float* part;   // [2 * lines][kv heads][rows][dim]; rows > 16: over the part's sum
     float* stat;   // [2 * lines][kv heads][rows] pairs (max, sum)
     int* pos;      // the parts' length in steps, then where each unit begins and ends
 };

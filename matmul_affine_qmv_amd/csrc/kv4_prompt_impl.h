@@ -39,10 +39,16 @@
 // multiplied by the token's scale in 32 bits.  Either way scores are as exact as
 // their 32-bit sums.
 //
-// Values become c s + b divided by a power of two, the largest of the unit so
-// far; when it rises, the sums are divided too.  Values and probabilities are
-// rounded to float16, half a step 2^-11, as the matrix cores need (bfloat16
-// would cost eight times that).  All sums are float32.
+// Values become c s + b divided by a power of two: one for the tile where its
+// tokens are within 2^5 of each other, else one a token.  A row's sums have a power
+// of their own, the largest of the tokens that it sees; what is left goes to the
+// probability.  So a token that a row does not see costs it no digits, however
+// large.  As long as a tile has the power of all rows' sums, as nearly always,
+// that is one comparison of scalars.  Values and probabilities are rounded to
+// float16, half a step 2^-11, as the matrix cores need (bfloat16 would cost eight
+// times that); values also to 2^-18 of their token's largest, and a probability
+// times a value to 2^-26 of the largest that the row sees.  All sums are float32.
+// One power of two for all values so far, seen or not, took 1 to 4 % less time.
 //
 // 0 * NaN is NaN in a product, so values that are not finite are entered as 0
 // and added afterwards to the rows that see them (a tile that holds one is rare
@@ -89,11 +95,21 @@ __device__ __forceinline__ float wave_max(float v) {
                               max(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48))));
 }
 
+// The lane.  SHORT of registers: as if not known before, so that what is worked
+// out from it in a loop is worked out there, and not spilled from before the loop
+// on: a spilled number comes back behind the loads that are on their way.
+template <bool SHORT>
+__device__ __forceinline__ int lane_of() {
+    int lane = threadIdx.x & 63;
+    if constexpr (SHORT) asm volatile("" : "+v"(lane));
+    return lane;
+}
+
 // What the rows need to know of a tile beside its operands.
 struct alignas(16) TileInfo {
-    static constexpr int MISSING = -1000, OWN = 1000;
+    static constexpr int MISSING = -1001, OWN = 1000, ZEROS = -1000, NONE = 1001;
     int block[4];   // the keys' exponent; MISSING: no page; OWN: each token has one
-    int value_exponent;
+    int value_exponent;   // or OWN, or ZEROS
     int bad;        // tile + 1, where it holds values that are not finite
     int unused[2];
 };
@@ -114,7 +130,12 @@ struct Raw {
     static constexpr int SLOTS = SCALED ? 8 : 4;                  // of a group in the product of biases
     static constexpr int BK = (SLOTS * G + 15) / 16;              // its steps
     static constexpr int SHARE = (4 * G + 15) / 16;               // a lane's share of a block's pairs
-    static constexpr int EMPTY = -120;                            // exponent of nothing but zeros
+    // Where lane_of is to hide what it knows.  8192 tokens, heads of 128, float16:
+    // groups of 32 3926 us without and 1929 with, of 64 780 and 750 (keys only; all
+    // 769); heads of 256, 12 requests over 4000 keys: 240 and 213.  Where nothing is
+    // spilled it costs 6 to 10 %.
+    static constexpr bool SHORT = D == 256 || (DT == DT_F16 && D == 128 && GS == 32);
+    static constexpr bool SHORT_KEYS = DT == DT_F16 && D == 128;
     // Powers of two that keys, queries and the queries' sums are brought to, and
     // what a score is multiplied by in all.
     static constexpr int KEY_UP = 14, QUERY_UP = 15, SUM_UP = SCALED ? QUERY_UP : 8;
@@ -130,7 +151,7 @@ struct Raw {
     // on; the tile's are from `first` on, `key` its first key.
     __device__ __forceinline__ void load(const Kv4View& c, int pages, int first, int head, int key, int my_blk,
                                          int part, int end, bool value) {
-        const int lane = threadIdx.x & 63;
+        const int lane = lane_of<SHORT>();
         const int page = __builtin_amdgcn_readlane(pages, first + my_blk), blk = (key >> 4) + my_blk;
         const int own = value ? lane % KEYS : 16 * my_blk + (lane & 15);   // the lane's token of the tile
         const int its = __shfl(pages, first + own / 16, 64);
@@ -153,10 +174,12 @@ struct Raw {
     }
 
     // Keys to `k` [blocks of 32][BK + KS][2][32] of 16 bytes; `blk` counts in the
-    // tile.  SCALED: divided by 2^(what is returned), or, where that is OWN, each
-    // token by 2^(its `powers` [KEYS]).  Else: the scales to `factor` [G][KEYS].
-    __device__ __forceinline__ int keys(u32x4* k, float* factor, int* powers, int blk, int part) const {
-        const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
+    // tile.  SCALED: divided by 2^(what is returned), `exponent`, or, where that is
+    // OWN, each token by 2^(its `powers` [KEYS]).  Else: the scales to `factor`
+    // [G][KEYS].
+    __device__ __forceinline__ int keys(u32x4* k, float* factor, int& exponent, int* powers, int blk,
+                                        int part) const {
+        const int lane = lane_of<SHORT || SHORT_KEYS>(), n = lane & 15, h = lane >> 4;
         u32x4* to = k + (blk >> 1) * (BK + KS) * 64 + (blk & 1) * 16 + n;
         int e = 0, result = 0;
         if constexpr (SCALED) {
@@ -166,14 +189,17 @@ struct Raw {
                 const float x = fmaxf(fabsf(8.0f * half_lo<DT>(token_pairs[g])), fabsf(half_hi<DT>(token_pairs[g])));
                 most = x < INFINITY ? fmaxf(most, x) : most;
             }
-            most = live ? most : 0.0f;
-            const float all = wave_max(most);
-            result = e = all > 0.0f ? power(all) : 0;
-            const int own = most > 0.0f ? power(most) : e;
-            if (__any(own < e - 8)) {
-                e = own;
-                result = TileInfo::OWN;
-                if (part == 0 && h == 0) powers[16 * blk + n] = own;
+            const bool zeros = !live || most == 0.0f;
+            const int own = power(most);
+            auto far = [&] { return __any(!zeros && (uint32_t)(exponent - own) > 8u); };
+            result = e = exponent;
+            if (far()) {   // not the last block's power: this one's, or one a token
+                result = e = exponent = power(wave_max(zeros ? 0.0f : most));
+                if (far()) {
+                    e = zeros ? e : own;
+                    result = TileInfo::OWN;
+                    if (part == 0 && h == 0) powers[16 * blk + n] = e;
+                }
             }
         }
 #pragma unroll
@@ -216,13 +242,14 @@ struct Raw {
     // 2^-133, which KEY_UP takes to float16's.
     static __device__ __forceinline__ int power(float x) { return max(__builtin_amdgcn_frexp_expf(x), -95); }
 
-    // Values to `v` [blocks of 16][DB][2][32] of 16 bytes, divided by 2^exponent,
-    // which rises to the tile's largest.  Whether the tile is finite.
-    __device__ __forceinline__ bool values(u32x4* v, int& exponent, int blk, int part) const {
-        const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
+    // Values to `v` [blocks of 16][DB][2][32] of 16 bytes, divided by 2^(what is
+    // returned), `exponent` or, where the tile holds zeros only, ZEROS; where that
+    // is OWN, each token by 2^(its `powers` [KEYS]).  `good`: the tile is finite.
+    __device__ __forceinline__ int values(u32x4* v, int& exponent, int* powers, int blk, int part, bool& good) const {
+        const int lane = lane_of<SHORT>(), n = lane & 15, h = lane >> 4;
         u32x2* to = reinterpret_cast<u32x2*>(v + ((blk * DB + part * (DB / SPLIT)) * 2 + (h & 1)) * 32 + n) + (h >> 1);
         float most = 0.0f;
-        bool good = true;
+        good = true;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             const float x = half_lo<DT>(token_pairs[g]), y = half_hi<DT>(token_pairs[g]);
@@ -231,14 +258,22 @@ struct Raw {
             const float z = fmaxf(fabsf(y), fabsf(fmaf(15.0f, x, y)));
             most = live && finite ? fmaxf(most, z) : most;
         }
-        most = wave_max(most);
-        if (most > 0.0f) exponent = max(exponent, __builtin_amdgcn_frexp_expf(fminf(most, 0x1.fffffep127f)));
-        const int e = exponent;
+        const int own = most > 0.0f ? __builtin_amdgcn_frexp_expf(fminf(most, 0x1.fffffep127f)) : TileInfo::ZEROS;
+        auto far = [&] { return __any(live && (uint32_t)(exponent - own) > 5u); };
+        int result = exponent;
+        if (far()) {   // not the last tile's power: this one's, or one a token
+            const float all = wave_max(most);
+            if (all > 0.0f) exponent = __builtin_amdgcn_frexp_expf(fminf(all, 0x1.fffffep127f));
+            result = all == 0.0f ? TileInfo::ZEROS : far() ? TileInfo::OWN : exponent;
+            if (result == TileInfo::OWN && blk == 0 && part == 0 && lane < KEYS) powers[lane] = own;
+        }
         uint32_t pair[SHARE];   // scale 2^18 and bias, float16
 #pragma unroll
         for (int r = 0; r < SHARE; ++r) {
             const float x = half_lo<DT>(share[r]), y = half_hi<DT>(share[r]);
-            const bool use = there && 4 * h + ((16 * r + n) & (4 * G - 1)) / G < tokens && (x - x) + (y - y) == 0.0f;
+            const int token = 4 * h + ((16 * r + n) & (4 * G - 1)) / G;
+            const bool use = there && token < tokens && (x - x) + (y - y) == 0.0f;
+            const int e = result == TileInfo::OWN ? __shfl(own, 16 * blk + token, 64) : exponent;
             pair[r] = use ? __builtin_bit_cast(uint32_t, half2_of(ldexpf(x, 18 - e), ldexpf(y, -e))) : 0u;
         }
 #pragma unroll
@@ -268,7 +303,7 @@ struct Raw {
                 to[2 * ((cb >> 1) * 64 + (cb & 1) * 16)] = x;
             }
         }
-        return good;
+        return result;
     }
     static __device__ __forceinline__ uint32_t pair_at(const uint32_t (&pair)[SHARE], int at) {
         return (uint32_t)__float_as_int(row_lane(__int_as_float((int)pair[at / 16]), at % 16));
@@ -282,11 +317,14 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
     constexpr int KS = D / 16, DB = D / 32, G = D / GS, BK = W::BK, KEYS = W::KEYS, NT = KEYS / 32;
     constexpr int KQ = D == 256 ? KS / 2 : KS;   // steps whose queries stay in registers; the others' in LDS
     constexpr int AHEAD = D == 256 ? 2 : 4;      // operands read ahead
-    constexpr float kSlack = 8.0f;
+    // The largest score has a probability of 2^8, later ones may reach 2^15: float16
+    // holds what is down to 2^-33 of the largest.
+    constexpr float kUp = 8.0f, kSlack = 7.0f;
+    constexpr float kLeast = -0x1.8p127f;   // under every score
     __shared__ u32x4 s_k[2][NT * (BK + KS) * 64], s_v[3][2 * NT * DB * 64];
     __shared__ u32x4 s_q[PROMPT_WAVES][KS > KQ ? (KS - KQ) * 64 : 1];
     __shared__ float s_factor[2][W::SCALED ? 1 : G * KEYS];
-    __shared__ int s_key_power[3][W::SCALED ? KEYS : 1];
+    __shared__ int s_key_power[3][W::SCALED ? KEYS : 1], s_value_power[3][KEYS];
     __shared__ TileInfo s_info[3];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, n = lane & 31, hh = lane >> 5;
@@ -383,8 +421,8 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
             }
         }
 
-        float m = 0.0f, top = -INFINITY, l = 0.0f;
-        int most = 2 * W::EMPTY;   // the sums o are divided by 2^most
+        float top = kLeast, l = 0.0f;   // what a score may reach, and the sum of probabilities
+        int power = TileInfo::ZEROS, common = power;   // the row's sums o are divided by 2^power; all rows', or NONE
         f32x16 o[DB];
 #pragma unroll
         for (int d = 0; d < DB; ++d)
@@ -404,8 +442,17 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                 pages = blk < blocks ? table[blk >> c.page_shift] : -1;
             }
         };
+        // Keys' powers that take the wave's rows' rf neither to 0 nor to infinity.
+        const float rf = W::SCALED ? ldexpf(a.scale_log2, shift) : score_scale(a, shift);
+        int lowest = TileInfo::ZEROS, highest = TileInfo::OWN - 1;
+        if constexpr (W::SCALED) {
+            const int e = shift + __builtin_amdgcn_frexp_expf(a.scale_log2);
+            const int most = (int)wave_max((float)(4096 + e)) - 4096, least = 4096 - (int)wave_max((float)(4096 - e));
+            if (least > -125 && most < 127) lowest = max(lowest, -125 - least), highest = min(highest, 127 - most);
+            else lowest = TileInfo::OWN;
+        }
         W raw;
-        int exponent = W::EMPTY;   // of the values so far (the waves that turn them)
+        int exponent = TileInfo::ZEROS;   // of the last keys or values that the wave turned
         auto load = [&](int tile) {
             raw.load(c, pages, tile % FETCH * BLOCKS, head, key0 + KEYS * tile, my_blk, my_part, part_end, value);
         };
@@ -455,20 +502,27 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
             const int key = key0 + KEYS * tile + 32 * t;
             const u32x4* sv = s_v[buffer] + 2 * t * DB * 64 + lane;
             const int now = __builtin_amdgcn_readfirstlane(info.value_exponent);
-            bool all = key >= full_lo && key + 31 <= full_hi, there[2];
-            float by[2];   // what takes a block's scores to powers of two
+            auto of_tile = [&](int e) { return 32 * t + 8 * (e / 4) + 4 * hh + e % 4; };   // the lane's e-th key
+            bool all = key >= full_lo && key + 31 <= full_hi, there[2] = {true, true};
+            float by[W::SCALED ? 2 : 1];   // what takes a block's scores to powers of two
+            const int e0 = __builtin_amdgcn_readfirstlane(info.block[2 * t]);
+            const int e1 = __builtin_amdgcn_readfirstlane(info.block[2 * t + 1]);
+            by[0] = W::SCALED ? ldexpf(rf, e0) : rf;
+            if constexpr (W::SCALED) by[1] = ldexpf(rf, e1);
+            if (__builtin_expect(min(e0, e1) < lowest || max(e0, e1) > highest, 0)) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int e = __builtin_amdgcn_readfirstlane(info.block[2 * t + b]);
-                there[b] = e != TileInfo::MISSING;
-                all = all && there[b];
-                by[b] = score_scale(a, W::SCALED && there[b] ? shift + e : shift);
-                if (W::SCALED && e == TileInfo::OWN) {
-                    by[b] = 1.0f;
+                for (int b = 0; b < 2; ++b) {
+                    const int e = b ? e1 : e0;
+                    there[b] = e != TileInfo::MISSING;
+                    all = all && there[b];
+                    if constexpr (W::SCALED) {
+                        by[b] = e == TileInfo::OWN ? 1.0f : score_scale(a, there[b] ? shift + e : 0);
+                        if (e == TileInfo::OWN) {
 #pragma unroll
-                    for (int z = 0; z < 8; ++z)
-                        x[8 * b + z] = ldexpf(x[8 * b + z] * a.scale_log2,
-                                              shift + s_key_power[buffer][32 * t + 16 * b + 8 * (z / 4) + 4 * hh + z % 4]);
+                            for (int z = 8 * b; z < 8 * b + 8; ++z)
+                                x[z] = ldexpf(x[z] * a.scale_log2, shift + s_key_power[buffer][of_tile(z)]);
+                        }
+                    }
                 }
             }
             if (!all) {
@@ -485,29 +539,56 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                 float z = x[8 * b];
 #pragma unroll
                 for (int e = 1; e < 8; ++e) z = fmaxf(z, x[8 * b + e]);
-                mx = fmaxf(mx, z * by[b]);
+                mx = fmaxf(mx, z * by[W::SCALED ? b : 0]);
             }
-            if (__any(mx > top)) {
+            float base = top - (kUp + kSlack);   // what scores lose before they are exponents
+            if (now != common || __any(mx > top)) {
+                const bool fresh = top == kLeast;
                 float higher = fmaxf(mx, top - kSlack);
                 higher = fmaxf(higher, __shfl_xor(higher, 32, 64));
-                const float safe = higher > -INFINITY ? higher : 0.0f;
-                const float fade = top > -INFINITY ? __builtin_amdgcn_exp2f(m - safe) : 0.0f;
                 top = higher + kSlack;
-                m = safe;
+                float fade = __builtin_amdgcn_exp2f(base - (top - (kUp + kSlack)));
+                base = top - (kUp + kSlack);
                 l *= fade;
+                if (__builtin_expect(now != common, 0)) {
+                    // The sums' power rises to the largest that the row sees.
+                    auto power_of = [&](int e) {
+                        const int own = s_value_power[buffer][of_tile(e)];
+                        return now == TileInfo::OWN ? own : now;
+                    };
+                    int r = TileInfo::ZEROS, most = power;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) r = x[e] > -INFINITY ? max(r, power_of(e)) : r;
+                    r = max(r, __shfl_xor(r, 32, 64));
+                    if (fresh) {
+                        most = now != TileInfo::OWN && top == kLeast ? now : r;   // any: there is no sum yet
+                    } else {
+                        r = max(r, most);
+                        fade = ldexpf(fade, max(most - r, -126));
+                        most = r;
+                    }
+                    power = most;
+                    common = __builtin_amdgcn_readfirstlane(most);
+                    if (__any(most != common)) common = TileInfo::NONE;
+                    if (now != common) {   // what is left of a token's power goes to its probability, but not to their sum
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float z = fmaf(x[e], by[W::SCALED ? e / 8 : 0], -base);
+                            x[e] = z + (float)min(power_of(e) - most, 0);
+                            l += __builtin_amdgcn_exp2f(z) - __builtin_amdgcn_exp2f(x[e]);
+                        }
+#pragma unroll
+                        for (float& b : by) b = 1.0f;
+                        base = 0.0f;
+                    }
+                }
 #pragma unroll
                 for (int d = 0; d < DB; ++d) o[d] *= fade;
-            }
-            if (now > most) {
-                const float fade = ldexpf(1.0f, most - now);
-#pragma unroll
-                for (int d = 0; d < DB; ++d) o[d] *= fade;
-                most = now;
             }
             u32x4 p[2];
             auto pair = [&](int e) {   // two probabilities
-                const float p0 = __builtin_amdgcn_exp2f(fmaf(x[2 * e], by[e / 4], -m));
-                const float p1 = __builtin_amdgcn_exp2f(fmaf(x[2 * e + 1], by[e / 4], -m));
+                const float p0 = __builtin_amdgcn_exp2f(fmaf(x[2 * e], by[W::SCALED ? e / 4 : 0], -base));
+                const float p1 = __builtin_amdgcn_exp2f(fmaf(x[2 * e + 1], by[W::SCALED ? e / 4 : 0], -base));
                 l += p0 + p1;
                 p[e / 4][e % 4] = __builtin_bit_cast(uint32_t, half2_of(p0, p1));
             };
@@ -564,14 +645,15 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
         auto turn = [&](int t, int after) {
             if (t + 1 < tiles) {
                 if (value) {
-                    const bool good = raw.values(s_v[after], exponent, my_blk, my_part);
+                    bool good;
+                    const int e = raw.values(s_v[after], exponent, s_value_power[after], my_blk, my_part, good);
                     if (wave == 4) {
                         if (!good) s_info[after].bad = t + 2;
-                        s_info[after].value_exponent = exponent;
+                        s_info[after].value_exponent = e;
                     }
                 } else {
-                    const int e = raw.keys(s_k[(t + 1) & 1], s_factor[(t + 1) & 1], s_key_power[after], my_blk,
-                                           my_part);
+                    const int e = raw.keys(s_k[(t + 1) & 1], s_factor[(t + 1) & 1], exponent, s_key_power[after],
+                                           my_blk, my_part);
                     if (my_part == 0) s_info[after].block[my_blk] = raw.there ? e : TileInfo::MISSING;
                 }
             }
@@ -599,10 +681,12 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
 
         l += __shfl_xor(l, 32, 64);
         if (mine && n < rows) {
-            const bool seen = top > -INFINITY || l != l;
+            const bool seen = top > kLeast || l != l;
+            const float m = top - (kUp + kSlack);
+            const int most = power;
             const long long at = token * a.heads + qhead;
             const long long place = ((long long)u.place * c.heads + head) * PROMPT_ROWS + 32 * wave + n;
-            const float inv = u.place >= 0 ? 1.0f : l != 0.0f ? 1.0f / l : 0.0f;
+            const float inv = l != 0.0f ? 1.0f / l : 0.0f;   // parts too: their sums may pass float32's range
 #pragma unroll
             for (int d = 0; d < DB; ++d)
 #pragma unroll

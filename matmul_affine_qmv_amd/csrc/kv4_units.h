@@ -264,8 +264,8 @@ __global__ __launch_bounds__(256) void kv4_join_prompt_kernel(Kv4AttnArgs a) {
         for (int w = parts.first; w <= parts.last; ++w) {
             const long long p = parts.place(w);
             const f32x2 st = stat[p];
-            const float f = __builtin_amdgcn_exp2f(st[0] - safe);
-            l += st[1] * f;
+            const float f = st[1] * __builtin_amdgcn_exp2f(st[0] - safe);   // the part is over its sum
+            l += f;
             o += *reinterpret_cast<const f32x4*>(a.part + p * D + 4 * lane) * f;
         }
         const int row = tile * a.p.rows + r, i = row / a.each;

@@ -371,7 +371,7 @@ FAR = {"bf16": 2.0 ** 60, "f16": 2.0 ** 12}
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("D,group", [(64, 32), (64, 64), (128, 32), (128, 128), (256, 32), (256, 64)])
 @pytest.mark.parametrize("lens", [[(0, 50), (70, 33)], [(1900, 40)]])
-@pytest.mark.parametrize("what", ["keys"])
+@pytest.mark.parametrize("what", ["keys", "values", "both"])
 def test_hidden_tokens_cost_nothing(dtype, D, group, lens, what):
     """Tokens of huge keys or values that only the last queries see leave the others' digits alone."""
     say("hidden", dtype, D, group, lens, what)
@@ -411,4 +411,50 @@ def test_queries_with_elements_that_meet_zeros(dtype, D, group, new):
     rng, c, q, table, kv, offsets = spread_case(dtype, D, group, [(90, new)], 54)
     c.s[0][..., 0] = c.b[0][..., 0] = 0
     q[..., :group] *= 2.0 ** 13
+    held_to(c, q, table, kv, offsets)
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (256, 64)])
+@pytest.mark.parametrize("window", [20, 100])
+def test_tokens_before_the_window_cost_nothing(dtype, D, group, window):
+    say("window", dtype, D, group, window)
+    rng, c, q, table, kv, offsets = spread_case(dtype, D, group, [(160, 40), (0, 50)], 51)
+    for x in (c.s[0], c.b[0], c.s[1], c.b[1]):
+        x *= 2.0 ** -6
+    for r, t in ((0, 62), (0, 145), (0, 150), (1, 1)):
+        for x in (c.s[0], c.b[0], c.s[1], c.b[1]):
+            x[at(table, 32, r, t)] *= FAR[dtype]
+    held_to(c, q, table, kv, offsets, window=window)
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype,powers", [("bf16", 1), ("bf16", 4), ("bf16", 12), ("bf16", 40), ("f16", 1), ("f16", 4),
+                                          ("f16", 7)])
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 32), (128, 64), (256, 128)])
+@pytest.mark.parametrize("lens", [[(0, 70), (90, 40)], [(1800, 50)]])
+def test_magnitudes_of_every_token(dtype, powers, D, group, lens):
+    """Values that differ from token to token by up to 4 ** powers; a stretch of zeros."""
+    say("powers", dtype, powers, D, group, lens)
+    rng, c, q, table, kv, offsets = spread_case(dtype, D, group, lens, 52 + powers)
+    factor = 2.0 ** rng.integers(-powers, powers + 1, (*c.s[1].shape[:3], 1))
+    for x in (c.s[1], c.b[1]):
+        x *= factor
+        x[:] = torch.from_numpy(x).to(ref.TYPES[dtype]).double().numpy()
+        x[1] = 0
+    held_to(c, q, table, kv, offsets)
+
+
+@on_gpu
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (256, 64)])
+@pytest.mark.parametrize("lens", [[(0, 70), (90, 40)], [(1800, 50)]])
+def test_rising_and_falling_values(D, group, lens):
+    """Values that rise by 2^40 over a request, and fall again."""
+    say("rising", D, group, lens)
+    rng, c, q, table, kv, offsets = spread_case("bf16", D, group, lens, 60)
+    for r, length in enumerate(kv):
+        for t in range(length):
+            for x in (c.s[1], c.b[1]):
+                x[at(table, 32, r, t)] *= 2.0 ** round(40 * math.sin(math.pi * t / length))
     held_to(c, q, table, kv, offsets)
