@@ -44,6 +44,9 @@ struct Kv4AttnPlan {
     int lines, least;
     int cost;     // what a unit costs beside its steps, in steps: on a line, units stand this far apart
 };
+// Waves of a work-group that takes few rows' units whole, by head size: eight of
+// 256 would leave a CU one work-group (138 KB of LDS).
+constexpr int few_row_waves(int dim) { return dim == 256 ? 4 : 8; }
 // Most units of a head that can be laid end to end, by a work-group's waves.
 constexpr int kv4_line_units(int waves) { return waves == 4 ? 1024 : 512; }
 

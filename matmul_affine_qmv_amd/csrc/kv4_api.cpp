@@ -97,7 +97,7 @@ Kv4AttnPlan kv4_attn_plan(int requests, int heads, int kv_heads, int dim, int ma
     const bool uneven = !prompt || groups < cus * 3 / 4 || (keys > 2ll * max_query && groups < 4ll * cus);
     const bool line = keys > 1536 && uneven && units > 0 && units <= kv4_line_units(prompt ? kv4::PROMPT_WAVES : 4) &&
                       units * (keys / 32 + 32) <= INT_MAX;
-    p.waves = prompt ? kv4::PROMPT_WAVES : line || dim == 256 ? 4 : 8;
+    p.waves = prompt ? kv4::PROMPT_WAVES : line ? 4 : few_row_waves(dim);
     p.lines = line ? std::max(1, (prompt ? 1 : 2) * cus / kv_heads) : 0;
     // A unit's queries, first loads and joining waves wait on memory about four
     // times, as long as its work-group takes for some 8 steps (48 tokens over up to

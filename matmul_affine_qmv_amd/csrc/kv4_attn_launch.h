@@ -10,9 +10,17 @@ namespace kv4 {
 template <int D, int GS, int DT>
 hipError_t launch_format(const Kv4AttnArgs& a, hipStream_t st) {
     const unsigned groups = (unsigned)(kv4_groups(a));
-    if (a.p.rows == PROMPT_ROWS) kv4_prompt_kernel<D, GS, DT><<<groups, 64 * PROMPT_WAVES, 0, st>>>(a);
-    else if (a.p.waves == 8) kv4_attn_kernel<D, GS, DT, 8><<<groups, 512, 0, st>>>(a);
-    else kv4_attn_kernel<D, GS, DT, 4><<<groups, 256, 0, st>>>(a);
+    if (a.p.rows == PROMPT_ROWS) {
+        kv4_prompt_kernel<D, GS, DT><<<groups, 64 * PROMPT_WAVES, 0, st>>>(a);
+        return hipGetLastError();
+    }
+    if constexpr (few_row_waves(D) == 8) {
+        if (a.p.waves == 8) {
+            kv4_attn_kernel<D, GS, DT, 8><<<groups, 512, 0, st>>>(a);
+            return hipGetLastError();
+        }
+    }
+    kv4_attn_kernel<D, GS, DT, 4><<<groups, 256, 0, st>>>(a);
     return hipGetLastError();
 }
 
