@@ -458,3 +458,25 @@ def test_rising_and_falling_values(D, group, lens):
             for x in (c.s[1], c.b[1]):
                 x[at(table, 32, r, t)] *= 2.0 ** round(40 * math.sin(math.pi * t / length))
     held_to(c, q, table, kv, offsets)
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype,limit", [("f16", 0.60), ("bf16", 0.45)])
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 64), (256, 128)])
+def test_prompts_add_little_to_the_rounding_of_the_output(dtype, limit, D, group):
+    """The root mean square of what a prompt's outputs are off, beside that of their own rounding.  A rounding is off by
+    u / sqrt(3) at a mantissa of 1 and half that at 2, r = 0.424 u over log-even mantissas, and a sum of random signs keeps
+    that relative to itself.  A float16 output has r of its own; one more, the values', gives sqrt(2) r = 0.60 u (a third,
+    the probabilities' as one float16 number, gave 0.63 to 0.66 u).  A bfloat16 output's own r is of 2^-8, whose square two
+    at 2^-11 raise by 2 / 64: 0.43, under 0.45 of 2^-8 with 9000 and more outputs drawn."""
+    say("rounding", dtype, D, group)
+    rng, c, q, table, kv, offsets = spread_case(dtype, D, group, [(400, 64), (0, 90)], 70)
+    for x in (c.s[0], c.b[0]):   # scores of about 1
+        x *= 0.3
+    for x in (*c.s, *c.b):
+        x[:] = torch.from_numpy(x).to(c.dtype).double().numpy()
+    out = qmx.kv4_attention(device_cache(c), q.to(DEV), torch.from_numpy(table).to(DEV), ints(kv), ints(offsets),
+                            max_query_len=90, max_kv_len=max(kv)).double().cpu().numpy()
+    want = expected(c, q, table, kv, offsets, prompt=True)[0]
+    off = np.sqrt(((out - want) ** 2).mean() / (want ** 2).mean())
+    assert off <= limit * ref.HALF[dtype], off / ref.HALF[dtype]
