@@ -80,20 +80,25 @@ Kv4AttnPlan kv4_attn_plan(int requests, int heads, int kv_heads, int dim, int ma
     Kv4AttnPlan p;
     const long long rows = (long long)max_query * (heads / kv_heads);
     const long long keys = window ? std::min((long long)max_kv, (long long)window + max_query) : (long long)max_kv;
-    // Few rows or many: 8 requests over 4000 keys (8 key heads of 128) take 43 us by
-    // units of 16 rows and 48 by the prompt kernel at 48 rows, 49 and 49 at 64, 69
-    // and 53 at 96; the same border at heads of 64 and 256.
+    // Few rows or many: 8 requests over 4000 keys (8 key heads of 128, bfloat16) take
+    // 44 us by units of 16 rows and 61 by the prompt kernel at 48 rows, 53 and 62 at
+    // 64, 71 and 65 at 96; heads of 64: 40 and 46 at 64, 51 and 48 at 96; of 256: 99
+    // and 109, 141 and 112.
     const bool prompt = rows > 64;
     p.rows = prompt ? kv4::PROMPT_ROWS : 16;
     p.tiles = (int)((rows + p.rows - 1) / p.rows);
     const long long units = (long long)requests * p.tiles, groups = units * kv_heads;
-    // Units whole or on a line.  Few rows: joining costs some 5 us, a wait through
-    // 1500 keys more than a short one as much (one request: 12.5 whole and 14.9 us on
-    // a line over 1000 keys, 15.8 and 15.6 over 1500, 22 and 16 over 2500; 64
-    // requests 17 and 21, 21 and 21, 26 and 25).  Prompts: units enough even each
-    // other out, and parts are written and joined in 32 bits (4096 tokens: 185 us
-    // whole, 222 on a line); behind a long prefix requests differ (12 of up to 512
-    // tokens over up to 4000: 168 and 152; 3 of up to 300 over 20000: 685 and 178).
+    // Units whole or on a line.  Few rows: joining costs some 5 us, which a walk of
+    // 1000 to 1500 keys more costs too (one token of 32 heads on 8 key heads of 128: 12.8
+    // us whole and on a line over 1000 keys, 16.6 and 12.8 over 1500, 24 and 13 over
+    // 2500; 64 such requests of one length are the same, whose parts are units).
+    // Prompts: units enough even each other out, and parts are written and joined in
+    // 32 bits (4096 tokens: 197 us whole, 233 on a line); behind a long prefix
+    // requests differ (12 of up to 512 tokens over up to 4000, heads of 256: 547 and
+    // 220; 3 of up to 300 over 20000: 704 and 185).  Few prompt rows take the same
+    // limit of keys, though a line is faster for one request from some 700 on (100
+    // tokens: 25 whole and 30 us over 300 keys, 49 and 39 over 1000, 64 and 48 over
+    // 1500; 8 requests 26 and 44, 51 and 58, 67 and 69).
     const bool uneven = !prompt || groups < cus * 3 / 4 || (keys > 2ll * max_query && groups < 4ll * cus);
     const bool line = keys > 1536 && uneven && units > 0 && units <= kv4_line_units(prompt ? kv4::PROMPT_WAVES : 4) &&
                       units * (keys / 32 + 32) <= INT_MAX;
@@ -101,7 +106,7 @@ Kv4AttnPlan kv4_attn_plan(int requests, int heads, int kv_heads, int dim, int ma
     p.lines = line ? std::max(1, (prompt ? 1 : 2) * cus / kv_heads) : 0;
     // A unit's queries, first loads and joining waves wait on memory about four
     // times, as long as its work-group takes for some 8 steps (48 tokens over up to
-    // 8000: 26.2 us with 8, 27.3 with 16, 31.6 with 32).
+    // 8000, joined: 33.3 us with 8, 34.4 with 16, 39.5 with 32).
     p.cost = 8;
     p.least = 8;
     return p;

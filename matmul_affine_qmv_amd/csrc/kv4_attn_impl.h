@@ -38,15 +38,16 @@
 // scores.  A step's loads go out into the registers that the step before has just
 // used, so a wave has a step under way in 60 registers fewer than with two sets.
 //
-// Measured: one token of 64 heads over 131000 cached ones (8 key heads of 128,
-// groups of 128, float16) 37 us and 5 us for joining the parts, 143 MB at 3.4 TB/s
-// (a large copy: 4.9); bound by what is in flight, two waves a SIMD with 4.6 KB
-// each (three, where registers allow: 34 + 6 us).  48 tokens over up to 8000
-// (40 heads, bfloat16) 27 + 5 us for 64 MB: half of it is the wait for lengths, block
-// table, queries and first codes, one after the other.  Cut by splits of one
-// length for all requests, as the host alone could do it, they took 55 + 14 and
-// 40 + 4 us.  Pairs read by every lane that needs them instead of shared by a row
-// cost 72 registers and 20 % of the time.
+// Measured: two tokens of 64 heads over up to 131000 cached ones (8 key heads of
+// 128, groups of 128, float16) 38 us and 5 us for joining the parts, 143 MB at 3.3
+// TB/s (a large copy: 4.9); bound by what is in flight, two waves a SIMD with 4.6 KB
+// each.  48 tokens over up to 8000 (40 heads, bfloat16) 28 + 5.5 us for 64 MB: half
+// of it is the wait for lengths, block table, queries and first codes, one after the
+// other.  Cut by splits of one length for all requests, as the host alone could do
+// it, they took 55 + 14 and 40 + 4 us.  Pairs read by every lane that needs them
+// instead of shared by a row cost 72 registers and 20 % of the time.  Heads of 256
+// spill 49 registers in groups of 64 and 240 in groups of 32, whose 48 tokens over up
+// to 8000 take 72 and 239 us (groups of 128, none spilled: 43).
 #pragma once
 
 #include <type_traits>

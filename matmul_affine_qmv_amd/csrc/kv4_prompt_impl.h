@@ -11,13 +11,16 @@
 // stand among the products for the scores of the next 32.
 //
 // Measured: a prompt of 8192 tokens, 32 heads of 128 on 8 key heads, groups of 64,
-// bfloat16: 651 us in a warm loop, 845 TFLOP/s, where a library matrix product
-// reaches 1209.  The matrix cores are busy 37 % of the cycles and the vector ALU
-// 55 %, 15 % both at once: a barrier a tile holds the waves together, and they do
+// bfloat16: 670 to 700 us in a warm loop, 785 to 820 TFLOP/s, where a library matrix
+// product reaches 1209.  The matrix cores are busy 38 % of the cycles and the vector
+// ALU 56 %, 15 % both at once: a barrier a tile holds the waves together, and they do
 // the same things at the same time.  Setting half the waves half a tile off, or a
 // priority for those at the products, changed nothing (1 %).  Turning the codes
 // costs a sixth.  Keys of rounded numbers instead of exact scores took the same
-// time, with scores off by 2^-12 each.
+// time, with scores off by 2^-12 each.  Groups of 32 and 128: 716 and 657 where 64
+// take 670; heads of 64 491; float16 935 (groups of 32 2180, of 128 907; heads of 64
+// 650).  What is spilled: of float16 at 128, 8 registers in groups of 128, 18 of 64
+// and 81 of 32; at 256, 17 to 48.
 //
 //   S^T[key, row] = K Q^T,  O^T[dim, row] += V^T P:  v_mfma_32x32x16, where the
 //   probabilities that a lane computes are the operand it needs (as in
