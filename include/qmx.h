@@ -457,13 +457,16 @@ int qmx_kv4_read(const qmx_kv4_cache* cache, void* k_out, void* v_out, const int
  *   scale : finite and above 0.
  *   workspace : qmx_kv4_attention_workspace_bytes bytes, 16-byte aligned (NULL
  *           where that is 0), overwritten; calls that share it are ordered.
- * Scores and sums are float32 on exact codes.  What the value codes are multiplied
- * by, a probability times a scale, is held in two bfloat16 numbers, to 2^-16 of
- * itself; with more than 64 query rows a key head (max_query_len * heads /
- * kv_heads), values and, in a bfloat16 cache, probabilities are rounded to float16
- * instead, to 2^-11 of themselves, values also to 2^-18 of their token's largest,
- * and the product of both to 2^-26 of the largest finite value that the query sees.  How the keys are
- * cut among work-groups follows the lengths and these arguments, so reruns with
+ * Scores and sums are float32 on exact codes; elements of queries count down
+ * to 2^-40 of their row's largest, with more than 64 query rows a key head
+ * those of bfloat16 keys to 2^-31 of their token's. What the value codes are
+ * multiplied by, a probability times a scale, is held in two bfloat16
+ * numbers, to 2^-16 of itself; with more than 64 query rows a key head
+ * (max_query_len * heads / kv_heads), values and, in a bfloat16 cache,
+ * probabilities are rounded to float16 instead, to 2^-11 of themselves,
+ * values also to 2^-18 of their token's largest, and the product of both to
+ * 2^-26 of the largest finite value that the query sees. How the keys are cut
+ * among work-groups follows the lengths and these arguments, so reruns with
  * the same are bit-identical. */
 int qmx_kv4_attention(const qmx_kv4_cache* cache, const void* q, long long q_token_stride,
                       long long q_head_stride, void* out, float* lse, const int32_t* block_table,

@@ -18,8 +18,8 @@
 // priority for those at the products, changed nothing (1 %).  Turning the codes
 // costs a sixth.  Keys of rounded numbers instead of exact scores took the same
 // time, with scores off by 2^-12 each.  Groups of 32 and 128: 716 and 657 where 64
-// take 670; heads of 64 491; float16 935 (groups of 32 2180, of 128 907; heads of 64
-// 650).  What is spilled: of float16 at 128, 8 registers in groups of 128, 18 of 64
+// take 670; heads of 64 491; float16 940 (groups of 32 2080, of 128 910; heads of 64
+// 650).  What is spilled: of float16 at 128, 12 registers in groups of 128, 23 of 64
 // and 81 of 32; at 256, 17 to 48.
 //
 //   S^T[key, row] = K Q^T,  O^T[dim, row] += V^T P:  v_mfma_32x32x16, where the
@@ -57,7 +57,7 @@
 // 3.2e-4 of the exact result where float32 products are off by 2.1e-4.  So there
 // what a probability loses enters as a second float16 number: 2.8e-4, for half as
 // many products again and 24 vector instructions per 32 keys (12 requests over
-// 4000 keys, heads of 256: 184 -> 201 us; 8192 tokens, heads of 128: 725 -> 935).
+// 4000 keys, heads of 256: 184 -> 201 us; 8192 tokens, heads of 128: 725 -> 940).
 // bfloat16 outputs are off by 1.7e-3 either way.
 //
 // 0 * NaN is NaN in a product, so values that are not finite are entered as 0
@@ -140,12 +140,11 @@ struct Raw {
     static constexpr int SLOTS = SCALED ? 8 : 4;                  // of a group in the product of biases
     static constexpr int BK = (SLOTS * G + 15) / 16;              // its steps
     static constexpr int SHARE = (4 * G + 15) / 16;               // a lane's share of a block's pairs
-    // Where lane_of is to hide what it knows.  8192 tokens, heads of 128, float16:
-    // groups of 32 3926 us without and 1929 with, of 64 780 and 750 (keys only; all
-    // 769); heads of 256, 12 requests over 4000 keys: 240 and 213.  Where nothing is
-    // spilled it costs 6 to 10 %.
+    // Where lane_of is to hide what it knows: 8192 tokens, heads of 128, float16 in
+    // groups of 32 2384 us without and 2079 with; heads of 256, 12 requests over 4000
+    // keys, float16 220 and 203, bfloat16 166 and 154.  Where little or nothing is
+    // spilled it costs 1 to 4 %.
     static constexpr bool SHORT = D == 256 || (DT == DT_F16 && D == 128 && GS == 32);
-    static constexpr bool SHORT_KEYS = DT == DT_F16 && D == 128;
     // Powers of two that keys, queries and the queries' sums are brought to, and
     // what a score is multiplied by in all.
     static constexpr int KEY_UP = 14, QUERY_UP = 15, SUM_UP = SCALED ? QUERY_UP : 8;
@@ -189,7 +188,7 @@ struct Raw {
     // [G][KEYS].
     __device__ __forceinline__ int keys(u32x4* k, float* factor, int& exponent, int* powers, int blk,
                                         int part) const {
-        const int lane = lane_of<SHORT || SHORT_KEYS>(), n = lane & 15, h = lane >> 4;
+        const int lane = lane_of<SHORT>(), n = lane & 15, h = lane >> 4;
         u32x4* to = k + (blk >> 1) * (BK + KS) * 64 + (blk & 1) * 16 + n;
         int e = 0, result = 0;
         if constexpr (SCALED) {
@@ -580,7 +579,7 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
                     power = most;
                     common = __builtin_amdgcn_readfirstlane(most);
                     if (__any(most != common)) common = TileInfo::NONE;
-                    if (now != common) {   // what is left of a token's power goes to its probability, but not to their sum
+                    if (now != common) {   // what is left of a power goes to the probability, but not to their sum
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const float z = fmaf(x[e], by[W::SCALED ? e / 8 : 0], -base);

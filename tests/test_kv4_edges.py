@@ -13,7 +13,6 @@ Bounds.  ``u`` is half a step of the type, 2^-24 that of float32.  For a token, 
   largest elements), which moves the output by sum p_t expm1(2 E_t) |v_t - out| and the logarithm of the sum by
   log sum p_t exp(E_t) at most.
 """
-import ctypes
 import math
 
 import numpy as np
@@ -22,7 +21,7 @@ import torch
 
 import kv4_reference as ref
 import matmul_affine_qmv_amd as qmx
-from test_kv4 import DEV, FAKE, ccache, device_cache, fake_ptr_test, ints, on_gpu, say
+from test_kv4 import DEV, FAKE, device_cache, fake_ptr_test, ints, on_gpu, say
 
 U32 = ref.U32
 
@@ -464,11 +463,11 @@ def test_rising_and_falling_values(D, group, lens):
 @pytest.mark.parametrize("dtype,limit", [("f16", 0.60), ("bf16", 0.45)])
 @pytest.mark.parametrize("D,group", [(64, 64), (128, 64), (256, 128)])
 def test_prompts_add_little_to_the_rounding_of_the_output(dtype, limit, D, group):
-    """The root mean square of what a prompt's outputs are off, beside that of their own rounding.  A rounding is off by
-    u / sqrt(3) at a mantissa of 1 and half that at 2, r = 0.424 u over log-even mantissas, and a sum of random signs keeps
-    that relative to itself.  A float16 output has r of its own; one more, the values', gives sqrt(2) r = 0.60 u (a third,
-    the probabilities' as one float16 number, gave 0.63 to 0.66 u).  A bfloat16 output's own r is of 2^-8, whose square two
-    at 2^-11 raise by 2 / 64: 0.43, under 0.45 of 2^-8 with 9000 and more outputs drawn."""
+    """The root mean square of what a prompt's outputs are off, beside that of their own rounding. A rounding is off
+    by u / sqrt(3) at a mantissa of 1 and half that at 2, r = 0.424 u over log-even mantissas, and a sum of random
+    signs keeps that relative to itself. A float16 output has r of its own; one more, the values', gives sqrt(2) r =
+    0.60 u (a third, the probabilities' as one float16 number, gave 0.63 to 0.66 u). A bfloat16 output's own r is of
+    2^-8, whose square two at 2^-11 raise by 2 / 64: 0.43, under 0.45 of 2^-8 with 9000 and more outputs drawn."""
     say("rounding", dtype, D, group)
     rng, c, q, table, kv, offsets = spread_case(dtype, D, group, [(400, 64), (0, 90)], 70)
     for x in (c.s[0], c.b[0]):   # scores of about 1
