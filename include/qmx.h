@@ -481,6 +481,102 @@ int qmx_kv4_attention(const qmx_kv4_cache* cache, const void* q, long long q_tok
 size_t qmx_kv4_attention_workspace_bytes(int kv_heads, int head_dim, int requests, int tokens,
                                          int heads, int max_query_len, int max_kv_len, int window);
 
+/* ------------------------------------------------------------------------
+ * 8-bit floats: a layer's products, and what stands before and between them.
+ *
+ * Elements are e4m3 codes (a sign, 4 bits of exponent with bias 7, 3 of
+ * mantissa; largest 448, no infinities, 0x7f a NaN), row-major, with one scale
+ * for each 128 neighbours of a row (activations: [rows, K / 128]) or for each
+ * block of 128 rows by 128 (weights: [ceil(rows / 128), K / 128]); an element
+ * with code c stands for c * s.
+ * QMX_SCALE_E8M0: one byte b, the power of two 2^(b - 127) (255: NaN).  Writing
+ * takes e, the least whole number from -127 on with amax <= 448 * 2^e for the
+ * group's largest magnitude amax, b = e + 127, and codes x * 2^-e rounded to
+ * nearest even: exact but for that rounding.  A group that holds a NaN or an
+ * infinity is NaN, whole (b = 255, codes 0x7f).
+ * QMX_SCALE_F32: float32 scales, as other programs write them for weights.
+ */
+typedef enum qmx_scale_type {
+    QMX_SCALE_E8M0 = 0,
+    QMX_SCALE_F32 = 1
+} qmx_scale_type;
+
+/* qmx_rms_norm -- root mean square norm of rows, after a residual's addition:
+ *   h = round(x + residual);   y = h * weight / sqrt(sum h^2 / width + eps).
+ * x, residual, sum: [rows, width] in `dtype` (QMX_F16 or QMX_BF16) with unit
+ * element stride, rows *_row_stride elements apart, at any address of whole
+ * elements; weight: [width] in `dtype`, or NULL for ones.  residual NULL: h = x,
+ * and sum must be NULL; otherwise sum receives h (QMX_ERR_NULL where only one of
+ * the two is given).  out_scales NULL: out is [rows, width] in `dtype`,
+ * contiguous.  Otherwise out is e4m3 codes [rows, width], 8-byte aligned, and
+ * out_scales [rows, width / 128] their E8M0 scales (width % 128 == 0, else
+ * QMX_ERR_GROUP).  sum may be x or residual itself, row for row, and an out in
+ * `dtype` may be x itself; otherwise outputs overlap nothing.  eps: finite and
+ * above 0.  y is formed in 64 bits and rounded once; a y beyond float32's range
+ * counts as infinite. */
+int qmx_rms_norm(const void* x, long long x_row_stride, const void* residual,
+                 long long residual_row_stride, const void* weight, void* sum,
+                 long long sum_row_stride, void* out, uint8_t* out_scales, int rows, int width,
+                 double eps, int dtype, void* stream);
+
+/* qmx_f8_quantize -- x [rows, width] in `dtype` (QMX_F16 or QMX_BF16; unit
+ * element stride, rows x_row_stride elements apart, any address of whole
+ * elements) into codes [rows, width], 16-byte aligned, and E8M0 scales: of each
+ * 128 of a row (block_rows = 1) or of each 128 x 128 (block_rows = 128; the last
+ * block of rows may be short).  width % 128 == 0 (QMX_ERR_GROUP);
+ * rows * width / 128 at most 2^31 - 1. */
+int qmx_f8_quantize(const void* x, long long x_row_stride, uint8_t* codes, uint8_t* scales,
+                    int rows, int width, int block_rows, int dtype, void* stream);
+
+/* qmx_f8_dequantize -- the values that codes stand for, c * s in float32 (exact
+ * for E8M0) rounded to `dtype`: out [rows, width], 16-byte aligned.  scale_type:
+ * qmx_scale_type, QMX_ERR_DTYPE otherwise; other arguments as qmx_f8_quantize. */
+int qmx_f8_dequantize(const uint8_t* codes, const void* scales, int scale_type, void* out,
+                      int rows, int width, int block_rows, int dtype, void* stream);
+
+/* qmx_qmm_f8 -- product of 8-bit floats on the matrix cores, for any M from one
+ * token on:
+ *   out[m,n] = sum_g xs[m,g] * ws[n/128,g] * sum_{k in g} x[m,k] * w[n,k]
+ * w: codes [N, K] with w_scales [ceil(N / 128), K / 128] of w_scale_type;
+ * x: codes [M, K] with E8M0 x_scales [M, K / 128]; out: [M, N] in `dtype`
+ * (QMX_F16 or QMX_BF16), rounded once.  K % 128 == 0 (QMX_ERR_GROUP), at most
+ * 2^24; w and x 16-byte aligned, out any address of whole elements.
+ * Sums are float32, but for the matrix instruction's own: it aligns the scaled
+ * products of 8 neighbouring k to the largest exponent among them and cuts each
+ * 2^-13 below that (measured; 1.6e-5 of the result on normal numbers).  A code or scale
+ * that is NaN makes the outputs of its row or block NaN.
+ * workspace: qmx_qmm_f8_workspace_bytes bytes, 16-byte aligned (NULL where that
+ * is 0), overwritten; calls that share it are ordered.  Reruns with the same
+ * arguments are bit-identical. */
+int qmx_qmm_f8(const uint8_t* w, const void* w_scales, int w_scale_type, const uint8_t* x,
+               const uint8_t* x_scales, void* out, int M, int N, int K, int dtype,
+               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes qmx_qmm_f8 needs (0 for arguments it refuses).  Depends on the
+ * compute units of the current device. */
+size_t qmx_qmm_f8_workspace_bytes(int M, int N, int K);
+
+/* qmx_rope -- rotary positions.  Of each head's elements the first 2 * pairs
+ * turn, pair i = 0..pairs-1 by t = positions[token] * frequencies[i]:
+ *   (a, b) -> scale * (a cos t - b sin t,  b cos t + a sin t),
+ * a and b being elements i and pairs + i, or, where `interleaved` is not 0, 2i
+ * and 2i + 1.  The others are copied, and so are whole tokens whose position is
+ * below 0 (as qmx_kv_maps writes behind the last token).
+ * q, k and their outputs: [tokens, heads or kv_heads, head_dim] in `dtype`
+ * (QMX_F16 or QMX_BF16), unit element stride, tokens and heads *_stride elements
+ * apart, any address of whole elements.  Either may have 0 heads (pointers may
+ * then be NULL).  An output is its own input, stride for stride (what does not
+ * turn is then left alone), or overlaps nothing.  positions: int32 [tokens];
+ * frequencies: float64 [pairs], radians a position; the angle is taken in 64
+ * bits, its sine and cosine in 32, the result is rounded once.  head_dim: 1 to
+ * 4096; 2 <= 2 * pairs <= head_dim; at most 8192 heads each; scale finite. */
+int qmx_rope(const void* q, long long q_token_stride, long long q_head_stride, void* q_out,
+             long long q_out_token_stride, long long q_out_head_stride, int heads, const void* k,
+             long long k_token_stride, long long k_head_stride, void* k_out,
+             long long k_out_token_stride, long long k_out_head_stride, int kv_heads,
+             const int32_t* positions, const double* frequencies, int tokens, int head_dim,
+             int pairs, int interleaved, float scale, int dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

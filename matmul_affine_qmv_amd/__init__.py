@@ -68,6 +68,19 @@ _EXPORTS = {
     "qmx_kv4_attention": (ctypes.c_int, [ctypes.c_void_p] * 2 + [ctypes.c_longlong] * 2 + [ctypes.c_void_p] * 3
                           + [ctypes.c_int, ctypes.c_longlong] + [ctypes.c_void_p] * 2 + [ctypes.c_int] * 6
                           + [ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qmx_rms_norm": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_longlong] * 2
+                     + [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_longlong] + [ctypes.c_void_p] * 2
+                     + [ctypes.c_int] * 2 + [ctypes.c_double, ctypes.c_int, ctypes.c_void_p]),
+    "qmx_f8_quantize": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_longlong] + [ctypes.c_void_p] * 2
+                        + [ctypes.c_int] * 4 + [ctypes.c_void_p]),
+    "qmx_f8_dequantize": (ctypes.c_int, [ctypes.c_void_p] * 2 + [ctypes.c_int, ctypes.c_void_p]
+                          + [ctypes.c_int] * 4 + [ctypes.c_void_p]),
+    "qmx_qmm_f8": (ctypes.c_int, [ctypes.c_void_p] * 2 + [ctypes.c_int] + [ctypes.c_void_p] * 3 + [ctypes.c_int] * 4
+                   + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qmx_qmm_f8_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 3),
+    "qmx_rope": (ctypes.c_int, ([ctypes.c_void_p] + [ctypes.c_longlong] * 2) * 2 + [ctypes.c_int]
+                 + ([ctypes.c_void_p] + [ctypes.c_longlong] * 2) * 2 + [ctypes.c_int] + [ctypes.c_void_p] * 2
+                 + [ctypes.c_int] * 4 + [ctypes.c_float, ctypes.c_int, ctypes.c_void_p]),
     "qmx_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "qmx_api_version": (ctypes.c_int, []),
 }
@@ -485,8 +498,12 @@ def tensor_bits(t: torch.Tensor):
 
 from .kv4 import (Kv4Cache, KvMaps, kv4_attention, kv4_attention_workspace_bytes, kv4_read,  # noqa: E402
                   kv4_write, kv_maps)
+from .f8 import (f8_dequantize, f8_quantize, qmm_f8, qmm_f8_workspace_bytes, rms_norm, rms_norm_f8)  # noqa: E402
+from .rope import rope, rope_frequencies  # noqa: E402
 
-__all__ = ["Kv4Cache", "KvMaps", "kv_maps", "kv4_write", "kv4_read", "kv4_attention",
+__all__ = ["rms_norm", "rms_norm_f8", "f8_quantize", "f8_dequantize", "qmm_f8", "qmm_f8_workspace_bytes",
+           "rope", "rope_frequencies",
+           "Kv4Cache", "KvMaps", "kv_maps", "kv4_write", "kv4_read", "kv4_attention",
            "kv4_attention_workspace_bytes",
            "qmv", "qmm_t", "qmm_t_splitk", "qmm_t_splitk_noalloc", "qmm", "qmm_batched", "gather_qmm", "plan", "plan_batched",
            "matvec_q8_0",

@@ -1,0 +1,158 @@
+// f8_api.cpp -- the C ABI of the 8-bit float operators, the norm before them and
+// the rotary positions: host-side validation and the launches.  Every check runs
+// before any launch.
+#include <hip/hip_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "f8.h"
+#include "qmx.h"
+#include "qmx_internal.h"
+
+namespace {
+
+bool is_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int launch_status(hipError_t e) { return e == hipSuccess ? QMX_OK : QMX_ERR_LAUNCH; }
+
+bool is_half(int dtype) { return dtype == QMX_F16 || dtype == QMX_BF16; }
+
+// Rows of codes in groups of 128: what quantize and dequantize share.
+int check_codes(int rows, int width, int block_rows, int dtype) {
+    if (!is_half(dtype)) return QMX_ERR_DTYPE;
+    if (rows < 0 || width < 0) return QMX_ERR_SHAPE;
+    if (width % 128 || (block_rows != 1 && block_rows != 128)) return QMX_ERR_GROUP;
+    if ((long long)rows * (width / 128) > INT_MAX) return QMX_ERR_SHAPE;
+    return QMX_OK;
+}
+
+// The partitions of a product, and the one rule of the call and of its workspace's size.
+qmx::F8Plan plan_for(int M, int N, int K) {
+    const int cus = qmx::device_cu_count();
+    return qmx::f8_plan(M, N, K, cus > 0 ? cus : 256);
+}
+
+int check_product(int M, int N, int K) {
+    if (M < 0 || N < 0 || K < 0 || K > (1 << 24)) return QMX_ERR_SHAPE;
+    if (K % 128) return QMX_ERR_GROUP;
+    return QMX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qmx_rms_norm(const void* x, long long x_row_stride, const void* residual, long long residual_row_stride,
+                 const void* weight, void* sum, long long sum_row_stride, void* out, uint8_t* out_scales, int rows,
+                 int width, double eps, int dtype, void* stream) {
+    if (!is_half(dtype)) return QMX_ERR_DTYPE;
+    if (rows < 0 || width < 0) return QMX_ERR_SHAPE;
+    if (!std::isfinite(eps) || eps <= 0.0) return QMX_ERR_SHAPE;
+    if (out_scales && width % 128) return QMX_ERR_GROUP;
+    if (rows == 0 || width == 0) return QMX_OK;
+    if (!x || !out || (residual != nullptr) != (sum != nullptr)) return QMX_ERR_NULL;
+    if (rows > 1 && sum && sum_row_stride < width && sum_row_stride > -(long long)width) return QMX_ERR_SHAPE;
+    if (!is_aligned(x, 2) || !is_aligned(residual, 2) || !is_aligned(weight, 2) || !is_aligned(sum, 2) ||
+        !is_aligned(out, out_scales ? 8 : 2))
+        return QMX_ERR_ALIGN;
+    const qmx::NormArgs a = {x, residual, weight, sum, out, out_scales, x_row_stride, residual_row_stride,
+                             sum_row_stride, rows, width, eps};
+    return launch_status(qmx::launch_rms_norm(a, dtype, static_cast<hipStream_t>(stream)));
+}
+
+int qmx_f8_quantize(const void* x, long long x_row_stride, uint8_t* codes, uint8_t* scales, int rows, int width,
+                    int block_rows, int dtype, void* stream) {
+    const int rc = check_codes(rows, width, block_rows, dtype);
+    if (rc) return rc;
+    if (rows == 0 || width == 0) return QMX_OK;
+    if (!x || !codes || !scales) return QMX_ERR_NULL;
+    if (!is_aligned(x, 2) || !is_aligned(codes, 16)) return QMX_ERR_ALIGN;
+    return launch_status(qmx::launch_f8_quantize(x, x_row_stride, codes, scales, rows, width, block_rows, dtype,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
+int qmx_f8_dequantize(const uint8_t* codes, const void* scales, int scale_type, void* out, int rows, int width,
+                      int block_rows, int dtype, void* stream) {
+    const int rc = check_codes(rows, width, block_rows, dtype);
+    if (rc) return rc;
+    if (scale_type != QMX_SCALE_E8M0 && scale_type != QMX_SCALE_F32) return QMX_ERR_DTYPE;
+    if (rows == 0 || width == 0) return QMX_OK;
+    if (!codes || !scales || !out) return QMX_ERR_NULL;
+    if (!is_aligned(codes, 16) || !is_aligned(out, 16) || (scale_type == QMX_SCALE_F32 && !is_aligned(scales, 4)))
+        return QMX_ERR_ALIGN;
+    return launch_status(qmx::launch_f8_dequantize(codes, scales, scale_type == QMX_SCALE_F32, out, rows, width,
+                                                   block_rows, dtype, static_cast<hipStream_t>(stream)));
+}
+
+size_t qmx_qmm_f8_workspace_bytes(int M, int N, int K) {
+    if (check_product(M, N, K) || M == 0 || N == 0 || K == 0) return 0;
+    const int splits = plan_for(M, N, K).splits;
+    return splits > 1 ? (size_t)splits * M * N * sizeof(float) : 0;
+}
+
+int qmx_qmm_f8(const uint8_t* w, const void* w_scales, int w_scale_type, const uint8_t* x, const uint8_t* x_scales,
+               void* out, int M, int N, int K, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!is_half(dtype) || (w_scale_type != QMX_SCALE_E8M0 && w_scale_type != QMX_SCALE_F32)) return QMX_ERR_DTYPE;
+    const int rc = check_product(M, N, K);
+    if (rc) return rc;
+    if (M == 0 || N == 0) return QMX_OK;
+    if (!out || (K > 0 && (!w || !w_scales || !x || !x_scales))) return QMX_ERR_NULL;
+    if (!is_aligned(out, 2) || !is_aligned(w, 16) || !is_aligned(x, 16) ||
+        (w_scale_type == QMX_SCALE_F32 && !is_aligned(w_scales, 4)))
+        return QMX_ERR_ALIGN;
+    // every kernel's grid and the accumulation's
+    if ((long long)(M + 15ll) / 16 * ((N + 15ll) / 16) > INT_MAX) return QMX_ERR_SHAPE;
+    const qmx::F8Plan p = plan_for(M, N, K);
+    const size_t need = K > 0 && p.splits > 1 ? (size_t)p.splits * M * N * sizeof(float) : 0;
+    if (need && (!workspace || !is_aligned(workspace, 16) || workspace_bytes < need)) return QMX_ERR_WORKSPACE;
+    const qmx::F8MmArgs a = {w, w_scales, w_scale_type == QMX_SCALE_F32, x, x_scales, out,
+                             static_cast<float*>(workspace), M, N, K};
+    return launch_status(qmx::launch_qmm_f8(a, p, dtype, static_cast<hipStream_t>(stream)));
+}
+
+int qmx_rope(const void* q, long long q_token_stride, long long q_head_stride, void* q_out,
+             long long q_out_token_stride, long long q_out_head_stride, int heads, const void* k,
+             long long k_token_stride, long long k_head_stride, void* k_out, long long k_out_token_stride,
+             long long k_out_head_stride, int kv_heads, const int32_t* positions, const double* frequencies,
+             int tokens, int head_dim, int pairs, int interleaved, float scale, int dtype, void* stream) {
+    if (!is_half(dtype)) return QMX_ERR_DTYPE;
+    if (tokens < 0 || heads < 0 || kv_heads < 0 || heads > 8192 || kv_heads > 8192) return QMX_ERR_SHAPE;
+    if (head_dim < 1 || head_dim > 4096 || pairs < 1 || 2 * pairs > head_dim) return QMX_ERR_SHAPE;
+    if (!std::isfinite(scale)) return QMX_ERR_SHAPE;
+    if (tokens == 0 || heads + kv_heads == 0) return QMX_OK;
+    if (!positions || !frequencies || (heads > 0 && (!q || !q_out)) || (kv_heads > 0 && (!k || !k_out)))
+        return QMX_ERR_NULL;
+    if (!is_aligned(q, 2) || !is_aligned(q_out, 2) || !is_aligned(k, 2) || !is_aligned(k_out, 2) ||
+        !is_aligned(positions, 4) || !is_aligned(frequencies, 8))
+        return QMX_ERR_ALIGN;
+    qmx::RopeArgs a = {};
+    a.in[0] = q;
+    a.in[1] = k;
+    a.out[0] = q_out;
+    a.out[1] = k_out;
+    a.in_ts[0] = q_token_stride;
+    a.in_ts[1] = k_token_stride;
+    a.in_hs[0] = q_head_stride;
+    a.in_hs[1] = k_head_stride;
+    a.out_ts[0] = q_out_token_stride;
+    a.out_ts[1] = k_out_token_stride;
+    a.out_hs[0] = q_out_head_stride;
+    a.out_hs[1] = k_out_head_stride;
+    a.heads[0] = heads;
+    a.heads[1] = kv_heads;
+    a.positions = positions;
+    a.frequencies = frequencies;
+    a.tokens = tokens;
+    a.dim = head_dim;
+    a.pairs = pairs;
+    a.scale = scale;
+    a.interleaved = interleaved != 0;
+    for (int i = 0; i < 2; ++i)
+        a.in_place[i] = a.in[i] == a.out[i] && (a.in_ts[i] == a.out_ts[i] || tokens == 1) &&
+                        (a.in_hs[i] == a.out_hs[i] || a.heads[i] == 1);
+    return launch_status(qmx::launch_rope(a, dtype, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,213 @@
+// norm.hip -- root mean square norm of rows, after the residual's addition, into
+// the rows' type or into 8-bit floats with a scale for each 128:
+//   h = round(x + residual),  y = h * w / sqrt(sum h^2 / width + eps).
+//
+// Bound by memory: x, residual and w are read once and h and y written once, the
+// row staying in registers between its sum and its use.  The sum of squares and
+// y are formed in 64 bits (the vector ALU does them at the rate of 32 while it
+// waits on memory), so y is the formula's to 2^-50 for any finite inputs, and
+// neither large nor tiny rows leave the range on the way; it is rounded once.
+#include "f8.h"
+#include "f8_device.h"
+
+namespace qmx {
+namespace {
+
+// A float that every rounding to fewer than 23 bits takes where it would take y:
+// y cut to 24 bits, the last of them set if anything was cut off.
+__device__ __forceinline__ float to_odd(double y) {
+    const float f = (float)y;
+    const uint32_t u = __float_as_uint(f);
+    const double back = (double)f;
+    const bool cut = back != y && !(u & 1u) && (u & 0x7fffffffu) < 0x7f800000u;
+    return __uint_as_float(cut ? (fabs(back) < fabs(y) ? u + 1u : u - 1u) : u);
+}
+
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+    return v;
+}
+
+// Eight elements, of which `n` are there (zeros behind them).
+__device__ __forceinline__ u32x4 load_part(const uint16_t* p, int n) {
+    if (n >= 8) return load_any(p);
+    u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n) v[i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
+    return v;
+}
+
+__device__ __forceinline__ void store_part(uint16_t* p, u32x4 v, int n) {
+    if (n >= 8) {
+        store_any(p, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n) p[i] = (uint16_t)(v[i / 2] >> (16 * (i % 2)));
+}
+
+template <int DT>
+__device__ __forceinline__ u32x4 add8(u32x4 x, u32x4 r) {
+    // two roundings, to 32 bits and to the type, give what one gives: 24 >= 2 * 11 + 2
+    u32x4 h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        h[i] = to_half<DT>(half_lo<DT>(x[i]) + half_lo<DT>(r[i])) |
+               (to_half<DT>(half_hi<DT>(x[i]) + half_hi<DT>(r[i])) << 16);
+    return h;
+}
+
+template <int DT>
+__device__ __forceinline__ double squares8(u32x4 h, double sum) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const double v = (double)elem<DT>(h, i);
+        sum = fma(v, v, sum);
+    }
+    return sum;
+}
+
+// y of eight elements from element `at` on, and where they go.
+template <int DT, bool F8>
+__device__ __forceinline__ void finish8(const NormArgs& a, size_t row, int at, int n, u32x4 h, double rstd) {
+    u32x4 w = {0, 0, 0, 0};
+    if (a.weight) w = load_part(static_cast<const uint16_t*>(a.weight) + at, n);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const double v = (double)elem<DT>(h, i) * rstd;
+        y[i] = to_odd(a.weight ? v * (double)elem<DT>(w, i) : v);
+    }
+    const size_t to = row * a.width + at;
+    if constexpr (F8) {   // 16 lanes hold a group
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(y[i]) & 0x7fffffffu);
+        const uint32_t byte = scale_byte(max16(most));
+        if (n > 0) {
+            *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.out) + to) = codes8(y, byte);
+            if (at % 128 == 0) a.scales[to / 128] = (uint8_t)byte;
+        }
+    } else {
+        u32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = to_half<DT>(y[2 * i]) | (to_half<DT>(y[2 * i + 1]) << 16);
+        store_part(static_cast<uint16_t*>(a.out) + to, o, n);
+    }
+}
+
+// LANES lanes a row, which hold up to VPT * 8 of its elements each; 256 threads
+// or more a work-group.
+template <int DT, bool F8, int LANES, int VPT>
+__global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_kernel(NormArgs a) {
+    constexpr int THREADS = LANES < 256 ? 256 : LANES, WAVES = LANES / 64;
+    __shared__ double part[WAVES];
+    const int lane = threadIdx.x % LANES;
+    const size_t row = (size_t)blockIdx.x * (THREADS / LANES) + threadIdx.x / LANES;
+    if (LANES == 64 && row >= (size_t)a.rows) return;
+    const uint16_t* x = static_cast<const uint16_t*>(a.x) + row * a.x_stride;
+    u32x4 h[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int at = (j * LANES + lane) * 8;
+        h[j] = load_part(x + at, a.width - at);
+    }
+    if (a.residual) {
+        const uint16_t* r = static_cast<const uint16_t*>(a.residual) + row * a.r_stride;
+        uint16_t* s = static_cast<uint16_t*>(a.sum) + row * a.s_stride;
+        u32x4 v[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int at = (j * LANES + lane) * 8;
+            v[j] = load_part(r + at, a.width - at);
+        }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int at = (j * LANES + lane) * 8;
+            h[j] = add8<DT>(h[j], v[j]);
+            store_part(s + at, h[j], a.width - at);
+        }
+    }
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) sum = squares8<DT>(h[j], sum);
+    sum = wave_sum64(sum);
+    if constexpr (WAVES > 1) {
+        if (lane % 64 == 0) part[lane / 64] = sum;
+        __syncthreads();
+        sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) sum += part[i];
+    }
+    const double rstd = 1.0 / sqrt(sum / a.width + a.eps);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int at = (j * LANES + lane) * 8;
+        if (F8 || at < a.width) finish8<DT, F8>(a, row, at, a.width - at, h[j], rstd);
+    }
+}
+
+// Rows of any length, read a second time: from the sum, if there is one.  Each
+// thread reads again only what it has itself read or written.
+template <int DT, bool F8>
+__global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
+    __shared__ double part[16];
+    const size_t row = blockIdx.x;
+    const int lane = threadIdx.x;
+    const uint16_t* x = static_cast<const uint16_t*>(a.x) + row * a.x_stride;
+    const uint16_t* r = static_cast<const uint16_t*>(a.residual) + row * a.r_stride;
+    uint16_t* s = static_cast<uint16_t*>(a.sum) + row * a.s_stride;
+    double sum = 0.0;
+    for (long long at = lane * 8; at < a.width; at += 1024 * 8) {
+        const int n = (int)min(8ll, a.width - at);
+        u32x4 h = load_part(x + at, n);
+        if (a.residual) {
+            h = add8<DT>(h, load_part(r + at, n));
+            store_part(s + at, h, n);
+        }
+        sum = squares8<DT>(h, sum);
+    }
+    sum = wave_sum64(sum);
+    if (lane % 64 == 0) part[lane / 64] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += part[i];
+    const double rstd = 1.0 / sqrt(sum / a.width + a.eps);
+    const uint16_t* from = a.residual ? s : x;
+    const long long end = F8 ? ((long long)a.width + 8191) / 8192 * 8192 : (long long)a.width;
+    for (long long at = lane * 8; at < end; at += 1024 * 8) {
+        const int n = (int)max(0ll, min(8ll, a.width - at));
+        finish8<DT, F8>(a, row, (int)min(at, (long long)a.width), n, load_part(from + at, n), rstd);
+    }
+}
+
+template <int DT, bool F8, int LANES, int VPT>
+void go(const NormArgs& a, hipStream_t st) {
+    constexpr int ROWS = LANES < 256 ? 256 / LANES : 1;
+    hipLaunchKernelGGL((norm_kernel<DT, F8, LANES, VPT>), dim3((unsigned)(((long long)a.rows + ROWS - 1) / ROWS)),
+                       dim3(LANES < 256 ? 256 : LANES), 0, st, a);
+}
+
+template <int DT, bool F8>
+void pick(const NormArgs& a, hipStream_t st) {
+    if (a.width <= 512) go<DT, F8, 64, 1>(a, st);
+    else if (a.width <= 2048) go<DT, F8, 256, 1>(a, st);
+    else if (a.width <= 4096) go<DT, F8, 256, 2>(a, st);
+    else if (a.width <= 8192) go<DT, F8, 256, 4>(a, st);
+    else if (a.width <= 16384) go<DT, F8, 1024, 2>(a, st);
+    else hipLaunchKernelGGL((norm_long_kernel<DT, F8>), dim3((unsigned)a.rows), dim3(1024), 0, st, a);
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormArgs& a, int dt, hipStream_t st) {
+    if (dt == DT_F16) a.scales ? pick<DT_F16, true>(a, st) : pick<DT_F16, false>(a, st);
+    else a.scales ? pick<DT_BF16, true>(a, st) : pick<DT_BF16, false>(a, st);
+    return hipGetLastError();
+}
+
+}  // namespace qmx

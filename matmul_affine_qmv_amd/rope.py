@@ -1,0 +1,119 @@
+"""Rotary positions of queries and keys: marshalling for qmx_rope (include/qmx.h
+says what it computes), and the frequencies that models stretch for long contexts.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from .f8 import _HALVES, _call
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
+                     original_length: int = 0, low: float = 1.0, high: float = 4.0, fast: float = 32.0,
+                     slow: float = 1.0, device="cuda") -> torch.Tensor:
+    """Radians a position of each pair, float64 [rotary_dim / 2] on `device`:
+    f_i = base ** (-2 i / rotary_dim), and for contexts `factor` times as long as
+    the original_length that a model was trained on:
+
+    scaling "linear": f_i / factor.
+    scaling "base":   base * factor ** (d / (d - 2)) for the base, which divides the
+                      last frequency by factor and leaves the first (d = rotary_dim > 2).
+    scaling "bands":  f_i / factor where a turn takes more than original_length / low
+                      positions, f_i where it takes less than original_length / high,
+                      and between them a blend, linear in turns (low < high).
+    scaling "yarn":   f_i / factor and f_i blended linearly in i, between the pairs
+                      that make `fast` and `slow` turns in original_length positions
+                      (fast > slow); YaRN also scales what it turns by 0.1 ln(factor)
+                      + 1 (rope's `scale`)."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError(f"rotary_dim must be even and at least 2, got {rotary_dim}")
+    if not base > 1 or not factor >= 1:
+        raise ValueError("base must be above 1 and factor at least 1")
+    if scaling not in (None, "linear", "base", "bands", "yarn"):
+        raise ValueError(f"scaling must be None, 'linear', 'base', 'bands' or 'yarn', got {scaling!r}")
+    if scaling in ("bands", "yarn") and original_length < 1:
+        raise ValueError(f"scaling {scaling!r} needs original_length")
+    if scaling == "base":
+        if rotary_dim < 4:
+            raise ValueError("scaling 'base' needs a rotary_dim of at least 4")
+        base *= factor ** (rotary_dim / (rotary_dim - 2))
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64)
+    f = float(base) ** (-2 * i / rotary_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "bands":
+        if not 0 < low < high:
+            raise ValueError("bands need 0 < low < high")
+        turns = original_length * f / (2 * math.pi)
+        keep = ((turns - low) / (high - low)).clamp(0, 1)
+        f = keep * f + (1 - keep) * f / factor
+    elif scaling == "yarn":
+        if not 0 < slow < fast:
+            raise ValueError("yarn needs 0 < slow < fast")
+
+        def pair_of(turns):  # the (fractional) pair that makes so many turns
+            return rotary_dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+        first = max(math.floor(pair_of(fast)), 0)
+        last = max(first + 0.001, min(math.ceil(pair_of(slow)), rotary_dim - 1))
+        stretched = ((i - first) / (last - first)).clamp(0, 1)
+        f = (1 - stretched) * f + stretched * f / factor
+    return f.to(device)
+
+
+def _heads(t, name, like=None):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    if not t.is_cuda:
+        raise ValueError("all tensors must be on a HIP device")
+    if t.dtype not in _HALVES:
+        raise ValueError(f"{name} has an unsupported dtype {t.dtype}")
+    if like is not None and (t.shape != like.shape or t.dtype is not like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must be {tuple(like.shape)} of dtype {like.dtype} on {like.device}")
+    token, head, last = t.stride()
+    if last != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name} must have a unit last stride")
+    return t.data_ptr(), token, head
+
+
+def rope(q, k, positions, frequencies, *, interleaved=False, scale=1.0, out=None):
+    """(q, k) turned by their tokens' positions (qmx_rope).
+
+    q, k: [tokens, heads, head_dim] and [tokens, kv_heads, head_dim] (any strides,
+    the last 1), k may be None; positions: int32 [tokens], below 0 for tokens that
+    are left as they are; frequencies: float64 [pairs] (rope_frequencies), the first
+    2 * pairs elements of a head turn, element i with pairs + i or, interleaved, 2i
+    with 2i + 1.  scale: of what turns.  out: the (q, k) to write into, q and k
+    themselves to turn them in place.  Returns (q, k), contiguous if made here."""
+    args = _heads(q, "q")
+    T, heads, D = q.shape
+    index = q.get_device()
+    if positions.dtype is not torch.int32 or positions.shape != (T,) or not positions.is_contiguous():
+        raise ValueError(f"positions must be a contiguous int32 vector of {T}")
+    if frequencies.dtype is not torch.float64 or frequencies.dim() != 1 or not frequencies.is_contiguous():
+        raise ValueError("frequencies must be a contiguous float64 vector")
+    pairs = frequencies.shape[0]
+    if not 2 <= 2 * pairs <= D:
+        raise ValueError(f"frequencies must have 1 to {D // 2} elements, got {pairs}")
+    if positions.get_device() != index or frequencies.get_device() != index:
+        raise ValueError(f"positions and frequencies must be on {q.device}")
+    if k is None:
+        key, kv_heads = (None, 0, 0), 0
+    else:
+        key, kv_heads = _heads(k, "k"), k.shape[1]
+        if k.shape[0] != T or k.shape[2] != D or k.dtype is not q.dtype or k.get_device() != index:
+            raise ValueError(f"k must be [{T}, kv_heads, {D}] of dtype {q.dtype} on {q.device}")
+    if out is None:
+        q_out = torch.empty((T, heads, D), dtype=q.dtype, device=q.device)
+        k_out = torch.empty((T, kv_heads, D), dtype=q.dtype, device=q.device) if k is not None else None
+    else:
+        q_out, k_out = out
+        if (k_out is None) != (k is None):
+            raise ValueError("out must be as many tensors as q and k")
+    to_q = _heads(q_out, "q's out", q)
+    to_k = _heads(k_out, "k's out", k) if k is not None else (None, 0, 0)
+    _call(index, "qmx_rope", *args, *to_q, heads, *key, *to_k, kv_heads, positions.data_ptr(),
+          frequencies.data_ptr(), T, D, pairs, int(interleaved), scale, _HALVES[q.dtype])
+    return q_out, k_out
