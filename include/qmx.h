@@ -512,8 +512,9 @@ typedef enum qmx_scale_type {
  * out_scales [rows, width / 128] their E8M0 scales (width % 128 == 0, else
  * QMX_ERR_GROUP).  sum may be x or residual itself, row for row, and an out in
  * `dtype` may be x itself; otherwise outputs overlap nothing.  eps: finite and
- * above 0.  y is formed in 64 bits and rounded once; a y beyond float32's range
- * counts as infinite. */
+ * above 0.  The sum is formed in 64 bits.  A y in `dtype` is formed in float32 from
+ * it and rounded once more; codes and scales are those of a y in 64 bits (beyond
+ * float32's range it counts as infinite). */
 int qmx_rms_norm(const void* x, long long x_row_stride, const void* residual,
                  long long residual_row_stride, const void* weight, void* sum,
                  long long sum_row_stride, void* out, uint8_t* out_scales, int rows, int width,

@@ -35,7 +35,7 @@ qmx::F8Plan plan_for(int M, int N, int K) {
 }
 
 int check_product(int M, int N, int K) {
-    if (M < 0 || N < 0 || K < 0 || K > (1 << 24)) return QMX_ERR_SHAPE;
+    if (M < 0 || N < 0 || K < 0 || K >= (1 << 24)) return QMX_ERR_SHAPE;
     if (K % 128) return QMX_ERR_GROUP;
     return QMX_OK;
 }

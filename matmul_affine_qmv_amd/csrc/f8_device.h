@@ -17,9 +17,21 @@ __device__ __forceinline__ float elem(const u32x4& w, int i) {
     return i % 2 ? half_hi<DT>(w[i / 2]) : half_lo<DT>(w[i / 2]);
 }
 
+// Two floats to nearest even: gfx950 has the pair of bfloat16 in one instruction.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (DT == DT_F16) {
+        return f32_to_f16_bits(a) | (f32_to_f16_bits(b) << 16);
+    } else {
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+    }
+}
+
 template <int DT>
 __device__ __forceinline__ uint32_t to_half(float v) {
-    return DT == DT_F16 ? f32_to_f16_bits(v) : f32_to_bf16_bits(v);
+    return pack2<DT>(v, 0.0f) & 0xffffu;
 }
 
 // The largest of the 16 lanes of a row, as whole numbers, in every one of them.

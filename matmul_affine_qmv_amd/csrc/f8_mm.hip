@@ -14,13 +14,14 @@ void rows(const F8MmArgs& a, hipStream_t st) {
                        dim3(WAVES * 64), 0, st, a);
 }
 
-template <int DT, bool F32, int BM, int BN, int WM, int WN>
+template <int DT, bool F32, int BM, int BN, int WM, int WN, int STAGES>
 void tiles(const F8MmArgs& a, int splits, hipStream_t st) {
-    const unsigned n = (unsigned)((a.M + BM - 1) / BM) * (unsigned)((a.N + BN - 1) / BN);
+    const long long n = (long long)((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN) * splits;
+    const unsigned grid = f8::tile_groups(n, f8::tile_fit<BM, BN, STAGES>() * device_cu_count());
     if (splits > 1)
-        hipLaunchKernelGGL((f8::tile_kernel<DT, F32, BM, BN, WM, WN, true>), dim3(n * splits), dim3(WM * WN * 64), 0, st, a, splits);
+        hipLaunchKernelGGL((f8::tile_kernel<DT, F32, BM, BN, WM, WN, STAGES, true>), dim3(grid), dim3(WM * WN * 64), 0, st, a, splits);
     else
-        hipLaunchKernelGGL((f8::tile_kernel<DT, F32, BM, BN, WM, WN, false>), dim3(n), dim3(WM * WN * 64), 0, st, a, 1);
+        hipLaunchKernelGGL((f8::tile_kernel<DT, F32, BM, BN, WM, WN, STAGES, false>), dim3(grid), dim3(WM * WN * 64), 0, st, a, 1);
 }
 
 // K = 0: a sum over nothing.
@@ -37,8 +38,8 @@ void pick(const F8MmArgs& a, F8Plan p, hipStream_t st) {
             else if (a.M <= 48) rows<DT, F32, 3, 2, 8>(a, st);
             else rows<DT, F32, 4, 2, 8>(a, st);
             break;
-        case 1: tiles<DT, F32, 128, 128, 2, 2>(a, p.splits, st); break;
-        default: tiles<DT, F32, 256, 256, 2, 4>(a, p.splits, st); break;
+        case 1: tiles<DT, F32, 128, 128, 2, 2, 4>(a, p.splits, st); break;
+        default: tiles<DT, F32, 256, 256, 2, 4, 2>(a, p.splits, st); break;
     }
 }
 

@@ -31,9 +31,10 @@ __device__ __forceinline__ uint32_t scales4(const uint8_t* row, int at, int G) {
     return v;
 }
 
-template <int WHICH>
+// A and B are the bytes of sa and sb that hold the scales.
+template <int A, int B>
 __device__ __forceinline__ f32x4 mfma(i32x8 a, i32x8 b, f32x4 c, int sa, int sb) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, WHICH, sa, WHICH, sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, A, sa, B, sb);
 }
 
 constexpr int ONE = 0x7f7f7f7f;   // scales of 1
@@ -42,9 +43,10 @@ __device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi) {
     return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
-// 16 bytes a lane from memory into LDS, the wave's one after the other from `to` on.
-__device__ __forceinline__ void copy16(const uint8_t* from, uint8_t* to) {
-    __builtin_amdgcn_global_load_lds(from, reinterpret_cast<void*>(to), 16, 0, 0);
+// 16 bytes a lane from a buffer into LDS, the wave's one after the other from `to` on.
+__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t from, uint32_t lane_at, uint32_t at, uint8_t* to) {
+    typedef __attribute__((address_space(3))) void lds_void;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void*)to, 16, (int)lane_at, (int)at, 0, 0);
 }
 
 // Four neighbouring results of row m from column n on.
@@ -52,8 +54,8 @@ template <int DT>
 __device__ __forceinline__ void store4(void* out, size_t N, size_t m, int n, f32x4 v, bool vec) {
     uint16_t* to = static_cast<uint16_t*>(out) + m * N + n;
     if (vec && n + 4 <= (int)N) {
-        *reinterpret_cast<u32x2*>(to) = u32x2{to_half<DT>(v[0]) | (to_half<DT>(v[1]) << 16),
-                                              to_half<DT>(v[2]) | (to_half<DT>(v[3]) << 16)};
+        *reinterpret_cast<u32x2*>(to) = u32x2{pack2<DT>(v[0], v[1]),
+                                              pack2<DT>(v[2], v[3])};
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -61,14 +63,37 @@ __device__ __forceinline__ void store4(void* out, size_t N, size_t m, int n, f32
     }
 }
 
-__device__ __forceinline__ void store4_partial(float* out, size_t N, size_t m, int n, f32x4 v, bool vec) {
-    float* to = out + m * N + n;
-    if (vec && n + 4 <= (int)N) {
-        *reinterpret_cast<f32x4*>(to) = v;
+// Eight neighbouring results of a row into a buffer that ends with the last of 16
+// rows, `wide` (8, 4 or 1) at a time: columns past N, and all of what is past the
+// buffer's end, are not written.
+template <int DT, bool PARTIAL>
+__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t out, uint32_t place, int n, int N, f32x4 v, f32x4 w, int wide) {
+    constexpr uint32_t NOWHERE = 0xffffffffu;
+    constexpr int SIZE = PARTIAL ? 4 : 2;
+    const int at = (int)(n < N ? place : NOWHERE), behind = (int)(n + 4 < N ? place + 4 * SIZE : NOWHERE);
+    if (wide > 1) {
+        if constexpr (PARTIAL) {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), out, at, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), out, behind, 0, 0);
+        } else {
+            const u32x4 p = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3])};
+            if (wide == 8) {
+                __builtin_amdgcn_raw_buffer_store_b128(p, out, at, 0, 0);
+            } else {
+                __builtin_amdgcn_raw_buffer_store_b64(u32x2{p[0], p[1]}, out, at, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b64(u32x2{p[2], p[3]}, out, behind, 0, 0);
+            }
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n + i < (int)N) to[i] = v[i];
+        for (int i = 0; i < 8; ++i) {
+            const int to = (int)(n + i < N ? place + i * SIZE : NOWHERE);
+            const float x = i < 4 ? v[i & 3] : w[i & 3];
+            if constexpr (PARTIAL)
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), out, to, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)to_half<DT>(x), out, to, 0, 0);
+        }
     }
 }
 
@@ -139,11 +164,11 @@ __global__ __launch_bounds__(WAVES * 64) void rows_kernel(F8MmArgs a) {
                 for (int n = 0; n < NT; ++n) {
                     const i32x8 A = join(wv[j][n][0], wv[j][n][1]), B = join(xv[j][m][0], xv[j][m][1]);
                     if constexpr (F32) {
-                        const f32x4 d = mfma<j>(A, B, f32x4{0.f, 0.f, 0.f, 0.f}, ONE, (int)sx[m]);
+                        const f32x4 d = mfma<j, j>(A, B, f32x4{0.f, 0.f, 0.f, 0.f}, ONE, (int)sx[m]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(fw[j], d[e], acc[m][n][e]);
                     } else {
-                        acc[m][n] = mfma<j>(A, B, acc[m][n], (int)sw, (int)sx[m]);
+                        acc[m][n] = mfma<j, j>(A, B, acc[m][n], (int)sw, (int)sx[m]);
                     }
                 }
         };
@@ -168,118 +193,329 @@ __global__ __launch_bounds__(WAVES * 64) void rows_kernel(F8MmArgs a) {
 }
 
 // ---------------------------------------------------------------- tiles
-// A work-group takes BM rows of x by BN rows of w; WM by WN waves.  A stage of LDS
-// holds 128 of K of both, rows of 128 bytes whose 16-byte pieces are turned by the
-// row's number, which spreads a column of pieces over the banks; it is copied from
-// memory without registers between, one stage ahead.
-template <int DT, bool F32, int BM, int BN, int WM, int WN, bool SPLIT>
+// Which tile is the t-th of a list that walks GROUP tiles of x by all of w, so that
+// neighbours in it share what an L2 holds.
+struct TileAt {
+    int part, m, n;
+};
+template <int GROUP>
+__device__ __forceinline__ TileAt tile_at(int t, int tiles_m, int tiles_n) {
+    const int tiles = tiles_m * tiles_n;
+    const int part = t / tiles;
+    t -= part * tiles;
+    const int band = t / (GROUP * tiles_n), left = t - band * GROUP * tiles_n;
+    const int rows = min(GROUP, tiles_m - band * GROUP);
+    return {part, band * GROUP + left % rows, left / rows};
+}
+
+// A work-group takes tiles of BM rows of x by BN rows of w, one after the other; WM by
+// WN waves.  A stage of LDS holds 128 of K of both, rows of 128 bytes whose 16-byte
+// pieces are turned by the row's number, which spreads a column of pieces over the
+// banks; it is copied from memory without registers between.  A wave holds its rows of
+// w (A) for a step and passes over its TM rows of 16 of x (B), reading one ahead.  Two
+// barriers a step: before the first half of x's rows is left, when every wave has read
+// A and the second half has come (w and x's first half of the stage are then copied
+// again, for STAGES steps later); and before the last row, when the whole stage is read
+// and the next one's w and first half have come (the second half is copied again, and
+// beside the last row A and B are read from the next stage).  So what is copied has a
+// step and a half to come with two stages only, and the copies run on into the next
+// tile while one is finished and written.
+// The scales of CHUNK groups stand beside the stages, the next ones' in a second place:
+// a lane's TM scales of x in neighbouring bytes, which the matrix instruction picks from
+// a register by itself.
+constexpr int CHUNK = 32;
+
+template <int BM, int BN, int STAGES>
+struct TileLds {
+    alignas(16) uint8_t data[STAGES][(BM + BN) * 128];
+    alignas(16) uint8_t sx[2 * CHUNK][BM];
+    uint32_t sw[2 * CHUNK][(BN + 127) / 128];   // a float, or a byte four times
+};
+
+// Work-groups that a compute unit holds at a time, and how many are launched.
+template <int BM, int BN, int STAGES>
+constexpr int tile_fit() { return 163840 / (int)sizeof(TileLds<BM, BN, STAGES>); }
+inline unsigned tile_groups(long long tiles, int most) { return (unsigned)(tiles < most ? tiles : most / 8 * 8); }
+
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// Until this wave's LDS reads are done.  Written ahead of the next reads: left to
+// itself the compiler waits for those too.
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xc07f); }
+
+template <int DT, bool F32, int BM, int BN, int WM, int WN, int STAGES, bool SPLIT>
 __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int splits) {
-    constexpr int THREADS = WM * WN * 64, ROWS = BM + BN, COPIES = ROWS * 8 / THREADS;
-    constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
-    static_assert(COPIES * THREADS == ROWS * 8 && BN * 8 % THREADS == 0, "copies");
-    static_assert(128 % (16 * TN) == 0 || (16 * TN) % 128 == 0, "scales");
-    __shared__ __align__(16) uint8_t lds[2][ROWS * 128];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    constexpr int THREADS = WM * WN * 64, TM = BM / WM / 16, TN = BN / WN / 16, BLOCKS = (BN + 127) / 128;
+    constexpr int HALF = TM / 2, W_COPIES = BN * 8 / THREADS, X_COPIES = BM * 4 / THREADS;   // of each half
+    constexpr int COPIES = W_COPIES + 2 * X_COPIES;
+    static_assert(W_COPIES * THREADS == BN * 8 && X_COPIES * THREADS == BM * 4, "copies");
+    static_assert(TM >= 2 && TM <= 8 && TM % 2 == 0, "rows of operands are held two at a time");
+    static_assert(TN % 2 == 0, "results are written eight at a time");
+    static_assert(128 % (16 * TN) == 0, "a wave's rows of w share their scales");
+    static_assert(BM * CHUNK / 16 <= THREADS && CHUNK * BLOCKS <= THREADS, "scales");
+    __shared__ TileLds<BM, BN, STAGES> lds;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, h = lane >> 4;
     const int wm = wave % WM, wn = wave / WM;
     const int G = a.K / 128;
     const int tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN;
-    const int tiles = tiles_m * tiles_n;
-    int id = blockIdx.x, p = 0;
-    if (SPLIT) {
-        p = id / tiles;
-        id -= p * tiles;
-    }
-    const int m0 = id % tiles_m * BM, n0 = id / tiles_m * BN;
-    const int k0 = SPLIT ? (int)((long long)G * p / splits) : 0, k1 = SPLIT ? (int)((long long)G * (p + 1) / splits) : G;
+    // Work-groups go to the 8 XCDs by turns; each XCD takes a run of the list.
+    const int total = tiles_m * tiles_n * (SPLIT ? splits : 1);
+    const int xcd = blockIdx.x & 7, run = total >> 3, more_runs = total & 7;
+    const int t_first = xcd * run + min(xcd, more_runs) + (int)(blockIdx.x >> 3);
+    const int t_end = xcd * run + min(xcd, more_runs) + run + (xcd < more_runs ? 1 : 0);
+    const int t_step = (int)((gridDim.x + 7 - xcd) >> 3);
+    auto tile_of = [&](int t) { return tile_at<(BM >= 256 ? 4 : 8)>(t, tiles_m, tiles_n); };
+    auto begin_of = [&](int part) { return SPLIT ? (int)((long long)G * part / splits) : 0; };
+    auto end_of = [&](int part) { return SPLIT ? (int)((long long)G * (part + 1) / splits) : G; };
+    // What is formed once a tile is formed anew from the thread's number: kept over the
+    // steps it would take registers that they need.
+    auto thread = [] {
+        int v = threadIdx.x;
+        asm volatile("" : "+v"(v));
+        return v;
+    };
 
-    const uint8_t* wbase = a.w + (size_t)n0 * a.K;
-    const uint8_t* xbase = a.x + (size_t)m0 * a.K;
+    // What is copied next: group `cg`, of a tile with `copies_left` more, then of tile `ct`.
+    // Rows of x stand in LDS by halves: those of every wave's first HALF rows of 16, then
+    // the others.  Rows past the end repeat the last.
+    int ct = t_first, cg = 0, copies_left = 0, cg_step = 1;
+    __amdgpu_buffer_rsrc_t wbuf, xbuf;
     uint32_t off[COPIES];
-#pragma unroll
-    for (int i = 0; i < COPIES; ++i) {
-        const int piece = i * THREADS + tid, row = piece >> 3, c = (piece & 7) ^ (row & 7);
-        const int at = i * THREADS < BN * 8 ? min(row, a.N - 1 - n0) : min(row - BN, a.M - 1 - m0);
-        off[i] = (uint32_t)at * (uint32_t)a.K + 16 * c;
-    }
-    auto copy = [&](int g, int stage) {
+    auto next_copies = [&] {
+        if (ct >= t_end) {   // nothing is left: the last group again, which nobody reads
+            cg -= cg_step;
+            cg_step = 0;
+            copies_left = 0x7fffffff;
+            return;
+        }
+        const TileAt at = tile_of(ct);
+        ct += t_step;
+        const int m0 = at.m * BM, n0 = at.n * BN, tid = thread();
+        cg = begin_of(at.part);
+        copies_left = end_of(at.part) - cg;
+        // at most 256 rows of 2^24 - 128 bytes
+        wbuf = buffer_over(a.w + (size_t)n0 * a.K, (size_t)min(BN, a.N - n0) * a.K);
+        xbuf = buffer_over(a.x + (size_t)m0 * a.K, (size_t)min(BM, a.M - m0) * a.K);
 #pragma unroll
         for (int i = 0; i < COPIES; ++i) {
-            const uint8_t* base = (i * THREADS < BN * 8 ? wbase : xbase) + (size_t)g * 128;
-            copy16(base + off[i], &lds[stage][(i * THREADS + wave * 64) * 16]);
+            const int piece = i * THREADS + tid, row = piece >> 3, c = (piece & 7) ^ (row & 7);
+            // Of 32 rows of w two operands hold those that leave 8 neighbouring results
+            // with a lane: the even one 0..3 of each 8, the odd one the others.
+            int from = min(row / 32 * 32 + row % 16 / 4 * 8 + row / 16 % 2 * 4 + row % 4, a.N - 1 - n0);
+            if (i >= W_COPIES) {
+                const int at = row - BN, half = at / (BM / 2), in = at % (BM / 2);
+                from = min(in / (HALF * 16) * (TM * 16) + half * (HALF * 16) + in % (HALF * 16), a.M - 1 - m0);
+            }
+            off[i] = (uint32_t)from * (uint32_t)a.K + 16 * c;
         }
     };
-    const int wn0 = n0 + wn * TN * 16;
-    const size_t block = (size_t)(min(wn0, a.N - 1) / 128) * G;
-    const uint8_t* wb = static_cast<const uint8_t*>(a.w_scales) + block;
-    const float* wf = static_cast<const float*>(a.w_scales) + block;
-    const uint8_t* xs[TM];
+    auto copy = [&](int first, int last, int stage) {   // of COPIES
 #pragma unroll
-    for (int i = 0; i < TM; ++i) xs[i] = a.x_scales + (size_t)min(m0 + (wm * TM + i) * 16 + r, a.M - 1) * G;
+        for (int i = 0; i < COPIES; ++i)
+            if (i >= first && i < last)
+                copy16(i < W_COPIES ? wbuf : xbuf, off[i], (uint32_t)cg * 128,
+                       &lds.data[stage][(i * THREADS + wave * 64) * 16]);
+    };
 
-    f32x4 acc[TM][TN] = {};
-    uint32_t sx[TM], nx[TM], sw = ONE, nw = ONE;
-    copy(k0, 0);
+    // The scales of a chunk of n groups from g on: 16 of a row of x a thread, and one of w.
+    u32x4 sv = {0, 0, 0, 0};
+    uint32_t wv = 0;
+    auto load_scales = [&](const TileAt& at, int g, int n) {
+        const int tid = thread(), row = tid / (CHUNK / 16), first = tid % (CHUNK / 16) * 16;
+        struct __attribute__((packed, aligned(1))) Any { u32x4 v; };
+        if (row < BM) {
+            const uint8_t* from = a.x_scales + (size_t)min(at.m * BM + row, a.M - 1) * G + g + first;
+            if (first + 16 <= n) {
+                sv = reinterpret_cast<const Any*>(from)->v;
+            } else {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) nx[i] = scales4(xs[i], k0, G);
-    if (!F32) nw = scales4(wb, k0, G);
-    for (int g = k0; g < k1; ++g) {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        const int stage = (g - k0) & 1;
-        if (g + 1 < k1) copy(g + 1, stage ^ 1);
-        if (((g - k0) & 3) == 0) {
-#pragma unroll
-            for (int i = 0; i < TM; ++i) sx[i] = nx[i];
-            sw = nw;
-            if (g + 4 < k1) {
-#pragma unroll
-                for (int i = 0; i < TM; ++i) nx[i] = scales4(xs[i], g + 4, G);
-                if (!F32) nw = scales4(wb, g + 4, G);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < TM; ++i) sx[i] >>= 8;
-            sw >>= 8;
-        }
-        const float fw = F32 ? wf[g] : 1.0f;
-        auto frag = [&](int row) {   // of 16 rows from `row` on
-            const uint8_t* at = &lds[stage][(row + r) * 128];
-            const u32x4 lo = *reinterpret_cast<const u32x4*>(at + 16 * (h ^ (r & 7)));
-            const u32x4 hi = *reinterpret_cast<const u32x4*>(at + 16 * ((h + 4) ^ (r & 7)));
-            return join(lo, hi);
-        };
-        i32x8 A[TN];
-#pragma unroll
-        for (int n = 0; n < TN; ++n) A[n] = frag((wn * TN + n) * 16);
-#pragma unroll
-        for (int m = 0; m < TM; ++m) {
-            const i32x8 B = frag(BN + (wm * TM + m) * 16);
-#pragma unroll
-            for (int n = 0; n < TN; ++n) {
-                if constexpr (F32) {
-                    const f32x4 d = mfma<0>(A[n], B, f32x4{0.f, 0.f, 0.f, 0.f}, ONE, (int)sx[m]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(fw, d[e], acc[m][n][e]);
-                } else {
-                    acc[m][n] = mfma<0>(A[n], B, acc[m][n], (int)sw, (int)sx[m]);
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t b = first + j < n ? from[j] : 0;
+                    sv[j / 4] = j % 4 ? sv[j / 4] | b << (8 * (j % 4)) : b;
                 }
             }
         }
-    }
-    const bool vec = a.N % 4 == 0 && (SPLIT || (reinterpret_cast<uintptr_t>(a.out) & 7) == 0);
-    float* part = SPLIT ? a.partials + (size_t)p * a.M * a.N : nullptr;
+        const int j = tid / BLOCKS, block = tid % BLOCKS;
+        if (j < n) {
+            const size_t from = (size_t)min(at.n * BN / 128 + block, (a.N - 1) / 128) * G + g + j;
+            wv = F32 ? static_cast<const uint32_t*>(a.w_scales)[from]
+                     : 0x01010101u * static_cast<const uint8_t*>(a.w_scales)[from];
+        }
+    };
+    auto write_scales = [&](int place) {
+        const int tid = thread(), row = tid / (CHUNK / 16), first = tid % (CHUNK / 16) * 16;
+        if (row < BM) {
+            uint8_t* to = &lds.sx[place * CHUNK + first][row / (TM * 16) * (TM * 16) + row % 16 * TM + row / 16 % TM];
 #pragma unroll
-    for (int m = 0; m < TM; ++m) {
-        const int row = m0 + (wm * TM + m) * 16 + r;
-        if (row >= a.M) continue;
+            for (int j = 0; j < 16; ++j) to[j * BM] = (uint8_t)(sv[j / 4] >> (8 * (j % 4)));
+        }
+        if (tid < CHUNK * BLOCKS) lds.sw[place * CHUNK + tid / BLOCKS][tid % BLOCKS] = wv;
+    };
+
+    f32x4 acc[TM][TN] = {};
+    const int col = wn * TN * 16;
+    auto frag = [&](int row, int stage) {   // of 16 rows from `row` on
+        const uint8_t* p = &lds.data[stage][(row + r) * 128];
+        return join(*reinterpret_cast<const u32x4*>(p + 16 * (h ^ (r & 7))),
+                    *reinterpret_cast<const u32x4*>(p + 16 * ((h + 4) ^ (r & 7))));
+    };
+    auto x_row = [&](int m) { return BN + m / HALF * (BM / 2) + wm * (HALF * 16) + m % HALF * 16; };
+    i32x8 A[TN], B[2];
+    uint32_t sx[(TM + 3) / 4], sw;
+    int block = 0;   // of w's scales in the tile
+    auto scales_of = [&](int at) {
+        const uint8_t* from = &lds.sx[at][wm * TM * 16 + r * TM];
+        if constexpr (TM >= 4) {
+#pragma unroll
+            for (int i = 0; i < TM / 4; ++i) sx[i] = reinterpret_cast<const uint32_t*>(from)[i];
+        } else {
+            sx[0] = *reinterpret_cast<const uint16_t*>(from);
+        }
+        sw = lds.sw[at][block];
+    };
+    auto row = [&](auto which, auto&& between) {
+        constexpr int m = decltype(which)::value;
 #pragma unroll
         for (int n = 0; n < TN; ++n) {
-            const int col = wn0 + n * 16 + 4 * h;
-            if (col >= a.N) continue;
-            if (SPLIT) store4_partial(part, a.N, row, col, acc[m][n], vec);
-            else store4<DT>(a.out, a.N, row, col, acc[m][n], vec);
+            if constexpr (F32) {
+                const f32x4 d = mfma<0, m % 4>(A[n], B[m % 2], f32x4{0.f, 0.f, 0.f, 0.f}, ONE, (int)sx[m / 4]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(__uint_as_float(sw), d[e], acc[m][n][e]);
+            } else {
+                acc[m][n] = mfma<0, m % 4>(A[n], B[m % 2], acc[m][n], (int)sw, (int)sx[m / 4]);
+            }
+            between(n);
         }
+    };
+    // A step, without a branch, so that its order stays as written.  `next_at`: the next
+    // step's scales.  `wait1` and `wait2`: what may be on its way at the two barriers.
+    int stage = 0;
+    auto step = [&](int next_at, auto wait1, auto wait2) {
+        const int next = stage + 1 == STAGES ? 0 : stage + 1;
+        auto one = [&](auto which) {
+            constexpr int m = decltype(which)::value, after = m - (HALF - 1);
+            if constexpr (m < TM - 1) {
+                if constexpr (after == 0) wait_copies<decltype(wait1)::value>();
+                else wait_lds();
+                B[(m + 1) % 2] = frag(x_row(m + 1), stage);
+                __builtin_amdgcn_sched_barrier(0);
+                row(which, [&](int i) {
+                    if (i == 0 && after >= 0) {
+                        constexpr int C = W_COPIES + X_COPIES, EACH = (C + HALF - 1) / HALF;
+                        __builtin_amdgcn_sched_barrier(0);
+                        copy(after * EACH, (after + 1) * EACH < C ? (after + 1) * EACH : C, stage);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        one(std::integral_constant<int, 0>());
+        one(std::integral_constant<int, 1>());
+        one(std::integral_constant<int, 2>());
+        one(std::integral_constant<int, 3>());
+        one(std::integral_constant<int, 4>());
+        one(std::integral_constant<int, 5>());
+        one(std::integral_constant<int, 6>());
+        wait_copies<decltype(wait2)::value>();
+        B[0] = frag(x_row(0), next);
+        __builtin_amdgcn_sched_barrier(0);
+        row(std::integral_constant<int, TM - 1>(), [&](int i) {
+            A[i] = frag(col + i * 16, next);
+            if (i == 0) {
+                __builtin_amdgcn_sched_barrier(0);
+                copy(W_COPIES + X_COPIES, COPIES, stage);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        });
+        scales_of(next_at);
+        __builtin_amdgcn_sched_barrier(0);
+        stage = next;
+        cg += cg_step;
+    };
+
+    // The tile that is computed: chunk by chunk, [g, g + n) of its groups up to k1.
+    int t = t_first, place = 0;
+    TileAt at = tile_of(t), next_tile = at;
+    int g = begin_of(at.part), k1 = end_of(at.part), n = min(CHUNK, k1 - g);
+    block = (at.n * BN % 128 + col) / 128;
+    load_scales(at, g, n);
+    write_scales(0);
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) {
+        if (copies_left == 0) next_copies();
+        copy(0, COPIES, i);
+        cg += cg_step;
+        --copies_left;
     }
+    wait_copies<0>();
+    scales_of(0);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) A[i] = frag(col + i * 16, 0);
+    B[0] = frag(x_row(0), 0);
+    const uintptr_t out_at = SPLIT ? 0 : reinterpret_cast<uintptr_t>(a.out);
+    const int wide = a.N % 8 == 0 && out_at % 16 == 0 ? 8 : a.N % 4 == 0 && out_at % 8 == 0 ? 4 : 1;
+    const std::integral_constant<int, COPIES * (STAGES - 1)> some;
+    for (;;) {
+        // The chunk after this one, whose scales come while this one's first steps go.
+        const bool last = g + n == k1, has_next = !last || t + t_step < t_end;
+        int next_g = g + n, next_k1 = k1;
+        next_tile = at;
+        if (last && has_next) {
+            next_tile = tile_of(t + t_step);
+            next_g = begin_of(next_tile.part);
+            next_k1 = end_of(next_tile.part);
+        }
+        const int next_n = min(CHUNK, next_k1 - next_g);
+        if (has_next) load_scales(next_tile, next_g, next_n);
+        int s = 0;
+        for (int until = min(2, n - 1);; until = n) {
+            while (s < until) {
+                if (copies_left == 0) next_copies();
+                const int many = min(until - s, copies_left);
+                copies_left -= many;
+                for (const int stop = s + many; s < stop;) {
+                    ++s;
+                    if (s == n) block = (next_tile.n * BN % 128 + col) / 128;
+                    const int next_at = s < n ? place * CHUNK + s : (place ^ 1) * CHUNK;
+                    step(next_at, some, some);
+                }
+            }
+            if (until == n) break;
+            if (has_next) write_scales(place ^ 1);
+        }
+        place ^= 1;
+        if (last) {
+            constexpr int SIZE = SPLIT ? 4 : 2;
+            uint8_t* out = SPLIT ? reinterpret_cast<uint8_t*>(a.partials + (size_t)at.part * a.M * a.N)
+                                 : static_cast<uint8_t*>(a.out);
+            const int lane = thread() & 63, r = lane & 15, h = lane >> 4;
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+                // 16 rows of out; what lies past the last is not written
+                const int row = at.m * BM + (wm * TM + m) * 16;
+                const auto to = buffer_over(out + (size_t)min(row, a.M) * a.N * SIZE,
+                                            (size_t)max(0, min(16, a.M - row)) * a.N * SIZE);
+#pragma unroll
+                for (int n = 0; n < TN; n += 2) {
+                    const int to_n = at.n * BN + col + n * 16 + 8 * h;
+                    store8<DT, SPLIT>(to, ((uint32_t)r * (uint32_t)a.N + to_n) * SIZE, to_n, a.N, acc[m][n], acc[m][n + 1], wide);
+                    acc[m][n] = acc[m][n + 1] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
+            }
+            if (!has_next) break;
+            t += t_step;
+        }
+        at = next_tile;
+        g = next_g;
+        k1 = next_k1;
+        n = next_n;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // LDS is written to until then
 }
 
 }  // namespace f8

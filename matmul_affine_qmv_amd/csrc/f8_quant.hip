@@ -119,8 +119,8 @@ __global__ __launch_bounds__(THREADS) void dequantize_kernel(const uint8_t* __re
         for (int i = 0; i < 4; ++i) {
             const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j][i], false);
             const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j][i], true);
-            o[i / 2][i % 2 * 2] = to_half<DT>(value_of(lo[0], s[j])) | (to_half<DT>(value_of(lo[1], s[j])) << 16);
-            o[i / 2][i % 2 * 2 + 1] = to_half<DT>(value_of(hi[0], s[j])) | (to_half<DT>(value_of(hi[1], s[j])) << 16);
+            o[i / 2][i % 2 * 2] = pack2<DT>(value_of(lo[0], s[j]), value_of(lo[1], s[j]));
+            o[i / 2][i % 2 * 2 + 1] = pack2<DT>(value_of(hi[0], s[j]), value_of(hi[1], s[j]));
         }
         u32x4* to = reinterpret_cast<u32x4*>(out + g * 128 + 16 * u);
         to[0] = o[0];

@@ -3,10 +3,11 @@
 //   h = round(x + residual),  y = h * w / sqrt(sum h^2 / width + eps).
 //
 // Bound by memory: x, residual and w are read once and h and y written once, the
-// row staying in registers between its sum and its use.  The sum of squares and
-// y are formed in 64 bits (the vector ALU does them at the rate of 32 while it
-// waits on memory), so y is the formula's to 2^-50 for any finite inputs, and
-// neither large nor tiny rows leave the range on the way; it is rounded once.
+// row staying in registers between its sum and its use.  The sum of squares is
+// formed in 64 bits, so neither large nor tiny rows leave the range on the way.  y
+// is two products in 32 bits, and its codes are those of 64 bits all the same: a
+// lane whose eight y's are not all clear of the middles between two codes forms
+// them again in 64 bits (one wave in 100 does on random numbers).
 #include "f8.h"
 #include "f8_device.h"
 
@@ -21,6 +22,21 @@ __device__ __forceinline__ float to_odd(double y) {
     const double back = (double)f;
     const bool cut = back != y && !(u & 1u) && (u & 0x7fffffffu) < 0x7f800000u;
     return __uint_as_float(cut ? (fabs(back) < fabs(y) ? u + 1u : u - 1u) : u);
+}
+
+// What a row is multiplied by, in 64 and in 32 bits.
+struct Rstd {
+    double whole;
+    float rounded;
+    bool ordinary;   // rounded is far from the ends of its range
+};
+
+__device__ __forceinline__ Rstd rstd_of(double sum, int width, double eps) {
+    Rstd r;
+    r.whole = 1.0 / sqrt(sum / width + eps);
+    r.rounded = (float)r.whole;
+    r.ordinary = r.rounded >= 0x1p-100f && r.rounded <= 0x1p100f;
+    return r;
 }
 
 __device__ __forceinline__ double wave_sum64(double v) {
@@ -55,8 +71,7 @@ __device__ __forceinline__ u32x4 add8(u32x4 x, u32x4 r) {
     u32x4 h;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        h[i] = to_half<DT>(half_lo<DT>(x[i]) + half_lo<DT>(r[i])) |
-               (to_half<DT>(half_hi<DT>(x[i]) + half_hi<DT>(r[i])) << 16);
+        h[i] = pack2<DT>(half_lo<DT>(x[i]) + half_lo<DT>(r[i]), half_hi<DT>(x[i]) + half_hi<DT>(r[i]));
     return h;
 }
 
@@ -70,16 +85,40 @@ __device__ __forceinline__ double squares8(u32x4 h, double sum) {
     return sum;
 }
 
+// Whether y, off by at most three of its last digits (three roundings of half a
+// digit, of a number up to twice its power of two), rounds to a code as what it
+// stands for does, for all eight: magnitudes of 2^-60 to 2^100, none within three
+// of a number of five digits, as middles between codes are.  (w below 2^60 then
+// leaves h * rstd a normal number.)
+template <int DT>
+__device__ __forceinline__ bool clear_of_middles(const float (&y)[8], u32x4 w) {
+    uint32_t least = 0xffffffffu, most = 0, near = 0xffffffffu, heavy = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t u = __float_as_uint(y[i]) & 0x7fffffffu;
+        least = min(least, u);
+        most = max(most, u);
+        near = min(near, (u + 3u) & 0x7ffffu);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) heavy = max(heavy, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+    return least >= (127u - 60u) << 23 && most <= (127u + 100u) << 23 && near > 6u &&
+           (DT == DT_F16 || heavy < (127u + 60u) << 7);
+}
+
 // y of eight elements from element `at` on, and where they go.
 template <int DT, bool F8>
-__device__ __forceinline__ void finish8(const NormArgs& a, size_t row, int at, int n, u32x4 h, double rstd) {
-    u32x4 w = {0, 0, 0, 0};
+__device__ __forceinline__ void finish8(const NormArgs& a, size_t row, int at, int n, u32x4 h, const Rstd& r) {
+    const uint32_t one = DT == DT_F16 ? 0x3c003c00u : 0x3f803f80u;
+    u32x4 w = {one, one, one, one};
     if (a.weight) w = load_part(static_cast<const uint16_t*>(a.weight) + at, n);
     float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const double v = (double)elem<DT>(h, i) * rstd;
-        y[i] = to_odd(a.weight ? v * (double)elem<DT>(w, i) : v);
+    for (int i = 0; i < 8; ++i) y[i] = elem<DT>(h, i) * r.rounded * elem<DT>(w, i);
+    const bool again = !r.ordinary || (F8 && n > 0 && !clear_of_middles<DT>(y, w));
+    if (again) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = to_odd((double)elem<DT>(h, i) * r.whole * (double)elem<DT>(w, i));
     }
     const size_t to = row * a.width + at;
     if constexpr (F8) {   // 16 lanes hold a group
@@ -94,25 +133,24 @@ __device__ __forceinline__ void finish8(const NormArgs& a, size_t row, int at, i
     } else {
         u32x4 o;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = to_half<DT>(y[2 * i]) | (to_half<DT>(y[2 * i + 1]) << 16);
+        for (int i = 0; i < 4; ++i) o[i] = pack2<DT>(y[2 * i], y[2 * i + 1]);
         store_part(static_cast<uint16_t*>(a.out) + to, o, n);
     }
 }
 
-// LANES lanes a row, which hold up to VPT * 8 of its elements each; 256 threads
-// or more a work-group.
-template <int DT, bool F8, int LANES, int VPT>
-__global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_kernel(NormArgs a) {
-    constexpr int THREADS = LANES < 256 ? 256 : LANES, WAVES = LANES / 64;
-    __shared__ double part[WAVES];
-    const int lane = threadIdx.x % LANES;
-    const size_t row = (size_t)blockIdx.x * (THREADS / LANES) + threadIdx.x / LANES;
-    if (LANES == 64 && row >= (size_t)a.rows) return;
+// One row for each wave (WAVE) or for the whole work-group, whose lanes hold up to
+// VPT * 8 of its elements each.
+template <int DT, bool F8, bool WAVE, int VPT>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
+    __shared__ double part[16];
+    const int lanes = WAVE ? 64 : blockDim.x, lane = WAVE ? threadIdx.x % 64 : threadIdx.x;
+    const size_t row = WAVE ? (size_t)blockIdx.x * 4 + threadIdx.x / 64 : blockIdx.x;
+    if (WAVE && row >= (size_t)a.rows) return;
     const uint16_t* x = static_cast<const uint16_t*>(a.x) + row * a.x_stride;
     u32x4 h[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int at = (j * LANES + lane) * 8;
+        const int at = (j * lanes + lane) * 8;
         h[j] = load_part(x + at, a.width - at);
     }
     if (a.residual) {
@@ -121,12 +159,12 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_kernel(NormArg
         u32x4 v[VPT];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int at = (j * LANES + lane) * 8;
+            const int at = (j * lanes + lane) * 8;
             v[j] = load_part(r + at, a.width - at);
         }
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int at = (j * LANES + lane) * 8;
+            const int at = (j * lanes + lane) * 8;
             h[j] = add8<DT>(h[j], v[j]);
             store_part(s + at, h[j], a.width - at);
         }
@@ -135,18 +173,17 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_kernel(NormArg
 #pragma unroll
     for (int j = 0; j < VPT; ++j) sum = squares8<DT>(h[j], sum);
     sum = wave_sum64(sum);
-    if constexpr (WAVES > 1) {
+    if (!WAVE) {
         if (lane % 64 == 0) part[lane / 64] = sum;
         __syncthreads();
         sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < WAVES; ++i) sum += part[i];
+        for (int i = 0; i < lanes / 64; ++i) sum += part[i];
     }
-    const double rstd = 1.0 / sqrt(sum / a.width + a.eps);
+    const Rstd r = rstd_of(sum, a.width, a.eps);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int at = (j * LANES + lane) * 8;
-        if (F8 || at < a.width) finish8<DT, F8>(a, row, at, a.width - at, h[j], rstd);
+        const int at = (j * lanes + lane) * 8;
+        if (F8 || at < a.width) finish8<DT, F8>(a, row, at, a.width - at, h[j], r);
     }
 }
 
@@ -176,29 +213,28 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
     sum = 0.0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) sum += part[i];
-    const double rstd = 1.0 / sqrt(sum / a.width + a.eps);
+    const Rstd scale = rstd_of(sum, a.width, a.eps);
     const uint16_t* from = a.residual ? s : x;
     const long long end = F8 ? ((long long)a.width + 8191) / 8192 * 8192 : (long long)a.width;
     for (long long at = lane * 8; at < end; at += 1024 * 8) {
         const int n = (int)max(0ll, min(8ll, a.width - at));
-        finish8<DT, F8>(a, row, (int)min(at, (long long)a.width), n, load_part(from + at, n), rstd);
+        finish8<DT, F8>(a, row, (int)min(at, (long long)a.width), n, load_part(from + at, n), scale);
     }
 }
 
-template <int DT, bool F8, int LANES, int VPT>
+template <int DT, bool F8, bool WAVE, int VPT>
 void go(const NormArgs& a, hipStream_t st) {
-    constexpr int ROWS = LANES < 256 ? 256 / LANES : 1;
-    hipLaunchKernelGGL((norm_kernel<DT, F8, LANES, VPT>), dim3((unsigned)(((long long)a.rows + ROWS - 1) / ROWS)),
-                       dim3(LANES < 256 ? 256 : LANES), 0, st, a);
+    const long long vectors = ((long long)a.width + 7) / 8;
+    const unsigned lanes = WAVE ? 256 : (unsigned)((vectors + 64 * VPT - 1) / (64 * VPT) * 64);
+    hipLaunchKernelGGL((norm_kernel<DT, F8, WAVE, VPT>), dim3(WAVE ? ((unsigned)a.rows + 3) / 4 : (unsigned)a.rows), dim3(lanes), 0,
+                       st, a);
 }
 
 template <int DT, bool F8>
 void pick(const NormArgs& a, hipStream_t st) {
-    if (a.width <= 512) go<DT, F8, 64, 1>(a, st);
-    else if (a.width <= 2048) go<DT, F8, 256, 1>(a, st);
-    else if (a.width <= 4096) go<DT, F8, 256, 2>(a, st);
-    else if (a.width <= 8192) go<DT, F8, 256, 4>(a, st);
-    else if (a.width <= 16384) go<DT, F8, 1024, 2>(a, st);
+    if (a.width <= 512) go<DT, F8, true, 1>(a, st);
+    else if (a.width <= 8192 && (a.width <= 2048 || a.rows < 512)) go<DT, F8, false, 1>(a, st);
+    else if (a.width <= 16384) go<DT, F8, false, 2>(a, st);
     else hipLaunchKernelGGL((norm_long_kernel<DT, F8>), dim3((unsigned)a.rows), dim3(1024), 0, st, a);
 }
 

@@ -101,7 +101,7 @@ __global__ __launch_bounds__(THREADS) void rope_kernel(RopeArgs a) {
                     const float2 c = cs[min(j, pairs - 1)];
                     const uint32_t w = j < 4 ? e.lo[j & 3] : e.hi[j & 3];
                     const float x = half_lo<DT>(w), y = half_hi<DT>(w);
-                    const uint32_t r = to_half<DT>(fmaf(x, c.x, -y * c.y)) | (to_half<DT>(fmaf(y, c.x, x * c.y)) << 16);
+                    const uint32_t r = pack2<DT>(fmaf(x, c.x, -y * c.y), fmaf(y, c.x, x * c.y));
                     if (j < 4) o.lo[j & 3] = r;
                     else o.hi[j & 3] = r;
                 }
@@ -111,8 +111,8 @@ __global__ __launch_bounds__(THREADS) void rope_kernel(RopeArgs a) {
                     const float2 c = cs[min(2 * j, pairs - 1)], d = cs[min(2 * j + 1, pairs - 1)];
                     const float x0 = half_lo<DT>(e.lo[j]), y0 = half_lo<DT>(e.hi[j]);
                     const float x1 = half_hi<DT>(e.lo[j]), y1 = half_hi<DT>(e.hi[j]);
-                    o.lo[j] = to_half<DT>(fmaf(x0, c.x, -y0 * c.y)) | (to_half<DT>(fmaf(x1, d.x, -y1 * d.y)) << 16);
-                    o.hi[j] = to_half<DT>(fmaf(y0, c.x, x0 * c.y)) | (to_half<DT>(fmaf(y1, d.x, x1 * d.y)) << 16);
+                    o.lo[j] = pack2<DT>(fmaf(x0, c.x, -y0 * c.y), fmaf(x1, d.x, -y1 * d.y));
+                    o.hi[j] = pack2<DT>(fmaf(y0, c.x, x0 * c.y), fmaf(y1, d.x, x1 * d.y));
                 }
             }
             e = o;

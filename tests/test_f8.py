@@ -193,12 +193,18 @@ def apart(t, gap=0, offset=0):
     return v
 
 
+def norm_bound(y, w, dtype):
+    """Half a step of the type, and float32's: the root, the product with it and that with w are each rounded by 2^-24 of
+    themselves, the first product also by 2^-150 where it leaves the normal numbers."""
+    return ref.half_step(y, dtype) * (1 + 1e-6) + 3 * 2.0 ** -24 * y.abs() + 2.0 ** -150 * (1 if w is None else w.double().abs())
+
+
 def check_norm(x, w, r, y, eps, got, total):
     want, h = ref.norm(x, w, r, eps)
     if r is not None:
         assert same(total, h)
     off = (got.cpu().double() - want).abs()
-    over = off - ref.half_step(want, x.dtype) * (1 + 1e-9)
+    over = off - norm_bound(want, w, x.dtype)
     assert (over <= 0).all(), f"{over.max().item()} over half a step"
 
 
@@ -276,7 +282,7 @@ def test_norm_ranges(dtype):
                 bad = ~torch.isfinite(y)
                 assert torch.equal(torch.isnan(got), torch.isnan(y))
                 fine = torch.where(bad, 0.0, got - y).abs()
-                most = ref.half_step(torch.where(bad, 0.0, y), dtype) * (1 + 1e-9)
+                most = norm_bound(torch.where(bad, 0.0, y), weight, dtype)
                 # past the largest number what is rounded is infinite
                 beyond = y.abs() > fi.max
                 assert ((fine <= most) | beyond).all()
