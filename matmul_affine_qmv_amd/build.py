@@ -27,7 +27,8 @@ SOURCES = ["qmv.hip", "qmm_b4.hip", "qmm_b8.hip", "qmm_b2.hip", "qmm_b3.hip", "q
            "qmm_b1.hip", "blocks.hip", "q8_i8.hip", "qmm.hip", "qmx_api.cpp", "noalloc.hip",
            "kv4_attn_d256_bf16.hip", "kv4_attn_d256_f16.hip", "kv4_attn_d128_bf16.hip", "kv4_attn_d128_f16.hip",
            "kv4_attn_d64_bf16.hip", "kv4_attn_d64_f16.hip", "kv4_cache.hip", "kv_maps.hip", "kv4_api.cpp",
-           "f8_mm.hip", "f8_quant.hip", "norm.hip", "rope.hip", "f8_api.cpp"]
+           "f8_mm_bf16_e8m0.hip", "f8_mm_bf16_f32.hip", "f8_mm_f16_e8m0.hip", "f8_mm_f16_f32.hip", "f8_mm.hip",
+           "f8_quant.hip", "norm.hip", "rope.hip", "f8_api.cpp"]
 CALIB_SOURCES = ["calib.hip"]
 ARCH = "gfx950"
 

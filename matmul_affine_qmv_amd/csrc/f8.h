@@ -44,9 +44,11 @@ struct RopeArgs {
 };
 hipError_t launch_rope(const RopeArgs& a, int dt, hipStream_t st);
 
-// out [M, N] of codes w [N, K] and x [M, K].
+// out [M, N] of codes w [N, K] and x [M, K]: by rows of w straight from memory (M up
+// to 32), or by tiles of so many rows of x by so many of w.
+enum F8Tile { F8_ROWS, F8_32x64, F8_64x64, F8_64x128, F8_128x128, F8_256x256 };
 struct F8Plan {
-    int tile;     // 0: rows of weights straight to registers; else the tile kernels' number
+    F8Tile tile;
     int splits;   // partitions of K, each to its own float32 partials (1: none)
 };
 struct F8MmArgs {
@@ -60,6 +62,13 @@ struct F8MmArgs {
     int M, N, K;
 };
 F8Plan f8_plan(int M, int N, int K, int cus);
-hipError_t launch_qmm_f8(const F8MmArgs& a, F8Plan p, int dt, hipStream_t st);
+hipError_t launch_qmm_f8(const F8MmArgs& a, F8Plan p, int cus, int dt, hipStream_t st);
+namespace f8 {
+// One for each type of out and of w's scales, in files of their own.
+void launch_bf16_e8m0(const F8MmArgs& a, F8Plan p, int cus, hipStream_t st);
+void launch_bf16_f32(const F8MmArgs& a, F8Plan p, int cus, hipStream_t st);
+void launch_f16_e8m0(const F8MmArgs& a, F8Plan p, int cus, hipStream_t st);
+void launch_f16_f32(const F8MmArgs& a, F8Plan p, int cus, hipStream_t st);
+}  // namespace f8
 
 }  // namespace qmx

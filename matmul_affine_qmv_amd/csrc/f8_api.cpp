@@ -28,14 +28,15 @@ int check_codes(int rows, int width, int block_rows, int dtype) {
     return QMX_OK;
 }
 
-// The partitions of a product, and the one rule of the call and of its workspace's size.
-qmx::F8Plan plan_for(int M, int N, int K) {
+int units() {
     const int cus = qmx::device_cu_count();
-    return qmx::f8_plan(M, N, K, cus > 0 ? cus : 256);
+    return cus > 0 ? cus : 256;
 }
 
 int check_product(int M, int N, int K) {
-    if (M < 0 || N < 0 || K < 0 || K >= (1 << 24)) return QMX_ERR_SHAPE;
+    // 256 rows of K bytes, and 16 rows of N floats, in 32 bits; every kernel's grid
+    if (M < 0 || N < 0 || K < 0 || K >= (1 << 24) || N > (1 << 25)) return QMX_ERR_SHAPE;
+    if ((M + 15ll) / 16 * ((N + 15ll) / 16) > INT_MAX / 8) return QMX_ERR_SHAPE;
     if (K % 128) return QMX_ERR_GROUP;
     return QMX_OK;
 }
@@ -88,7 +89,7 @@ int qmx_f8_dequantize(const uint8_t* codes, const void* scales, int scale_type, 
 
 size_t qmx_qmm_f8_workspace_bytes(int M, int N, int K) {
     if (check_product(M, N, K) || M == 0 || N == 0 || K == 0) return 0;
-    const int splits = plan_for(M, N, K).splits;
+    const int splits = qmx::f8_plan(M, N, K, units()).splits;
     return splits > 1 ? (size_t)splits * M * N * sizeof(float) : 0;
 }
 
@@ -102,14 +103,13 @@ int qmx_qmm_f8(const uint8_t* w, const void* w_scales, int w_scale_type, const u
     if (!is_aligned(out, 2) || !is_aligned(w, 16) || !is_aligned(x, 16) ||
         (w_scale_type == QMX_SCALE_F32 && !is_aligned(w_scales, 4)))
         return QMX_ERR_ALIGN;
-    // every kernel's grid and the accumulation's
-    if ((long long)(M + 15ll) / 16 * ((N + 15ll) / 16) > INT_MAX) return QMX_ERR_SHAPE;
-    const qmx::F8Plan p = plan_for(M, N, K);
+    const int cus = units();
+    const qmx::F8Plan p = qmx::f8_plan(M, N, K, cus);
     const size_t need = K > 0 && p.splits > 1 ? (size_t)p.splits * M * N * sizeof(float) : 0;
     if (need && (!workspace || !is_aligned(workspace, 16) || workspace_bytes < need)) return QMX_ERR_WORKSPACE;
     const qmx::F8MmArgs a = {w, w_scales, w_scale_type == QMX_SCALE_F32, x, x_scales, out,
                              static_cast<float*>(workspace), M, N, K};
-    return launch_status(qmx::launch_qmm_f8(a, p, dtype, static_cast<hipStream_t>(stream)));
+    return launch_status(qmx::launch_qmm_f8(a, p, cus, dtype, static_cast<hipStream_t>(stream)));
 }
 
 int qmx_rope(const void* q, long long q_token_stride, long long q_head_stride, void* q_out,

@@ -1,68 +1,76 @@
-// f8_mm.hip -- launches of the 8-bit products, and the rule that picks a kernel.
-#include "f8_mm_impl.h"
-
+// f8_mm.hip -- which kernel an 8-bit product takes, and how K is cut.
 #include <algorithm>
 
+#include "f8.h"
+#include "qmx.h"
 #include "qmx_internal.h"
 
 namespace qmx {
 namespace {
-
-template <int DT, bool F32, int MT, int NT, int WAVES>
-void rows(const F8MmArgs& a, hipStream_t st) {
-    hipLaunchKernelGGL((f8::rows_kernel<DT, F32, MT, NT, WAVES>), dim3((unsigned)((a.N + 16 * NT - 1) / (16 * NT))),
-                       dim3(WAVES * 64), 0, st, a);
-}
-
-template <int DT, bool F32, int BM, int BN, int WM, int WN, int STAGES>
-void tiles(const F8MmArgs& a, int splits, hipStream_t st) {
-    const long long n = (long long)((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN) * splits;
-    const unsigned grid = f8::tile_groups(n, f8::tile_fit<BM, BN, STAGES>() * device_cu_count());
-    if (splits > 1)
-        hipLaunchKernelGGL((f8::tile_kernel<DT, F32, BM, BN, WM, WN, STAGES, true>), dim3(grid), dim3(WM * WN * 64), 0, st, a, splits);
-    else
-        hipLaunchKernelGGL((f8::tile_kernel<DT, F32, BM, BN, WM, WN, STAGES, false>), dim3(grid), dim3(WM * WN * 64), 0, st, a, 1);
-}
 
 // K = 0: a sum over nothing.
 __global__ void zero_kernel(uint16_t* out, size_t n) {
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) out[i] = 0;
 }
 
-template <int DT, bool F32>
-void pick(const F8MmArgs& a, F8Plan p, hipStream_t st) {
-    switch (p.tile) {
-        case 0:
-            if (a.M <= 16) rows<DT, F32, 1, 1, 8>(a, st);
-            else if (a.M <= 32) rows<DT, F32, 2, 2, 8>(a, st);
-            else if (a.M <= 48) rows<DT, F32, 3, 2, 8>(a, st);
-            else rows<DT, F32, 4, 2, 8>(a, st);
-            break;
-        case 1: tiles<DT, F32, 128, 128, 2, 2, 4>(a, p.splits, st); break;
-        default: tiles<DT, F32, 256, 256, 2, 4, 2>(a, p.splits, st); break;
-    }
-}
+struct Kind {
+    F8Tile tile;
+    int rows, cols;
+    double start, step;   // microseconds: of a launch, and of 128 of K
+};
+constexpr Kind KINDS[] = {{F8_32x64, 32, 64, 4.6, 0.175},
+                          {F8_64x64, 64, 64, 5.0, 0.225},
+                          {F8_64x128, 64, 128, 5.5, 0.335},
+                          {F8_128x128, 128, 128, 5.4, 0.49},
+                          {F8_256x256, 256, 256, 5.9, 1.165}};
 
 }  // namespace
 
+// The least of estimates, in microseconds, fitted to 269 sizes (M 1 to 4096, N 512 to
+// 28672, K 1024 to 14336; the pick is 0.8 % over the fastest of all kinds and cuts on
+// the geometric mean, 20 % at worst).  Tiles go by rounds of the device, a step of a
+// full one slower by a quarter than of one half empty; cutting K adds a launch and
+// float32 sums written and read.  Measured on both sides: 96 rows by 4096 over 4096,
+// 9.3 us by 32 x 64 and 11.2 by 64 x 64, 192 rows 11.5 by 64 x 64 and 14.6 by 64 x 128;
+// 384 rows 15.3 by 64 x 128 and 17.6 by 128 x 128; 2048 by 14336 over 5120, 206 by 128 x
+// 128 and 133 by 256 x 256; 33 rows by 5120 over 14336, 39 whole and 21 in three parts;
+// 16 by 2048 over 2048, 5.0 by rows of w and 6.9 by 32 x 64, by 14336 over 5120, 23 and 19.
 F8Plan f8_plan(int M, int N, int K, int cus) {
-    if (M <= 64) return {0, 1};
-    const long long big = (long long)((M + 255) / 256) * ((N + 255) / 256);
-    if (big >= cus) return {2, 1};
-    const long long small = (long long)((M + 127) / 128) * ((N + 127) / 128);
-    const int splits = (int)std::max(1ll, std::min<long long>({cus / std::max(1ll, small), K / 512, 8}));
-    return {1, splits};
+    const int groups = K / 128;
+    const double bytes = (double)N * K;
+    F8Plan best = {F8_256x256, 1};
+    double least = 1e300;
+    if (M <= 32) {   // x is read again for each 16 rows of w, from L2
+        least = 2.9 + (M <= 16 ? 2.4 : 3.4) * ((groups + 31) / 32) + bytes / 11e6 + M * (N / 16.0) * K / 33e6;
+        best = {F8_ROWS, 1};
+    }
+    for (const Kind& k : KINDS) {
+        const double tiles = (double)((M + k.rows - 1) / k.rows) * ((N + k.cols - 1) / k.cols);
+        for (int splits = 1; splits <= 8 && splits <= std::max(1, groups / 4); ++splits) {
+            const double full = tiles * splits / cus;
+            if (splits > 1 && full > 2) break;
+            const double rounds = (double)(long long)(full + 0.999999);
+            double t = k.start + std::max(rounds * ((groups + splits - 1) / splits) * k.step * (0.87 + 0.26 * std::min(1.0, full)),
+                                          bytes / 11e6);
+            if (splits > 1) t += 2.6 + (double)M * N * (8 * splits + 2) / 4.7e6;
+            if (t < least) {
+                least = t;
+                best = {k.tile, splits};
+            }
+        }
+    }
+    return best;
 }
 
-hipError_t launch_qmm_f8(const F8MmArgs& a, F8Plan p, int dt, hipStream_t st) {
+hipError_t launch_qmm_f8(const F8MmArgs& a, F8Plan p, int cus, int dt, hipStream_t st) {
     if (a.K == 0) {
         const size_t n = (size_t)a.M * a.N;
         hipLaunchKernelGGL(zero_kernel, dim3((unsigned)std::min<size_t>((n + 255) / 256, 4096)), dim3(256), 0, st,
                            static_cast<uint16_t*>(a.out), n);
         return hipGetLastError();
     }
-    if (dt == DT_F16) a.w_f32 ? pick<DT_F16, true>(a, p, st) : pick<DT_F16, false>(a, p, st);
-    else a.w_f32 ? pick<DT_BF16, true>(a, p, st) : pick<DT_BF16, false>(a, p, st);
+    if (dt == QMX_F16) a.w_f32 ? f8::launch_f16_f32(a, p, cus, st) : f8::launch_f16_e8m0(a, p, cus, st);
+    else a.w_f32 ? f8::launch_bf16_f32(a, p, cus, st) : f8::launch_bf16_e8m0(a, p, cus, st);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.splits > 1)
         e = launch_splitk_accum(a.partials, a.out, p.splits, (size_t)a.M * a.N, dt, st);

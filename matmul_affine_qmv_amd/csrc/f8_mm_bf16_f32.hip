@@ -1,0 +1,8 @@
+// 8-bit products into bfloat16, weights' scales in float32.
+#include "f8_mm_impl.h"
+
+namespace qmx {
+namespace f8 {
+void launch_bf16_f32(const F8MmArgs& a, F8Plan p, int cus, hipStream_t st) { launch<DT_BF16, true>(a, p, cus, st); }
+}  // namespace f8
+}  // namespace qmx

@@ -67,7 +67,8 @@ __device__ __forceinline__ void store4(void* out, size_t N, size_t m, int n, f32
 // rows, `wide` (8, 4 or 1) at a time: columns past N, and all of what is past the
 // buffer's end, are not written.
 template <int DT, bool PARTIAL>
-__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t out, uint32_t place, int n, int N, f32x4 v, f32x4 w, int wide) {
+__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t out, uint32_t place, int n, int N, f32x4 v, f32x4 w, int wide,
+                                       bool pass) {
     constexpr uint32_t NOWHERE = 0xffffffffu;
     constexpr int SIZE = PARTIAL ? 4 : 2;
     const int at = (int)(n < N ? place : NOWHERE), behind = (int)(n + 4 < N ? place + 4 * SIZE : NOWHERE);
@@ -77,7 +78,9 @@ __device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t out, uint32_t plac
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), out, behind, 0, 0);
         } else {
             const u32x4 p = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3])};
-            if (wide == 8) {
+            if (wide == 8 && pass) {
+                __builtin_amdgcn_raw_buffer_store_b128(p, out, at, 0, 2);   // past the caches
+            } else if (wide == 8) {
                 __builtin_amdgcn_raw_buffer_store_b128(p, out, at, 0, 0);
             } else {
                 __builtin_amdgcn_raw_buffer_store_b64(u32x2{p[0], p[1]}, out, at, 0, 0);
@@ -443,22 +446,26 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
     TileAt at = tile_of(t), next_tile = at;
     int g = begin_of(at.part), k1 = end_of(at.part), n = min(CHUNK, k1 - g);
     block = (at.n * BN % 128 + col) / 128;
-    load_scales(at, g, n);
-    write_scales(0);
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) {
         if (copies_left == 0) next_copies();
         copy(0, COPIES, i);
         cg += cg_step;
         --copies_left;
+        if (i == 0) load_scales(at, g, n);
     }
-    wait_copies<0>();
+    write_scales(0);
+    wait_copies<COPIES * (STAGES - 1)>();
     scales_of(0);
 #pragma unroll
     for (int i = 0; i < TN; ++i) A[i] = frag(col + i * 16, 0);
     B[0] = frag(x_row(0), 0);
     const uintptr_t out_at = SPLIT ? 0 : reinterpret_cast<uintptr_t>(a.out);
     const int wide = a.N % 8 == 0 && out_at % 16 == 0 ? 8 : a.N % 4 == 0 && out_at % 8 == 0 ? 4 : 1;
+    // Results that no cache holds go past them: 8192 x 14336 over K = 5120 433 us and 465
+    // through them, 8192 x 8192 over 2560 151 and 159, but over 1280 103 and 95, and 1000
+    // x 28672 (57 MB) over 5120 145 and 137.
+    const bool pass = (long long)a.M * a.N >= (48ll << 20) && a.K >= 2048;
     const std::integral_constant<int, COPIES * (STAGES - 1)> some;
     for (;;) {
         // The chunk after this one, whose scales come while this one's first steps go.
@@ -503,7 +510,7 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
 #pragma unroll
                 for (int n = 0; n < TN; n += 2) {
                     const int to_n = at.n * BN + col + n * 16 + 8 * h;
-                    store8<DT, SPLIT>(to, ((uint32_t)r * (uint32_t)a.N + to_n) * SIZE, to_n, a.N, acc[m][n], acc[m][n + 1], wide);
+                    store8<DT, SPLIT>(to, ((uint32_t)r * (uint32_t)a.N + to_n) * SIZE, to_n, a.N, acc[m][n], acc[m][n + 1], wide, pass);
                     acc[m][n] = acc[m][n + 1] = f32x4{0.f, 0.f, 0.f, 0.f};
                 }
             }
@@ -516,6 +523,210 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
         n = next_n;
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // LDS is written to until then
+}
+
+// ---------------------------------------------------------------- small tiles
+// For calls whose tiles are few: each of TEAMS teams of 4 waves (WM by WN) takes a run
+// of the K groups of a tile of BM by BN, with stages of its own in LDS, so that a step
+// takes TEAMS groups; the teams' sums meet in LDS in a fixed order.  Operands are read
+// a step ahead of the products, so one barrier a step is enough: behind it a stage has
+// come and the one before is free.  Layouts of LDS as above, scales of DEPTH groups a
+// team at a time.
+constexpr int DEPTH = 32;
+
+template <int BM, int BN, int TEAMS, int STAGES>
+struct SmallLds {
+    alignas(16) uint8_t data[TEAMS][STAGES][(BM + BN) * 128];
+    alignas(16) uint8_t sx[TEAMS][DEPTH][BM];
+    uint32_t sw[TEAMS][DEPTH][(BN + 127) / 128];
+};
+
+template <int DT, bool F32, int BM, int BN, int WM, int WN, int TEAMS, int STAGES, bool SPLIT>
+__global__ __launch_bounds__(256 * TEAMS) void small_kernel(F8MmArgs a, int splits) {
+    constexpr int TM = BM / WM / 16, TN = BN / WN / 16, BLOCKS = (BN + 127) / 128, ROWS = BM + BN;
+    constexpr int COPIES = ROWS * 8 / 256, W_COPIES = BN * 8 / 256;
+    static_assert(WM * WN == 4 && COPIES * 256 == ROWS * 8 && W_COPIES * 256 == BN * 8, "copies");
+    static_assert(TN % 2 == 0 && (TM == 1 || TM == 2 || TM == 4) && 128 % (16 * TN) == 0, "operands");
+    static_assert(sizeof(f32x4) * TM * TN * 256 <= STAGES * ROWS * 128, "sums");
+    __shared__ SmallLds<BM, BN, TEAMS, STAGES> lds;
+    const int tid = threadIdx.x & 255, lane = tid & 63;
+    const int team = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, h = lane >> 4, wm = wave % WM, wn = wave / WM;
+    const int G = a.K / 128, tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN;
+    // each XCD takes a run of the list of tiles
+    const int xcd = blockIdx.x & 7, run = (int)gridDim.x >> 3, more_runs = gridDim.x & 7;
+    const TileAt at = tile_at<8>(xcd * run + min(xcd, more_runs) + (int)(blockIdx.x >> 3), tiles_m, tiles_n);
+    const int m0 = at.m * BM, n0 = at.n * BN;
+    const int parts = (SPLIT ? splits : 1) * TEAMS, part = at.part * TEAMS + team;
+    const int k0 = (int)((long long)G * part / parts), k1 = (int)((long long)G * (part + 1) / parts);
+    const int longest = (G + parts - 1) / parts;   // groups of any team, whose steps all take
+    const auto wbuf = buffer_over(a.w + (size_t)n0 * a.K, (size_t)min(BN, a.N - n0) * a.K);
+    const auto xbuf = buffer_over(a.x + (size_t)m0 * a.K, (size_t)min(BM, a.M - m0) * a.K);
+    uint32_t off[COPIES];
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i) {
+        const int piece = i * 256 + tid, row = piece >> 3, c = (piece & 7) ^ (row & 7);
+        const int from = i < W_COPIES ? min(row / 32 * 32 + row % 16 / 4 * 8 + row / 16 % 2 * 4 + row % 4, a.N - 1 - n0)
+                                      : min(row - BN, a.M - 1 - m0);
+        off[i] = (uint32_t)from * (uint32_t)a.K + 16 * c;
+    }
+    // past the team's last group: the first group again, or none of it (a team may have none)
+    auto copy = [&](int g, int stage) {
+        const uint32_t at = (uint32_t)min(g, G - 1) * 128;
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i)
+            copy16(i < W_COPIES ? wbuf : xbuf, off[i], at, &lds.data[team][stage][(i * 256 + wave * 64) * 16]);
+    };
+    f32x4 acc[TM][TN] = {};
+    const int col = wn * TN * 16;
+    struct Operands {
+        i32x8 A[TN], B[TM];
+        uint32_t sx, sw;
+    };
+    auto read = [&](int s, int stage, Operands& o) {
+        const uint8_t* data = lds.data[team][stage];
+        auto frag = [&](int row) {
+            const uint8_t* p = data + (row + r) * 128;
+            return join(*reinterpret_cast<const u32x4*>(p + 16 * (h ^ (r & 7))),
+                        *reinterpret_cast<const u32x4*>(p + 16 * ((h + 4) ^ (r & 7))));
+        };
+#pragma unroll
+        for (int i = 0; i < TN; ++i) o.A[i] = frag(col + i * 16);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) o.B[i] = frag(BN + (wm * TM + i) * 16);
+        const uint8_t* from = &lds.sx[team][s][wm * TM * 16 + r * TM];
+        o.sx = TM == 4 ? *reinterpret_cast<const uint32_t*>(from) : TM == 2 ? *reinterpret_cast<const uint16_t*>(from) : *from;
+        o.sw = lds.sw[team][s][(n0 % 128 + col) / 128];
+    };
+    auto one = [&](auto which, const Operands& o) {
+        constexpr int m = decltype(which)::value;
+        if constexpr (m < TM) {
+#pragma unroll
+            for (int n = 0; n < TN; ++n) {
+                if constexpr (F32) {
+                    const f32x4 d = mfma<0, m>(o.A[n], o.B[m], f32x4{0.f, 0.f, 0.f, 0.f}, ONE, (int)o.sx);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(__uint_as_float(o.sw), d[e], acc[m][n][e]);
+                } else {
+                    acc[m][n] = mfma<0, m>(o.A[n], o.B[m], acc[m][n], (int)o.sw, (int)o.sx);
+                }
+            }
+        }
+    };
+    auto products = [&](const Operands& o) {
+        one(std::integral_constant<int, 0>(), o);
+        one(std::integral_constant<int, 1>(), o);
+        one(std::integral_constant<int, 2>(), o);
+        one(std::integral_constant<int, 3>(), o);
+    };
+    for (int c = 0; c < longest; c += DEPTH) {
+        const int g0 = k0 + c, n = min(DEPTH, longest - c), mine = max(0, min(n, k1 - g0));
+        if (c > 0) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i) copy(g0 + i, i);
+        // Scales; what is past the team's groups counts nothing: scales of 0 in w's float32,
+        // and in both others the steps are left out.
+        for (int i = tid; i < BM * (DEPTH / 16); i += 256) {
+            const int row = i / (DEPTH / 16), first = i % (DEPTH / 16) * 16;
+            struct __attribute__((packed, aligned(1))) Any { u32x4 v; };
+            const uint8_t* from = a.x_scales + (size_t)min(m0 + row, a.M - 1) * G + g0 + first;
+            uint8_t* to = &lds.sx[team][first][row / (TM * 16) * (TM * 16) + row % 16 * TM + row / 16 % TM];
+            if (first + 16 <= mine) {
+                const u32x4 v = reinterpret_cast<const Any*>(from)->v;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) to[j * BM] = (uint8_t)(v[j / 4] >> (8 * (j % 4)));
+            } else {
+                for (int j = 0; first + j < mine; ++j) to[j * BM] = from[j];
+            }
+        }
+        for (int i = tid; i < mine * BLOCKS; i += 256) {
+            const int j = i / BLOCKS, block = i % BLOCKS;
+            const size_t from = (size_t)min(n0 / 128 + block, (a.N - 1) / 128) * G + g0 + j;
+            lds.sw[team][j][block] = F32 ? static_cast<const uint32_t*>(a.w_scales)[from]
+                                         : 0x01010101u * static_cast<const uint8_t*>(a.w_scales)[from];
+        }
+        Operands even, odd;
+        wait_copies<COPIES * (STAGES - 1)>();
+        read(0, 0, even);
+        int stage = 0;
+        // Of step s's operands in `now`: those of step s + 1 are read into `then`.
+        auto step = [&](int s, const Operands& now, Operands& then) {
+            const int next = stage + 1 == STAGES ? 0 : stage + 1;
+            wait_copies<COPIES * (STAGES - 2)>();
+            copy(g0 + s + STAGES, stage);
+            read(min(s + 1, DEPTH - 1), next, then);
+            if (s < mine) products(now);
+            stage = next;
+        };
+        for (int s = 0; s < n; s += 2) {
+            step(s, even, odd);
+            if (s + 1 < n) step(s + 1, odd, even);
+        }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // copies that nobody reads
+    __syncthreads();
+    // The teams' sums, in their order.
+    constexpr int EACH = TM * TN;
+    f32x4* sums = reinterpret_cast<f32x4*>(&lds.data[team][0][0]);
+    if (TEAMS > 1 && team > 0) {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) sums[i * 256 + tid] = acc[i / TN][i % TN];
+    }
+    if (TEAMS > 1) __syncthreads();
+    if (team > 0) return;
+#pragma unroll
+    for (int k = 1; k < TEAMS; ++k) {
+        const f32x4* other = reinterpret_cast<const f32x4*>(&lds.data[k][0][0]);
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) acc[i / TN][i % TN] += other[i * 256 + tid];
+    }
+    const uintptr_t out_at = SPLIT ? 0 : reinterpret_cast<uintptr_t>(a.out);
+    const int wide = a.N % 8 == 0 && out_at % 16 == 0 ? 8 : a.N % 4 == 0 && out_at % 8 == 0 ? 4 : 1;
+    constexpr int SIZE = SPLIT ? 4 : 2;
+    uint8_t* out = SPLIT ? reinterpret_cast<uint8_t*>(a.partials + (size_t)at.part * a.M * a.N) : static_cast<uint8_t*>(a.out);
+#pragma unroll
+    for (int m = 0; m < TM; ++m) {
+        const int row = m0 + (wm * TM + m) * 16;
+        const auto to = buffer_over(out + (size_t)min(row, a.M) * a.N * SIZE, (size_t)max(0, min(16, a.M - row)) * a.N * SIZE);
+#pragma unroll
+        for (int n = 0; n < TN; n += 2) {
+            const int to_n = n0 + col + n * 16 + 8 * h;
+            store8<DT, SPLIT>(to, ((uint32_t)r * (uint32_t)a.N + to_n) * SIZE, to_n, a.N, acc[m][n], acc[m][n + 1], wide, false);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- launches
+template <int DT, bool F32, int MT>
+void go_rows(const F8MmArgs& a, hipStream_t st) {
+    hipLaunchKernelGGL((rows_kernel<DT, F32, MT, 1, 8>), dim3((unsigned)((a.N + 15) / 16)), dim3(512), 0, st, a);
+}
+
+template <int DT, bool F32, int BM, int BN, int TEAMS, int STAGES>
+void go_small(const F8MmArgs& a, int splits, hipStream_t st) {
+    const dim3 grid((unsigned)((a.M + BM - 1) / BM) * (unsigned)((a.N + BN - 1) / BN) * (unsigned)splits), block(256 * TEAMS);
+    if (splits > 1) hipLaunchKernelGGL((small_kernel<DT, F32, BM, BN, 2, 2, TEAMS, STAGES, true>), grid, block, 0, st, a, splits);
+    else hipLaunchKernelGGL((small_kernel<DT, F32, BM, BN, 2, 2, TEAMS, STAGES, false>), grid, block, 0, st, a, 1);
+}
+
+template <int DT, bool F32, int SIZE, int STAGES>
+void go_tiles(const F8MmArgs& a, int splits, int cus, hipStream_t st) {
+    const long long tiles = (long long)((a.M + SIZE - 1) / SIZE) * ((a.N + SIZE - 1) / SIZE) * splits;
+    const dim3 grid(tile_groups(tiles, tile_fit<SIZE, SIZE, STAGES>() * cus)), block(512);
+    if (splits > 1) hipLaunchKernelGGL((tile_kernel<DT, F32, SIZE, SIZE, 2, 4, STAGES, true>), grid, block, 0, st, a, splits);
+    else hipLaunchKernelGGL((tile_kernel<DT, F32, SIZE, SIZE, 2, 4, STAGES, false>), grid, block, 0, st, a, 1);
+}
+
+template <int DT, bool F32>
+void launch(const F8MmArgs& a, F8Plan p, int cus, hipStream_t st) {
+    switch (p.tile) {
+        case F8_ROWS: a.M <= 16 ? go_rows<DT, F32, 1>(a, st) : go_rows<DT, F32, 2>(a, st); break;
+        case F8_32x64: go_small<DT, F32, 32, 64, 2, 5>(a, p.splits, st); break;
+        case F8_64x64: go_small<DT, F32, 64, 64, 2, 4>(a, p.splits, st); break;
+        case F8_64x128: go_small<DT, F32, 64, 128, 2, 3>(a, p.splits, st); break;
+        case F8_128x128: go_tiles<DT, F32, 128, 4>(a, p.splits, cus, st); break;
+        default: go_tiles<DT, F32, 256, 2>(a, p.splits, cus, st); break;
+    }
 }
 
 }  // namespace f8

@@ -494,14 +494,17 @@ def test_product_special_values(M):
         x.view(torch.uint8)[3, 200] = 0xff
     got = qmx.qmm_f8(*[t.to(DEV) for t in (w, ws, x, xs)], dtype=torch.bfloat16).cpu().double()
     want = ref.values(x, xs) @ ref.values(w, ws).T
-    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    # where magnitudes sum up beyond float32, parts of a sum may be infinities of both signs
+    inside = ref.values(x, xs).abs() @ ref.values(w, ws).abs().T <= torch.finfo(torch.float32).max
+    nan = torch.isnan(want)
+    assert torch.equal(torch.isnan(got)[inside | nan], nan[inside | nan])
     if M > 2:
         assert torch.isnan(got[2:4]).all()
     row0, bound = ref.product(w, ws, x[:1], xs[:1])
     assert ((got[:1] - row0).abs() <= bound + ref.half_step(row0.abs() + bound, torch.bfloat16) + 2.0 ** -133).all()
-    # 2^127 and numbers beside 1: beyond the type, so infinite
+    # 2^127 and numbers beside 1: beyond the type
     big = want[1, 128:256].abs() > 3.5e38
-    assert big.any() and torch.isinf(got[1, 128:256][big]).all()
+    assert big.any() and not torch.isfinite(got[1, 128:256][big]).any()
     empty = torch.zeros(M, 0, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
     none = torch.zeros(300, 0, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
     zero = qmx.qmm_f8(none, torch.zeros(3, 0, dtype=torch.uint8, device=DEV), empty,
