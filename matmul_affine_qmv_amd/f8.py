@@ -18,70 +18,85 @@ from . import QMX_BF16, QMX_F16, QmxError, lib
 _HALVES = {torch.float16: QMX_F16, torch.bfloat16: QMX_BF16}
 _CODES, _SCALES = torch.float8_e4m3fn, torch.float8_e8m0fnu
 _BYTES = (_SCALES, torch.uint8)
+_ANY_SCALES = (*_BYTES, torch.float32)
 _SCALE_E8M0, _SCALE_F32 = 0, 1
 
+# A call's own cost on the host counts beside kernels of a few microseconds: the
+# checks are written out where they are made, the stream is asked for as a number,
+# and pointers go to the library as numbers.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_like = torch.empty_like
 
 
-def _on(index, name, *args):
-    """The library's function on a device, which is made the current one if it is not."""
-    if index == _current_device():
-        return getattr(lib(), name)(*args)
-    with torch.cuda.device(index):
-        return getattr(lib(), name)(*args)
+_WHOLE = torch.contiguous_format
 
 
-def _call(index, name, *args):
-    """The same on its current stream, its status checked."""
-    status = _on(index, name, *args, _raw_stream(index))
+@lru_cache(maxsize=None)
+def _function(name):
+    return getattr(lib(), name)
+
+
+def _check(status, name):
     if status:
         raise QmxError(status, name)
 
 
-def _rows(t, name, dtype=None, shape=None):
-    """Row stride of a 16-bit matrix with unit element stride."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be [rows, width]")
-    if not t.is_cuda:
-        raise ValueError("all tensors must be on a HIP device")
-    if t.dtype not in _HALVES:
-        raise ValueError(f"{name} has an unsupported dtype {t.dtype}")
-    stride, last = t.stride()
-    if last != 1 and t.shape[1] > 1:
-        raise ValueError(f"{name} must have a unit last stride")
-    if dtype is not None and (t.dtype is not dtype or t.shape != shape):
+def _rows(t, name, dtype, shape, index):
+    """Row stride of another 16-bit matrix with unit element stride."""
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)} of dtype {dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on HIP device {index}")
+    stride, last = t.stride()
+    if last != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have a unit last stride")
     return stride
 
 
+def _first(x):
+    """dtype code, shape, row stride and device index of a 16-bit matrix."""
+    code = _HALVES.get(x.dtype)
+    if code is None or x.dim() != 2:
+        raise ValueError(f"x must be [rows, width] in float16 or bfloat16, got {x.dim()}-D {x.dtype}")
+    if not x.is_cuda:
+        raise ValueError("all tensors must be on a HIP device")
+    stride, last = x.stride()
+    shape = x.shape
+    if last != 1 and shape[1] > 1:
+        raise ValueError("x must have a unit last stride")
+    return code, shape, stride, x.get_device()
+
+
 def _dense(t, name, shape, dtypes, index):
-    if tuple(t.shape) != shape or t.dtype not in dtypes or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {shape} of dtype {' or '.join(str(d) for d in dtypes)}")
+    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} of dtype {' or '.join(str(d) for d in dtypes)}")
     if t.get_device() != index:
         raise ValueError(f"{name} must be on HIP device {index}")
 
 
-def _norm(x, weight, residual, eps, sum_out, out, scales):
-    stride = _rows(x, "x")
-    shape, index = x.shape, x.get_device()
-    rows, width = shape
-    if weight is not None:
-        _dense(weight, "weight", (width,), (x.dtype,), index)
+def _norm(x, first, weight, residual, eps, sum_out, out, scales):
+    code, shape, stride, index = first
+    weight_at = residual_at = sum_at = None
     r_stride = s_stride = 0
+    if weight is not None:
+        if weight.dtype is not x.dtype or weight.shape != shape[1:] or not weight.is_contiguous() \
+                or weight.get_device() != index:
+            raise ValueError(f"weight must be a contiguous [{shape[1]}] of dtype {x.dtype} on {x.device}")
+        weight_at = weight.data_ptr()
     if residual is not None:
-        r_stride = _rows(residual, "residual", x.dtype, shape)
+        r_stride = _rows(residual, "residual", x.dtype, shape, index)
+        residual_at = residual.data_ptr()
         if sum_out is None:
-            sum_out = torch.empty((rows, width), dtype=x.dtype, device=x.device)
-        s_stride = _rows(sum_out, "sum_out", x.dtype, shape)
-        if residual.get_device() != index or sum_out.get_device() != index:
-            raise ValueError(f"residual and sum_out must be on {x.device}")
+            sum_out = _like(x, memory_format=_WHOLE)
+            s_stride = shape[1]
+        else:
+            s_stride = _rows(sum_out, "sum_out", x.dtype, shape, index)
+        sum_at = sum_out.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out goes with a residual")
-    _call(index, "qmx_rms_norm", x.data_ptr(), stride, residual.data_ptr() if residual is not None else None, r_stride,
-          weight.data_ptr() if weight is not None else None, sum_out.data_ptr() if sum_out is not None else None,
-          s_stride, out.data_ptr(), scales.data_ptr() if scales is not None else None, rows, width, eps,
-          _HALVES[x.dtype])
+    _check(_function("qmx_rms_norm")(x.data_ptr(), stride, residual_at, r_stride, weight_at, sum_at, s_stride,
+                                     out.data_ptr(), scales, *shape, eps, code, _raw_stream(index)), "qmx_rms_norm")
     return sum_out
 
 
@@ -92,11 +107,15 @@ def rms_norm(x, weight=None, residual=None, *, eps=1e-6, sum_out=None, out=None)
     residual: added to x before; then (out, sum) are returned, sum being what was
     normed.  sum_out: where it goes, x or residual itself for instance.  out:
     contiguous, x itself for instance."""
+    first = _first(x)
+    if first[3] != _current_device():
+        with torch.cuda.device(first[3]):
+            return rms_norm(x, weight, residual, eps=eps, sum_out=sum_out, out=out)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif x.is_cuda:
-        _dense(out, "out", tuple(x.shape), (x.dtype,), x.get_device())
-    total = _norm(x, weight, residual, eps, sum_out, out, None)
+        out = _like(x, memory_format=_WHOLE)
+    else:
+        _dense(out, "out", x.shape, (x.dtype,), first[3])
+    total = _norm(x, first, weight, residual, eps, sum_out, out, None)
     return out if residual is None else (out, total)
 
 
@@ -104,23 +123,26 @@ def rms_norm_f8(x, weight=None, residual=None, *, eps=1e-6, sum_out=None, out=No
     """rms_norm into 8 bits: (codes [rows, width], scales [rows, width / 128]), or
     (codes, scales, sum) with a residual.  width is a multiple of 128.  out: the
     two to write into."""
-    codes, scales = _outputs(x, 1, out)
-    total = _norm(x, weight, residual, eps, sum_out, codes, scales)
+    first = _first(x)
+    if first[3] != _current_device():
+        with torch.cuda.device(first[3]):
+            return rms_norm_f8(x, weight, residual, eps=eps, sum_out=sum_out, out=out)
+    codes, scales = _outputs(x, first, 1, out)
+    total = _norm(x, first, weight, residual, eps, sum_out, codes, scales.data_ptr())
     return (codes, scales) if residual is None else (codes, scales, total)
 
 
-def _outputs(x, block_rows, out):
+def _outputs(x, first, block_rows, out):
     """Codes and scales for x, made or checked."""
-    if x.dim() != 2 or x.shape[1] % 128:
+    rows, width = first[1]
+    if width % 128:
         raise ValueError("x must be [rows, a multiple of 128]")
-    rows, width = x.shape
     shape = (-(-rows // block_rows), width // 128)
     if out is None:
-        return (torch.empty((rows, width), dtype=_CODES, device=x.device),
-                torch.empty(shape, dtype=_SCALES, device=x.device))
+        return _like(x, dtype=_CODES, memory_format=_WHOLE), x.new_empty(shape, dtype=_SCALES)
     codes, scales = out
-    _dense(codes, "codes", (rows, width), (_CODES,), x.get_device())
-    _dense(scales, "scales", shape, _BYTES, x.get_device())
+    _dense(codes, "codes", (rows, width), (_CODES,), first[3])
+    _dense(scales, "scales", shape, _BYTES, first[3])
     return codes, scales
 
 
@@ -131,46 +153,51 @@ def f8_quantize(x, *, block_rows=1, out=None):
     weights (qmx_f8_quantize)."""
     if block_rows not in (1, 128):
         raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
-    stride = _rows(x, "x")
-    codes, scales = _outputs(x, block_rows, out)
-    _call(x.get_device(), "qmx_f8_quantize", x.data_ptr(), stride, codes.data_ptr(), scales.data_ptr(), *x.shape,
-          block_rows, _HALVES[x.dtype])
+    first = code, shape, stride, index = _first(x)
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return f8_quantize(x, block_rows=block_rows, out=out)
+    codes, scales = _outputs(x, first, block_rows, out)
+    _check(_function("qmx_f8_quantize")(x.data_ptr(), stride, codes.data_ptr(), scales.data_ptr(), *shape, block_rows,
+                                        code, _raw_stream(index)), "qmx_f8_quantize")
     return codes, scales
-
-
-def _coded(codes, scales, name, types):
-    """Rows of codes to a scale, and the scales' type."""
-    if codes.dim() != 2 or codes.dtype is not _CODES or codes.shape[1] % 128:
-        raise ValueError(f"{name} must be float8_e4m3fn [rows, a multiple of 128]")
-    if not codes.is_cuda:
-        raise ValueError("all tensors must be on a HIP device")
-    if not codes.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    rows, width = codes.shape
-    block_rows = 1 if scales.dim() != 2 or scales.shape[0] == rows else 128
-    _dense(scales, f"{name}_scales", (-(-rows // block_rows), width // 128), types, codes.get_device())
-    return block_rows, _SCALE_F32 if scales.dtype is torch.float32 else _SCALE_E8M0
 
 
 def f8_dequantize(codes, scales, *, dtype=torch.bfloat16, out=None):
     """The values that codes [rows, width] stand for, in float16 or bfloat16.
     scales: [rows, width / 128], or [ceil(rows / 128), width / 128] of blocks; E8M0
     or float32 (qmx_f8_dequantize)."""
-    block_rows, kind = _coded(codes, scales, "codes", (*_BYTES, torch.float32))
+    if codes.dtype is not _CODES or codes.dim() != 2 or codes.shape[1] % 128:
+        raise ValueError("codes must be float8_e4m3fn [rows, a multiple of 128]")
+    if not codes.is_cuda:
+        raise ValueError("all tensors must be on a HIP device")
+    if not codes.is_contiguous():
+        raise ValueError("codes must be contiguous")
+    rows, width = codes.shape
+    index = codes.get_device()
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return f8_dequantize(codes, scales, dtype=dtype, out=out)
+    block_rows = 1 if scales.dim() != 2 or scales.shape[0] == rows else 128
+    _dense(scales, "scales", (-(-rows // block_rows), width // 128), _ANY_SCALES, index)
     if out is None:
-        if dtype not in _HALVES:
+        code = _HALVES.get(dtype)
+        if code is None:
             raise ValueError(f"unsupported dtype {dtype}")
-        out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+        out = _like(codes, dtype=dtype)
     else:
-        _dense(out, "out", tuple(codes.shape), tuple(_HALVES), codes.get_device())
-    _call(codes.get_device(), "qmx_f8_dequantize", codes.data_ptr(), scales.data_ptr(), kind, out.data_ptr(),
-          *codes.shape, block_rows, _HALVES[out.dtype])
+        _dense(out, "out", codes.shape, tuple(_HALVES), index)
+        code = _HALVES[out.dtype]
+    kind = _SCALE_F32 if scales.dtype is torch.float32 else _SCALE_E8M0
+    _check(_function("qmx_f8_dequantize")(codes.data_ptr(), scales.data_ptr(), kind, out.data_ptr(), rows, width,
+                                          block_rows, code, _raw_stream(index)), "qmx_f8_dequantize")
     return out
 
 
 @lru_cache(maxsize=4096)
 def _workspace_bytes(index, M, N, K):
-    return _on(index, "qmx_qmm_f8_workspace_bytes", M, N, K)
+    with torch.cuda.device(index):
+        return lib().qmx_qmm_f8_workspace_bytes(M, N, K)
 
 
 def qmm_f8_workspace_bytes(M, N, K, device="cuda") -> int:
@@ -185,31 +212,40 @@ def qmm_f8(w, w_scales, x, x_scales, out=None, *, dtype=torch.bfloat16, workspac
     w: codes [N, K], w_scales [ceil(N / 128), K / 128] E8M0 or float32;
     x: codes [M, K], x_scales [M, K / 128] E8M0; all contiguous.  workspace: of
     qmm_f8_workspace_bytes bytes, where the caller keeps one."""
-    if x.dim() != 2 or w.dim() != 2 or w.dtype is not _CODES or x.dtype is not _CODES:
+    if x.dtype is not _CODES or w.dtype is not _CODES or x.dim() != 2 or w.dim() != 2:
         raise ValueError("w and x must be float8_e4m3fn [N, K] and [M, K]")
     M, K = x.shape
-    N, index = w.shape[0], x.get_device()
-    if w.shape[1] != K or K % 128:
-        raise ValueError(f"w and x must have one K, a multiple of 128; got {w.shape[1]} and {K}")
-    if not x.is_cuda or w.get_device() != index:
+    N, K_w = w.shape
+    index = x.get_device()
+    if K_w != K or K % 128:
+        raise ValueError(f"w and x must have one K, a multiple of 128; got {K_w} and {K}")
+    if index < 0 or w.get_device() != index:
         raise ValueError("all tensors must be on one HIP device")
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return qmm_f8(w, w_scales, x, x_scales, out, dtype=dtype, workspace=workspace)
     if not w.is_contiguous() or not x.is_contiguous():
         raise ValueError("w and x must be contiguous")
-    _dense(w_scales, "w_scales", (-(-N // 128), K // 128), (*_BYTES, torch.float32), index)
+    _dense(w_scales, "w_scales", (-(-N // 128), K // 128), _ANY_SCALES, index)
     _dense(x_scales, "x_scales", (M, K // 128), _BYTES, index)
     if out is None:
-        if dtype not in _HALVES:
+        code = _HALVES.get(dtype)
+        if code is None:
             raise ValueError(f"unsupported dtype {dtype}")
-        out = torch.empty((M, N), dtype=dtype, device=x.device)
+        out = x.new_empty((M, N), dtype=dtype)
     else:
         _dense(out, "out", (M, N), tuple(_HALVES), index)
+        code = _HALVES[out.dtype]
     need = _workspace_bytes(index, M, N, K)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    elif workspace is not None and (workspace.get_device() != index or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be contiguous on {x.device}")
-    _call(index, "qmx_qmm_f8", w.data_ptr(), w_scales.data_ptr(),
-          _SCALE_F32 if w_scales.dtype is torch.float32 else _SCALE_E8M0, x.data_ptr(), x_scales.data_ptr(),
-          out.data_ptr(), M, N, K, _HALVES[out.dtype], workspace.data_ptr() if workspace is not None else None,
-          workspace.nbytes if workspace is not None else 0)
+    room, size = None, 0
+    if workspace is not None:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {x.device}")
+        room, size = workspace.data_ptr(), workspace.nbytes
+    elif need:
+        workspace = x.new_empty(need, dtype=torch.uint8)
+        room, size = workspace.data_ptr(), need
+    kind = _SCALE_F32 if w_scales.dtype is torch.float32 else _SCALE_E8M0
+    _check(_function("qmx_qmm_f8")(w.data_ptr(), w_scales.data_ptr(), kind, x.data_ptr(), x_scales.data_ptr(),
+                                   out.data_ptr(), M, N, K, code, room, size, _raw_stream(index)), "qmx_qmm_f8")
     return out

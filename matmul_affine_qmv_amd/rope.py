@@ -7,7 +7,7 @@ import math
 
 import torch
 
-from .f8 import _HALVES, _call
+from .f8 import _HALVES, _WHOLE, _check, _current_device, _function, _like, _raw_stream
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
@@ -63,17 +63,12 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | N
     return f.to(device)
 
 
-def _heads(t, name, like=None):
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    if not t.is_cuda:
-        raise ValueError("all tensors must be on a HIP device")
-    if t.dtype not in _HALVES:
-        raise ValueError(f"{name} has an unsupported dtype {t.dtype}")
-    if like is not None and (t.shape != like.shape or t.dtype is not like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must be {tuple(like.shape)} of dtype {like.dtype} on {like.device}")
+def _heads(t, name, shape, dtype, index):
+    """Address, token and head stride."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be {tuple(shape)} of dtype {dtype} on HIP device {index}")
     token, head, last = t.stride()
-    if last != 1 and t.shape[2] > 1:
+    if last != 1 and shape[2] > 1:
         raise ValueError(f"{name} must have a unit last stride")
     return t.data_ptr(), token, head
 
@@ -87,9 +82,16 @@ def rope(q, k, positions, frequencies, *, interleaved=False, scale=1.0, out=None
     2 * pairs elements of a head turn, element i with pairs + i or, interleaved, 2i
     with 2i + 1.  scale: of what turns.  out: the (q, k) to write into, q and k
     themselves to turn them in place.  Returns (q, k), contiguous if made here."""
-    args = _heads(q, "q")
-    T, heads, D = q.shape
-    index = q.get_device()
+    code = _HALVES.get(q.dtype)
+    if code is None or q.dim() != 3:
+        raise ValueError(f"q must be [tokens, heads, head_dim] in float16 or bfloat16, got {q.dim()}-D {q.dtype}")
+    if not q.is_cuda:
+        raise ValueError("all tensors must be on a HIP device")
+    index, shape, dtype = q.get_device(), q.shape, q.dtype
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return rope(q, k, positions, frequencies, interleaved=interleaved, scale=scale, out=out)
+    T, heads, D = shape
     if positions.dtype is not torch.int32 or positions.shape != (T,) or not positions.is_contiguous():
         raise ValueError(f"positions must be a contiguous int32 vector of {T}")
     if frequencies.dtype is not torch.float64 or frequencies.dim() != 1 or not frequencies.is_contiguous():
@@ -99,21 +101,28 @@ def rope(q, k, positions, frequencies, *, interleaved=False, scale=1.0, out=None
         raise ValueError(f"frequencies must have 1 to {D // 2} elements, got {pairs}")
     if positions.get_device() != index or frequencies.get_device() != index:
         raise ValueError(f"positions and frequencies must be on {q.device}")
-    if k is None:
-        key, kv_heads = (None, 0, 0), 0
-    else:
-        key, kv_heads = _heads(k, "k"), k.shape[1]
-        if k.shape[0] != T or k.shape[2] != D or k.dtype is not q.dtype or k.get_device() != index:
-            raise ValueError(f"k must be [{T}, kv_heads, {D}] of dtype {q.dtype} on {q.device}")
+    from_q = _heads(q, "q", shape, dtype, index)
+    from_k = to_k = (None, 0, 0)
+    kv_heads = 0
+    if k is not None:
+        if k.dim() != 3:
+            raise ValueError("k must be [tokens, kv_heads, head_dim]")
+        kv_heads = k.shape[1]
+        from_k = _heads(k, "k", (T, kv_heads, D), dtype, index)
     if out is None:
-        q_out = torch.empty((T, heads, D), dtype=q.dtype, device=q.device)
-        k_out = torch.empty((T, kv_heads, D), dtype=q.dtype, device=q.device) if k is not None else None
+        q_out, k_out = _like(q, memory_format=_WHOLE), None
+        to_q = (q_out.data_ptr(), heads * D, D)
+        if k is not None:
+            k_out = _like(k, memory_format=_WHOLE)
+            to_k = (k_out.data_ptr(), kv_heads * D, D)
     else:
         q_out, k_out = out
         if (k_out is None) != (k is None):
             raise ValueError("out must be as many tensors as q and k")
-    to_q = _heads(q_out, "q's out", q)
-    to_k = _heads(k_out, "k's out", k) if k is not None else (None, 0, 0)
-    _call(index, "qmx_rope", *args, *to_q, heads, *key, *to_k, kv_heads, positions.data_ptr(),
-          frequencies.data_ptr(), T, D, pairs, int(interleaved), scale, _HALVES[q.dtype])
+        to_q = _heads(q_out, "q's out", shape, dtype, index)
+        if k is not None:
+            to_k = _heads(k_out, "k's out", (T, kv_heads, D), dtype, index)
+    _check(_function("qmx_rope")(*from_q, *to_q, heads, *from_k, *to_k, kv_heads, positions.data_ptr(),
+                                 frequencies.data_ptr(), T, D, pairs, int(interleaved), scale, code,
+                                 _raw_stream(index)), "qmx_rope")
     return q_out, k_out
