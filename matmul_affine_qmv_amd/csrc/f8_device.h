@@ -10,7 +10,31 @@ namespace qmx {
 // 16-byte loads at any alignment).
 struct __attribute__((packed, aligned(2))) Any16 { u32x4 v; };
 __device__ __forceinline__ u32x4 load_any(const uint16_t* p) { return reinterpret_cast<const Any16*>(p)->v; }
-__device__ __forceinline__ void store_any(uint16_t* p, u32x4 v) { reinterpret_cast<Any16*>(p)->v = v; }
+// PASS: past the caches, where a call writes more than they are worth.
+template <bool PASS>
+__device__ __forceinline__ void store_any(uint16_t* p, u32x4 v) {
+    if constexpr (PASS) __builtin_nontemporal_store(v, &reinterpret_cast<Any16*>(p)->v);
+    else reinterpret_cast<Any16*>(p)->v = v;
+}
+// Eight elements or, from the end of a row on, the `n` that are there (zeros behind).
+__device__ __forceinline__ u32x4 load_part(const uint16_t* p, int n) {
+    if (n >= 8) return load_any(p);
+    u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n) v[i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
+    return v;
+}
+template <bool PASS>
+__device__ __forceinline__ void store_part(uint16_t* p, u32x4 v, int n) {
+    if (n >= 8) {
+        store_any<PASS>(p, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n) p[i] = (uint16_t)(v[i / 2] >> (16 * (i % 2)));
+}
 
 template <int DT>
 __device__ __forceinline__ float elem(const u32x4& w, int i) {

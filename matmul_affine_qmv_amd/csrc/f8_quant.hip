@@ -128,48 +128,51 @@ __global__ __launch_bounds__(THREADS) void dequantize_kernel(const uint8_t* __re
     }
 }
 
+template <int DT>
+void quantize(const uint16_t* x, long long stride, uint8_t* codes, uint8_t* scales, int rows, int width, int block,
+              hipStream_t st) {
+    const unsigned per_row = (unsigned)width / 128;
+    if (block == 1) {
+        constexpr int U = 4;
+        const long long groups = (long long)rows * per_row;
+        hipLaunchKernelGGL((quantize_kernel<DT, U>), dim3((unsigned)((groups + TEAMS * U - 1) / (TEAMS * U))),
+                           dim3(THREADS), 0, st, x, stride, codes, scales, per_row, groups);
+    } else {
+        hipLaunchKernelGGL((quantize_block_kernel<DT>), dim3((unsigned)(((long long)rows + 127) / 128 * per_row)),
+                           dim3(THREADS), 0, st, x, stride, codes, scales, rows, width);
+    }
+}
+
+template <int DT>
+void dequantize(const uint8_t* codes, const void* scales, bool f32, uint16_t* out, int rows, int width, int block,
+                hipStream_t st) {
+    constexpr int U = 4;
+    const unsigned per_row = (unsigned)width / 128;
+    const long long groups = (long long)rows * per_row;
+    const dim3 grid((unsigned)((groups + THREADS / 8 * U - 1) / (THREADS / 8 * U)));
+    if (f32)
+        hipLaunchKernelGGL((dequantize_kernel<DT, true, U>), grid, dim3(THREADS), 0, st, codes, scales, out, per_row,
+                           block, groups);
+    else
+        hipLaunchKernelGGL((dequantize_kernel<DT, false, U>), grid, dim3(THREADS), 0, st, codes, scales, out, per_row,
+                           block, groups);
+}
+
 }  // namespace
 
 hipError_t launch_f8_quantize(const void* x, long long stride, uint8_t* codes, uint8_t* scales, int rows, int width,
                               int block, int dt, hipStream_t st) {
     const uint16_t* p = static_cast<const uint16_t*>(x);
-    const unsigned per_row = (unsigned)width / 128;
-    if (block == 1) {
-        constexpr int U = 4;
-        const long long groups = (long long)rows * per_row;
-        const dim3 grid((unsigned)((groups + TEAMS * U - 1) / (TEAMS * U)));
-        if (dt == DT_F16)
-            hipLaunchKernelGGL((quantize_kernel<DT_F16, U>), grid, dim3(THREADS), 0, st, p, stride, codes, scales,
-                               per_row, groups);
-        else
-            hipLaunchKernelGGL((quantize_kernel<DT_BF16, U>), grid, dim3(THREADS), 0, st, p, stride, codes, scales,
-                               per_row, groups);
-    } else {
-        const dim3 grid((unsigned)(((long long)rows + 127) / 128 * per_row));
-        if (dt == DT_F16)
-            hipLaunchKernelGGL(quantize_block_kernel<DT_F16>, grid, dim3(THREADS), 0, st, p, stride, codes, scales,
-                               rows, width);
-        else
-            hipLaunchKernelGGL(quantize_block_kernel<DT_BF16>, grid, dim3(THREADS), 0, st, p, stride, codes, scales,
-                               rows, width);
-    }
+    if (dt == DT_F16) quantize<DT_F16>(p, stride, codes, scales, rows, width, block, st);
+    else quantize<DT_BF16>(p, stride, codes, scales, rows, width, block, st);
     return hipGetLastError();
 }
 
 hipError_t launch_f8_dequantize(const uint8_t* codes, const void* scales, bool f32, void* out, int rows, int width,
                                 int block, int dt, hipStream_t st) {
-    constexpr int U = 4;
     uint16_t* o = static_cast<uint16_t*>(out);
-    const unsigned per_row = (unsigned)width / 128;
-    const long long groups = (long long)rows * per_row;
-    const dim3 grid((unsigned)((groups + THREADS / 8 * U - 1) / (THREADS / 8 * U)));
-    if (dt == DT_F16) {
-        if (f32) hipLaunchKernelGGL((dequantize_kernel<DT_F16, true, U>), grid, dim3(THREADS), 0, st, codes, scales, o, per_row, block, groups);
-        else hipLaunchKernelGGL((dequantize_kernel<DT_F16, false, U>), grid, dim3(THREADS), 0, st, codes, scales, o, per_row, block, groups);
-    } else {
-        if (f32) hipLaunchKernelGGL((dequantize_kernel<DT_BF16, true, U>), grid, dim3(THREADS), 0, st, codes, scales, o, per_row, block, groups);
-        else hipLaunchKernelGGL((dequantize_kernel<DT_BF16, false, U>), grid, dim3(THREADS), 0, st, codes, scales, o, per_row, block, groups);
-    }
+    if (dt == DT_F16) dequantize<DT_F16>(codes, scales, f32, o, rows, width, block, st);
+    else dequantize<DT_BF16>(codes, scales, f32, o, rows, width, block, st);
     return hipGetLastError();
 }
 

@@ -45,26 +45,6 @@ __device__ __forceinline__ double wave_sum64(double v) {
     return v;
 }
 
-// Eight elements, of which `n` are there (zeros behind them).
-__device__ __forceinline__ u32x4 load_part(const uint16_t* p, int n) {
-    if (n >= 8) return load_any(p);
-    u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) v[i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
-    return v;
-}
-
-__device__ __forceinline__ void store_part(uint16_t* p, u32x4 v, int n) {
-    if (n >= 8) {
-        store_any(p, v);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = (uint16_t)(v[i / 2] >> (16 * (i % 2)));
-}
-
 template <int DT>
 __device__ __forceinline__ u32x4 add8(u32x4 x, u32x4 r) {
     // two roundings, to 32 bits and to the type, give what one gives: 24 >= 2 * 11 + 2
@@ -134,14 +114,14 @@ __device__ __forceinline__ void finish8(const NormArgs& a, size_t row, int at, i
         u32x4 o;
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = pack2<DT>(y[2 * i], y[2 * i + 1]);
-        store_part(static_cast<uint16_t*>(a.out) + to, o, n);
+        store_part<false>(static_cast<uint16_t*>(a.out) + to, o, n);
     }
 }
 
 // One row for each wave (WAVE) or for the whole work-group, whose lanes hold up to
 // VPT * 8 of its elements each.
-template <int DT, bool F8, bool WAVE, int VPT>
-__global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
+template <int DT, bool F8, bool PASS, bool WAVE, int VPT>
+__global__ __launch_bounds__(WAVE ? 256 : VPT == 1 ? 1024 : 512) void norm_kernel(NormArgs a) {
     __shared__ double part[16];
     const int lanes = WAVE ? 64 : blockDim.x, lane = WAVE ? threadIdx.x % 64 : threadIdx.x;
     const size_t row = WAVE ? (size_t)blockIdx.x * 4 + threadIdx.x / 64 : blockIdx.x;
@@ -166,7 +146,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
         for (int j = 0; j < VPT; ++j) {
             const int at = (j * lanes + lane) * 8;
             h[j] = add8<DT>(h[j], v[j]);
-            store_part(s + at, h[j], a.width - at);
+            store_part<PASS>(s + at, h[j], a.width - at);
         }
     }
     double sum = 0.0;
@@ -203,7 +183,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
         u32x4 h = load_part(x + at, n);
         if (a.residual) {
             h = add8<DT>(h, load_part(r + at, n));
-            store_part(s + at, h, n);
+            store_part<false>(s + at, h, n);
         }
         sum = squares8<DT>(h, sum);
     }
@@ -222,27 +202,44 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
     }
 }
 
-template <int DT, bool F8, bool WAVE, int VPT>
-void go(const NormArgs& a, hipStream_t st) {
-    const long long vectors = ((long long)a.width + 7) / 8;
-    const unsigned lanes = WAVE ? 256 : (unsigned)((vectors + 64 * VPT - 1) / (64 * VPT) * 64);
-    hipLaunchKernelGGL((norm_kernel<DT, F8, WAVE, VPT>), dim3(WAVE ? ((unsigned)a.rows + 3) / 4 : (unsigned)a.rows), dim3(lanes), 0,
-                       st, a);
+template <int DT, bool F8, bool PASS, bool WAVE, int VPT>
+void go(const NormArgs& a, int lanes, hipStream_t st) {
+    hipLaunchKernelGGL((norm_kernel<DT, F8, PASS, WAVE, VPT>), dim3(WAVE ? ((unsigned)a.rows + 3) / 4 : (unsigned)a.rows),
+                       dim3((unsigned)lanes), 0, st, a);
 }
 
-template <int DT, bool F8>
+// Lanes and elements of a row (for rows of 5120 into 8 bits, 7812 of them: 66.5 us with
+// 256 lanes of 24, 71.5 with 320 of 16, 70.7 with 640 of 8; 8192 wide 66.6 with 512 of
+// 16, 74.1 with 256 of 32; 1024 wide 61.7 with a wave a row, 88 with four).  Few rows
+// take as many lanes as they have eights (1 of 5120: 3.7 us, 5.9 with 256 lanes).
+template <int DT, bool F8, bool PASS>
 void pick(const NormArgs& a, hipStream_t st) {
-    if (a.width <= 512) go<DT, F8, true, 1>(a, st);
-    else if (a.width <= 8192 && (a.width <= 2048 || a.rows < 512)) go<DT, F8, false, 1>(a, st);
-    else if (a.width <= 16384) go<DT, F8, false, 2>(a, st);
+    const int eights = (int)(((long long)a.width + 7) / 8);
+    if (eights <= 64) go<DT, F8, PASS, true, 1>(a, 256, st);
+    else if (a.rows < 256 && eights <= 1024) go<DT, F8, PASS, false, 1>(a, (eights + 63) / 64 * 64, st);
+    else if (eights <= 128) go<DT, F8, PASS, true, 2>(a, 256, st);
+    else if (eights <= 256) go<DT, F8, PASS, false, 2>(a, 128, st);
+    else if (eights <= 512) go<DT, F8, PASS, false, 2>(a, 256, st);
+    else if (eights <= 768) go<DT, F8, PASS, false, 3>(a, 256, st);
+    else if (eights <= 1024) go<DT, F8, PASS, false, 2>(a, 512, st);
+    else if (eights <= 1536) go<DT, F8, PASS, false, 3>(a, 512, st);
+    else if (eights <= 2048) go<DT, F8, PASS, false, 4>(a, 512, st);
     else hipLaunchKernelGGL((norm_long_kernel<DT, F8>), dim3((unsigned)a.rows), dim3(1024), 0, st, a);
 }
 
 }  // namespace
 
+// The sum is read again only a layer's products later: large ones go past the caches,
+// which keep the result for what comes next.
 hipError_t launch_rms_norm(const NormArgs& a, int dt, hipStream_t st) {
-    if (dt == DT_F16) a.scales ? pick<DT_F16, true>(a, st) : pick<DT_F16, false>(a, st);
-    else a.scales ? pick<DT_BF16, true>(a, st) : pick<DT_BF16, false>(a, st);
+    const bool f8 = a.scales != nullptr, pass = a.sum && (long long)a.rows * a.width >= (4ll << 20);
+    if (dt == DT_F16) {
+        if (pass) f8 ? pick<DT_F16, true, true>(a, st) : pick<DT_F16, false, true>(a, st);
+        else f8 ? pick<DT_F16, true, false>(a, st) : pick<DT_F16, false, false>(a, st);
+    } else {
+        if (pass) f8 ? pick<DT_BF16, true, true>(a, st) : pick<DT_BF16, false, true>(a, st);
+        else f8 ? pick<DT_BF16, true, false>(a, st) : pick<DT_BF16, false, false>(a, st);
+    }
     return hipGetLastError();
 }
 

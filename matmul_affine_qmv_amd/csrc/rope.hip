@@ -19,25 +19,6 @@ struct Ends {   // what an item holds of its two runs of 8 elements
     u32x4 lo, hi;
 };
 
-__device__ __forceinline__ u32x4 load_run(const uint16_t* p, int n) {
-    if (n >= 8) return load_any(p);
-    u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) v[i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
-    return v;
-}
-
-__device__ __forceinline__ void store_run(uint16_t* p, u32x4 v, int n) {
-    if (n >= 8) {
-        store_any(p, v);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = (uint16_t)(v[i / 2] >> (16 * (i % 2)));
-}
-
 // TOK tokens a work-group; a token's heads may be spread over gridDim.y groups.
 template <int DT, bool INTER, int TOK>
 __global__ __launch_bounds__(THREADS) void rope_kernel(RopeArgs a) {
@@ -90,7 +71,7 @@ __global__ __launch_bounds__(THREADS) void rope_kernel(RopeArgs a) {
         }
         const bool turned = item < rotated && a.positions[t] >= 0;
         if (!turned && a.in_place[which]) continue;
-        Ends e = {load_run(in + p0, n0), load_run(in + p1, n1)};
+        Ends e = {load_part(in + p0, n0), load_part(in + p1, n1)};
         if (turned) {
             const float2* cs = turn + k * n + 8 * item;
             const int pairs = min(8, n - 8 * item);
@@ -117,8 +98,8 @@ __global__ __launch_bounds__(THREADS) void rope_kernel(RopeArgs a) {
             }
             e = o;
         }
-        store_run(out + p0, e.lo, n0);
-        store_run(out + p1, e.hi, n1);
+        store_part<false>(out + p0, e.lo, n0);
+        store_part<false>(out + p1, e.hi, n1);
     }
 }
 
