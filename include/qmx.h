@@ -511,7 +511,8 @@ typedef enum qmx_scale_type {
  * contiguous.  Otherwise out is e4m3 codes [rows, width], 8-byte aligned, and
  * out_scales [rows, width / 128] their E8M0 scales (width % 128 == 0, else
  * QMX_ERR_GROUP).  sum may be x or residual itself, row for row, and an out in
- * `dtype` may be x itself; otherwise outputs overlap nothing.  eps: finite and
+ * `dtype` may be x itself; otherwise outputs overlap nothing, nor sum's rows each
+ * other (QMX_ERR_OVERLAP where rows or whole arguments coincide).  eps: finite and
  * above 0.  The sum is formed in 64 bits.  A y in `dtype` is formed in float32 from
  * it and rounded once more; codes and scales are those of a y in 64 bits (beyond
  * float32's range it counts as infinite). */
@@ -525,7 +526,7 @@ int qmx_rms_norm(const void* x, long long x_row_stride, const void* residual,
  * elements) into codes [rows, width], 16-byte aligned, and E8M0 scales: of each
  * 128 of a row (block_rows = 1) or of each 128 x 128 (block_rows = 128; the last
  * block of rows may be short).  width % 128 == 0 (QMX_ERR_GROUP);
- * rows * width / 128 at most 2^31 - 1. */
+ * rows * width / 128 at most 2^29 (QMX_ERR_SHAPE). */
 int qmx_f8_quantize(const void* x, long long x_row_stride, uint8_t* codes, uint8_t* scales,
                     int rows, int width, int block_rows, int dtype, void* stream);
 
@@ -541,7 +542,7 @@ int qmx_f8_dequantize(const uint8_t* codes, const void* scales, int scale_type, 
  * w: codes [N, K] with w_scales [ceil(N / 128), K / 128] of w_scale_type;
  * x: codes [M, K] with E8M0 x_scales [M, K / 128]; out: [M, N] in `dtype`
  * (QMX_F16 or QMX_BF16), rounded once.  K % 128 == 0 (QMX_ERR_GROUP), below
- * 2^24; N at most 2^25, M * N some 2^36 (QMX_ERR_SHAPE); w and x 16-byte aligned,
+ * 2^24; N at most 2^25, M 2^30, M * N some 2^36 (QMX_ERR_SHAPE); w and x 16-byte aligned,
  * out any address of whole elements.
  * Sums are float32, but for the matrix instruction's own: it aligns the scaled
  * products of 8 neighbouring k to the largest exponent among them and cuts each
@@ -569,10 +570,10 @@ size_t qmx_qmm_f8_workspace_bytes(int M, int N, int K);
  * (QMX_F16 or QMX_BF16), unit element stride, tokens and heads *_stride elements
  * apart, any address of whole elements.  Either may have 0 heads (pointers may
  * then be NULL).  An output is its own input, stride for stride (what does not
- * turn is then left alone), or overlaps nothing.  positions: int32 [tokens];
- * frequencies: float64 [pairs], radians a position; the angle is taken in 64
- * bits, its sine and cosine in 32, the result is rounded once.  head_dim: 1 to
- * 4096; 2 <= 2 * pairs <= head_dim; at most 8192 heads each; scale finite. */
+ * turn is then left alone), or overlaps nothing; its heads never each other
+ * (QMX_ERR_OVERLAP).  positions: int32 [tokens]; frequencies: float64 [pairs],
+ * radians a position; the angle is taken in 64 bits, its sine and cosine in 32, the
+ * result is rounded once.  head_dim: 2 to 4096; 2 <= 2 * pairs <= head_dim; at most 8192 heads each; scale finite. */
 int qmx_rope(const void* q, long long q_token_stride, long long q_head_stride, void* q_out,
              long long q_out_token_stride, long long q_out_head_stride, int heads, const void* k,
              long long k_token_stride, long long k_head_stride, void* k_out,

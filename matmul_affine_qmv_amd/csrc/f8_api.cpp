@@ -3,9 +3,12 @@
 // before any launch.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
+#include <utility>
 
 #include "f8.h"
 #include "qmx.h"
@@ -24,8 +27,23 @@ int check_codes(int rows, int width, int block_rows, int dtype) {
     if (!is_half(dtype)) return QMX_ERR_DTYPE;
     if (rows < 0 || width < 0) return QMX_ERR_SHAPE;
     if (width % 128 || (block_rows != 1 && block_rows != 128)) return QMX_ERR_GROUP;
-    if ((long long)rows * (width / 128) > INT_MAX) return QMX_ERR_SHAPE;
+    if ((long long)rows * (width / 128) > (1 << 29)) return QMX_ERR_SHAPE;   // below 2^32 threads
     return QMX_OK;
+}
+
+// Whether rows of `n` neighbours, `count` of them `stride` apart, `sets` times
+// `set_stride` apart, share no element.
+bool apart(long long n, long long count, long long stride, long long sets, long long set_stride) {
+    stride = std::llabs(stride);
+    set_stride = std::llabs(set_stride);
+    if (count <= 1) stride = 0;
+    if (sets <= 1) set_stride = 0;
+    if (stride > set_stride) {
+        std::swap(stride, set_stride);
+        std::swap(count, sets);
+    }
+    const __int128 span = (__int128)std::max(0ll, count - 1) * stride + n;
+    return (count <= 1 || stride >= n) && (sets <= 1 || set_stride >= span);
 }
 
 int units() {
@@ -35,7 +53,7 @@ int units() {
 
 int check_product(int M, int N, int K) {
     // 256 rows of K bytes, and 16 rows of N floats, in 32 bits; every kernel's grid
-    if (M < 0 || N < 0 || K < 0 || K >= (1 << 24) || N > (1 << 25)) return QMX_ERR_SHAPE;
+    if (M < 0 || N < 0 || K < 0 || K >= (1 << 24) || N > (1 << 25) || M > (1 << 30)) return QMX_ERR_SHAPE;
     if ((M + 15ll) / 16 * ((N + 15ll) / 16) > INT_MAX / 8) return QMX_ERR_SHAPE;
     if (K % 128) return QMX_ERR_GROUP;
     return QMX_OK;
@@ -54,10 +72,11 @@ int qmx_rms_norm(const void* x, long long x_row_stride, const void* residual, lo
     if (out_scales && width % 128) return QMX_ERR_GROUP;
     if (rows == 0 || width == 0) return QMX_OK;
     if (!x || !out || (residual != nullptr) != (sum != nullptr)) return QMX_ERR_NULL;
-    if (rows > 1 && sum && sum_row_stride < width && sum_row_stride > -(long long)width) return QMX_ERR_SHAPE;
     if (!is_aligned(x, 2) || !is_aligned(residual, 2) || !is_aligned(weight, 2) || !is_aligned(sum, 2) ||
         !is_aligned(out, out_scales ? 8 : 2))
         return QMX_ERR_ALIGN;
+    if (sum && (sum == out || !apart(width, rows, sum_row_stride, 1, 0))) return QMX_ERR_OVERLAP;
+    if (out_scales && (out == x || out == residual)) return QMX_ERR_OVERLAP;
     const qmx::NormArgs a = {x, residual, weight, sum, out, out_scales, x_row_stride, residual_row_stride,
                              sum_row_stride, rows, width, eps};
     return launch_status(qmx::launch_rms_norm(a, dtype, static_cast<hipStream_t>(stream)));
@@ -127,6 +146,9 @@ int qmx_rope(const void* q, long long q_token_stride, long long q_head_stride, v
     if (!is_aligned(q, 2) || !is_aligned(q_out, 2) || !is_aligned(k, 2) || !is_aligned(k_out, 2) ||
         !is_aligned(positions, 4) || !is_aligned(frequencies, 8))
         return QMX_ERR_ALIGN;
+    if ((heads > 0 && !apart(head_dim, heads, q_out_head_stride, tokens, q_out_token_stride)) ||
+        (kv_heads > 0 && !apart(head_dim, kv_heads, k_out_head_stride, tokens, k_out_token_stride)))
+        return QMX_ERR_OVERLAP;
     qmx::RopeArgs a = {};
     a.in[0] = q;
     a.in[1] = k;

@@ -17,12 +17,13 @@ struct Kind {
     F8Tile tile;
     int rows, cols;
     double start, step;   // microseconds: of a launch, and of 128 of K
+    double most;          // tiles that a launch can take (kernels that go on by themselves: any)
 };
-constexpr Kind KINDS[] = {{F8_32x64, 32, 64, 4.6, 0.174},
-                          {F8_64x64, 64, 64, 4.9, 0.226},
-                          {F8_64x128, 64, 128, 4.9, 0.34},
-                          {F8_128x128, 128, 128, 4.6, 0.50},
-                          {F8_256x256, 256, 256, 4.7, 1.195}};
+constexpr Kind KINDS[] = {{F8_32x64, 32, 64, 4.6, 0.174, 0x1p22},
+                          {F8_64x64, 64, 64, 4.9, 0.226, 0x1p22},
+                          {F8_64x128, 64, 128, 4.9, 0.34, 0x1p22},
+                          {F8_128x128, 128, 128, 4.6, 0.50, 0x1p31},
+                          {F8_256x256, 256, 256, 4.7, 1.195, 0x1p31}};
 
 }  // namespace
 
@@ -46,6 +47,7 @@ F8Plan f8_plan(int M, int N, int K, int cus) {
     }
     for (const Kind& k : KINDS) {
         const double tiles = (double)((M + k.rows - 1) / k.rows) * ((N + k.cols - 1) / k.cols);
+        if (tiles > k.most) continue;
         for (int splits = 1; splits <= 8 && splits <= std::max(1, groups / 4); ++splits) {
             const double full = tiles * splits / cus;
             if (splits > 1 && full > 2) break;

@@ -18,7 +18,6 @@ namespace qmx {
 namespace f8 {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 // Four neighbouring scale bytes of a row from `at` on; 0 past its end.
 __device__ __forceinline__ uint32_t scales4(const uint8_t* row, int at, int G) {
@@ -54,8 +53,7 @@ template <int DT>
 __device__ __forceinline__ void store4(void* out, size_t N, size_t m, int n, f32x4 v, bool vec) {
     uint16_t* to = static_cast<uint16_t*>(out) + m * N + n;
     if (vec && n + 4 <= (int)N) {
-        *reinterpret_cast<u32x2*>(to) = u32x2{pack2<DT>(v[0], v[1]),
-                                              pack2<DT>(v[2], v[3])};
+        *reinterpret_cast<u32x2*>(to) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -101,23 +99,21 @@ __device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t out, uint32_t plac
 }
 
 // ---------------------------------------------------------------- few rows of x
-// A work-group takes 16 * NT rows of weights, its WAVES waves a part of K each, in
+// A work-group takes 16 rows of weights, its WAVES waves a part of K each, in
 // steps of four groups of 128, straight from memory into the operands' registers:
 // a lane's operand is 32 of a row's 128, here the 16 from 16h and from 64 + 16h on
 // (h = lane / 16), the same of w and x, so that a load takes 64 neighbouring bytes
 // of each row.  The waves' sums meet in LDS in a fixed order.
-template <int DT, bool F32, int MT, int NT, int WAVES>
+template <int DT, bool F32, int MT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void rows_kernel(F8MmArgs a) {
-    __shared__ f32x4 part[WAVES][MT * NT][64];
+    __shared__ f32x4 part[WAVES][MT][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane & 15, h = lane >> 4;
-    const int G = a.K / 128, n0 = blockIdx.x * 16 * NT;
-    const uint8_t* w[NT];
+    const int G = a.K / 128, n0 = blockIdx.x * 16;
+    const uint8_t* w = a.w + (size_t)min(n0 + r, a.N - 1) * a.K + 16 * h;
     const uint8_t* x[MT];
     const uint8_t* xs[MT];
     bool there[MT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) w[i] = a.w + (size_t)min(n0 + 16 * i + r, a.N - 1) * a.K + 16 * h;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         const int m = 16 * i + r;
@@ -125,22 +121,19 @@ __global__ __launch_bounds__(WAVES * 64) void rows_kernel(F8MmArgs a) {
         x[i] = a.x + (size_t)min(m, a.M - 1) * a.K + 16 * h;
         xs[i] = a.x_scales + (size_t)min(m, a.M - 1) * G;
     }
-    const size_t block = (size_t)(n0 / 128) * G;   // 16 * NT divides 128: one row of scales
+    const size_t block = (size_t)(n0 / 128) * G;
     const uint8_t* wb = static_cast<const uint8_t*>(a.w_scales) + block;
     const float* wf = static_cast<const float*>(a.w_scales) + block;
-    f32x4 acc[MT][NT] = {};
+    f32x4 acc[MT] = {};
     for (int g0 = 4 * wave; g0 < G; g0 += 4 * WAVES) {
-        u32x4 wv[4][NT][2], xv[4][MT][2];
+        u32x4 wv[4][2], xv[4][MT][2];
         uint32_t sx[MT], sw = ONE;
         float fw[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const size_t at = (size_t)min(g0 + j, G - 1) * 128;
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                wv[j][i][0] = *reinterpret_cast<const u32x4*>(w[i] + at);
-                wv[j][i][1] = *reinterpret_cast<const u32x4*>(w[i] + at + 64);
-            }
+            wv[j][0] = *reinterpret_cast<const u32x4*>(w + at);
+            wv[j][1] = *reinterpret_cast<const u32x4*>(w + at + 64);
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i) sx[i] = scales4(xs[i], g0, G);
@@ -162,18 +155,16 @@ __global__ __launch_bounds__(WAVES * 64) void rows_kernel(F8MmArgs a) {
             constexpr int j = decltype(which)::value;
             if (g0 + j >= G) return;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m) {
+                const i32x8 A = join(wv[j][0], wv[j][1]), B = join(xv[j][m][0], xv[j][m][1]);
+                if constexpr (F32) {
+                    const f32x4 d = mfma<j, j>(A, B, f32x4{0.f, 0.f, 0.f, 0.f}, ONE, (int)sx[m]);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const i32x8 A = join(wv[j][n][0], wv[j][n][1]), B = join(xv[j][m][0], xv[j][m][1]);
-                    if constexpr (F32) {
-                        const f32x4 d = mfma<j, j>(A, B, f32x4{0.f, 0.f, 0.f, 0.f}, ONE, (int)sx[m]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(fw[j], d[e], acc[m][n][e]);
-                    } else {
-                        acc[m][n] = mfma<j, j>(A, B, acc[m][n], (int)sw, (int)sx[m]);
-                    }
+                    for (int e = 0; e < 4; ++e) acc[m][e] = fmaf(fw[j], d[e], acc[m][e]);
+                } else {
+                    acc[m] = mfma<j, j>(A, B, acc[m], (int)sw, (int)sx[m]);
                 }
+            }
         };
         step(std::integral_constant<int, 0>());
         step(std::integral_constant<int, 1>());
@@ -181,16 +172,14 @@ __global__ __launch_bounds__(WAVES * 64) void rows_kernel(F8MmArgs a) {
         step(std::integral_constant<int, 3>());
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) part[wave][m * NT + n][lane] = acc[m][n];
+    for (int m = 0; m < MT; ++m) part[wave][m][lane] = acc[m];
     __syncthreads();
     const bool vec = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 7) == 0;
-    for (int t = wave; t < MT * NT; t += WAVES) {
-        f32x4 sum = part[0][t][lane];
+    if (wave < MT) {
+        f32x4 sum = part[0][wave][lane];
 #pragma unroll
-        for (int i = 1; i < WAVES; ++i) sum += part[i][t][lane];
-        const int m = 16 * (t / NT) + r, n = n0 + 16 * (t % NT) + 4 * h;
+        for (int i = 1; i < WAVES; ++i) sum += part[i][wave][lane];
+        const int m = 16 * wave + r, n = n0 + 4 * h;
         if (m < a.M && n < a.N) store4<DT>(a.out, a.N, m, n, sum, vec);
     }
 }
@@ -255,7 +244,7 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
     constexpr int HALF = TM / 2, W_COPIES = BN * 8 / THREADS, X_COPIES = BM * 4 / THREADS;   // of each half
     constexpr int COPIES = W_COPIES + 2 * X_COPIES;
     static_assert(W_COPIES * THREADS == BN * 8 && X_COPIES * THREADS == BM * 4, "copies");
-    static_assert(TM >= 2 && TM <= 8 && TM % 2 == 0, "rows of operands are held two at a time");
+    static_assert(TM == 4 || TM == 8, "scales of a lane's rows are read four at a time");
     static_assert(TN % 2 == 0, "results are written eight at a time");
     static_assert(128 % (16 * TN) == 0, "a wave's rows of w share their scales");
     static_assert(BM * CHUNK / 16 <= THREADS && CHUNK * BLOCKS <= THREADS, "scales");
@@ -368,16 +357,12 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
     };
     auto x_row = [&](int m) { return BN + m / HALF * (BM / 2) + wm * (HALF * 16) + m % HALF * 16; };
     i32x8 A[TN], B[2];
-    uint32_t sx[(TM + 3) / 4], sw;
+    uint32_t sx[TM / 4], sw;
     int block = 0;   // of w's scales in the tile
     auto scales_of = [&](int at) {
         const uint8_t* from = &lds.sx[at][wm * TM * 16 + r * TM];
-        if constexpr (TM >= 4) {
 #pragma unroll
-            for (int i = 0; i < TM / 4; ++i) sx[i] = reinterpret_cast<const uint32_t*>(from)[i];
-        } else {
-            sx[0] = *reinterpret_cast<const uint16_t*>(from);
-        }
+        for (int i = 0; i < TM / 4; ++i) sx[i] = reinterpret_cast<const uint32_t*>(from)[i];
         sw = lds.sw[at][block];
     };
     auto row = [&](auto which, auto&& between) {
@@ -395,14 +380,15 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
         }
     };
     // A step, without a branch, so that its order stays as written.  `next_at`: the next
-    // step's scales.  `wait1` and `wait2`: what may be on its way at the two barriers.
+    // step's scales.
+    constexpr int ON_THE_WAY = COPIES * (STAGES - 1);   // at either barrier
     int stage = 0;
-    auto step = [&](int next_at, auto wait1, auto wait2) {
+    auto step = [&](int next_at) {
         const int next = stage + 1 == STAGES ? 0 : stage + 1;
         auto one = [&](auto which) {
             constexpr int m = decltype(which)::value, after = m - (HALF - 1);
             if constexpr (m < TM - 1) {
-                if constexpr (after == 0) wait_copies<decltype(wait1)::value>();
+                if constexpr (after == 0) wait_copies<ON_THE_WAY>();
                 else wait_lds();
                 B[(m + 1) % 2] = frag(x_row(m + 1), stage);
                 __builtin_amdgcn_sched_barrier(0);
@@ -424,7 +410,7 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
         one(std::integral_constant<int, 4>());
         one(std::integral_constant<int, 5>());
         one(std::integral_constant<int, 6>());
-        wait_copies<decltype(wait2)::value>();
+        wait_copies<ON_THE_WAY>();
         B[0] = frag(x_row(0), next);
         __builtin_amdgcn_sched_barrier(0);
         row(std::integral_constant<int, TM - 1>(), [&](int i) {
@@ -455,7 +441,7 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
         if (i == 0) load_scales(at, g, n);
     }
     write_scales(0);
-    wait_copies<COPIES * (STAGES - 1)>();
+    wait_copies<ON_THE_WAY>();
     scales_of(0);
 #pragma unroll
     for (int i = 0; i < TN; ++i) A[i] = frag(col + i * 16, 0);
@@ -466,7 +452,6 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
     // through them, 8192 x 8192 over 2560 151 and 159, but over 1280 103 and 95, and 1000
     // x 28672 (57 MB) over 5120 145 and 137.
     const bool pass = (long long)a.M * a.N >= (48ll << 20) && a.K >= 2048;
-    const std::integral_constant<int, COPIES * (STAGES - 1)> some;
     for (;;) {
         // The chunk after this one, whose scales come while this one's first steps go.
         const bool last = g + n == k1, has_next = !last || t + t_step < t_end;
@@ -489,7 +474,7 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
                     ++s;
                     if (s == n) block = (next_tile.n * BN % 128 + col) / 128;
                     const int next_at = s < n ? place * CHUNK + s : (place ^ 1) * CHUNK;
-                    step(next_at, some, some);
+                    step(next_at);
                 }
             }
             if (until == n) break;
@@ -510,7 +495,8 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
 #pragma unroll
                 for (int n = 0; n < TN; n += 2) {
                     const int to_n = at.n * BN + col + n * 16 + 8 * h;
-                    store8<DT, SPLIT>(to, ((uint32_t)r * (uint32_t)a.N + to_n) * SIZE, to_n, a.N, acc[m][n], acc[m][n + 1], wide, pass);
+                    store8<DT, SPLIT>(to, ((uint32_t)r * (uint32_t)a.N + to_n) * SIZE, to_n, a.N, acc[m][n], acc[m][n + 1],
+                                      wide, pass);
                     acc[m][n] = acc[m][n + 1] = f32x4{0.f, 0.f, 0.f, 0.f};
                 }
             }
@@ -546,7 +532,7 @@ __global__ __launch_bounds__(256 * TEAMS) void small_kernel(F8MmArgs a, int spli
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16, BLOCKS = (BN + 127) / 128, ROWS = BM + BN;
     constexpr int COPIES = ROWS * 8 / 256, W_COPIES = BN * 8 / 256;
     static_assert(WM * WN == 4 && COPIES * 256 == ROWS * 8 && W_COPIES * 256 == BN * 8, "copies");
-    static_assert(TN % 2 == 0 && (TM == 1 || TM == 2 || TM == 4) && 128 % (16 * TN) == 0, "operands");
+    static_assert(TN % 2 == 0 && (TM == 1 || TM == 2) && 128 % (16 * TN) == 0, "operands");
     static_assert(sizeof(f32x4) * TM * TN * 256 <= STAGES * ROWS * 128, "sums");
     __shared__ SmallLds<BM, BN, TEAMS, STAGES> lds;
     const int tid = threadIdx.x & 255, lane = tid & 63;
@@ -595,7 +581,7 @@ __global__ __launch_bounds__(256 * TEAMS) void small_kernel(F8MmArgs a, int spli
 #pragma unroll
         for (int i = 0; i < TM; ++i) o.B[i] = frag(BN + (wm * TM + i) * 16);
         const uint8_t* from = &lds.sx[team][s][wm * TM * 16 + r * TM];
-        o.sx = TM == 4 ? *reinterpret_cast<const uint32_t*>(from) : TM == 2 ? *reinterpret_cast<const uint16_t*>(from) : *from;
+        o.sx = TM == 2 ? *reinterpret_cast<const uint16_t*>(from) : *from;
         o.sw = lds.sw[team][s][(n0 % 128 + col) / 128];
     };
     auto one = [&](auto which, const Operands& o) {
@@ -616,8 +602,6 @@ __global__ __launch_bounds__(256 * TEAMS) void small_kernel(F8MmArgs a, int spli
     auto products = [&](const Operands& o) {
         one(std::integral_constant<int, 0>(), o);
         one(std::integral_constant<int, 1>(), o);
-        one(std::integral_constant<int, 2>(), o);
-        one(std::integral_constant<int, 3>(), o);
     };
     for (int c = 0; c < longest; c += DEPTH) {
         const int g0 = k0 + c, n = min(DEPTH, longest - c), mine = max(0, min(n, k1 - g0));
@@ -668,11 +652,11 @@ __global__ __launch_bounds__(256 * TEAMS) void small_kernel(F8MmArgs a, int spli
     // The teams' sums, in their order.
     constexpr int EACH = TM * TN;
     f32x4* sums = reinterpret_cast<f32x4*>(&lds.data[team][0][0]);
-    if (TEAMS > 1 && team > 0) {
+    if (team > 0) {
 #pragma unroll
         for (int i = 0; i < EACH; ++i) sums[i * 256 + tid] = acc[i / TN][i % TN];
     }
-    if (TEAMS > 1) __syncthreads();
+    __syncthreads();
     if (team > 0) return;
 #pragma unroll
     for (int k = 1; k < TEAMS; ++k) {
@@ -691,7 +675,8 @@ __global__ __launch_bounds__(256 * TEAMS) void small_kernel(F8MmArgs a, int spli
 #pragma unroll
         for (int n = 0; n < TN; n += 2) {
             const int to_n = n0 + col + n * 16 + 8 * h;
-            store8<DT, SPLIT>(to, ((uint32_t)r * (uint32_t)a.N + to_n) * SIZE, to_n, a.N, acc[m][n], acc[m][n + 1], wide, false);
+            store8<DT, SPLIT>(to, ((uint32_t)r * (uint32_t)a.N + to_n) * SIZE, to_n, a.N, acc[m][n], acc[m][n + 1], wide,
+                              false);
         }
     }
 }
@@ -699,7 +684,7 @@ __global__ __launch_bounds__(256 * TEAMS) void small_kernel(F8MmArgs a, int spli
 // ---------------------------------------------------------------- launches
 template <int DT, bool F32, int MT>
 void go_rows(const F8MmArgs& a, hipStream_t st) {
-    hipLaunchKernelGGL((rows_kernel<DT, F32, MT, 1, 8>), dim3((unsigned)((a.N + 15) / 16)), dim3(512), 0, st, a);
+    hipLaunchKernelGGL((rows_kernel<DT, F32, MT, 8>), dim3((unsigned)((a.N + 15) / 16)), dim3(512), 0, st, a);
 }
 
 template <int DT, bool F32, int BM, int BN, int TEAMS, int STAGES>

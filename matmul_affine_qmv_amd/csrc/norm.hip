@@ -8,6 +8,8 @@
 // is two products in 32 bits, and its codes are those of 64 bits all the same: a
 // lane whose eight y's are not all clear of the middles between two codes forms
 // them again in 64 bits (one wave in 100 does on random numbers).
+#include <algorithm>
+
 #include "f8.h"
 #include "f8_device.h"
 
@@ -208,6 +210,8 @@ void go(const NormArgs& a, int lanes, hipStream_t st) {
                        dim3((unsigned)lanes), 0, st, a);
 }
 
+constexpr int MOST_ROWS = 1 << 21;   // of a launch, whose grid has below 2^32 threads
+
 // Lanes and elements of a row (for rows of 5120 into 8 bits, 7812 of them: 66.5 us with
 // 256 lanes of 24, 71.5 with 320 of 16, 70.7 with 640 of 8; 8192 wide 66.6 with 512 of
 // 16, 74.1 with 256 of 32; 1024 wide 61.7 with a wave a row, 88 with four).  Few rows
@@ -231,8 +235,10 @@ void pick(const NormArgs& a, hipStream_t st) {
 
 // The sum is read again only a layer's products later: large ones go past the caches,
 // which keep the result for what comes next.
-hipError_t launch_rms_norm(const NormArgs& a, int dt, hipStream_t st) {
-    const bool f8 = a.scales != nullptr, pass = a.sum && (long long)a.rows * a.width >= (4ll << 20);
+hipError_t launch_rms_norm(const NormArgs& all, int dt, hipStream_t st) {
+    const bool f8 = all.scales != nullptr, pass = all.sum && (long long)all.rows * all.width >= (4ll << 20);
+    NormArgs a = all;
+    a.rows = std::min(all.rows, MOST_ROWS);
     if (dt == DT_F16) {
         if (pass) f8 ? pick<DT_F16, true, true>(a, st) : pick<DT_F16, false, true>(a, st);
         else f8 ? pick<DT_F16, true, false>(a, st) : pick<DT_F16, false, false>(a, st);
@@ -240,7 +246,17 @@ hipError_t launch_rms_norm(const NormArgs& a, int dt, hipStream_t st) {
         if (pass) f8 ? pick<DT_BF16, true, true>(a, st) : pick<DT_BF16, false, true>(a, st);
         else f8 ? pick<DT_BF16, true, false>(a, st) : pick<DT_BF16, false, false>(a, st);
     }
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.rows == all.rows) return e;
+    const auto behind = [](const void* p, long long bytes) {
+        return p ? const_cast<char*>(static_cast<const char*>(p)) + bytes : nullptr;
+    };
+    const long long n = a.rows;
+    return launch_rms_norm({behind(a.x, 2 * n * a.x_stride), behind(a.residual, 2 * n * a.r_stride), a.weight,
+                            behind(a.sum, 2 * n * a.s_stride), behind(a.out, n * a.width * (f8 ? 1 : 2)),
+                            f8 ? a.scales + n * (a.width / 128) : nullptr, a.x_stride, a.r_stride, a.s_stride,
+                            all.rows - a.rows, a.width, a.eps},
+                           dt, st);
 }
 
 }  // namespace qmx

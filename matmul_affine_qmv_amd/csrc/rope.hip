@@ -7,6 +7,8 @@
 // bits, of which a whole number is taken off exactly, the rest in 32.  An item is
 // eight pairs, two loads of 16 bytes: of both halves of the rotated part, or of
 // 16 neighbours; the part that is not rotated is copied in items of 16 elements.
+#include <algorithm>
+
 #include "f8.h"
 #include "f8_device.h"
 
@@ -14,6 +16,7 @@ namespace qmx {
 namespace {
 
 constexpr int THREADS = 256;
+constexpr int MOST_TOKENS = 1 << 23;   // of a launch, whose grid has below 2^32 threads
 
 struct Ends {   // what an item holds of its two runs of 8 elements
     u32x4 lo, hi;
@@ -119,10 +122,20 @@ void pick(const RopeArgs& a, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_rope(const RopeArgs& a, int dt, hipStream_t st) {
+hipError_t launch_rope(const RopeArgs& all, int dt, hipStream_t st) {
+    RopeArgs a = all;
+    a.tokens = std::min(all.tokens, MOST_TOKENS);
     if (dt == DT_F16) a.interleaved ? pick<DT_F16, true>(a, st) : pick<DT_F16, false>(a, st);
     else a.interleaved ? pick<DT_BF16, true>(a, st) : pick<DT_BF16, false>(a, st);
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.tokens == all.tokens) return e;
+    for (int i = 0; i < 2; ++i) {
+        a.in[i] = static_cast<const uint16_t*>(a.in[i]) + a.in_ts[i] * a.tokens;
+        a.out[i] = static_cast<uint16_t*>(a.out[i]) + a.out_ts[i] * a.tokens;
+    }
+    a.positions += a.tokens;
+    a.tokens = all.tokens - a.tokens;
+    return launch_rope(a, dt, st);
 }
 
 }  // namespace qmx

@@ -20,6 +20,7 @@ _CODES, _SCALES = torch.float8_e4m3fn, torch.float8_e8m0fnu
 _BYTES = (_SCALES, torch.uint8)
 _ANY_SCALES = (*_BYTES, torch.float32)
 _SCALE_E8M0, _SCALE_F32 = 0, 1
+_MOST = 2 ** 31 - 1   # sizes go to the library as ints
 
 # A call's own cost on the host counts beside kernels of a few microseconds: the
 # checks are written out where they are made, the stream is asked for as a number,
@@ -27,8 +28,6 @@ _SCALE_E8M0, _SCALE_F32 = 0, 1
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 _like = torch.empty_like
-
-
 _WHOLE = torch.contiguous_format
 
 
@@ -65,6 +64,8 @@ def _first(x):
     shape = x.shape
     if last != 1 and shape[1] > 1:
         raise ValueError("x must have a unit last stride")
+    if shape[0] > _MOST or shape[1] > _MOST:
+        raise ValueError("x must have below 2^31 rows and columns")
     return code, shape, stride, x.get_device()
 
 
@@ -174,6 +175,8 @@ def f8_dequantize(codes, scales, *, dtype=torch.bfloat16, out=None):
     if not codes.is_contiguous():
         raise ValueError("codes must be contiguous")
     rows, width = codes.shape
+    if rows > _MOST or width > _MOST:
+        raise ValueError("codes must have below 2^31 rows and columns")
     index = codes.get_device()
     if index != _current_device():
         with torch.cuda.device(index):
@@ -202,6 +205,8 @@ def _workspace_bytes(index, M, N, K):
 
 def qmm_f8_workspace_bytes(M, N, K, device="cuda") -> int:
     """Bytes of workspace that qmm_f8 needs for these sizes (a host rule)."""
+    if not all(0 <= size <= _MOST for size in (M, N, K)):
+        raise ValueError("M, N and K must be 0 or more and below 2^31")
     index = torch.device(device).index
     return _workspace_bytes(_current_device() if index is None else index, M, N, K)
 
@@ -221,6 +226,8 @@ def qmm_f8(w, w_scales, x, x_scales, out=None, *, dtype=torch.bfloat16, workspac
         raise ValueError(f"w and x must have one K, a multiple of 128; got {K_w} and {K}")
     if index < 0 or w.get_device() != index:
         raise ValueError("all tensors must be on one HIP device")
+    if M > _MOST or N > _MOST or K > _MOST:
+        raise ValueError("M, N and K must be below 2^31")
     if index != _current_device():
         with torch.cuda.device(index):
             return qmm_f8(w, w_scales, x, x_scales, out, dtype=dtype, workspace=workspace)

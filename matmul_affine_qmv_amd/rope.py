@@ -7,7 +7,7 @@ import math
 
 import torch
 
-from .f8 import _HALVES, _WHOLE, _check, _current_device, _function, _like, _raw_stream
+from .f8 import _HALVES, _MOST, _WHOLE, _check, _current_device, _function, _like, _raw_stream
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
@@ -92,6 +92,8 @@ def rope(q, k, positions, frequencies, *, interleaved=False, scale=1.0, out=None
         with torch.cuda.device(index):
             return rope(q, k, positions, frequencies, interleaved=interleaved, scale=scale, out=out)
     T, heads, D = shape
+    if T > _MOST or heads > _MOST or D > _MOST:
+        raise ValueError("q must have sizes below 2^31")
     if positions.dtype is not torch.int32 or positions.shape != (T,) or not positions.is_contiguous():
         raise ValueError(f"positions must be a contiguous int32 vector of {T}")
     if frequencies.dtype is not torch.float64 or frequencies.dim() != 1 or not frequencies.is_contiguous():
@@ -108,6 +110,8 @@ def rope(q, k, positions, frequencies, *, interleaved=False, scale=1.0, out=None
         if k.dim() != 3:
             raise ValueError("k must be [tokens, kv_heads, head_dim]")
         kv_heads = k.shape[1]
+        if kv_heads > _MOST:
+            raise ValueError("k must have sizes below 2^31")
         from_k = _heads(k, "k", (T, kv_heads, D), dtype, index)
     if out is None:
         q_out, k_out = _like(q, memory_format=_WHOLE), None

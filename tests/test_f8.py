@@ -14,7 +14,7 @@ import matmul_affine_qmv_amd as qmx
 if not os.path.exists(qmx.LIB_PATH):
     pytest.skip("libqmx.so not built", allow_module_level=True)
 
-OK, ENULL, ESHAPE, EGROUP, EDTYPE, EALIGN, EWS = 0, -1, -2, -4, -5, -6, -7
+OK, ENULL, ESHAPE, EGROUP, EDTYPE, EALIGN, EWS, EOVER = 0, -1, -2, -4, -5, -6, -7, -12
 F32, F16, BF16 = 0, 1, 2
 E8M0, SF32 = 0, 1
 FAKE, ODD = 0x10000, 0x10001
@@ -53,9 +53,12 @@ def test_norm_refusals():
         return qmx.lib().qmx_rms_norm(x, 256, r, 256, w, s, ss, out, sc, rows, width, eps, dt, None)
 
     assert norm(dt=F32) == EDTYPE and norm(dt=9) == EDTYPE
-    for bad in (dict(rows=-1), dict(width=-1), dict(eps=0.0), dict(eps=-1e-6), dict(eps=math.nan), dict(eps=math.inf),
-                dict(r=FAKE, s=FAKE, ss=255), dict(r=FAKE, s=FAKE, ss=0), dict(r=FAKE, s=FAKE, ss=-255)):
+    for bad in (dict(rows=-1), dict(width=-1), dict(eps=0.0), dict(eps=-1e-6), dict(eps=math.nan), dict(eps=math.inf)):
         assert norm(**bad) == ESHAPE, bad
+    for stride in (255, 0, -255):
+        assert norm(r=FAKE, s=FAKE + 2 ** 20, ss=stride) == EOVER
+    for both in (dict(r=FAKE + 2 ** 20, s=FAKE), dict(sc=FAKE), dict(r=FAKE, s=FAKE + 2 ** 20, x=FAKE + 2 ** 20, sc=FAKE)):
+        assert norm(**both) == EOVER, both
     assert norm(sc=FAKE, width=200) == EGROUP
     for bad in (dict(x=None), dict(out=None), dict(r=FAKE), dict(s=FAKE)):
         assert norm(**bad) == ENULL, bad
@@ -78,6 +81,7 @@ def test_codes_refusals():
     for f in (quantize, dequantize):
         assert f(dt=F32) == EDTYPE
         assert f(rows=-1) == ESHAPE and f(width=-128) == ESHAPE and f(rows=2 ** 31 - 1, width=256) == ESHAPE
+        assert f(rows=2 ** 29 + 1, width=128) == ESHAPE
         assert f(width=100) == EGROUP and f(block=2) == EGROUP and f(block=0) == EGROUP
         assert f(c=None) == ENULL and f(s=None) == ENULL
         assert f(c=0x10008) == EALIGN
@@ -96,7 +100,8 @@ def test_product_refusals():
         return L.qmx_qmm_f8(w, ws, kind, x, xs, out, M, N, K, dt, work, size, None)
 
     assert mm(dt=F32) == EDTYPE and mm(kind=2) == EDTYPE
-    for bad in (dict(M=-1), dict(N=-1), dict(K=-128), dict(K=2 ** 24 + 128), dict(M=2 ** 31 - 1, N=2 ** 31 - 1)):
+    for bad in (dict(M=-1), dict(N=-1), dict(K=-128), dict(K=2 ** 24), dict(M=2 ** 31 - 1, N=2 ** 31 - 1),
+                dict(N=2 ** 25 + 1), dict(M=2 ** 30 + 1, N=1), dict(M=2 ** 30, N=1024)):
         assert mm(**bad) == ESHAPE, bad
     assert mm(K=200) == EGROUP and mm(K=64) == EGROUP
     for bad in (dict(w=None), dict(ws=None), dict(x=None), dict(xs=None), dict(out=None)):
@@ -115,8 +120,8 @@ def test_product_refusals():
 @fake_ptr_test
 def test_rope_refusals():
     def rope(q=FAKE, qo=FAKE, heads=4, k=FAKE, ko=FAKE, kv=2, pos=FAKE, f=FAKE, T=3, D=128, pairs=64, scale=1.0,
-             dt=BF16):
-        return qmx.lib().qmx_rope(q, 512, 128, qo, 512, 128, heads, k, 256, 128, ko, 256, 128, kv, pos, f, T, D, pairs,
+             dt=BF16, out=(512, 128), kout=(256, 128)):
+        return qmx.lib().qmx_rope(q, 512, 128, qo, *out, heads, k, 256, 128, ko, *kout, kv, pos, f, T, D, pairs,
                                   0, scale, dt, None)
 
     assert rope(dt=F32) == EDTYPE
@@ -127,6 +132,9 @@ def test_rope_refusals():
         assert rope(**bad) == ENULL, bad
     for bad in (dict(q=ODD), dict(qo=ODD), dict(k=ODD), dict(ko=ODD), dict(pos=0x10002), dict(f=0x10004)):
         assert rope(**bad) == EALIGN, bad
+    for bad in (dict(out=(0, 128)), dict(out=(512, 0)), dict(out=(511, 128)), dict(out=(512, 127)), dict(out=(128, 383)),
+                dict(kout=(255, 128)), dict(kout=(-255, 128)), dict(kout=(256, 2 ** 62), D=129, pairs=1, T=2 ** 31 - 1)):
+        assert rope(**bad) == EOVER, bad
     assert rope(T=0, q=None) == OK and rope(heads=0, kv=0, q=None) == OK
 
 
@@ -326,6 +334,14 @@ def test_norm_shared_rows_and_nothing():
     one = qmx.rms_norm(x.to(DEV), w)
     many = qmx.rms_norm(x.to(DEV).expand(70, 300), w)
     assert same(many, one.expand(70, 300))
+    total, sums = qmx.rms_norm(x.to(DEV).expand(70, 300), w, x.to(DEV).expand(70, 300))
+    assert total.is_contiguous() and sums.is_contiguous() and same(sums, (x + x).expand(70, 300))
+    for f in (qmx.rms_norm_f8, qmx.f8_quantize):
+        part = x[:, :256].to(DEV)
+        for a, b in zip(f(part.expand(70, 256)), f(part)):
+            assert a.is_contiguous() and same(a, b.view(torch.uint8).expand(70, b.shape[1]).view(b.dtype))
+    with pytest.raises(qmx.QmxError):
+        qmx.rms_norm(x.to(DEV).expand(70, 300), w, x.to(DEV).expand(70, 300), sum_out=x.to(DEV).expand(70, 300))
     assert qmx.rms_norm(torch.empty(0, 300, device=DEV, dtype=torch.half), w).shape == (0, 300)
     assert qmx.rms_norm(torch.empty(4, 0, device=DEV, dtype=torch.half), w[:0]).shape == (4, 0)
 
@@ -627,6 +643,52 @@ def test_rope_binding():
         with pytest.raises(ValueError):
             call()
     assert qmx.rope(q[:0], q[:0], at[:0], f)[0].shape == (0, 2, 64)
+    wide = q[:1].expand(4, 2, 64)
+    assert same(qmx.rope(wide, wide, at, f)[1], q)
+    with pytest.raises(qmx.QmxError):
+        qmx.rope(wide, None, at, f, out=(wide, None))
+
+
+@pytest.mark.gpu
+def test_more_rows_than_a_grid_holds():
+    """2^32 threads and more would be needed at once: the same as of the rows in parts."""
+    say("norm")
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.randn(2 ** 22 + 2 ** 21 + 5, 128, device=DEV, generator=g).half()
+    w = torch.randn(128, device=DEV, generator=g).half()
+    cuts = [0, 3, 2 ** 20 + 1, 2 ** 21 + 7, 2 ** 22 - 1, 2 ** 22 + 1, len(x)]
+    parts = list(zip(cuts, cuts[1:]))
+    whole = qmx.rms_norm_f8(x, w, x)
+    for a, b in parts:
+        for one, every in zip(qmx.rms_norm_f8(x[a:b], w, x[a:b]), whole):
+            assert torch.equal(one.view(torch.uint8), every[a:b].view(torch.uint8))
+    y = qmx.rms_norm(x[:, :9])
+    assert all(torch.equal(qmx.rms_norm(x[a:b, :9]), y[a:b]) for a, b in parts)
+    say("rope")
+    q = x.view(-1)[:4 * (2 ** 24 + 3)].view(-1, 2, 2)
+    at = torch.randint(-1, 2 ** 20, (len(q),), device=DEV, generator=g, dtype=torch.int32)
+    f = qmx.rope_frequencies(2, device=DEV)
+    turned = qmx.rope(q, q[:, :1], at, f)
+    cuts = [0, 5, 2 ** 23 - 1, 2 ** 23 + 9, 2 ** 24 - 2, len(q)]
+    for a, b in zip(cuts, cuts[1:]):
+        for one, every in zip(qmx.rope(q[a:b], q[a:b, :1], at[a:b], f), turned):
+            assert torch.equal(one.view(torch.uint8), every[a:b].view(torch.uint8))
+
+
+@pytest.mark.gpu
+def test_sizes_past_an_int():
+    x = torch.ones(1, 1, dtype=torch.half, device=DEV).expand(2 ** 31, 1)
+    codes = torch.empty(2 ** 31, 0, dtype=torch.float8_e4m3fn, device=DEV)
+    scales = torch.empty(2 ** 31, 0, dtype=torch.uint8, device=DEV)
+    at, f = torch.zeros(1, dtype=torch.int32, device=DEV), qmx.rope_frequencies(2, device=DEV)
+    q = x.view(-1, 1, 1).expand(-1, 1, 2)
+    for call in (lambda: qmx.rms_norm(x), lambda: qmx.rms_norm_f8(x), lambda: qmx.f8_quantize(x),
+                 lambda: qmx.f8_dequantize(codes, scales), lambda: qmx.qmm_f8(codes[:1], scales[:1], codes, scales),
+                 lambda: qmx.qmm_f8(codes, scales[:2 ** 24], codes[:1], scales[:1]),
+                 lambda: qmx.qmm_f8_workspace_bytes(2 ** 32 + 1, 128, 128),
+                 lambda: qmx.rope(q, None, at.expand(2 ** 31), f)):
+        with pytest.raises(ValueError):
+            call()
 
 
 # ---------------------------------------------------------------- together
