@@ -731,3 +731,16 @@ def test_a_layer_in_a_graph_and_on_a_stream(T):
         graph.replay()
         torch.cuda.synchronize()
         assert all(same(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.gpu
+def test_example_of_layers():
+    """Prompts, then graph replays of one token each.  Of a row's largest output a product is off by half a step of
+    bfloat16, 2^-9, and by the matrix instruction's cuts: at most 7 * 2^-13 of the largest of each 8 products, of which a
+    row of 512 or 1024 has 64 or 128 of some 3 (or 6 with its outliers) deviations, beside outputs of 3 * sqrt(512): again
+    2^-9; a rotation is off by half a step; attention by 8 roundings, as examples/kv4_decode.py."""
+    say("example")
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import f8_layers
+    errors = f8_layers.main(steps=12)
+    assert len(errors) == 13 and max(errors) <= 8 * 2.0 ** -8, errors
