@@ -207,26 +207,34 @@ __device__ __forceinline__ TileAt tile_at(int t, int tiles_m, int tiles_n) {
 // w (A) for a step and passes over its TM rows of 16 of x (B), reading one ahead.  Two
 // barriers a step: before the first half of x's rows is left, when every wave has read
 // A and the second half has come (w and x's first half of the stage are then copied
-// again, for STAGES steps later); and before the last row, when the whole stage is read
+// again, for two steps later); and before the last row, when the whole stage is read
 // and the next one's w and first half have come (the second half is copied again, and
 // beside the last row A and B are read from the next stage).  So what is copied has a
 // step and a half to come with two stages only, and the copies run on into the next
 // tile while one is finished and written.
+// Bound by LDS and the matrix cores, whose power limit takes the clock to some 2.0 GHz:
+// a step of 256 x 256 writes 64 KB into LDS and reads 192 (about 2500 cycles) beside
+// 2048 cycles of products on each SIMD.  8192 x 14336 over K = 5120: 448 us, 2685 TFLOP/s
+// (a library's 8-bit product without group scales: 2758).  Four waves of 128 x 128 read
+// a third less, but take 595 us: one wave on a SIMD waits at every barrier.  Of 128 x 128
+// tiles a compute unit holds two work-groups, each filling the other's waits: 1024 x 5120
+// over 14336 120 us, 139 with one of four stages.
 // The scales of CHUNK groups stand beside the stages, the next ones' in a second place:
 // a lane's TM scales of x in neighbouring bytes, which the matrix instruction picks from
 // a register by itself.
 constexpr int CHUNK = 32;
+constexpr int TILE_STAGES = 2;
 
-template <int BM, int BN, int STAGES>
+template <int BM, int BN>
 struct TileLds {
-    alignas(16) uint8_t data[STAGES][(BM + BN) * 128];
+    alignas(16) uint8_t data[TILE_STAGES][(BM + BN) * 128];
     alignas(16) uint8_t sx[2 * CHUNK][BM];
     uint32_t sw[2 * CHUNK][(BN + 127) / 128];   // a float, or a byte four times
 };
 
 // Work-groups that a compute unit holds at a time, and how many are launched.
-template <int BM, int BN, int STAGES>
-constexpr int tile_fit() { return 163840 / (int)sizeof(TileLds<BM, BN, STAGES>); }
+template <int BM, int BN>
+constexpr int tile_fit() { return 163840 / (int)sizeof(TileLds<BM, BN>); }
 inline unsigned tile_groups(long long tiles, int most) { return (unsigned)(tiles < most ? tiles : most / 8 * 8); }
 
 template <int N>
@@ -238,7 +246,7 @@ __device__ __forceinline__ void wait_copies() {
 // itself the compiler waits for those too.
 __device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xc07f); }
 
-template <int DT, bool F32, int BM, int BN, int WM, int WN, int STAGES, bool SPLIT>
+template <int DT, bool F32, int BM, int BN, int WM, int WN, bool SPLIT>
 __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int splits) {
     constexpr int THREADS = WM * WN * 64, TM = BM / WM / 16, TN = BN / WN / 16, BLOCKS = (BN + 127) / 128;
     constexpr int HALF = TM / 2, W_COPIES = BN * 8 / THREADS, X_COPIES = BM * 4 / THREADS;   // of each half
@@ -248,7 +256,7 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
     static_assert(TN % 2 == 0, "results are written eight at a time");
     static_assert(128 % (16 * TN) == 0, "a wave's rows of w share their scales");
     static_assert(BM * CHUNK / 16 <= THREADS && CHUNK * BLOCKS <= THREADS, "scales");
-    __shared__ TileLds<BM, BN, STAGES> lds;
+    __shared__ TileLds<BM, BN> lds;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, h = lane >> 4;
     const int wm = wave % WM, wn = wave / WM;
@@ -381,10 +389,10 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
     };
     // A step, without a branch, so that its order stays as written.  `next_at`: the next
     // step's scales.
-    constexpr int ON_THE_WAY = COPIES * (STAGES - 1);   // at either barrier
+    constexpr int ON_THE_WAY = COPIES * (TILE_STAGES - 1);   // at either barrier
     int stage = 0;
     auto step = [&](int next_at) {
-        const int next = stage + 1 == STAGES ? 0 : stage + 1;
+        const int next = stage ^ 1;
         auto one = [&](auto which) {
             constexpr int m = decltype(which)::value, after = m - (HALF - 1);
             if constexpr (m < TM - 1) {
@@ -433,7 +441,7 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
     int g = begin_of(at.part), k1 = end_of(at.part), n = min(CHUNK, k1 - g);
     block = (at.n * BN % 128 + col) / 128;
 #pragma unroll
-    for (int i = 0; i < STAGES; ++i) {
+    for (int i = 0; i < TILE_STAGES; ++i) {
         if (copies_left == 0) next_copies();
         copy(0, COPIES, i);
         cg += cg_step;
@@ -512,12 +520,17 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
 }
 
 // ---------------------------------------------------------------- small tiles
-// For calls whose tiles are few: each of TEAMS teams of 4 waves (WM by WN) takes a run
+// For calls whose tiles are few: each of TEAMS teams of WM by WN waves takes a run
 // of the K groups of a tile of BM by BN, with stages of its own in LDS, so that a step
 // takes TEAMS groups; the teams' sums meet in LDS in a fixed order.  Operands are read
 // a step ahead of the products, so one barrier a step is enough: behind it a stage has
 // come and the one before is free.  Layouts of LDS as above, scales of DEPTH groups a
 // team at a time.
+// Bound by the way from L2 over LDS into registers, some 70 bytes a nanosecond and
+// compute unit whatever the tile; weights straight into registers, as few rows take
+// them, come at half of that, four lanes of a quad reading four rows.  Eight waves a
+// team hide more of it in 64 x 128 (300 x 4100 over 4096: 13.1 us, 14.0 with four),
+// the smaller tiles gain nothing by more.
 constexpr int DEPTH = 32;
 
 template <int BM, int BN, int TEAMS, int STAGES>
@@ -528,15 +541,15 @@ struct SmallLds {
 };
 
 template <int DT, bool F32, int BM, int BN, int WM, int WN, int TEAMS, int STAGES, bool SPLIT>
-__global__ __launch_bounds__(256 * TEAMS) void small_kernel(F8MmArgs a, int splits) {
+__global__ __launch_bounds__(64 * WM * WN * TEAMS) void small_kernel(F8MmArgs a, int splits) {
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16, BLOCKS = (BN + 127) / 128, ROWS = BM + BN;
-    constexpr int COPIES = ROWS * 8 / 256, W_COPIES = BN * 8 / 256;
-    static_assert(WM * WN == 4 && COPIES * 256 == ROWS * 8 && W_COPIES * 256 == BN * 8, "copies");
+    constexpr int T = 64 * WM * WN, COPIES = ROWS * 8 / T, W_COPIES = BN * 8 / T;
+    static_assert(COPIES * T == ROWS * 8 && W_COPIES * T == BN * 8 && COPIES * (STAGES - 1) <= 63, "copies");
     static_assert(TN % 2 == 0 && (TM == 1 || TM == 2) && 128 % (16 * TN) == 0, "operands");
-    static_assert(sizeof(f32x4) * TM * TN * 256 <= STAGES * ROWS * 128, "sums");
+    static_assert(sizeof(f32x4) * TM * TN * T <= STAGES * ROWS * 128, "sums");
     __shared__ SmallLds<BM, BN, TEAMS, STAGES> lds;
-    const int tid = threadIdx.x & 255, lane = tid & 63;
-    const int team = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tid = threadIdx.x % T, lane = tid & 63;
+    const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / T), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, h = lane >> 4, wm = wave % WM, wn = wave / WM;
     const int G = a.K / 128, tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN;
     // each XCD takes a run of the list of tiles
@@ -551,7 +564,7 @@ __global__ __launch_bounds__(256 * TEAMS) void small_kernel(F8MmArgs a, int spli
     uint32_t off[COPIES];
 #pragma unroll
     for (int i = 0; i < COPIES; ++i) {
-        const int piece = i * 256 + tid, row = piece >> 3, c = (piece & 7) ^ (row & 7);
+        const int piece = i * T + tid, row = piece >> 3, c = (piece & 7) ^ (row & 7);
         const int from = i < W_COPIES ? min(row / 32 * 32 + row % 16 / 4 * 8 + row / 16 % 2 * 4 + row % 4, a.N - 1 - n0)
                                       : min(row - BN, a.M - 1 - m0);
         off[i] = (uint32_t)from * (uint32_t)a.K + 16 * c;
@@ -561,7 +574,7 @@ __global__ __launch_bounds__(256 * TEAMS) void small_kernel(F8MmArgs a, int spli
         const uint32_t at = (uint32_t)min(g, G - 1) * 128;
 #pragma unroll
         for (int i = 0; i < COPIES; ++i)
-            copy16(i < W_COPIES ? wbuf : xbuf, off[i], at, &lds.data[team][stage][(i * 256 + wave * 64) * 16]);
+            copy16(i < W_COPIES ? wbuf : xbuf, off[i], at, &lds.data[team][stage][(i * T + wave * 64) * 16]);
     };
     f32x4 acc[TM][TN] = {};
     const int col = wn * TN * 16;
@@ -610,7 +623,7 @@ __global__ __launch_bounds__(256 * TEAMS) void small_kernel(F8MmArgs a, int spli
         for (int i = 0; i < STAGES; ++i) copy(g0 + i, i);
         // Scales; what is past the team's groups counts nothing: scales of 0 in w's float32,
         // and in both others the steps are left out.
-        for (int i = tid; i < BM * (DEPTH / 16); i += 256) {
+        for (int i = tid; i < BM * (DEPTH / 16); i += T) {
             const int row = i / (DEPTH / 16), first = i % (DEPTH / 16) * 16;
             struct __attribute__((packed, aligned(1))) Any { u32x4 v; };
             const uint8_t* from = a.x_scales + (size_t)min(m0 + row, a.M - 1) * G + g0 + first;
@@ -623,7 +636,7 @@ __global__ __launch_bounds__(256 * TEAMS) void small_kernel(F8MmArgs a, int spli
                 for (int j = 0; first + j < mine; ++j) to[j * BM] = from[j];
             }
         }
-        for (int i = tid; i < mine * BLOCKS; i += 256) {
+        for (int i = tid; i < mine * BLOCKS; i += T) {
             const int j = i / BLOCKS, block = i % BLOCKS;
             const size_t from = (size_t)min(n0 / 128 + block, (a.N - 1) / 128) * G + g0 + j;
             lds.sw[team][j][block] = F32 ? static_cast<const uint32_t*>(a.w_scales)[from]
@@ -654,7 +667,7 @@ __global__ __launch_bounds__(256 * TEAMS) void small_kernel(F8MmArgs a, int spli
     f32x4* sums = reinterpret_cast<f32x4*>(&lds.data[team][0][0]);
     if (team > 0) {
 #pragma unroll
-        for (int i = 0; i < EACH; ++i) sums[i * 256 + tid] = acc[i / TN][i % TN];
+        for (int i = 0; i < EACH; ++i) sums[i * T + tid] = acc[i / TN][i % TN];
     }
     __syncthreads();
     if (team > 0) return;
@@ -662,7 +675,7 @@ __global__ __launch_bounds__(256 * TEAMS) void small_kernel(F8MmArgs a, int spli
     for (int k = 1; k < TEAMS; ++k) {
         const f32x4* other = reinterpret_cast<const f32x4*>(&lds.data[k][0][0]);
 #pragma unroll
-        for (int i = 0; i < EACH; ++i) acc[i / TN][i % TN] += other[i * 256 + tid];
+        for (int i = 0; i < EACH; ++i) acc[i / TN][i % TN] += other[i * T + tid];
     }
     const uintptr_t out_at = SPLIT ? 0 : reinterpret_cast<uintptr_t>(a.out);
     const int wide = a.N % 8 == 0 && out_at % 16 == 0 ? 8 : a.N % 4 == 0 && out_at % 8 == 0 ? 4 : 1;
@@ -687,30 +700,30 @@ void go_rows(const F8MmArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((rows_kernel<DT, F32, MT, 8>), dim3((unsigned)((a.N + 15) / 16)), dim3(512), 0, st, a);
 }
 
-template <int DT, bool F32, int BM, int BN, int TEAMS, int STAGES>
+template <int DT, bool F32, int BM, int BN, int WN, int TEAMS, int STAGES>
 void go_small(const F8MmArgs& a, int splits, hipStream_t st) {
-    const dim3 grid((unsigned)((a.M + BM - 1) / BM) * (unsigned)((a.N + BN - 1) / BN) * (unsigned)splits), block(256 * TEAMS);
-    if (splits > 1) hipLaunchKernelGGL((small_kernel<DT, F32, BM, BN, 2, 2, TEAMS, STAGES, true>), grid, block, 0, st, a, splits);
-    else hipLaunchKernelGGL((small_kernel<DT, F32, BM, BN, 2, 2, TEAMS, STAGES, false>), grid, block, 0, st, a, 1);
+    const dim3 grid((unsigned)((a.M + BM - 1) / BM) * (unsigned)((a.N + BN - 1) / BN) * (unsigned)splits), block(128 * WN * TEAMS);
+    if (splits > 1) hipLaunchKernelGGL((small_kernel<DT, F32, BM, BN, 2, WN, TEAMS, STAGES, true>), grid, block, 0, st, a, splits);
+    else hipLaunchKernelGGL((small_kernel<DT, F32, BM, BN, 2, WN, TEAMS, STAGES, false>), grid, block, 0, st, a, 1);
 }
 
-template <int DT, bool F32, int SIZE, int STAGES>
+template <int DT, bool F32, int SIZE>
 void go_tiles(const F8MmArgs& a, int splits, int cus, hipStream_t st) {
     const long long tiles = (long long)((a.M + SIZE - 1) / SIZE) * ((a.N + SIZE - 1) / SIZE) * splits;
-    const dim3 grid(tile_groups(tiles, tile_fit<SIZE, SIZE, STAGES>() * cus)), block(512);
-    if (splits > 1) hipLaunchKernelGGL((tile_kernel<DT, F32, SIZE, SIZE, 2, 4, STAGES, true>), grid, block, 0, st, a, splits);
-    else hipLaunchKernelGGL((tile_kernel<DT, F32, SIZE, SIZE, 2, 4, STAGES, false>), grid, block, 0, st, a, 1);
+    const dim3 grid(tile_groups(tiles, tile_fit<SIZE, SIZE>() * cus)), block(512);
+    if (splits > 1) hipLaunchKernelGGL((tile_kernel<DT, F32, SIZE, SIZE, 2, 4, true>), grid, block, 0, st, a, splits);
+    else hipLaunchKernelGGL((tile_kernel<DT, F32, SIZE, SIZE, 2, 4, false>), grid, block, 0, st, a, 1);
 }
 
 template <int DT, bool F32>
 void launch(const F8MmArgs& a, F8Plan p, int cus, hipStream_t st) {
     switch (p.tile) {
         case F8_ROWS: a.M <= 16 ? go_rows<DT, F32, 1>(a, st) : go_rows<DT, F32, 2>(a, st); break;
-        case F8_32x64: go_small<DT, F32, 32, 64, 2, 5>(a, p.splits, st); break;
-        case F8_64x64: go_small<DT, F32, 64, 64, 2, 4>(a, p.splits, st); break;
-        case F8_64x128: go_small<DT, F32, 64, 128, 2, 3>(a, p.splits, st); break;
-        case F8_128x128: go_tiles<DT, F32, 128, 4>(a, p.splits, cus, st); break;
-        default: go_tiles<DT, F32, 256, 2>(a, p.splits, cus, st); break;
+        case F8_32x64: go_small<DT, F32, 32, 64, 2, 2, 5>(a, p.splits, st); break;
+        case F8_64x64: go_small<DT, F32, 64, 64, 2, 2, 4>(a, p.splits, st); break;
+        case F8_64x128: go_small<DT, F32, 64, 128, 4, 2, 3>(a, p.splits, st); break;
+        case F8_128x128: go_tiles<DT, F32, 128>(a, p.splits, cus, st); break;
+        default: go_tiles<DT, F32, 256>(a, p.splits, cus, st); break;
     }
 }
 
