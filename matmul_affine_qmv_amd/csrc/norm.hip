@@ -8,6 +8,10 @@
 // is two products in 32 bits, and its codes are those of 64 bits all the same: a
 // lane whose eight y's are not all clear of the middles between two codes forms
 // them again in 64 bits (one wave in 100 does on random numbers).
+//
+// 8192 rows of 5120 in bfloat16 with a residual into 8 bits: 59 us, 4.9 TB/s, a large
+// copy's rate; 2500 of 4097 in float16 11 us, 3.7 TB/s, all rows being read before the
+// first is written; one row of 5120 3.7 us, a launch and two ways to memory.
 #include <algorithm>
 
 #include "f8.h"
@@ -69,23 +73,45 @@ __device__ __forceinline__ double squares8(u32x4 h, double sum) {
 
 // Whether y, off by at most three of its last digits (three roundings of half a
 // digit, of a number up to twice its power of two), rounds to a code as what it
-// stands for does, for all eight: magnitudes of 2^-60 to 2^100, none within three
-// of a number of five digits, as middles between codes are.  (w below 2^60 then
-// leaves h * rstd a normal number.)
+// stands for does, for all eight: magnitudes of 2^-60 to 2^100 (`most` the largest),
+// none within three of a number of five digits, as middles between codes are.  (w
+// below 2^60 then leaves h * rstd a normal number.)
 template <int DT>
-__device__ __forceinline__ bool clear_of_middles(const float (&y)[8], u32x4 w) {
-    uint32_t least = 0xffffffffu, most = 0, near = 0xffffffffu, heavy = 0;
+__device__ __forceinline__ bool clear_of_middles(const float (&y)[8], u32x4 w, uint32_t most) {
+    uint32_t least = 0xffffffffu, near = 0xffffffffu, heavy = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint32_t u = __float_as_uint(y[i]) & 0x7fffffffu;
-        least = min(least, u);
-        most = max(most, u);
+        const uint32_t u = __float_as_uint(y[i]);
+        least = min(least, u & 0x7fffffffu);
         near = min(near, (u + 3u) & 0x7ffffu);
     }
+    if constexpr (DT == DT_BF16) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) heavy = max(heavy, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-    return least >= (127u - 60u) << 23 && most <= (127u + 100u) << 23 && near > 6u &&
-           (DT == DT_F16 || heavy < (127u + 60u) << 7);
+        for (int i = 0; i < 4; ++i) heavy = max(heavy, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+    }
+    return least >= (127u - 60u) << 23 && most <= (127u + 100u) << 23 && near > 6u && heavy < (127u + 60u) << 7;
+}
+
+__device__ __forceinline__ uint32_t most_of(const float (&y)[8]) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(y[i]) & 0x7fffffffu);
+    return most;
+}
+
+// Eight elements of a row of which `n` are left.  Into 8 bits rows are whole groups.
+template <bool F8>
+__device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
+    if constexpr (F8) return n > 0 ? load_any(p) : u32x4{0, 0, 0, 0};
+    else return load_part(p, n);
+}
+template <bool F8, bool PASS>
+__device__ __forceinline__ void store8(uint16_t* p, u32x4 v, int n) {
+    if constexpr (F8) {
+        if (n > 0) store_any<PASS>(p, v);
+    } else {
+        store_part<PASS>(p, v, n);
+    }
 }
 
 // y of eight elements from element `at` on, and where they go.
@@ -93,20 +119,18 @@ template <int DT, bool F8>
 __device__ __forceinline__ void finish8(const NormArgs& a, size_t row, int at, int n, u32x4 h, const Rstd& r) {
     const uint32_t one = DT == DT_F16 ? 0x3c003c00u : 0x3f803f80u;
     u32x4 w = {one, one, one, one};
-    if (a.weight) w = load_part(static_cast<const uint16_t*>(a.weight) + at, n);
+    if (a.weight) w = load8<F8>(static_cast<const uint16_t*>(a.weight) + at, n);
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = elem<DT>(h, i) * r.rounded * elem<DT>(w, i);
-    const bool again = !r.ordinary || (F8 && n > 0 && !clear_of_middles<DT>(y, w));
-    if (again) {
+    uint32_t most = F8 ? most_of(y) : 0;
+    if (!r.ordinary || (F8 && n > 0 && !clear_of_middles<DT>(y, w, most))) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = to_odd((double)elem<DT>(h, i) * r.whole * (double)elem<DT>(w, i));
+        if (F8) most = most_of(y);
     }
     const size_t to = row * a.width + at;
     if constexpr (F8) {   // 16 lanes hold a group
-        uint32_t most = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(y[i]) & 0x7fffffffu);
         const uint32_t byte = scale_byte(max16(most));
         if (n > 0) {
             *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.out) + to) = codes8(y, byte);
@@ -120,20 +144,18 @@ __device__ __forceinline__ void finish8(const NormArgs& a, size_t row, int at, i
     }
 }
 
-// One row for each wave (WAVE) or for the whole work-group, whose lanes hold up to
-// VPT * 8 of its elements each.
-template <int DT, bool F8, bool PASS, bool WAVE, int VPT>
-__global__ __launch_bounds__(WAVE ? 256 : VPT == 1 ? 1024 : 512) void norm_kernel(NormArgs a) {
+// A row for each work-group, whose lanes hold up to VPT * 8 of its elements each.
+template <int DT, bool F8, bool PASS, int VPT>
+__global__ __launch_bounds__(VPT == 1 ? 1024 : 512) void norm_kernel(NormArgs a) {
     __shared__ double part[16];
-    const int lanes = WAVE ? 64 : blockDim.x, lane = WAVE ? threadIdx.x % 64 : threadIdx.x;
-    const size_t row = WAVE ? (size_t)blockIdx.x * 4 + threadIdx.x / 64 : blockIdx.x;
-    if (WAVE && row >= (size_t)a.rows) return;
+    const int lanes = blockDim.x, lane = threadIdx.x;
+    const size_t row = blockIdx.x;
     const uint16_t* x = static_cast<const uint16_t*>(a.x) + row * a.x_stride;
     u32x4 h[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int at = (j * lanes + lane) * 8;
-        h[j] = load_part(x + at, a.width - at);
+        h[j] = load8<F8>(x + at, a.width - at);
     }
     if (a.residual) {
         const uint16_t* r = static_cast<const uint16_t*>(a.residual) + row * a.r_stride;
@@ -142,26 +164,32 @@ __global__ __launch_bounds__(WAVE ? 256 : VPT == 1 ? 1024 : 512) void norm_kerne
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int at = (j * lanes + lane) * 8;
-            v[j] = load_part(r + at, a.width - at);
+            v[j] = load8<F8>(r + at, a.width - at);
         }
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int at = (j * lanes + lane) * 8;
             h[j] = add8<DT>(h[j], v[j]);
-            store_part<PASS>(s + at, h[j], a.width - at);
+            store8<F8, PASS>(s + at, h[j], a.width - at);
         }
     }
     double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) sum = squares8<DT>(h[j], sum);
     sum = wave_sum64(sum);
-    if (!WAVE) {
+    if (lanes > 64) {
         if (lane % 64 == 0) part[lane / 64] = sum;
         __syncthreads();
         sum = 0.0;
         for (int i = 0; i < lanes / 64; ++i) sum += part[i];
     }
     const Rstd r = rstd_of(sum, a.width, a.eps);
+    // What the elements are as floats and doubles is formed anew: kept from the sum it
+    // would take three to six times the registers.
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(h[j][i]));
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int at = (j * lanes + lane) * 8;
@@ -182,10 +210,10 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
     double sum = 0.0;
     for (long long at = lane * 8; at < a.width; at += 1024 * 8) {
         const int n = (int)min(8ll, a.width - at);
-        u32x4 h = load_part(x + at, n);
+        u32x4 h = load8<F8>(x + at, n);
         if (a.residual) {
-            h = add8<DT>(h, load_part(r + at, n));
-            store_part<false>(s + at, h, n);
+            h = add8<DT>(h, load8<F8>(r + at, n));
+            store8<F8, false>(s + at, h, n);
         }
         sum = squares8<DT>(h, sum);
     }
@@ -200,35 +228,41 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
     const long long end = F8 ? ((long long)a.width + 8191) / 8192 * 8192 : (long long)a.width;
     for (long long at = lane * 8; at < end; at += 1024 * 8) {
         const int n = (int)max(0ll, min(8ll, a.width - at));
-        finish8<DT, F8>(a, row, (int)min(at, (long long)a.width), n, load_part(from + at, n), scale);
+        finish8<DT, F8>(a, row, (int)min(at, (long long)a.width), n, load8<F8>(from + at, n), scale);
     }
-}
-
-template <int DT, bool F8, bool PASS, bool WAVE, int VPT>
-void go(const NormArgs& a, int lanes, hipStream_t st) {
-    hipLaunchKernelGGL((norm_kernel<DT, F8, PASS, WAVE, VPT>), dim3(WAVE ? ((unsigned)a.rows + 3) / 4 : (unsigned)a.rows),
-                       dim3((unsigned)lanes), 0, st, a);
 }
 
 constexpr int MOST_ROWS = 1 << 21;   // of a launch, whose grid has below 2^32 threads
 
-// Lanes and elements of a row (for rows of 5120 into 8 bits, 7812 of them: 66.5 us with
-// 256 lanes of 24, 71.5 with 320 of 16, 70.7 with 640 of 8; 8192 wide 66.6 with 512 of
-// 16, 74.1 with 256 of 32; 1024 wide 61.7 with a wave a row, 88 with four).  Few rows
-// take as many lanes as they have eights (1 of 5120: 3.7 us, 5.9 with 256 lanes).
+template <int DT, bool F8, bool PASS, int VPT>
+void go(const NormArgs& a, int waves, hipStream_t st) {
+    hipLaunchKernelGGL((norm_kernel<DT, F8, PASS, VPT>), dim3((unsigned)a.rows), dim3((unsigned)waves * 64), 0, st, a);
+}
+
+// A lane takes as many eights of a row as leave the device full of waves: one while all
+// the rows' waves are at most half of what it holds (1024 rows of 2048 into 8 bits: 5.1
+// us, two 5.2, four 5.8), two while they are at most all (1024 rows of 5120: 8.3, one
+// 9.7, four 8.7), then up to four, so that few waves meet for a row's sum and each has
+// more on its way (8192 rows of 5120: 33.7 us, 37.6 with two and 55.7 with one; of 8192
+// 44.8, 50.4 and 69.9), and no more than fill its waves (2500 rows of 4104 into 16 bits
+// 12.1 with three, 12.4 with four).
 template <int DT, bool F8, bool PASS>
 void pick(const NormArgs& a, hipStream_t st) {
     const int eights = (int)(((long long)a.width + 7) / 8);
-    if (eights <= 64) go<DT, F8, PASS, true, 1>(a, 256, st);
-    else if (a.rows < 256 && eights <= 1024) go<DT, F8, PASS, false, 1>(a, (eights + 63) / 64 * 64, st);
-    else if (eights <= 128) go<DT, F8, PASS, true, 2>(a, 256, st);
-    else if (eights <= 256) go<DT, F8, PASS, false, 2>(a, 128, st);
-    else if (eights <= 512) go<DT, F8, PASS, false, 2>(a, 256, st);
-    else if (eights <= 768) go<DT, F8, PASS, false, 3>(a, 256, st);
-    else if (eights <= 1024) go<DT, F8, PASS, false, 2>(a, 512, st);
-    else if (eights <= 1536) go<DT, F8, PASS, false, 3>(a, 512, st);
-    else if (eights <= 2048) go<DT, F8, PASS, false, 4>(a, 512, st);
-    else hipLaunchKernelGGL((norm_long_kernel<DT, F8>), dim3((unsigned)a.rows), dim3(1024), 0, st, a);
+    if (eights > 2048) {
+        hipLaunchKernelGGL((norm_long_kernel<DT, F8>), dim3((unsigned)a.rows), dim3(1024), 0, st, a);
+        return;
+    }
+    const int one = (eights + 63) / 64, two = (eights + 127) / 128;
+    const int waves = one <= 16 && (long long)a.rows * one <= 4096 ? one
+                      : (long long)a.rows * two <= 8192            ? std::min(two, 8)
+                                                                   : (eights + 255) / 256;
+    switch ((eights + 64 * waves - 1) / (64 * waves)) {
+        case 1: go<DT, F8, PASS, 1>(a, waves, st); break;
+        case 2: go<DT, F8, PASS, 2>(a, waves, st); break;
+        case 3: go<DT, F8, PASS, 3>(a, waves, st); break;
+        default: go<DT, F8, PASS, 4>(a, waves, st); break;
+    }
 }
 
 }  // namespace

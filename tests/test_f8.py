@@ -265,6 +265,29 @@ def test_norm_f8(width, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows", [600, 1500, 8300])
+@pytest.mark.parametrize("width", [64, 512, 1000, 1536, 2048, 2049, 2560, 4096, 4097, 5120, 8192, 9216, 12290, 16384])
+def test_norm_many_rows(width, rows):
+    """Lanes and elements a lane are picked by rows and width; large sums are stored another way."""
+    say("norm many", rows, width)
+    g = torch.Generator(device=DEV).manual_seed(width)
+    x = torch.randn(rows, width, device=DEV, generator=g).bfloat16()
+    r = torch.randn(rows, width, device=DEV, generator=g).bfloat16()
+    w = (1 + 0.3 * torch.randn(width, device=DEV, generator=g)).bfloat16()
+    some = torch.cat((torch.arange(20), torch.randint(rows, (20,), generator=gen(1)), torch.arange(rows - 20, rows)))
+    got, total = qmx.rms_norm(x, w, r)
+    y, h = ref.norm(x[some].cpu(), w.cpu(), r[some].cpu(), 1e-6)
+    assert torch.equal(total, x + r)
+    check_norm(x[some].cpu(), w.cpu(), r[some].cpu(), None, 1e-6, got[some], total[some])
+    if width % 128 == 0:
+        codes, scales, total = qmx.rms_norm_f8(x, w, r)
+        assert torch.equal(total, x + r)
+        check_codes(codes.view(torch.uint8)[some].view(codes.dtype), scales.view(torch.uint8)[some].view(scales.dtype), y)
+        codes, scales = qmx.rms_norm_f8(total, w)
+        check_codes(codes.view(torch.uint8)[some].view(codes.dtype), scales.view(torch.uint8)[some].view(scales.dtype), y)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 def test_norm_ranges(dtype):
     """Rows of the largest, of the smallest and of no magnitude, and rows that hold a NaN or an infinity, which
