@@ -596,7 +596,8 @@ def check_rope(q, k, positions, f, interleaved, scale, got):
                                             (5, 3, 3, 80, 40), (2, 2, 1, 81, 40), (4, 6, 2, 96, 13), (9, 1, 0, 256, 128),
                                             (6, 0, 4, 100, 3), (130, 40, 8, 128, 64), (300, 3, 1, 48, 20),
                                             (2049, 5, 2, 64, 32), (2050, 2, 1, 70, 9), (2, 2, 2, 4096, 2048),
-                                            (2050, 1, 1, 1200, 600)])
+                                            (2050, 1, 1, 1200, 600), (6, 1, 0, 3056, 1528), (3, 1, 0, 3080, 1532),
+                                            (1030, 40, 8, 128, 64), (4100, 24, 4, 40, 20), (4099, 30, 9, 64, 30)])
 def test_rope(T, heads, kv, D, n, interleaved, dtype):
     say("rope", T, heads, kv, D, n, interleaved, dtype)
     g = gen(T + D)
