@@ -104,6 +104,8 @@ __device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t out, uint32_t plac
 // a lane's operand is 32 of a row's 128, here the 16 from 16h and from 64 + 16h on
 // (h = lane / 16), the same of w and x, so that a load takes 64 neighbouring bytes
 // of each row.  The waves' sums meet in LDS in a fixed order.
+// Bound by memory: 1 row by 27648 over 5120 takes 26 us, 5.4 TB/s (some of the weights
+// from the Infinity Cache), by 2048 over 2048 3.9 us, a launch and two ways to memory.
 template <int DT, bool F32, int MT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void rows_kernel(F8MmArgs a) {
     __shared__ f32x4 part[WAVES][MT][64];
@@ -212,13 +214,12 @@ __device__ __forceinline__ TileAt tile_at(int t, int tiles_m, int tiles_n) {
 // beside the last row A and B are read from the next stage).  So what is copied has a
 // step and a half to come with two stages only, and the copies run on into the next
 // tile while one is finished and written.
-// Bound by LDS and the matrix cores, whose power limit takes the clock to some 2.0 GHz:
-// a step of 256 x 256 writes 64 KB into LDS and reads 192 (about 2500 cycles) beside
-// 2048 cycles of products on each SIMD.  8192 x 14336 over K = 5120: 448 us, 2685 TFLOP/s
-// (a library's 8-bit product without group scales: 2758).  Four waves of 128 x 128 read
-// a third less, but take 595 us: one wave on a SIMD waits at every barrier.  Of 128 x 128
-// tiles a compute unit holds two work-groups, each filling the other's waits: 1024 x 5120
-// over 14336 120 us, 139 with one of four stages.
+// Bound by the matrix cores and the card's power: 8192 x 14336 over K = 5120 takes 448
+// us, 2685 TFLOP/s (a library's 8-bit product without group scales: 2758), in which the
+// matrix cores are busy 66 % of the cycles and the clock is at 1.94 GHz.  Four waves of
+// 128 x 128 read a third less of LDS, but take 595 us: one wave on a SIMD waits at every
+// barrier.  Of 128 x 128 tiles a compute unit holds two work-groups, each filling the
+// other's waits: 1024 x 5120 over 14336 120 us, 139 with one of four stages.
 // The scales of CHUNK groups stand beside the stages, the next ones' in a second place:
 // a lane's TM scales of x in neighbouring bytes, which the matrix instruction picks from
 // a register by itself.
@@ -526,11 +527,12 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
 // a step ahead of the products, so one barrier a step is enough: behind it a stage has
 // come and the one before is free.  Layouts of LDS as above, scales of DEPTH groups a
 // team at a time.
-// Bound by the way from L2 over LDS into registers, some 70 bytes a nanosecond and
-// compute unit whatever the tile; weights straight into registers, as few rows take
-// them, come at half of that, four lanes of a quad reading four rows.  Eight waves a
-// team hide more of it in 64 x 128 (300 x 4100 over 4096: 13.1 us, 14.0 with four),
-// the smaller tiles gain nothing by more.
+// Bound by what is on its way: some 70 bytes a nanosecond and compute unit whatever
+// the tile, waves waiting 44 % of their time and the matrix cores busy 28 % (300 x 4100
+// over 4096: 13.1 us; 14.0 with four waves a team in place of eight, while the smaller
+// tiles gain nothing by more).  Weights straight into registers, as few rows take them,
+// come at half of that (26 us), four lanes of a quad reading four rows; a wave that
+// reads one word of each line ahead, to have it in L2, holds the copies up (22 us).
 constexpr int DEPTH = 32;
 
 template <int BM, int BN, int TEAMS, int STAGES>
