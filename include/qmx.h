@@ -452,8 +452,7 @@ int qmx_kv4_read(const qmx_kv4_cache* cache, void* k_out, void* v_out, const int
  *           scaled scores (-inf where nothing is seen).
  *   max_query_len, max_kv_len : at least the longest request's new and cached
  *           tokens (host numbers: they size the launch; queries of a request
- *           past max_query_len are left unwritten); max_query_len is at most
- *           `tokens`.
+ *           past max_query_len get zeros); max_query_len is at most `tokens`.
  *   scale : finite and above 0.
  *   workspace : qmx_kv4_attention_workspace_bytes bytes, 16-byte aligned (NULL
  *           where that is 0), overwritten; calls that share it are ordered.

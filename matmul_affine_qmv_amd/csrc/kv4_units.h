@@ -57,19 +57,21 @@ __device__ __forceinline__ Unit unit_of(const Kv4AttnArgs& a, int v) {
 }
 
 // Zeros for the tokens of no request, before the first offset and from the last
-// on: group `id` of `of`.
+// on, and for a request's tokens past max_query: group `id` of `of`.
 __device__ __forceinline__ void clear_rest(const Kv4AttnArgs& a, int id, int of) {
     const long long thread = (long long)id * blockDim.x + threadIdx.x, threads = (long long)of * blockDim.x;
     const int first = min(max(a.offsets[0], 0), a.tokens), begin = max(a.offsets[a.requests], 0);
-    auto clear = [&](long long from, long long to) {
+    auto clear = [&](long long from, long long to, long long at, long long step) {
         const int per = a.heads * (a.c.dim / 8);
-        for (long long i = from * per + thread; i < to * per; i += threads)
+        for (long long i = from * per + at; i < to * per; i += step)
             reinterpret_cast<u32x4*>(a.out)[i] = u32x4{0, 0, 0, 0};
         if (a.lse)
-            for (long long i = from * a.heads + thread; i < to * a.heads; i += threads) a.lse[i] = -INFINITY;
+            for (long long i = from * a.heads + at; i < to * a.heads; i += step) a.lse[i] = -INFINITY;
     };
-    clear(0, first);
-    clear(begin, a.tokens);
+    clear(0, first, thread, threads);
+    clear(begin, a.tokens, thread, threads);
+    for (long long r = thread; r < a.requests; r += threads)   // a caller's bound that is too low: no need for speed
+        clear((long long)max(a.offsets[r], 0) + a.max_query, min(a.offsets[r + 1], a.tokens), 0, 1);
 }
 
 // The units of work-group `id` of a head, one after the other.

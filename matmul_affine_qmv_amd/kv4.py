@@ -231,8 +231,8 @@ def kv4_attention(cache: Kv4Cache, q, block_table, kv_lens, query_offsets, *, ma
     block_table: int32 [R, columns]; kv_lens: int32 [R]; query_offsets: int32
     [R + 1], request r's queries being the last of its kv_lens[r] tokens.
     max_query_len, max_kv_len: host bounds of both; what a request has past them
-    is not computed: its later queries' outputs are left unwritten, its later
-    keys unseen.  window: 0, or how many tokens a query sees, itself among them.
+    is not computed: its later queries' outputs are zeros, its later keys
+    unseen.  window: 0, or how many tokens a query sees, itself among them.
     scale: above 0, head_dim ** -0.5 by default.  workspace: of
     kv4_attention_workspace_bytes bytes, where the caller keeps one.  Returns
     out, or (out, lse) with float32 lse [tokens, heads]."""

@@ -258,6 +258,33 @@ def test_workspace_of_the_caller(each, D, most, new):
 
 
 @on_gpu
+@pytest.mark.parametrize("each,most,kv", [(1, 3, 3000), (4, 1, 200), (2, 40, 1700), (4, 25, 90)])
+def test_queries_past_their_bound(each, most, kv):
+    """Requests with more queries than the bound: those within it as ever, zeros and -inf past it, all else as given."""
+    say("past the bound", each, most, kv)
+    rng = np.random.default_rng(34)
+    lens, D = [kv, kv // 2, kv // 3, 70], 64
+    table, pages = tables(lens, 64)
+    cache = device_cache(ref.Cache(pages, 2, D, 64, 64, "bf16", rng))
+    new = [most + 20, most, most + 1, 1]
+    offsets = [2, *(2 + sum(new[:i + 1]) for i in range(4))]
+    T, heads = offsets[-1] + 3, 2 * each
+    q = torch.from_numpy(rng.normal(0, 1, (T, heads, D))).bfloat16().to(DEV)
+    args = (cache, q, torch.from_numpy(table).to(DEV), ints(lens), ints(offsets))
+    want, want_lse = qmx.kv4_attention(*args, max_query_len=max(new), max_kv_len=kv, return_lse=True)
+    for fill in (7.0, float("nan")):
+        out, lse = qmx.kv4_attention(*args, max_query_len=most, max_kv_len=kv, return_lse=True,
+                                     out=torch.full_like(q, fill))
+        for start, n in zip(offsets, new):
+            within, past = slice(start, start + min(n, most)), slice(start + most, start + n)
+            assert not out[past].any() and torch.isneginf(lse[past]).all()
+            assert torch.isfinite(out[within]).all()
+            assert (out[within] - want[within]).abs().max() <= 2 ** -5 * want.abs().max()
+            assert (lse[within] - want_lse[within]).abs().max() <= 2 ** -5
+        assert not out[:2].any() and not out[T - 3:].any()
+
+
+@on_gpu
 @pytest.mark.parametrize("D,group", [(64, 32), (128, 128), (256, 64)])
 @pytest.mark.parametrize("power", range(-133, -95, 3))
 def test_write_of_tiny_groups(D, group, power):
