@@ -46,7 +46,7 @@
 // other.  Cut by splits of one length for all requests, as the host alone could do
 // it, they took 55 + 14 and 40 + 4 us.  Pairs read by every lane that needs them
 // instead of shared by a row cost 72 registers and 20 % of the time.  Heads of 256
-// spill 49 registers in groups of 64 and 240 in groups of 32, whose 48 tokens over up
+// spill 46 registers in groups of 64 and 230 in groups of 32, whose 48 tokens over up
 // to 8000 take 72 and 239 us (groups of 128, none spilled: 43).
 #pragma once
 
@@ -379,6 +379,7 @@ __global__ __launch_bounds__(64 * WK, 2) void kv4_attn_kernel(Kv4AttnArgs a) {
     const Kv4View& c = a.c;
     const int head = blockIdx.x % c.heads;
 
+    if (clears(a, blockIdx.x / c.heads, head)) return;
     Units<64 * WK> units(a, blockIdx.x / c.heads, head);
     for (Unit u; units.next(a, u);) {
         const int last = u.rows - 1;

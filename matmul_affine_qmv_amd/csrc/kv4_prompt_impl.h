@@ -19,8 +19,8 @@
 // costs a sixth.  Keys of rounded numbers instead of exact scores took the same
 // time, with scores off by 2^-12 each.  Groups of 32 and 128: 716 and 657 where 64
 // take 670; heads of 64 491; float16 940 (groups of 32 2080, of 128 910; heads of 64
-// 650).  What is spilled: of float16 at 128, 12 registers in groups of 128, 23 of 64
-// and 81 of 32; at 256, 17 to 48.
+// 650).  What is spilled: of float16 at 128, 8 registers in groups of 128, 16 of 64
+// and 70 of 32; at 256, 9 to 40.
 //
 //   S^T[key, row] = K Q^T,  O^T[dim, row] += V^T P:  v_mfma_32x32x16, where the
 //   probabilities that a lane computes are the operand it needs (as in
@@ -342,6 +342,7 @@ __global__ __launch_bounds__(64 * PROMPT_WAVES, 2) void kv4_prompt_kernel(Kv4Att
     const bool value = wave >= 4;   // which codes this wave turns into operands
     const int my_blk = (wave & 3) / W::SPLIT, my_part = (wave & 3) % W::SPLIT;
 
+    if (clears(a, blockIdx.x / c.heads, head)) return;
     for (int i = threadIdx.x; i < 2 * NT * BK * 64; i += 64 * PROMPT_WAVES)   // slots that no group has
         s_k[i / (NT * BK * 64)][i / (BK * 64) % NT * (BK + KS) * 64 + i % (BK * 64)] = u32x4{0, 0, 0, 0};
 

@@ -74,6 +74,13 @@ __device__ __forceinline__ void clear_rest(const Kv4AttnArgs& a, int id, int of)
         clear((long long)max(a.offsets[r], 0) + a.max_query, min(a.offsets[r + 1], a.tokens), 0, 1);
 }
 
+// Whether work-group `id` of a head is the one behind the units, which clears.
+__device__ __forceinline__ bool clears(const Kv4AttnArgs& a, int id, int head) {
+    if (a.p.lines || id < a.requests * a.p.tiles) return false;
+    clear_rest(a, head, a.c.heads);
+    return true;
+}
+
 // The units of work-group `id` of a head, one after the other.
 template <int THREADS>
 class Units {
@@ -130,10 +137,6 @@ class Units {
         if (at_ >= stop_) return false;
         if (!a.p.lines) {
             at_ = stop_;
-            if (id_ >= count_) {
-                clear_rest(a, id_ - count_ + (int)(blockIdx.x % a.c.heads), a.c.heads);
-                return false;
-            }
             u = unit_of(a, id_);
             return u.rows > 0;
         }
