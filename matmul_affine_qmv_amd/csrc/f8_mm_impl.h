@@ -521,46 +521,44 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
 }
 
 // ---------------------------------------------------------------- small tiles
-// For calls whose tiles are few: each of TEAMS teams of WM by WN waves takes a run
-// of the K groups of a tile of BM by BN, with stages of its own in LDS, so that a step
-// takes TEAMS groups; the teams' sums meet in LDS in a fixed order.  Operands are read
-// a step ahead of the products, so one barrier a step is enough: behind it a stage has
-// come and the one before is free.  Layouts of LDS as above, scales of DEPTH groups a
-// team at a time.
-// Bound by what is on its way: some 70 bytes a nanosecond and compute unit whatever
-// the tile, waves waiting 44 % of their time and the matrix cores busy 28 % (300 x 4100
-// over 4096: 13.1 us; 14.0 with four waves a team in place of eight, while the smaller
-// tiles gain nothing by more).  Weights straight into registers, as few rows take them,
-// come at half of that (26 us), four lanes of a quad reading four rows; a wave that
-// reads one word of each line ahead, to have it in L2, holds the copies up (22 us).
+// For calls whose tiles are few: four waves (WM by WN) to a tile of BM by BN, of whose
+// work-groups a compute unit holds two or more.  Operands are read a step ahead of the
+// products, so one barrier a step is enough: behind it a stage has come and the one
+// before is free.  Reads and copies stand between the products, which run beside them
+// (behind them all: 5 to 12 % slower).  Layouts of LDS as above, scales of DEPTH groups
+// at a time.
+// Bound by the way from L2 into LDS: a compute unit takes in some 75 bytes a nanosecond
+// whatever the tile, of the 120 that it can, waves waiting for what was copied two steps
+// before.  300 x 4100 over 4096 13.5 us.  Weights straight into registers, as few rows
+// take them, come at half of that (26 us), four lanes of a quad reading four rows; a
+// wave that reads one word of each line ahead, to have it in L2, holds the copies up
+// (22 us); two halves of K in a work-group, joined in LDS, take as long, and are a
+// coarser choice for the rule (1 % more over all sizes).
 constexpr int DEPTH = 32;
 
-template <int BM, int BN, int TEAMS, int STAGES>
+template <int BM, int BN, int STAGES>
 struct SmallLds {
-    alignas(16) uint8_t data[TEAMS][STAGES][(BM + BN) * 128];
-    alignas(16) uint8_t sx[TEAMS][DEPTH][BM];
-    uint32_t sw[TEAMS][DEPTH][(BN + 127) / 128];
+    alignas(16) uint8_t data[STAGES][(BM + BN) * 128];
+    alignas(16) uint8_t sx[DEPTH][BM];
+    uint32_t sw[DEPTH][(BN + 127) / 128];
 };
 
-template <int DT, bool F32, int BM, int BN, int WM, int WN, int TEAMS, int STAGES, bool SPLIT>
-__global__ __launch_bounds__(64 * WM * WN * TEAMS) void small_kernel(F8MmArgs a, int splits) {
+template <int DT, bool F32, int BM, int BN, int WM, int WN, int STAGES, bool SPLIT>
+__global__ __launch_bounds__(64 * WM * WN) void small_kernel(F8MmArgs a, int splits) {
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16, BLOCKS = (BN + 127) / 128, ROWS = BM + BN;
     constexpr int T = 64 * WM * WN, COPIES = ROWS * 8 / T, W_COPIES = BN * 8 / T;
     static_assert(COPIES * T == ROWS * 8 && W_COPIES * T == BN * 8 && COPIES * (STAGES - 1) <= 63, "copies");
-    static_assert(TN % 2 == 0 && (TM == 1 || TM == 2) && 128 % (16 * TN) == 0, "operands");
-    static_assert(sizeof(f32x4) * TM * TN * T <= STAGES * ROWS * 128, "sums");
-    __shared__ SmallLds<BM, BN, TEAMS, STAGES> lds;
-    const int tid = threadIdx.x % T, lane = tid & 63;
-    const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / T), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    static_assert(TN % 2 == 0 && (TM == 1 || TM == 2) && TM * TN <= 8 && 128 % (16 * TN) == 0, "operands");
+    __shared__ SmallLds<BM, BN, STAGES> lds;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, h = lane >> 4, wm = wave % WM, wn = wave / WM;
     const int G = a.K / 128, tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN;
     // each XCD takes a run of the list of tiles
     const int xcd = blockIdx.x & 7, run = (int)gridDim.x >> 3, more_runs = gridDim.x & 7;
     const TileAt at = tile_at<8>(xcd * run + min(xcd, more_runs) + (int)(blockIdx.x >> 3), tiles_m, tiles_n);
     const int m0 = at.m * BM, n0 = at.n * BN;
-    const int parts = (SPLIT ? splits : 1) * TEAMS, part = at.part * TEAMS + team;
-    const int k0 = (int)((long long)G * part / parts), k1 = (int)((long long)G * (part + 1) / parts);
-    const int longest = (G + parts - 1) / parts;   // groups of any team, whose steps all take
+    const int k0 = SPLIT ? (int)((long long)G * at.part / splits) : 0;
+    const int k1 = SPLIT ? (int)((long long)G * (at.part + 1) / splits) : G;
     const auto wbuf = buffer_over(a.w + (size_t)n0 * a.K, (size_t)min(BN, a.N - n0) * a.K);
     const auto xbuf = buffer_over(a.x + (size_t)m0 * a.K, (size_t)min(BM, a.M - m0) * a.K);
     uint32_t off[COPIES];
@@ -571,12 +569,10 @@ __global__ __launch_bounds__(64 * WM * WN * TEAMS) void small_kernel(F8MmArgs a,
                                       : min(row - BN, a.M - 1 - m0);
         off[i] = (uint32_t)from * (uint32_t)a.K + 16 * c;
     }
-    // past the team's last group: the first group again, or none of it (a team may have none)
-    auto copy = [&](int g, int stage) {
-        const uint32_t at = (uint32_t)min(g, G - 1) * 128;
-#pragma unroll
-        for (int i = 0; i < COPIES; ++i)
-            copy16(i < W_COPIES ? wbuf : xbuf, off[i], at, &lds.data[team][stage][(i * T + wave * 64) * 16]);
+    // The i-th of COPIES of a group; past the last, of that again.
+    auto copy_one = [&](int i, int g, int stage) {
+        copy16(i < W_COPIES ? wbuf : xbuf, off[i], (uint32_t)min(g, G - 1) * 128,
+               &lds.data[stage][(i * T + wave * 64) * 16]);
     };
     f32x4 acc[TM][TN] = {};
     const int col = wn * TN * 16;
@@ -584,77 +580,99 @@ __global__ __launch_bounds__(64 * WM * WN * TEAMS) void small_kernel(F8MmArgs a,
         i32x8 A[TN], B[TM];
         uint32_t sx, sw;
     };
-    auto read = [&](int s, int stage, Operands& o) {
-        const uint8_t* data = lds.data[team][stage];
-        auto frag = [&](int row) {
-            const uint8_t* p = data + (row + r) * 128;
-            return join(*reinterpret_cast<const u32x4*>(p + 16 * (h ^ (r & 7))),
-                        *reinterpret_cast<const u32x4*>(p + 16 * ((h + 4) ^ (r & 7))));
-        };
-#pragma unroll
-        for (int i = 0; i < TN; ++i) o.A[i] = frag(col + i * 16);
-#pragma unroll
-        for (int i = 0; i < TM; ++i) o.B[i] = frag(BN + (wm * TM + i) * 16);
-        const uint8_t* from = &lds.sx[team][s][wm * TM * 16 + r * TM];
-        o.sx = TM == 2 ? *reinterpret_cast<const uint16_t*>(from) : *from;
-        o.sw = lds.sw[team][s][(n0 % 128 + col) / 128];
+    auto frag = [&](int row, int stage) {   // of 16 rows from `row` on
+        const uint8_t* p = &lds.data[stage][(row + r) * 128];
+        return join(*reinterpret_cast<const u32x4*>(p + 16 * (h ^ (r & 7))),
+                    *reinterpret_cast<const u32x4*>(p + 16 * ((h + 4) ^ (r & 7))));
     };
-    auto one = [&](auto which, const Operands& o) {
-        constexpr int m = decltype(which)::value;
-        if constexpr (m < TM) {
-#pragma unroll
-            for (int n = 0; n < TN; ++n) {
-                if constexpr (F32) {
-                    const f32x4 d = mfma<0, m>(o.A[n], o.B[m], f32x4{0.f, 0.f, 0.f, 0.f}, ONE, (int)o.sx);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(__uint_as_float(o.sw), d[e], acc[m][n][e]);
-                } else {
-                    acc[m][n] = mfma<0, m>(o.A[n], o.B[m], acc[m][n], (int)o.sw, (int)o.sx);
-                }
-            }
+    // The i-th of a step's TN + TM operands; the scales come with the first.
+    auto read_one = [&](int i, int s, int stage, Operands& o) {
+        if (i < TN) o.A[i < TN ? i : 0] = frag(col + i * 16, stage);
+        else o.B[i < TN ? 0 : i - TN] = frag(BN + (wm * TM + i - TN) * 16, stage);
+        if (i == 0) {
+            const uint8_t* from = &lds.sx[s][wm * TM * 16 + r * TM];
+            o.sx = TM == 2 ? *reinterpret_cast<const uint16_t*>(from) : *from;
+            o.sw = lds.sw[s][(n0 % 128 + col) / 128];
         }
     };
-    auto products = [&](const Operands& o) {
-        one(std::integral_constant<int, 0>(), o);
-        one(std::integral_constant<int, 1>(), o);
+    // The i-th product of a step, and its sum where w's scales are float32.
+    auto product = [&](auto which, const Operands& o, f32x4& d) {
+        constexpr int m = decltype(which)::value / TN, n = decltype(which)::value % TN;
+        if constexpr (F32) d = mfma<0, m>(o.A[n], o.B[m], f32x4{0.f, 0.f, 0.f, 0.f}, ONE, (int)o.sx);
+        else acc[m][n] = mfma<0, m>(o.A[n], o.B[m], acc[m][n], (int)o.sw, (int)o.sx);
     };
-    for (int c = 0; c < longest; c += DEPTH) {
-        const int g0 = k0 + c, n = min(DEPTH, longest - c), mine = max(0, min(n, k1 - g0));
-        if (c > 0) __syncthreads();
+    auto add = [&](auto which, const Operands& o, const f32x4& d) {
+        constexpr int m = decltype(which)::value / TN, n = decltype(which)::value % TN;
+        if constexpr (F32) {
 #pragma unroll
-        for (int i = 0; i < STAGES; ++i) copy(g0 + i, i);
-        // Scales; what is past the team's groups counts nothing: scales of 0 in w's float32,
-        // and in both others the steps are left out.
+            for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(__uint_as_float(o.sw), d[e], acc[m][n][e]);
+        }
+    };
+    for (int g0 = k0; g0 < k1; g0 += DEPTH) {
+        const int n = min(DEPTH, k1 - g0);
+        if (g0 > k0) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i)
+#pragma unroll
+            for (int e = 0; e < COPIES; ++e) copy_one(e, g0 + i, i);
         for (int i = tid; i < BM * (DEPTH / 16); i += T) {
             const int row = i / (DEPTH / 16), first = i % (DEPTH / 16) * 16;
             struct __attribute__((packed, aligned(1))) Any { u32x4 v; };
             const uint8_t* from = a.x_scales + (size_t)min(m0 + row, a.M - 1) * G + g0 + first;
-            uint8_t* to = &lds.sx[team][first][row / (TM * 16) * (TM * 16) + row % 16 * TM + row / 16 % TM];
-            if (first + 16 <= mine) {
+            uint8_t* to = &lds.sx[first][row / (TM * 16) * (TM * 16) + row % 16 * TM + row / 16 % TM];
+            if (first + 16 <= n) {
                 const u32x4 v = reinterpret_cast<const Any*>(from)->v;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) to[j * BM] = (uint8_t)(v[j / 4] >> (8 * (j % 4)));
             } else {
-                for (int j = 0; first + j < mine; ++j) to[j * BM] = from[j];
+                for (int j = 0; first + j < n; ++j) to[j * BM] = from[j];
             }
         }
-        for (int i = tid; i < mine * BLOCKS; i += T) {
+        for (int i = tid; i < n * BLOCKS; i += T) {
             const int j = i / BLOCKS, block = i % BLOCKS;
             const size_t from = (size_t)min(n0 / 128 + block, (a.N - 1) / 128) * G + g0 + j;
-            lds.sw[team][j][block] = F32 ? static_cast<const uint32_t*>(a.w_scales)[from]
+            lds.sw[j][block] = F32 ? static_cast<const uint32_t*>(a.w_scales)[from]
                                          : 0x01010101u * static_cast<const uint8_t*>(a.w_scales)[from];
         }
         Operands even, odd;
         wait_copies<COPIES * (STAGES - 1)>();
-        read(0, 0, even);
+#pragma unroll
+        for (int i = 0; i < TN + TM; ++i) read_one(i, 0, 0, even);
         int stage = 0;
-        // Of step s's operands in `now`: those of step s + 1 are read into `then`.
+        // Of step s's operands in `now`: those of step s + 1 are read into `then`, and a
+        // stage is copied, a part of both ahead of each product.
         auto step = [&](int s, const Operands& now, Operands& then) {
-            const int next = stage + 1 == STAGES ? 0 : stage + 1;
+            constexpr int ALL = TM * TN, READS = (TN + TM + ALL - 1) / ALL, COPY = (COPIES + ALL - 1) / ALL;
+            const int next = stage + 1 == STAGES ? 0 : stage + 1, next_s = min(s + 1, DEPTH - 1);
             wait_copies<COPIES * (STAGES - 2)>();
-            copy(g0 + s + STAGES, stage);
-            read(min(s + 1, DEPTH - 1), next, then);
-            if (s < mine) products(now);
+            auto ahead = [&](int e) {
+#pragma unroll
+                for (int i = 0; i < TN + TM; ++i)
+                    if (i / READS == e) read_one(i, next_s, next, then);
+#pragma unroll
+                for (int i = 0; i < COPIES; ++i)
+                    if (i / COPY == e) copy_one(i, g0 + s + STAGES, stage);
+            };
+            f32x4 d[2];
+            auto one = [&](auto which) {
+                constexpr int e = decltype(which)::value;
+                if constexpr (e < ALL) {
+                    ahead(e);
+                    __builtin_amdgcn_sched_barrier(0);
+                    product(which, now, d[e % 2]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if constexpr (e > 0) add(std::integral_constant<int, e - 1>(), now, d[(e - 1) % 2]);
+                    if constexpr (e + 1 == ALL) add(which, now, d[e % 2]);
+                }
+            };
+            one(std::integral_constant<int, 0>());
+            one(std::integral_constant<int, 1>());
+            one(std::integral_constant<int, 2>());
+            one(std::integral_constant<int, 3>());
+            one(std::integral_constant<int, 4>());
+            one(std::integral_constant<int, 5>());
+            one(std::integral_constant<int, 6>());
+            one(std::integral_constant<int, 7>());
             stage = next;
         };
         for (int s = 0; s < n; s += 2) {
@@ -662,23 +680,7 @@ __global__ __launch_bounds__(64 * WM * WN * TEAMS) void small_kernel(F8MmArgs a,
             if (s + 1 < n) step(s + 1, odd, even);
         }
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // copies that nobody reads
-    __syncthreads();
-    // The teams' sums, in their order.
-    constexpr int EACH = TM * TN;
-    f32x4* sums = reinterpret_cast<f32x4*>(&lds.data[team][0][0]);
-    if (team > 0) {
-#pragma unroll
-        for (int i = 0; i < EACH; ++i) sums[i * T + tid] = acc[i / TN][i % TN];
-    }
-    __syncthreads();
-    if (team > 0) return;
-#pragma unroll
-    for (int k = 1; k < TEAMS; ++k) {
-        const f32x4* other = reinterpret_cast<const f32x4*>(&lds.data[k][0][0]);
-#pragma unroll
-        for (int i = 0; i < EACH; ++i) acc[i / TN][i % TN] += other[i * T + tid];
-    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // LDS is written to until then
     const uintptr_t out_at = SPLIT ? 0 : reinterpret_cast<uintptr_t>(a.out);
     const int wide = a.N % 8 == 0 && out_at % 16 == 0 ? 8 : a.N % 4 == 0 && out_at % 8 == 0 ? 4 : 1;
     constexpr int SIZE = SPLIT ? 4 : 2;
@@ -702,11 +704,11 @@ void go_rows(const F8MmArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((rows_kernel<DT, F32, MT, 8>), dim3((unsigned)((a.N + 15) / 16)), dim3(512), 0, st, a);
 }
 
-template <int DT, bool F32, int BM, int BN, int WN, int TEAMS, int STAGES>
+template <int DT, bool F32, int BM, int BN, int STAGES>
 void go_small(const F8MmArgs& a, int splits, hipStream_t st) {
-    const dim3 grid((unsigned)((a.M + BM - 1) / BM) * (unsigned)((a.N + BN - 1) / BN) * (unsigned)splits), block(128 * WN * TEAMS);
-    if (splits > 1) hipLaunchKernelGGL((small_kernel<DT, F32, BM, BN, 2, WN, TEAMS, STAGES, true>), grid, block, 0, st, a, splits);
-    else hipLaunchKernelGGL((small_kernel<DT, F32, BM, BN, 2, WN, TEAMS, STAGES, false>), grid, block, 0, st, a, 1);
+    const dim3 grid((unsigned)((a.M + BM - 1) / BM) * (unsigned)((a.N + BN - 1) / BN) * (unsigned)splits), block(256);
+    if (splits > 1) hipLaunchKernelGGL((small_kernel<DT, F32, BM, BN, 2, 2, STAGES, true>), grid, block, 0, st, a, splits);
+    else hipLaunchKernelGGL((small_kernel<DT, F32, BM, BN, 2, 2, STAGES, false>), grid, block, 0, st, a, 1);
 }
 
 template <int DT, bool F32, int SIZE>
@@ -721,9 +723,9 @@ template <int DT, bool F32>
 void launch(const F8MmArgs& a, F8Plan p, int cus, hipStream_t st) {
     switch (p.tile) {
         case F8_ROWS: a.M <= 16 ? go_rows<DT, F32, 1>(a, st) : go_rows<DT, F32, 2>(a, st); break;
-        case F8_32x64: go_small<DT, F32, 32, 64, 2, 2, 5>(a, p.splits, st); break;
-        case F8_64x64: go_small<DT, F32, 64, 64, 2, 2, 4>(a, p.splits, st); break;
-        case F8_64x128: go_small<DT, F32, 64, 128, 4, 2, 3>(a, p.splits, st); break;
+        case F8_32x64: go_small<DT, F32, 32, 64, 5>(a, p.splits, st); break;
+        case F8_64x64: go_small<DT, F32, 64, 64, 4>(a, p.splits, st); break;
+        case F8_64x128: go_small<DT, F32, 64, 128, 3>(a, p.splits, st); break;
         case F8_128x128: go_tiles<DT, F32, 128>(a, p.splits, cus, st); break;
         default: go_tiles<DT, F32, 256>(a, p.splits, cus, st); break;
     }
