@@ -502,6 +502,40 @@ def test_product_many_tiles(M, N, K, f32):
     check_product(M, N, K, torch.bfloat16, f32, seed=M, most_rows=24)
 
 
+# On 256 compute units: of each kernel, whole and cut calls whose scales fit in LDS at once, and others.
+EVERY = [(1, 512, 2048), (30, 2048, 2048), (16, 1001, 8192), (17, 8192, 5120), (1, 1000, 5120), (16, 4100, 12800),
+         (640, 4100, 128), (33, 14001, 5120), (33, 2048, 5120), (40, 4100, 12800), (33, 20000, 1024), (48, 20004, 5120),
+         (160, 2047, 12800), (1300, 512, 12800), (1300, 14000, 128), (512, 4100, 5120), (128, 4097, 12800),
+         (640, 2048, 12800), (800, 14008, 1024), (2048, 4100, 5120), (300, 8192, 12800), (192, 20000, 12800)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("f32", [False, True], ids=["e8m0", "f32"])
+@pytest.mark.parametrize("M,N,K", EVERY)
+def test_product_every_kernel(M, N, K, f32):
+    """Rows at both ends and every 61st, against 64 bits, with the reference's bound of the kernel's own errors, in which
+    the largest of 8 products is at most the sum of their magnitudes; half a step of bfloat16 is 2^-8 of the result."""
+    say("product every", M, N, K, f32)
+    g = torch.Generator(device=DEV).manual_seed(M + N + K)
+    w, ws = qmx.f8_quantize((torch.randn(N, K, generator=g, device=DEV) * K ** -0.5).bfloat16(), block_rows=128)
+    x, xs = qmx.f8_quantize(torch.randn(M, K, generator=g, device=DEV).bfloat16())
+    if f32:
+        ws = ws.float() * (0.5 + torch.rand(ws.shape, generator=g, device=DEV))
+    got = qmx.qmm_f8(w, ws, x, xs)
+    X = x.double().view(M, -1, 128) * xs.double()[:, :, None]
+    rows = torch.cat((torch.arange(min(M, 24)), torch.arange(max(0, M - 24), M), torch.arange(0, M, 61))).unique().to(DEV)
+    X = X.view(M, K)[rows]
+    step = 2048
+    for n in range(0, N, step):
+        W = w[n:n + step].double().view(-1, K // 128, 128)
+        W = (W * ws[n // 128:(n + step) // 128].double().repeat_interleave(128, 0)[:len(W), :, None]).view(-1, K)
+        want, most = X @ W.T, X.abs() @ W.abs().T * (7 * 2.0 ** -13 + (K // 128 + 20) * 2.0 ** -23)
+        off = (got[rows, n:n + step].double() - want).abs()
+        assert (off <= most + 2.0 ** -8 * (want.abs() + most)).all(), (n, (off - most).max().item())
+        assert off.norm() <= (2.0 ** -8 / 3 ** 0.5 + 4e-5) * want.norm()
+    assert same(got, qmx.qmm_f8(w, ws, x, xs))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 40, 100, 300])
 def test_product_long_rows(M):
