@@ -74,10 +74,10 @@ __device__ __forceinline__ double squares8(u32x4 h, double sum) {
 // Whether y, off by at most three of its last digits (three roundings of half a
 // digit, of a number up to twice its power of two), rounds to a code as what it
 // stands for does, for all eight: magnitudes of 2^-60 to 2^100 (`most` the largest),
-// none within three of a number of five digits, as middles between codes are.  (w
-// below 2^60 then leaves h * rstd a normal number.)
+// none within three of a number of five digits, as middles between codes are (w below
+// 2^60 then leaves h * rstd a normal number); or all 0 because h is, as in padding.
 template <int DT>
-__device__ __forceinline__ bool clear_of_middles(const float (&y)[8], u32x4 w, uint32_t most) {
+__device__ __forceinline__ bool clear_of_middles(const float (&y)[8], u32x4 h, u32x4 w, uint32_t most) {
     uint32_t least = 0xffffffffu, near = 0xffffffffu, heavy = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -89,7 +89,9 @@ __device__ __forceinline__ bool clear_of_middles(const float (&y)[8], u32x4 w, u
 #pragma unroll
         for (int i = 0; i < 4; ++i) heavy = max(heavy, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
     }
-    return least >= (127u - 60u) << 23 && most <= (127u + 100u) << 23 && near > 6u && heavy < (127u + 60u) << 7;
+    const bool clear = least >= (127u - 60u) << 23 && most <= (127u + 100u) << 23 && near > 6u;
+    const bool none = ((h[0] | h[1] | h[2] | h[3]) & 0x7fff7fffu) == 0 && most == 0;
+    return (clear && heavy < (127u + 60u) << 7) || none;
 }
 
 __device__ __forceinline__ uint32_t most_of(const float (&y)[8]) {
@@ -124,7 +126,7 @@ __device__ __forceinline__ void finish8(const NormArgs& a, size_t row, int at, i
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = elem<DT>(h, i) * r.rounded * elem<DT>(w, i);
     uint32_t most = F8 ? most_of(y) : 0;
-    if (!r.ordinary || (F8 && n > 0 && !clear_of_middles<DT>(y, w, most))) {
+    if (!r.ordinary || (F8 && n > 0 && !clear_of_middles<DT>(y, h, w, most))) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = to_odd((double)elem<DT>(h, i) * r.whole * (double)elem<DT>(w, i));
         if (F8) most = most_of(y);

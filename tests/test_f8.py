@@ -322,6 +322,30 @@ def test_norm_ranges(dtype):
 
 
 @pytest.mark.gpu
+def test_norm_of_nothing_and_next_to_nothing():
+    """Groups of zeros, with weights of any kind, and groups that only a large weight brings back into range."""
+    x = torch.zeros(6, 640)
+    x[:, :128] = 2.0 ** 30
+    x[1, 128:256] = 2.0 ** -133
+    x[2, 256::3] = 2.0 ** -120
+    x[3, 130] = -2.0 ** -133
+    x[4, 128:] = -0.0
+    x[5] = 0
+    x = x.bfloat16()
+    w = torch.ones(640)
+    w[128:] = 2.0 ** 59
+    w[384:512] = 2.0 ** 127
+    w[512:514] = torch.tensor([math.inf, math.nan])
+    w = w.bfloat16()
+    for weight in (w, w.flip(0), None):
+        for lead in (1, 400):   # few rows and many
+            codes, scales = qmx.rms_norm_f8(x.to(DEV).repeat(lead, 1), None if weight is None else weight.to(DEV))
+            y, _ = ref.norm(x, weight, None, 1e-6)
+            y = torch.where(y.abs() > torch.finfo(torch.float32).max, math.inf, y)
+            check_codes(codes.view(torch.uint8)[-6:].view(codes.dtype), scales.view(torch.uint8)[-6:].view(scales.dtype), y)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("width", [640, 5000, 20480])
 def test_norm_in_place(width):
     """The sum over x or over the residual, the result over x."""
