@@ -46,7 +46,7 @@
 // other.  Cut by splits of one length for all requests, as the host alone could do
 // it, they took 55 + 14 and 40 + 4 us.  Pairs read by every lane that needs them
 // instead of shared by a row cost 72 registers and 20 % of the time.  Heads of 256
-// spill 46 registers in groups of 64 and 230 in groups of 32, whose 48 tokens over up
+// spill 46 registers in groups of 64 and 225 in groups of 32, whose 48 tokens over up
 // to 8000 take 72 and 239 us (groups of 128, none spilled: 43).
 #pragma once
 

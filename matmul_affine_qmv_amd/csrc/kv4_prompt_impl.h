@@ -19,8 +19,8 @@
 // costs a sixth.  Keys of rounded numbers instead of exact scores took the same
 // time, with scores off by 2^-12 each.  Groups of 32 and 128: 716 and 657 where 64
 // take 670; heads of 64 491; float16 940 (groups of 32 2080, of 128 910; heads of 64
-// 650).  What is spilled: of float16 at 128, 8 registers in groups of 128, 16 of 64
-// and 70 of 32; at 256, 9 to 40.
+// 650).  What is spilled: of float16 at 128, 1 register in groups of 128, 15 of 64
+// and 60 of 32; at 256, 8 to 39.
 //
 //   S^T[key, row] = K Q^T,  O^T[dim, row] += V^T P:  v_mfma_32x32x16, where the
 //   probabilities that a lane computes are the operand it needs (as in

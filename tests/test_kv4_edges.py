@@ -285,6 +285,55 @@ def test_queries_past_their_bound(each, most, kv):
 
 
 @on_gpu
+@pytest.mark.parametrize("R,most,kv", [(70, 3, 40), (700, 1, 40), (700, 2, 1700), (1100, 3, 33), (1, 1, 3000)])
+def test_many_requests_past_their_bound(R, most, kv):
+    """Some of many requests have more queries than the bound: zeros and -inf there, and nowhere else."""
+    say("many past the bound", R, most, kv)
+    rng = np.random.default_rng(R)
+    D, heads = 64, 4
+    new = rng.integers(1, most + 1, R)
+    new[rng.integers(0, R, 1 + R // 20)] = rng.integers(most + 1, kv, 1 + R // 20)
+    new[-1] = most + 5
+    offsets = np.concatenate(([3], 3 + np.cumsum(new)))
+    T = int(offsets[-1]) + 2
+    cache = device_cache(ref.Cache(-(-kv // 64), 2, D, 64, 64, "bf16", rng))
+    table = torch.arange(-(-kv // 64), dtype=torch.int32, device=DEV).repeat(R, 1)
+    q = torch.from_numpy(rng.normal(0, 1, (T, heads, D))).bfloat16().to(DEV)
+    for limit in (kv, 2000):   # units whole and on a line
+        out, lse = qmx.kv4_attention(cache, q, table, ints([kv] * R), ints(offsets.tolist()), max_query_len=most,
+                                     max_kv_len=limit, return_lse=True, out=torch.full_like(q, 7.0))
+        within = torch.zeros(T, dtype=torch.bool)
+        for start, n in zip(offsets, new):
+            within[start:start + min(n, most)] = True
+        within = within.to(DEV)
+        assert not out[~within].any() and torch.isneginf(lse[~within]).all()
+        assert torch.isfinite(lse[within]).all() and (out[within].abs().amax(-1) > 0).all() and (out[within] != 7).any(-1).all()
+
+
+@on_gpu
+@pytest.mark.parametrize("kv", [1000, 4096])
+def test_tokens_past_a_bound_are_cleared_together(kv):
+    """All queries but one of a long prompt past the bound: 21 and 84 MB of zeros, which a copy's rate writes in 4 and
+    17 us, a few compute units in less than 1 ms, and one lane in more than 15."""
+    say("cleared together", kv)
+    rng = np.random.default_rng(kv)
+    cache = device_cache(ref.Cache(kv // 64 + 1, 8, 128, 64, 64, "bf16", rng))
+    q = torch.zeros(kv, 40, 128, dtype=torch.bfloat16, device=DEV)
+    table = torch.arange(kv // 64 + 1, dtype=torch.int32, device=DEV)[None]
+    lens, offsets, out = ints([kv]), ints([0, kv]), torch.empty_like(q)
+    times = []
+    for _ in range(4):
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        qmx.kv4_attention(cache, q, table, lens, offsets, max_query_len=1, max_kv_len=kv, out=out)
+        end.record()
+        torch.cuda.synchronize()
+        times.append(start.elapsed_time(end))
+    assert not out[1:].any()
+    assert min(times) < 3.0, times
+
+
+@on_gpu
 @pytest.mark.parametrize("D,group", [(64, 32), (128, 128), (256, 64)])
 @pytest.mark.parametrize("power", range(-133, -95, 3))
 def test_write_of_tiny_groups(D, group, power):
