@@ -509,9 +509,10 @@ typedef enum qmx_scale_type {
  * the two is given).  out_scales NULL: out is [rows, width] in `dtype`,
  * contiguous.  Otherwise out is e4m3 codes [rows, width], 8-byte aligned, and
  * out_scales [rows, width / 128] their E8M0 scales (width % 128 == 0, else
- * QMX_ERR_GROUP).  sum may be x or residual itself, row for row, and an out in
- * `dtype` may be x itself; otherwise outputs overlap nothing, nor sum's rows each
- * other (QMX_ERR_OVERLAP where rows or whole arguments coincide).  eps: finite and
+ * QMX_ERR_GROUP).  sum, and an out in `dtype`, may each be x or residual itself,
+ * row for row (not both the same); otherwise outputs share nothing with inputs or
+ * each other, nor sum's rows with each other (QMX_ERR_OVERLAP, by the bytes that rows
+ * take, unless it would take thousands of pairs of rows to find one).  eps: finite and
  * above 0.  The sum is formed in 64 bits.  A y in `dtype` is formed in float32 from
  * it and rounded once more; codes and scales are those of a y in 64 bits (beyond
  * float32's range it counts as infinite). */

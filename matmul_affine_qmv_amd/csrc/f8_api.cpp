@@ -46,6 +46,64 @@ bool apart(long long n, long long count, long long stride, long long sets, long 
     return (count <= 1 || stride >= n) && (sets <= 1 || set_stride >= span);
 }
 
+typedef __int128 wide;   // of addresses and strides: rows may be any distance apart
+
+// Where an argument's bytes are: runs of `n`, counted and apart by an outer and an
+// inner step, in bytes and not below 0.
+struct Area {
+    wide at, n, count[2], step[2];
+    wide span(int level) const {
+        return level == 2 ? n : span(level + 1) + (count[level] - 1) * step[level];
+    }
+};
+Area area(const void* p, int size, long long n, long long rows = 1, long long stride = 0, long long sets = 1,
+          long long set_stride = 0) {
+    Area a = {(wide)reinterpret_cast<uintptr_t>(p), (wide)n * size, {sets, rows},
+              {(wide)set_stride * size, (wide)stride * size}};
+    for (int i = 0; i < 2; ++i) {
+        if (a.count[i] == 1) a.step[i] = 0;
+        if (a.step[i] < 0) {
+            a.at += (a.count[i] - 1) * a.step[i];
+            a.step[i] = -a.step[i];
+        }
+        if (a.step[i] == 0) a.count[i] = 1;   // the same run again
+    }
+    if (a.step[0] < a.step[1]) {
+        std::swap(a.step[0], a.step[1]);
+        std::swap(a.count[0], a.count[1]);
+    }
+    return a;
+}
+
+wide floor_div(wide a, wide b) { return a / b - (a % b < 0 ? 1 : 0); }   // b above 0
+
+// Whether x, from level i of its steps on, and y, from level j on, share a byte.
+// Looks at up to `left` pairs of runs: two areas that are laid into one another with
+// different steps more often than that without a byte in common count as apart.
+bool share(Area x, int i, Area y, int j, int& left) {
+    if (--left < 0 || x.at + x.span(i) <= y.at || y.at + y.span(j) <= x.at) return false;
+    while (i < 2 && x.count[i] == 1) ++i;
+    while (j < 2 && y.count[j] == 1) ++j;
+    if (i == 2 && j == 2) return true;
+    if (i == 2 || (j < 2 && y.step[j] > x.step[i])) return share(y, j, x, i, left);
+    // x's outer step is the larger.  Where y's is the same, how many steps they are
+    // apart is all that matters.
+    const bool both = j < 2 && x.step[i] == y.step[j];
+    const wide step = x.step[i], x_span = x.span(i + 1), y_span = y.span(both ? j + 1 : j);
+    const wide first = std::max(both ? 1 - y.count[j] : (wide)0, floor_div(y.at - x.at - x_span, step) + 1);
+    const wide last = std::min(x.count[i] - 1, floor_div(y.at + y_span - x.at - 1, step));
+    const wide from = x.at;
+    for (wide k = first; k <= last && left > 0; ++k) {
+        x.at = from + k * step;
+        if (share(x, i + 1, y, both ? j + 1 : j, left)) return true;
+    }
+    return false;
+}
+bool share(const Area& x, const Area& y) {
+    int left = 4096;
+    return share(x, 0, y, 0, left);
+}
+
 int units() {
     const int cus = qmx::device_cu_count();
     return cus > 0 ? cus : 256;
@@ -75,8 +133,24 @@ int qmx_rms_norm(const void* x, long long x_row_stride, const void* residual, lo
     if (!is_aligned(x, 2) || !is_aligned(residual, 2) || !is_aligned(weight, 2) || !is_aligned(sum, 2) ||
         !is_aligned(out, out_scales ? 8 : 2))
         return QMX_ERR_ALIGN;
-    if (sum && (sum == out || !apart(width, rows, sum_row_stride, 1, 0))) return QMX_ERR_OVERLAP;
-    if (out_scales && (out == x || out == residual)) return QMX_ERR_OVERLAP;
+    if (sum && !apart(width, rows, sum_row_stride, 1, 0)) return QMX_ERR_OVERLAP;
+    const Area in[3] = {area(x, 2, width, rows, x_row_stride), area(residual, 2, width, rows, residual_row_stride),
+                        area(weight, 2, width)};
+    const long long in_strides[2] = {x_row_stride, residual_row_stride};
+    const Area to[3] = {area(sum, 2, width, rows, sum_row_stride), area(out, out_scales ? 1 : 2, (long long)rows * width),
+                        area(out_scales, 1, (long long)rows * (width / 128))};
+    const long long to_strides[2] = {sum_row_stride, width};
+    const void *from[3] = {x, residual, weight}, *into[3] = {sum, out, out_scales};
+    for (int i = 0; i < 3; ++i) {
+        if (!into[i]) continue;
+        for (int j = 0; j < 3; ++j) {
+            // rows over their own: each work-group reads a row before it writes it
+            const bool own = j < 2 && (i == 0 || (i == 1 && !out_scales)) && into[i] == from[j] &&
+                             (rows == 1 || to_strides[i] == in_strides[j]);
+            if (from[j] && !own && share(to[i], in[j])) return QMX_ERR_OVERLAP;
+            if (j < i && into[j] && share(to[i], to[j])) return QMX_ERR_OVERLAP;
+        }
+    }
     const qmx::NormArgs a = {x, residual, weight, sum, out, out_scales, x_row_stride, residual_row_stride,
                              sum_row_stride, rows, width, eps};
     return launch_status(qmx::launch_rms_norm(a, dtype, static_cast<hipStream_t>(stream)));

@@ -107,7 +107,8 @@ def rms_norm(x, weight=None, residual=None, *, eps=1e-6, sum_out=None, out=None)
 
     residual: added to x before; then (out, sum) are returned, sum being what was
     normed.  sum_out: where it goes, x or residual itself for instance.  out:
-    contiguous, x itself for instance."""
+    contiguous, x or residual itself for instance.  Over anything else of the call's
+    tensors both are refused."""
     first = _first(x)
     if first[3] != _current_device():
         with torch.cuda.device(first[3]):
