@@ -570,8 +570,8 @@ size_t qmx_qmm_f8_workspace_bytes(int M, int N, int K);
  * (QMX_F16 or QMX_BF16), unit element stride, tokens and heads *_stride elements
  * apart, any address of whole elements.  Either may have 0 heads (pointers may
  * then be NULL).  An output is its own input, stride for stride (what does not
- * turn is then left alone), or overlaps nothing; its heads never each other
- * (QMX_ERR_OVERLAP).  positions: int32 [tokens]; frequencies: float64 [pairs],
+ * turn is then left alone), or overlaps nothing of the call; its heads never each
+ * other (QMX_ERR_OVERLAP, found as qmx_rms_norm finds it).  positions: int32 [tokens]; frequencies: float64 [pairs],
  * radians a position; the angle is taken in 64 bits, its sine and cosine in 32, the
  * result is rounded once.  head_dim: 2 to 4096; 2 <= 2 * pairs <= head_dim; at most 8192 heads each; scale finite. */
 int qmx_rope(const void* q, long long q_token_stride, long long q_head_stride, void* q_out,

@@ -220,9 +220,6 @@ int qmx_rope(const void* q, long long q_token_stride, long long q_head_stride, v
     if (!is_aligned(q, 2) || !is_aligned(q_out, 2) || !is_aligned(k, 2) || !is_aligned(k_out, 2) ||
         !is_aligned(positions, 4) || !is_aligned(frequencies, 8))
         return QMX_ERR_ALIGN;
-    if ((heads > 0 && !apart(head_dim, heads, q_out_head_stride, tokens, q_out_token_stride)) ||
-        (kv_heads > 0 && !apart(head_dim, kv_heads, k_out_head_stride, tokens, k_out_token_stride)))
-        return QMX_ERR_OVERLAP;
     qmx::RopeArgs a = {};
     a.in[0] = q;
     a.in[1] = k;
@@ -245,9 +242,23 @@ int qmx_rope(const void* q, long long q_token_stride, long long q_head_stride, v
     a.pairs = pairs;
     a.scale = scale;
     a.interleaved = interleaved != 0;
-    for (int i = 0; i < 2; ++i)
+    Area from[2], to[2];
+    for (int i = 0; i < 2; ++i) {
         a.in_place[i] = a.in[i] == a.out[i] && (a.in_ts[i] == a.out_ts[i] || tokens == 1) &&
                         (a.in_hs[i] == a.out_hs[i] || a.heads[i] == 1);
+        if (a.heads[i] == 0) continue;
+        from[i] = area(a.in[i], 2, head_dim, a.heads[i], a.in_hs[i], tokens, a.in_ts[i]);
+        to[i] = area(a.out[i], 2, head_dim, a.heads[i], a.out_hs[i], tokens, a.out_ts[i]);
+        if (!apart(head_dim, a.heads[i], a.out_hs[i], tokens, a.out_ts[i]) ||
+            share(to[i], area(positions, 4, tokens)) || share(to[i], area(frequencies, 8, pairs)))
+            return QMX_ERR_OVERLAP;
+    }
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j) {
+            if (a.heads[i] == 0 || a.heads[j] == 0) continue;
+            if (!(i == j && a.in_place[i]) && share(to[i], from[j])) return QMX_ERR_OVERLAP;
+            if (j < i && share(to[i], to[j])) return QMX_ERR_OVERLAP;
+        }
     return launch_status(qmx::launch_rope(a, dtype, static_cast<hipStream_t>(stream)));
 }
 

@@ -91,3 +91,61 @@ def test_norm_into_the_residual(width):
         dx, dr = apart(x, 3, 1) if over else x.to(DEV), r.to(DEV)
         got, total = qmx.rms_norm(dx, w, dr, sum_out=dx if over else None, out=dr)
         assert got is dr and same(dr, y) and same(total, h) and same(dx, h if over else x)
+
+
+@fake_ptr_test
+def test_rope_refuses_outputs_over_heads():
+    """An output may be its own input, stride for stride; anything else that shares a byte is refused."""
+    T, H, G, D = 3, 4, 2, 64
+    fused = dict(qs=(512, 64), os=(512, 64), ks=(512, 64), kos=(512, 64))   # of 8 heads
+
+    def rope(q=0, qs=(H * D, D), qo=20000, os=(H * D, D), k=40000, ks=(G * D, D), ko=60000, kos=(G * D, D), pos=80000,
+             f=80104, T=T, H=H, G=G):
+        at = [BASE + v for v in (q, qo, k, ko, pos, f)]
+        return qmx.lib().qmx_rope(at[0], *qs, at[1], *os, H, at[2], *ks, at[3], *kos, G, at[4], at[5], T, D, D // 2, 0, 1.0,
+                                  BF16, None)
+
+    good = [dict(), dict(qo=0), dict(ko=40000), dict(qo=0, ko=40000), dict(q=40000), dict(fused, qo=0, k=512, ko=512),
+            dict(fused, qo=0, k=512), dict(fused, k=512, ko=512), dict(fused, k=512, qo=40000, ko=40512),
+            dict(fused, q=0, k=512, qo=768, os=(512, 64), H=2, G=2, ko=1000000),   # each its own quarter of a token
+            dict(T=1, qs=(5, 64), qo=0, os=(9999, 64)), dict(H=1, qs=(64, 7), qo=0, os=(64, 64)), dict(H=0, qo=40000, G=2),
+            dict(G=0, ko=0), dict(qs=(0, 64)), dict(k=0, ks=(H * D, D), ko=40000),
+            dict(qs=(192 * 4, 192), k=128, ks=(192 * 4, 192), G=4, qo=0, os=(192 * 4, 192), ko=128, kos=(192 * 4, 192))]
+    bad = [dict(fused, qo=40000, ko=40512), dict(qo=0, os=(512, 64)), dict(qs=(512, 64), qo=0), dict(qs=(64, 256), qo=0, os=(256, 64)), dict(qo=2),
+           dict(qo=512), dict(qo=2 * H * D * T - 2), dict(qo=40000), dict(ko=0), dict(qo=60000), dict(qo=60000 + 128),
+           dict(qo=0, ko=0), dict(qo=79000), dict(ko=80000), dict(ko=80104 - 2), dict(qo=80000 - 2 * H * D * T + 4),
+           dict(fused, qo=0, k=510, ko=1000000), dict(fused, qo=0, k=512, ko=514), dict(fused, qo=0, k=512, ko=512 - 128),
+           dict(ko=40000, kos=(128, 64), ks=(129, 64)), dict(T=2, qs=(5, 64), qo=0, os=(9999, 64)), dict(qo=0, qs=(0, 64)),
+           dict(q=40000, ko=40000), dict(k=0, ks=(H * D, D), qo=0, ko=0, kos=(H * D, D))]
+    for case in good:
+        assert rope(**case) == ELAUNCH, case
+    for case in bad:
+        assert rope(**case) == EOVER, case
+
+
+@fake_ptr_test
+def test_rope_overlaps_by_their_bytes():
+    """Keys turned into places among the queries', against the bytes themselves."""
+    T, D = 3, 2
+    layouts = [(2, 8, 2), (3, 6, 2), (2, 12, 5), (2, 2, 9), (1, 4, 0), (4, 8, 2), (2, -8, 2)]   # heads, token and head strides
+    for (H, ts, hs), (G, kts, khs), off in itertools.product(layouts, layouts, range(-60, 61, 7)):
+        q, ko = BASE, BASE + 2 * off
+        shared = elements(q, D, H, hs, 2, T, ts) & elements(ko, D, G, khs, 2, T, kts)
+        got = qmx.lib().qmx_rope(q, ts, hs, BASE + 10000, 8, 2, H, BASE + 20000, 8, 2, ko, kts, khs, G, BASE + 30000,
+                                 BASE + 31000, T, D, 1, 0, 1.0, F16, None)
+        assert got == (EOVER if shared else ELAUNCH), (H, ts, hs, G, kts, khs, off)
+
+
+@pytest.mark.gpu
+def test_rope_refuses_views_over_their_own_heads():
+    T, H, D = 5, 4, 64
+    room = torch.randn(T * H * 96, generator=gen(3)).half().to(DEV)
+    q, view = room.view(T, H, 96)[..., :D], room[:T * H * D].view(T, H, D)
+    at, f = torch.arange(T, dtype=torch.int32, device=DEV), qmx.rope_frequencies(D, device=DEV)
+    other, before = torch.empty_like(view), room.clone()
+    for call in (lambda: qmx.rope(q, None, at, f, out=(view, None)), lambda: qmx.rope(q, q, at, f, out=(q, q)),
+                 lambda: qmx.rope(q, q, at, f, out=(other, other)), lambda: qmx.rope(q, q, at, f, out=(q, other)),
+                 lambda: qmx.rope(q[:, :2], q[:, 1:], at, f, out=(q[:, :2], q[:, 1:]))):
+        with pytest.raises(qmx.QmxError, match="overlap"):
+            call()
+    assert same(room, before)
