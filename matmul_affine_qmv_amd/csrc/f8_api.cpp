@@ -48,39 +48,57 @@ bool apart(long long n, long long count, long long stride, long long sets, long 
 
 typedef __int128 wide;   // of addresses and strides: rows may be any distance apart
 
-// Where an argument's bytes are: runs of `n`, counted and apart by an outer and an
-// inner step, in bytes and not below 0.
+// Where an argument's bytes are: `rows` runs of n elements, `sets` times.
 struct Area {
-    wide at, n, count[2], step[2];
-    wide span(int level) const {
-        return level == 2 ? n : span(level + 1) + (count[level] - 1) * step[level];
-    }
+    const void* p;
+    int size;   // of an element
+    long long n, rows, stride, sets, set_stride;
+    long long lo, hi;   // its first byte and the one behind its last,
+    bool beyond;        // unless 64 bits do not hold that
 };
 Area area(const void* p, int size, long long n, long long rows = 1, long long stride = 0, long long sets = 1,
           long long set_stride = 0) {
-    Area a = {(wide)reinterpret_cast<uintptr_t>(p), (wide)n * size, {sets, rows},
-              {(wide)set_stride * size, (wide)stride * size}};
-    for (int i = 0; i < 2; ++i) {
-        if (a.count[i] == 1) a.step[i] = 0;
-        if (a.step[i] < 0) {
-            a.at += (a.count[i] - 1) * a.step[i];
-            a.step[i] = -a.step[i];
-        }
-        if (a.step[i] == 0) a.count[i] = 1;   // the same run again
-    }
-    if (a.step[0] < a.step[1]) {
-        std::swap(a.step[0], a.step[1]);
-        std::swap(a.count[0], a.count[1]);
-    }
+    Area a = {p, size, n, rows, stride, sets, set_stride};
+    long long row, set, bytes;
+    a.beyond = __builtin_mul_overflow((rows - 1) * size, stride, &row) |
+               __builtin_mul_overflow((sets - 1) * size, set_stride, &set) |
+               __builtin_mul_overflow(n, (long long)size, &bytes);
+    a.lo = a.hi = (long long)reinterpret_cast<uintptr_t>(p);
+    a.beyond |= row < 0 ? __builtin_add_overflow(a.lo, row, &a.lo) : __builtin_add_overflow(a.hi, row, &a.hi);
+    a.beyond |= set < 0 ? __builtin_add_overflow(a.lo, set, &a.lo) : __builtin_add_overflow(a.hi, set, &a.hi);
+    a.beyond |= __builtin_add_overflow(a.hi, bytes, &a.hi);
     return a;
 }
+
+// The same as runs of n bytes, counted and apart by an outer and an inner step.
+struct Runs {
+    wide at, n, count[2], step[2];   // steps not below 0
+
+    explicit Runs(const Area& a)
+        : at((wide)reinterpret_cast<uintptr_t>(a.p)), n((wide)a.n * a.size), count{a.sets, a.rows},
+          step{(wide)a.set_stride * a.size, (wide)a.stride * a.size} {
+        for (int i = 0; i < 2; ++i) {
+            if (count[i] == 1) step[i] = 0;
+            if (step[i] < 0) {
+                at += (count[i] - 1) * step[i];
+                step[i] = -step[i];
+            }
+            if (step[i] == 0) count[i] = 1;   // the same run again
+        }
+        if (step[0] < step[1]) {
+            std::swap(step[0], step[1]);
+            std::swap(count[0], count[1]);
+        }
+    }
+    wide span(int level) const { return level == 2 ? n : span(level + 1) + (count[level] - 1) * step[level]; }
+};
 
 wide floor_div(wide a, wide b) { return a / b - (a % b < 0 ? 1 : 0); }   // b above 0
 
 // Whether x, from level i of its steps on, and y, from level j on, share a byte.
 // Looks at up to `left` pairs of runs: two areas that are laid into one another with
 // different steps more often than that without a byte in common count as apart.
-bool share(Area x, int i, Area y, int j, int& left) {
+bool share(Runs x, int i, const Runs& y, int j, int& left) {
     if (--left < 0 || x.at + x.span(i) <= y.at || y.at + y.span(j) <= x.at) return false;
     while (i < 2 && x.count[i] == 1) ++i;
     while (j < 2 && y.count[j] == 1) ++j;
@@ -100,8 +118,9 @@ bool share(Area x, int i, Area y, int j, int& left) {
     return false;
 }
 bool share(const Area& x, const Area& y) {
+    if (!x.beyond && !y.beyond && (x.hi <= y.lo || y.hi <= x.lo)) return false;
     int left = 4096;
-    return share(x, 0, y, 0, left);
+    return share(Runs(x), 0, Runs(y), 0, left);
 }
 
 int units() {
@@ -137,7 +156,8 @@ int qmx_rms_norm(const void* x, long long x_row_stride, const void* residual, lo
     const Area in[3] = {area(x, 2, width, rows, x_row_stride), area(residual, 2, width, rows, residual_row_stride),
                         area(weight, 2, width)};
     const long long in_strides[2] = {x_row_stride, residual_row_stride};
-    const Area to[3] = {area(sum, 2, width, rows, sum_row_stride), area(out, out_scales ? 1 : 2, (long long)rows * width),
+    const Area to[3] = {area(sum, 2, width, rows, sum_row_stride),
+                        area(out, out_scales ? 1 : 2, (long long)rows * width),
                         area(out_scales, 1, (long long)rows * (width / 128))};
     const long long to_strides[2] = {sum_row_stride, width};
     const void *from[3] = {x, residual, weight}, *into[3] = {sum, out, out_scales};
