@@ -556,6 +556,13 @@ int qmx_qmm_f8(const uint8_t* w, const void* w_scales, int w_scale_type, const u
                const uint8_t* x_scales, void* out, int M, int N, int K, int dtype,
                void* workspace, size_t workspace_bytes, void* stream);
 
+/* qmx_plan_f8 -- the tile that qmx_qmm_f8 takes for these sizes on a device with
+ * num_cus compute units (num_cus <= 0: 256), rows of x by rows of w, and the parts it
+ * cuts K into (1: none): 16 or 32 by 16 for few rows of x, straight from memory;
+ * 32 x 64, 64 x 64 and 64 x 128; 128 x 128 and 256 x 256, one after the other.  0 by 0
+ * for empty problems.  Performs no HIP call.  The pointers are host pointers. */
+int qmx_plan_f8(int M, int N, int K, int num_cus, int* tile_rows, int* tile_cols, int* splits);
+
 /* Workspace bytes qmx_qmm_f8 needs (0 for arguments it refuses).  Depends on the
  * compute units of the current device. */
 size_t qmx_qmm_f8_workspace_bytes(int M, int N, int K);

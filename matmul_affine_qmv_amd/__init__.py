@@ -77,6 +77,7 @@ _EXPORTS = {
                           + [ctypes.c_int] * 4 + [ctypes.c_void_p]),
     "qmx_qmm_f8": (ctypes.c_int, [ctypes.c_void_p] * 2 + [ctypes.c_int] + [ctypes.c_void_p] * 3 + [ctypes.c_int] * 4
                    + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qmx_plan_f8": (ctypes.c_int, [ctypes.c_int] * 4 + [ctypes.POINTER(ctypes.c_int)] * 3),
     "qmx_qmm_f8_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 3),
     "qmx_rope": (ctypes.c_int, ([ctypes.c_void_p] + [ctypes.c_longlong] * 2) * 2 + [ctypes.c_int]
                  + ([ctypes.c_void_p] + [ctypes.c_longlong] * 2) * 2 + [ctypes.c_int] + [ctypes.c_void_p] * 2
@@ -498,10 +499,11 @@ def tensor_bits(t: torch.Tensor):
 
 from .kv4 import (Kv4Cache, KvMaps, kv4_attention, kv4_attention_workspace_bytes, kv4_read,  # noqa: E402
                   kv4_write, kv_maps)
-from .f8 import (f8_dequantize, f8_quantize, qmm_f8, qmm_f8_workspace_bytes, rms_norm, rms_norm_f8)  # noqa: E402
+from .f8 import (f8_dequantize, f8_quantize, plan_f8, qmm_f8, qmm_f8_workspace_bytes, rms_norm,  # noqa: E402
+                 rms_norm_f8)
 from .rope import rope, rope_frequencies  # noqa: E402
 
-__all__ = ["rms_norm", "rms_norm_f8", "f8_quantize", "f8_dequantize", "qmm_f8", "qmm_f8_workspace_bytes",
+__all__ = ["rms_norm", "rms_norm_f8", "f8_quantize", "f8_dequantize", "qmm_f8", "qmm_f8_workspace_bytes", "plan_f8",
            "rope", "rope_frequencies",
            "Kv4Cache", "KvMaps", "kv_maps", "kv4_write", "kv4_read", "kv4_attention",
            "kv4_attention_workspace_bytes",

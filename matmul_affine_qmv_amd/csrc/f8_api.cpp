@@ -200,6 +200,26 @@ int qmx_f8_dequantize(const uint8_t* codes, const void* scales, int scale_type, 
                                                    block_rows, dtype, static_cast<hipStream_t>(stream)));
 }
 
+int qmx_plan_f8(int M, int N, int K, int num_cus, int* tile_rows, int* tile_cols, int* splits) {
+    const int rc = check_product(M, N, K);
+    if (rc) return rc;
+    if (!tile_rows || !tile_cols || !splits) return QMX_ERR_NULL;
+    *tile_rows = *tile_cols = 0;
+    *splits = 1;
+    if (M == 0 || N == 0 || K == 0) return QMX_OK;
+    const qmx::F8Plan p = qmx::f8_plan(M, N, K, num_cus > 0 ? num_cus : 256);
+    *splits = p.splits;
+    switch (p.tile) {
+        case qmx::F8_ROWS: *tile_rows = M <= 16 ? 16 : 32; *tile_cols = 16; break;
+        case qmx::F8_32x64: *tile_rows = 32; *tile_cols = 64; break;
+        case qmx::F8_64x64: *tile_rows = 64; *tile_cols = 64; break;
+        case qmx::F8_64x128: *tile_rows = 64; *tile_cols = 128; break;
+        case qmx::F8_128x128: *tile_rows = *tile_cols = 128; break;
+        default: *tile_rows = *tile_cols = 256; break;
+    }
+    return QMX_OK;
+}
+
 size_t qmx_qmm_f8_workspace_bytes(int M, int N, int K) {
     if (check_product(M, N, K) || M == 0 || N == 0 || K == 0) return 0;
     const int splits = qmx::f8_plan(M, N, K, units()).splits;

@@ -9,6 +9,7 @@ synchronises or copies to the host, so a step can be captured into a graph.
 """
 from __future__ import annotations
 
+import ctypes
 from functools import lru_cache
 
 import torch
@@ -196,6 +197,16 @@ def f8_dequantize(codes, scales, *, dtype=torch.bfloat16, out=None):
     _check(_function("qmx_f8_dequantize")(codes.data_ptr(), scales.data_ptr(), kind, out.data_ptr(), rows, width,
                                           block_rows, code, _raw_stream(index)), "qmx_f8_dequantize")
     return out
+
+
+def plan_f8(M, N, K, num_cus=0):
+    """(tile rows, tile columns, parts of K) that qmm_f8 takes (qmx_plan_f8, a host rule)."""
+    tile_rows, tile_cols, splits = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
+    if not all(abs(size) <= _MOST for size in (M, N, K)):
+        raise ValueError("M, N and K must be below 2^31")
+    _check(lib().qmx_plan_f8(M, N, K, num_cus, ctypes.byref(tile_rows), ctypes.byref(tile_cols), ctypes.byref(splits)),
+           "qmx_plan_f8")
+    return tile_rows.value, tile_cols.value, splits.value
 
 
 @lru_cache(maxsize=4096)
