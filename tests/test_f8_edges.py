@@ -266,3 +266,51 @@ def test_product_of_few_rows_at_any_element(M, N, K, dtype):
         room = torch.full((M * N + 9,), 7.0, dtype=dtype, device=DEV)
         assert same(qmx.qmm_f8(*args, out=room[at:at + M * N].view(M, N)), want)
         assert (room[:at] == 7).all() and (room[at + M * N:] == 7).all()
+
+
+MORE_TILES = [((4100, 6200, 4224), (256, 256)), ((3000, 6200, 4224), (128, 128)), ((8200, 6205, 4224), (256, 256)),
+              ((8200, 6200, 4224), (256, 256)), ((3000, 6203, 4224), (128, 128)), ((4100, 6204, 4352), (256, 256))]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("f32", [False, True], ids=["e8m0", "f32"])
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("size,tile", MORE_TILES)
+def test_product_of_prompts(size, tile, dtype, f32):
+    """More tiles than work-groups stay, over more groups than one chunk of scales, so that copies and the scales' two
+    places go on from tile to tile; results past the caches (from 48 Mi on), written eight, four and one at a time."""
+    say("prompts", size, dtype, f32)
+    _, _, parts = takes(*size, tile)
+    assert parts == 1
+    args = operands(*size, f32)
+    got = qmx.qmm_f8(*args, dtype=dtype)
+    hold(args, got, dtype)
+    assert same(got, qmx.qmm_f8(*args, dtype=dtype))
+
+
+# On 256 compute units: every tile whole and cut, with one chunk of scales and with more.
+TILES = {(32, 64): [(33, 300, 1024), (16, 1001, 8192), (16, 4100, 12800), (1, 1000, 5120)],
+         (64, 64): [(640, 4100, 128), (33, 14001, 5120), (33, 2048, 5120), (40, 4100, 12800)],
+         (64, 128): [(33, 20000, 1024), (48, 20004, 5120), (160, 2047, 12800), (1300, 512, 12800)],
+         (128, 128): [(1300, 14000, 128), (512, 4100, 5120), (128, 4097, 12800), (640, 2048, 12800)],
+         (256, 256): [(800, 14008, 1024), (2048, 4100, 5120), (300, 8192, 12800), (192, 20000, 12800)]}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("f32", [False, True], ids=["e8m0", "f32"])
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("tile,size", [(t, s) for t, sizes in TILES.items() for s in sizes])
+def test_product_of_every_tile(tile, size, dtype, f32):
+    say("every tile", tile, size, dtype, f32)
+    takes(*size, tile)
+    args = operands(*size, f32)
+    got = qmx.qmm_f8(*args, dtype=dtype)
+    hold(args, got, dtype)
+    assert same(got, qmx.qmm_f8(*args, dtype=dtype))
+
+
+@pytest.mark.parametrize("tile", TILES)
+def test_every_tile_is_cut_and_not(tile):
+    plans = [(qmx.plan_f8(*s), s[2] > 4096) for s in TILES[tile]]
+    assert all(p[:2] == tile for p, _ in plans)
+    assert {p[2] > 1 for p, _ in plans} == {False, True}
