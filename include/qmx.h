@@ -544,9 +544,14 @@ int qmx_f8_dequantize(const uint8_t* codes, const void* scales, int scale_type, 
  * (QMX_F16 or QMX_BF16), rounded once.  K % 128 == 0 (QMX_ERR_GROUP), below
  * 2^24; N at most 2^25, M 2^30, M * N some 2^36 (QMX_ERR_SHAPE); w and x 16-byte aligned,
  * out any address of whole elements.
- * Sums are float32, but for the matrix instruction's own: it aligns the scaled
- * products of 8 neighbouring k to the largest exponent among them and cuts each
- * 2^-13 below that (measured; 1.6e-5 of the result on normal numbers).  A code or scale
+ * Sums are float32, but for the matrix instruction's own: of 8 neighbouring k it cuts
+ * each product towards zero to a multiple of 2^(E - 13), E the largest sum of the
+ * exponents of two codes multiplied there (neither of them 0): at most 7 * 2^-13 of the
+ * largest of each 8, where codes are normal numbers.  How much that is of a result depends on how unlike the operands
+ * are: 1.5e-5 with random numbers, 4.5e-5 where one channel of x in 100 is 20 times as
+ * large as the others and 9.1e-5 where it is 1000 times (norms; a float16 out's own
+ * rounding is 2.1e-4, with these 2.09e-4, 2.11e-4 and 2.25e-4, a bfloat16 out's
+ * 1.7e-3).  A code or scale
  * that is NaN makes the outputs of its row or block NaN; a sum some part of which
  * leaves float32's range is infinite or NaN.
  * workspace: qmx_qmm_f8_workspace_bytes bytes, 16-byte aligned (NULL where that
@@ -578,9 +583,9 @@ size_t qmx_qmm_f8_workspace_bytes(int M, int N, int K);
  * apart, any address of whole elements.  Either may have 0 heads (pointers may
  * then be NULL).  An output is its own input, stride for stride (what does not
  * turn is then left alone), or overlaps nothing of the call; its heads never each
- * other (QMX_ERR_OVERLAP, found as qmx_rms_norm finds it).  positions: int32 [tokens]; frequencies: float64 [pairs],
- * radians a position; the angle is taken in 64 bits, its sine and cosine in 32, the
- * result is rounded once.  head_dim: 2 to 4096; 2 <= 2 * pairs <= head_dim; at most 8192 heads each; scale finite. */
+ * other (QMX_ERR_OVERLAP, found as qmx_rms_norm finds it).  positions: int32
+ * [tokens]; frequencies: float64 [pairs], radians a position; the angle is taken in 64
+ * bits, its sine and cosine in 32, the result is rounded once.  head_dim: 2 to 4096; 2 <= 2 * pairs <= head_dim; at most 8192 heads each; scale finite. */
 int qmx_rope(const void* q, long long q_token_stride, long long q_head_stride, void* q_out,
              long long q_out_token_stride, long long q_out_head_stride, int heads, const void* k,
              long long k_token_stride, long long k_head_stride, void* k_out,
