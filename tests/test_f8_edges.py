@@ -337,3 +337,106 @@ def test_what_the_products_lose(often):
     kept = cut_sums(w[:64], ws.float()[torch.arange(64) // 128], x, xs.float())
     size = spread(x, xs, 1, torch.float64).abs() @ spread(w, ws, 128, torch.float64).abs().T
     assert ((got[:, :64] - kept).abs() <= (K // 128 + 20) * 2.0 ** -23 * size[:, :64]).all()
+
+
+CUT = [(100, 128, 8192), (33, 2048, 5120), (160, 2047, 12800), (640, 2048, 12800), (192, 2000, 12800)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("M,N,K", CUT)
+def test_workspace_of_a_cut_product(M, N, K, dtype):
+    """A caller's workspace, whatever it holds, gives the same bits; one that is short or off its alignment is refused."""
+    say("workspace", M, N, K, dtype)
+    parts = qmx.plan_f8(M, N, K, torch.cuda.get_device_properties(0).multi_processor_count)[2]
+    need = qmx.qmm_f8_workspace_bytes(M, N, K)
+    assert parts > 1 and need == parts * M * N * 4
+    args = operands(M, N, K, True)
+    want = qmx.qmm_f8(*args, dtype=dtype)
+    hold(args, want, dtype)
+    room = torch.full((need + 64,), 0xff, dtype=torch.uint8, device=DEV)   # float32 NaNs
+    assert same(qmx.qmm_f8(*args, dtype=dtype, workspace=room[:need]), want) and (room[need:] == 0xff).all()
+    assert same(qmx.qmm_f8(*args, dtype=dtype, workspace=room[32:need + 32]), want)   # over the last call's sums
+    for short in (room[:need - 1], room[:0], room[8:need + 8], room[1:need + 1]):
+        with pytest.raises(qmx.QmxError):
+            qmx.qmm_f8(*args, dtype=dtype, workspace=short)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("given", [False, True], ids=["made", "given"])
+def test_cut_products_in_a_graph_and_on_streams(given):
+    """Two cut products and one that is not in one graph, with workspaces made while it is captured or one of the caller's
+    for both; replayed over new inputs between eager calls on the main and on a side stream."""
+    sizes = [(33, 2048, 5120), (100, 128, 8192), (40, 512, 512)]
+    say("graph", given)
+    buffers = [list(operands(*s, False, seed=0)) for s in sizes]
+    needs = [qmx.qmm_f8_workspace_bytes(*s) for s in sizes]
+    assert needs[0] and needs[1] and not needs[2]
+    room = torch.empty(max(needs), dtype=torch.uint8, device=DEV) if given else None
+
+    def step():
+        return [qmx.qmm_f8(*b, workspace=room) for b in buffers]
+
+    inputs = [[operands(*s, False, seed=i) for s in sizes] for i in range(1, 5)]
+    wanted = [[qmx.qmm_f8(*a) for a in i] for i in inputs]
+    for want, args in zip(wanted[0], inputs[0]):
+        hold(args, want, torch.bfloat16)
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    side = torch.cuda.Stream()
+    for args, want in zip(inputs + inputs, wanted + wanted):
+        for b, new in zip(buffers, args):
+            for old, fresh in zip(b, new):
+                old.view(torch.uint8).copy_(fresh.view(torch.uint8))
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            again = [qmx.qmm_f8(*a) for a in inputs[0]]
+        graph.replay()
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(out, want)) and all(same(a, b) for a, b in zip(again, wanted[0]))
+
+
+SPECIAL = [(1, 5001, 5248), (3, 4001, 3968), (19, 1001, 2176), (100, 260, 8192), (33, 2048, 5120), (48, 20004, 5120),
+           (512, 4100, 5120), (640, 2048, 12800), (2048, 4100, 5120), (192, 20000, 12800)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("f32", [False, True], ids=["e8m0", "f32"])
+@pytest.mark.parametrize("M,N,K", SPECIAL)
+def test_products_that_hold_nan(M, N, K, f32):
+    """NaN codes and scales of either operand, and an infinite float32 scale: NaN (not finite) in their row, column or block
+    and, to the bit, nothing else anywhere.  Rows and columns at the ends, where tiles repeat the last."""
+    say("nan", M, N, K, f32)
+    G, blocks = K // 128, -(-N // 128)
+    w, ws, x, xs = operands(M, N, K, f32)
+    clean = qmx.qmm_f8(w, ws, x, xs)
+    assert torch.isfinite(clean).all()
+    x, w, xs, ws = x.clone(), w.clone(), xs.clone(), ws.clone()
+    rows, cols = torch.zeros(M, dtype=torch.bool, device=DEV), torch.zeros(N, dtype=torch.bool, device=DEV)
+    for row, at in ((M - 1, K - 1), (M // 2, 130)) if M > 1 else ():
+        x.view(torch.uint8)[row, at] = 0x7f
+        rows[row] = True
+    if M > 16:
+        xs.view(torch.uint8)[5, G - 1] = 255
+        rows[5] = True
+    for col, at in ((N - 1, 0), (7, K - 2)):
+        w.view(torch.uint8)[col, at] = 0xff
+        cols[col] = True
+    last = slice(128 * (blocks - 1), N) if blocks > 2 else slice(0, 0)
+    if blocks > 2:
+        first = slice(128, 256)
+        if f32:
+            ws[1, G // 2] = float("nan")
+            ws[blocks - 1, G - 1] = float("inf")
+        else:
+            ws.view(torch.uint8)[1, G // 2] = 255
+        cols[first] = True
+    got = qmx.qmm_f8(w, ws, x, xs)
+    assert torch.isnan(got[rows]).all() and torch.isnan(got[:, cols]).all()
+    if f32 and blocks > 2:
+        assert not torch.isfinite(got[:, last]).any()
+        cols[last] = True
+    assert same(got[~rows][:, ~cols], clean[~rows][:, ~cols])
