@@ -440,3 +440,71 @@ def test_products_that_hold_nan(M, N, K, f32):
         assert not torch.isfinite(got[:, last]).any()
         cols[last] = True
     assert same(got[~rows][:, ~cols], clean[~rows][:, ~cols])
+
+
+# ---------------------------------------------------------------- sizes past 31 and 32 bits
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K,tile", [(300, 300, 2 ** 24 - 128, (64, 64)), (40, 300, 2 ** 24 - 128, (32, 64)),
+                                        (1, 300, 2 ** 24 - 128, (32, 64)), (70000, 33000, 128, (256, 256)),
+                                        (70001, 33003, 2176, (256, 256)), (2 ** 25, 70, 128, (128, 128)),
+                                        (3, 2 ** 25 - 3, 128, (16, 16)), (19, 2 ** 25 - 1, 128, (32, 64)),
+                                        (512, 600, 2 ** 24 - 128, (64, 128)), (512, 1000, 2 ** 24 - 128, (128, 128)),
+                                        (2048, 2048, 2 ** 24 - 128, (256, 256))])
+def test_products_of_the_largest_sizes(M, N, K, tile):
+    """Operands and results past 2^31 and 2^32 bytes.  A row of x has a single 1 under a power of two, so that a result is
+    one code of w under its scale, exactly."""
+    say("largest", M, N, K)
+    takes(M, N, K, tile)
+    g = torch.Generator(device=DEV).manual_seed(N)
+    torch.cuda.empty_cache()
+    w = torch.randint(0, 256, (N, K), generator=g, device=DEV, dtype=torch.uint8)
+    w &= 0xf7   # no NaN
+    ws = torch.randint(125, 130, (-(-N // 128), K // 128), generator=g, device=DEV, dtype=torch.uint8)
+    at = (torch.arange(M, device=DEV) * (K // 7 + 1) + K - 1) % K
+    x = torch.zeros(M, K, dtype=torch.uint8, device=DEV)
+    x[torch.arange(M, device=DEV), at] = 0x38
+    xs = torch.randint(125, 130, (M, K // 128), generator=g, device=DEV, dtype=torch.uint8)
+    got = qmx.qmm_f8(w.view(torch.float8_e4m3fn), ws, x.view(torch.float8_e4m3fn), xs)
+    values = ref.CODE.float().to(DEV)
+    places, which = torch.unique(at, return_inverse=True)
+    columns = values[w[:, places].int()].T.contiguous()                # [places, N]
+    columns *= torch.exp2(ws[:, places // 128].float() - 127).repeat_interleave(128, 0)[:N].T
+    rows = max(1, 2 ** 27 // N)
+    for m in range(0, M, rows):
+        want = columns[which[m:m + rows]] * torch.exp2(xs[m:m + rows].gather(1, at[m:m + rows, None] // 128).float() - 127)
+        assert torch.equal(got[m:m + rows].float(), want), m
+    del w, x, got, columns
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+def test_rows_past_2_to_the_31_elements():
+    """The last rows of 2.4e9 elements as of themselves."""
+    rows, width = 300000, 8192
+    x = torch.empty(rows, width, dtype=torch.half, device=DEV)
+    for r in range(0, rows, 20000):
+        x[r:r + 20000].normal_(generator=torch.Generator(device=DEV).manual_seed(r))
+    w = torch.randn(width, generator=gen(1)).half().to(DEV)
+    a = rows - 32 - rows % 32
+    a -= a % 128
+    tail = x[a:]
+    say("norm")
+    whole = qmx.rms_norm(x, w, x)
+    assert all(same(p[a:], q) for p, q in zip(whole, qmx.rms_norm(tail, w, tail)))
+    del whole
+    for name, f in (("norm f8", lambda t: qmx.rms_norm_f8(t, w)), ("groups", qmx.f8_quantize),
+                    ("blocks", lambda t: qmx.f8_quantize(t, block_rows=128))):
+        say(name)
+        codes, scales = f(x)
+        c, s = f(tail)
+        assert same(codes[a:], c) and same(scales[-len(s):], s)
+        back = qmx.f8_dequantize(codes, scales, dtype=torch.half)
+        assert same(back[a:], qmx.f8_dequantize(c, s, dtype=torch.half))
+        del back, codes
+    say("rope")
+    q = x.view(rows, 64, 128)
+    at, f = torch.arange(rows, dtype=torch.int32, device=DEV), qmx.rope_frequencies(128, device=DEV)
+    want = qmx.rope(q[a:], q[a:, :3], at[a:], f)
+    assert all(same(p[a:], t) for p, t in zip(qmx.rope(q, q[:, :3], at, f), want))
+    qmx.rope(q, None, at, f, out=(q, None))
+    assert same(q[a:], want[0])
