@@ -217,12 +217,15 @@ __device__ __forceinline__ TileAt tile_at(int t, int tiles_m, int tiles_n) {
 // beside the last row A and B are read from the next stage).  So what is copied has a
 // step and a half to come with two stages only, and the copies run on into the next
 // tile while one is finished and written.
-// Bound by the matrix cores and the card's power: 8192 x 14336 over K = 5120 takes 448
-// us, 2685 TFLOP/s (a library's 8-bit product without group scales: 2758), in which the
-// matrix cores are busy 66 % of the cycles and the clock is at 1.94 GHz.  Four waves of
-// 128 x 128 read a third less of LDS, but take 595 us: one wave on a SIMD waits at every
-// barrier.  Of 128 x 128 tiles a compute unit holds two work-groups, each filling the
-// other's waits: 1024 x 5120 over 14336 120 us, 139 with one of four stages.
+// Bound by the matrix cores and the card's power: 8192 x 14336 over K = 5120 takes 468
+// us among other calls, 2570 TFLOP/s (a library's 8-bit product without group scales:
+// 2758), in which the matrix cores are busy 66 % of the cycles; the clock that the power
+// limit leaves, 1.74 GHz under a profiler, makes that 455 to 520 from run to run.  With
+// float32 scales 552: each group's sum is multiplied and added by the vector ALU right
+// behind its product.  Four waves of 128 x 128 read a third less of LDS, but took a third
+// longer: one wave on a SIMD waits at every barrier.  Of 128 x 128 tiles a compute unit
+// holds two work-groups, each filling the other's waits: 2048 x 4096 over 4096 36.0 us,
+// 38.3 with one.
 // The scales of CHUNK groups stand beside the stages, the next ones' in a second place:
 // a lane's TM scales of x in neighbouring bytes, which the matrix instruction picks from
 // a register by itself.
@@ -460,9 +463,11 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(F8MmArgs a, int spli
     B[0] = frag(x_row(0), 0);
     const uintptr_t out_at = SPLIT ? 0 : reinterpret_cast<uintptr_t>(a.out);
     const int wide = a.N % 8 == 0 && out_at % 16 == 0 ? 8 : a.N % 4 == 0 && out_at % 8 == 0 ? 4 : 1;
-    // Results that no cache holds go past them: 8192 x 14336 over K = 5120 433 us and 465
-    // through them, 8192 x 8192 over 2560 151 and 159, but over 1280 103 and 95, and 1000
-    // x 28672 (57 MB) over 5120 145 and 137.
+    // Results that no cache holds go past them.  Among other calls that takes 143 us, and
+    // 156 through them, for 8192 x 8192 over K = 2560, 348 and 378 for 8192 x 20480, 204
+    // and 210 over 4096, but 468 and 461 for 8192 x 14336 over 5120, and 139 and 135 for
+    // 1000 x 28672 (57 MB).  A call after which the device is waited for pays for it where
+    // K is short: 109 and 101 for 8192 x 8192 over 1280 (91 and 98 among others).
     const bool pass = (long long)a.M * a.N >= (48ll << 20) && a.K >= 2048;
     for (;;) {
         // The chunk after this one, whose scales come while this one's first steps go.
