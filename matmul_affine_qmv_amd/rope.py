@@ -26,7 +26,11 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | N
     scaling "yarn":   f_i / factor and f_i blended linearly in i, between the pairs
                       that make `fast` and `slow` turns in original_length positions
                       (fast > slow); YaRN also scales what it turns by 0.1 ln(factor)
-                      + 1 (rope's `scale`)."""
+                      + 1 (rope's `scale`).  The published method blends linearly in
+                      turns.  Blending in i, from the pair rounded down to the one
+                      rounded up, these held to 0 .. rotary_dim - 1 and at least 0.001
+                      apart, is what the programs do that models are trained and run
+                      with, whose frequencies a model needs."""
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError(f"rotary_dim must be even and at least 2, got {rotary_dim}")
     if not base > 1 or not factor >= 1:

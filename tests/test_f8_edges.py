@@ -508,3 +508,20 @@ def test_rows_past_2_to_the_31_elements():
     assert all(same(p[a:], t) for p, t in zip(qmx.rope(q, q[:, :3], at, f), want))
     qmx.rope(q, None, at, f, out=(q, None))
     assert same(q[a:], want[0])
+
+
+def test_yarn_blends_in_the_number_of_a_pair():
+    """Against the steps that the docstring names, one pair at a time; ends past both ends of the pairs, and ends that meet."""
+    import math
+    for d, base, factor, length, fast, slow in ((128, 10000.0, 8.0, 4096, 32.0, 1.0), (64, 5e5, 32.0, 8192, 32.0, 1.0),
+                                                (32, 10000.0, 4.0, 64, 40.0, 2.0), (64, 100.0, 2.0, 10 ** 6, 2.0, 1e-3),
+                                                (8, 10000.0, 4.0, 9, 1.0001, 1.0)):
+        got = qmx.rope_frequencies(d, base, scaling="yarn", factor=factor, original_length=length, fast=fast, slow=slow,
+                                   device="cpu")
+        pair = [d * math.log(length / (turns * 2 * math.pi)) / (2 * math.log(base)) for turns in (fast, slow)]
+        lo = max(math.floor(pair[0]), 0)
+        hi = max(min(math.ceil(pair[1]), d - 1), lo + 0.001)
+        for i in range(d // 2):
+            f = base ** (-2 * i / d)
+            part = min(max((i - lo) / (hi - lo), 0.0), 1.0)
+            assert abs(got[i].item() / (f * (1 - part) + f / factor * part) - 1) < 1e-12, (d, i)
