@@ -585,7 +585,8 @@ size_t qmx_qmm_f8_workspace_bytes(int M, int N, int K);
  * turn is then left alone), or overlaps nothing of the call; its heads never each
  * other (QMX_ERR_OVERLAP, found as qmx_rms_norm finds it).  positions: int32
  * [tokens]; frequencies: float64 [pairs], radians a position; the angle is taken in 64
- * bits, its sine and cosine in 32, the result is rounded once.  head_dim: 2 to 4096; 2 <= 2 * pairs <= head_dim; at most 8192 heads each; scale finite. */
+ * bits, its sine and cosine in 32, the result is rounded once.  head_dim: 2 to 4096;
+ * 2 <= 2 * pairs <= head_dim; at most 8192 heads each; scale finite. */
 int qmx_rope(const void* q, long long q_token_stride, long long q_head_stride, void* q_out,
              long long q_out_token_stride, long long q_out_head_stride, int heads, const void* k,
              long long k_token_stride, long long k_head_stride, void* k_out,
